@@ -6,11 +6,11 @@ package does not load the library; the first use of an API name does, and
 raises if the library has not been built.
 """
 
-_API = ("Buffer", "EventOverlap", "capi")
+_API = ("Buffer", "EventOverlap", "ExpertOrder", "capi")
 
 
 def __getattr__(name):
-    if name in ("Buffer", "EventOverlap"):
+    if name in ("Buffer", "EventOverlap", "ExpertOrder"):
         from . import buffer
         return getattr(buffer, name)
     if name == "capi":

@@ -47,6 +47,14 @@ MOEDX_T_NUM_RECV = 8
 MOEDX_T_LL_SRC_IDX = 9
 MOEDX_T_LL_SLOT_OF = 10
 
+# element types
+MOEDX_BF16 = 0
+MOEDX_F16 = 1
+MOEDX_F32 = 2
+
+MOEDX_GATE_SOFTMAX = 0
+MOEDX_GATE_SIGMOID = 1
+
 
 class moedx_exec(ctypes.Structure):
     _fields_ = [("stream", ctypes.c_void_p), ("prev", ctypes.c_void_p),
@@ -66,6 +74,16 @@ class moedx_fp8(ctypes.Structure):
                 ("tensor_scale", ctypes.c_float), ("x_scales", ctypes.c_void_p)]
 
 
+class moedx_gate(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("groups", ctypes.c_int), ("groups_kept", ctypes.c_int),
+                ("renormalize", ctypes.c_int), ("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
+
+
+class moedx_expert_rows(ctypes.Structure):
+    _fields_ = [("offsets", ctypes.c_void_p), ("counts", ctypes.c_void_p),
+                ("rows", ctypes.c_int64)]
+
+
 class MoedxError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"moedx error {code}: {msg}")
@@ -78,6 +96,8 @@ _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _EX = ctypes.POINTER(moedx_exec)
+_GATE = ctypes.POINTER(moedx_gate)
+_ROWS = ctypes.POINTER(moedx_expert_rows)
 
 SIGNATURES = {
     "moedx_last_error": (ctypes.c_char_p, []),
@@ -108,6 +128,16 @@ SIGNATURES = {
     "moedx_ll_dispatch": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _SZ, _PP, _EX]),
     "moedx_ll_dispatch_recv": (_I, [_P, _P, _P, _P, _I, _P, _EX]),
     "moedx_ll_combine": (_I, [_P, _P, _P, _P, _P, _I, _P, _EX]),
+    "moedx_gate_topk": (_I, [_P, _P, _I, _I, _I, _GATE, _P, _P, _EX]),
+    "moedx_gate_topk_backward": (_I, [_P, _P, _I, _I, _I, _GATE, _P, _P, _P, _EX]),
+    "moedx_expert_order_workspace_bytes": (_I, [_P, _I, _I, ctypes.POINTER(_SZ)]),
+    "moedx_expert_order": (_I, [_P, _P, _I, _I, _P, _P, _P, _P, _P, _SZ, _EX]),
+    "moedx_expert_sort": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _EX]),
+    "moedx_expert_unsort": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _EX]),
+    "moedx_expert_unsort_backward": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _EX]),
+    "moedx_expert_linear": (_I, [_P, _P, _P, _I, _I, _I, _ROWS, _I, _P, _P, _EX]),
+    "moedx_expert_linear_backward": (_I, [_P, _P, _P, _P, _I, _I, _I, _ROWS, _P, _P, _I, _EX]),
+    "moedx_expert_swiglu_backward": (_I, [_P, _P, _P, _I, _I, _ROWS, _P, _EX]),
 }
 
 

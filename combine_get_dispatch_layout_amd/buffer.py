@@ -173,6 +173,24 @@ class Handle:
             self.ptr = None
 
 
+_DTYPES = {torch.bfloat16: C.MOEDX_BF16, torch.float16: C.MOEDX_F16, torch.float32: C.MOEDX_F32}
+_PRODUCT_DTYPES = (torch.bfloat16, torch.float16)
+_SCORES = {"softmax": C.MOEDX_GATE_SOFTMAX, "sigmoid": C.MOEDX_GATE_SIGMOID}
+
+
+class ExpertOrder:
+    """Rows in expert order (Buffer.expert_order): expert e has rows
+    [expert_offsets[e], expert_offsets[e + 1]); ``row_of_slot`` [T, K] is the
+    row of each pair (-1 = empty slot) and ``slot_of_row`` [T * K] its inverse
+    (t * K + k, -1 past the last row).  All int32 on the device."""
+
+    def __init__(self, expert_offsets: torch.Tensor, row_of_slot: torch.Tensor,
+                 slot_of_row: torch.Tensor):
+        self.expert_offsets = expert_offsets
+        self.row_of_slot = row_of_slot
+        self.slot_of_row = slot_of_row
+
+
 class Buffer:
     """One GPU's share of the expert-parallel exchange: ``num_ranks`` logical
     ranks are buckets of ``num_experts / num_ranks`` experts in this GPU's HBM."""
@@ -486,3 +504,302 @@ class Buffer:
         ex, done = self._exec(previous_event, async_finish, False, no_sync)
         run(ex)
         return combined, self._event(done), None
+
+    # -- router, rows in expert order, the experts' products -----------------------
+    def _check(self, name: str, t, dtypes, shape) -> torch.Tensor:
+        """`t` is a tensor on this Buffer's device, of one of `dtypes` and of
+        `shape` (None = any size); made contiguous."""
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a tensor")
+        if t.device != self._torch_device:
+            raise ValueError(f"{name} is on {t.device}, the Buffer on {self._torch_device}")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected one of {list(dtypes)}")
+        if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        return t.contiguous()
+
+    def _out(self, name: str, out, dtype, shape) -> torch.Tensor:
+        """`out` checked (it must be contiguous), or a new tensor."""
+        if out is None:
+            return torch.empty(shape, dtype=dtype, device=self._torch_device)
+        if self._check(name, out, (dtype,), shape) is not out:
+            raise ValueError(f"{name} must be contiguous")
+        return out
+
+    @property
+    def _torch_device(self) -> "torch.device":
+        return torch.device("cuda", self.device)
+
+    def _exec_here(self, previous_event, async_finish, allocate_on_comm_stream, no_sync):
+        """As _exec, on the current stream of this Buffer's device."""
+        if _deferred:
+            _flush_deferred()
+        done = ctypes.c_void_p() if async_finish else None
+        flags = (C.MOEDX_ON_CTX_STREAM if allocate_on_comm_stream else 0) | (
+            C.MOEDX_ASYNC if no_sync else 0)
+        prev = previous_event.event if previous_event is not None else None
+        stream = torch.cuda.current_stream(self.device).cuda_stream
+        return C.make_exec(stream, prev, done, flags), done
+
+    def _gate_options(self, score, num_groups, groups_kept, renormalize, scale, bias):
+        if score not in _SCORES:
+            raise ValueError(f"score={score!r} must be one of {sorted(_SCORES)}")
+        if bias is not None:
+            bias = self._check("bias", bias, (torch.float32,), (self.num_experts,))
+        return C.moedx_gate(_SCORES[score], num_groups,
+                            num_groups if groups_kept is None else groups_kept,
+                            1 if renormalize else 0, scale, _ptr(bias)), bias
+
+    def gate_topk(self, logits: torch.Tensor, topk: int, score: str = "softmax",
+                  num_groups: int = 1, groups_kept: Optional[int] = None,
+                  renormalize: bool = False, scale: float = 1.0,
+                  bias: Optional[torch.Tensor] = None,
+                  previous_event: Optional[EventOverlap] = None, async_finish: bool = False,
+                  allocate_on_comm_stream: bool = False, no_sync: bool = False):
+        """Returns (topk_idx [T, topk] int64, topk_weights [T, topk] fp32,
+        event) from the router's ``logits`` [T, E] (fp32, bf16 or fp16): what
+        get_dispatch_layout and dispatch take.  ``score``: "softmax" or
+        "sigmoid"; ``bias`` [E] fp32 is added to the scores for the choice
+        only; with ``num_groups`` > 1 only the ``groups_kept`` groups with the
+        best two-expert sums are chosen from; ``renormalize`` divides the
+        chosen scores by their sum; ``scale`` multiplies the weights.  Experts
+        with a logit of -inf or NaN are never chosen; slots that stay empty
+        are -1 with weight 0."""
+        logits = self._check("logits", logits, _DTYPES, (None, self.num_experts))
+        T = logits.shape[0]
+        opts, bias = self._gate_options(score, num_groups, groups_kept, renormalize, scale, bias)
+        dev = logits.device
+        idx = torch.empty(T, max(topk, 0), dtype=torch.int64, device=dev)
+        w = torch.empty(T, max(topk, 0), dtype=torch.float32, device=dev)
+        ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
+        C.check(C.moedx_gate_topk(self.ctx, _ptr(logits), _DTYPES[logits.dtype], T, topk,
+                                  ctypes.byref(opts), _ptr(idx), _ptr(w), ctypes.byref(ex)))
+        self._keep(allocate_on_comm_stream, logits, bias, idx, w)
+        return idx, w, self._event(done)
+
+    def gate_topk_backward(self, d_topk_weights: torch.Tensor, logits: torch.Tensor,
+                           topk_idx: torch.Tensor, score: str = "softmax", num_groups: int = 1,
+                           groups_kept: Optional[int] = None, renormalize: bool = False,
+                           scale: float = 1.0, bias: Optional[torch.Tensor] = None,
+                           previous_event: Optional[EventOverlap] = None,
+                           async_finish: bool = False, allocate_on_comm_stream: bool = False,
+                           no_sync: bool = False):
+        """Returns (d_logits [T, E] of the logits' dtype, event): the gradient
+        of gate_topk's weights for its choice ``topk_idx`` with the same
+        options (the choice, and so ``bias``, has no gradient)."""
+        logits = self._check("logits", logits, _DTYPES, (None, self.num_experts))
+        T = logits.shape[0]
+        topk_idx = self._check("topk_idx", topk_idx, (torch.int64,), (T, None))
+        K = topk_idx.shape[1]
+        dw = self._check("d_topk_weights", d_topk_weights, (torch.float32,), (T, K))
+        opts, bias = self._gate_options(score, num_groups, groups_kept, renormalize, scale, bias)
+        d = torch.empty_like(logits)
+        ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
+        C.check(C.moedx_gate_topk_backward(self.ctx, _ptr(logits), _DTYPES[logits.dtype], T, K,
+                                           ctypes.byref(opts), _ptr(topk_idx), _ptr(dw), _ptr(d),
+                                           ctypes.byref(ex)))
+        self._keep(allocate_on_comm_stream, logits, bias, topk_idx, dw, d)
+        return d, self._event(done)
+
+    def expert_order(self, topk_idx: torch.Tensor, handle: Optional[Handle] = None,
+                     previous_event: Optional[EventOverlap] = None, async_finish: bool = False,
+                     allocate_on_comm_stream: bool = False, no_sync: bool = False):
+        """Returns (ExpertOrder, event): the filled (token, slot) pairs of
+        ``topk_idx`` [T, K] sorted by expert, then token, then slot.  With
+        ``handle``, ``topk_idx`` is the recv_topk_idx of its first dispatch
+        (ids local to the row's bucket; rows past N are empty).  Nothing is
+        read on the host."""
+        topk_idx = self._check("topk_idx", topk_idx, (torch.int64,), (None, None))
+        T, K = topk_idx.shape
+        nbytes = ctypes.c_size_t()
+        C.check(C.moedx_expert_order_workspace_bytes(self.ctx, T, K, ctypes.byref(nbytes)))
+        dev = topk_idx.device
+        offsets = torch.empty(self.num_experts + 1, dtype=torch.int32, device=dev)
+        row_of_slot = torch.empty(T, K, dtype=torch.int32, device=dev)
+        slot_of_row = torch.empty(T * K, dtype=torch.int32, device=dev)
+        ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+        ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
+        C.check(C.moedx_expert_order(self.ctx, _ptr(topk_idx), T, K,
+                                     handle.ptr if handle is not None else None, _ptr(offsets),
+                                     _ptr(row_of_slot), _ptr(slot_of_row), _ptr(ws), nbytes.value,
+                                     ctypes.byref(ex)))
+        self._keep(allocate_on_comm_stream, topk_idx, offsets, row_of_slot, slot_of_row, ws,
+                   handle.workspace if handle is not None else None)
+        return ExpertOrder(offsets, row_of_slot, slot_of_row), self._event(done)
+
+    def expert_sort(self, x: torch.Tensor, order: ExpertOrder, out: Optional[torch.Tensor] = None,
+                    previous_event: Optional[EventOverlap] = None, async_finish: bool = False,
+                    allocate_on_comm_stream: bool = False, no_sync: bool = False):
+        """Returns (rows [T * K, H], event): every filled pair's row of ``x``
+        [T, H] (bf16, fp16 or fp32) in expert order.  Rows past the last pair
+        are left as they were (unspecified without ``out``)."""
+        T, K = order.row_of_slot.shape
+        x = self._check("x", x, _DTYPES, (T, None))
+        H = x.shape[1]
+        ros = self._check("row_of_slot", order.row_of_slot, (torch.int32,), (T, K))
+        rows = self._out("out", out, x.dtype, (T * K, H))
+        ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
+        C.check(C.moedx_expert_sort(self.ctx, _ptr(x), _DTYPES[x.dtype], T, K, H, _ptr(ros),
+                                    _ptr(rows), ctypes.byref(ex)))
+        self._keep(allocate_on_comm_stream, x, ros, rows)
+        return rows, self._event(done)
+
+    def expert_unsort(self, rows: torch.Tensor, order: ExpertOrder,
+                      topk_weights: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None,
+                      previous_event: Optional[EventOverlap] = None, async_finish: bool = False,
+                      allocate_on_comm_stream: bool = False, no_sync: bool = False):
+        """Returns (out [T, H], event): each token's rows back from expert
+        order, scaled by ``topk_weights`` [T, K] fp32 (None = 1) and summed in
+        fp32 over its filled slots; zero for a token without any."""
+        T, K = order.row_of_slot.shape
+        rows = self._check("rows", rows, _DTYPES, (T * K, None))
+        H = rows.shape[1]
+        ros = self._check("row_of_slot", order.row_of_slot, (torch.int32,), (T, K))
+        w = None if topk_weights is None else self._check("topk_weights", topk_weights,
+                                                          (torch.float32,), (T, K))
+        out = self._out("out", out, rows.dtype, (T, H))
+        ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
+        C.check(C.moedx_expert_unsort(self.ctx, _ptr(rows), _DTYPES[rows.dtype], T, K, H,
+                                      _ptr(ros), _ptr(w), _ptr(out), ctypes.byref(ex)))
+        self._keep(allocate_on_comm_stream, rows, ros, w, out)
+        return out, self._event(done)
+
+    def expert_sort_backward(self, d_rows: torch.Tensor, order: ExpertOrder,
+                             out: Optional[torch.Tensor] = None,
+                             previous_event: Optional[EventOverlap] = None,
+                             async_finish: bool = False, allocate_on_comm_stream: bool = False,
+                             no_sync: bool = False):
+        """Returns (d_x [T, H], event), the gradient of expert_sort: each
+        token's row gradients summed (expert_unsort without weights)."""
+        return self.expert_unsort(d_rows, order, None, out, previous_event, async_finish,
+                                  allocate_on_comm_stream, no_sync)
+
+    def expert_unsort_backward(self, d_out: torch.Tensor, rows: torch.Tensor, order: ExpertOrder,
+                               topk_weights: torch.Tensor, out: Optional[torch.Tensor] = None,
+                               previous_event: Optional[EventOverlap] = None,
+                               async_finish: bool = False, allocate_on_comm_stream: bool = False,
+                               no_sync: bool = False):
+        """Returns (d_rows [T * K, H], d_topk_weights [T, K] fp32, event), the
+        gradients of expert_unsort.  ``out``: where d_rows goes; rows past the
+        last pair are left as they were."""
+        T, K = order.row_of_slot.shape
+        rows = self._check("rows", rows, _DTYPES, (T * K, None))
+        H = rows.shape[1]
+        d_out = self._check("d_out", d_out, (rows.dtype,), (T, H))
+        ros = self._check("row_of_slot", order.row_of_slot, (torch.int32,), (T, K))
+        w = self._check("topk_weights", topk_weights, (torch.float32,), (T, K))
+        d_rows = self._out("out", out, rows.dtype, (T * K, H))
+        d_w = torch.empty(T, K, dtype=torch.float32, device=rows.device)
+        ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
+        C.check(C.moedx_expert_unsort_backward(self.ctx, _ptr(d_out), _ptr(rows),
+                                               _DTYPES[rows.dtype], T, K, H, _ptr(ros), _ptr(w),
+                                               _ptr(d_rows), _ptr(d_w), ctypes.byref(ex)))
+        self._keep(allocate_on_comm_stream, d_out, rows, ros, w, d_rows, d_w)
+        return d_rows, d_w, self._event(done)
+
+    def _expert_rows(self, rows, x: torch.Tensor):
+        """The moedx_expert_rows of x's leading dimensions: an ExpertOrder or
+        int32 offsets [E + 1] for [M, *], int32 counts [E] for [E, cap, *]."""
+        E = self.num_experts
+        t = rows.expert_offsets if isinstance(rows, ExpertOrder) else rows
+        if x.dim() == 3:
+            t = self._check("recv_count", t, (torch.int32,), (E,))
+            return C.moedx_expert_rows(None, _ptr(t), x.shape[0] * x.shape[1]), t
+        t = self._check("expert_offsets", t, (torch.int32,), (E + 1,))
+        return C.moedx_expert_rows(_ptr(t), None, x.shape[0]), t
+
+    def _lead(self, name: str, x) -> tuple:
+        """Leading dimensions of a row buffer: (M,) or (E, cap)."""
+        if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
+            raise ValueError(f"{name} must be a [M, *] or [num_experts, cap, *] tensor")
+        if x.dim() == 3 and x.shape[0] != self.num_experts:
+            raise ValueError(f"{name} has {x.shape[0]} experts, expected {self.num_experts}")
+        return tuple(x.shape[:-1])
+
+    def expert_linear(self, x: torch.Tensor, w: torch.Tensor, rows, swiglu: bool = False,
+                      return_pre: bool = False, out: Optional[torch.Tensor] = None,
+                      previous_event: Optional[EventOverlap] = None, async_finish: bool = False,
+                      allocate_on_comm_stream: bool = False, no_sync: bool = False):
+        """Returns (y, pre, event): every row of ``x`` times its expert's
+        matrix, y[m] = w[e] x[m], for ``w`` [E, N, K] (bf16 or fp16).  ``x`` is
+        [M, K] with ``rows`` an ExpertOrder (or its int32 expert_offsets
+        [E + 1]), or low_latency_dispatch's [E, cap, K] with ``rows`` its int32
+        recv_count [E].  With ``swiglu``, ``w`` is [E, 2N, K] (gate rows, then
+        up rows) and y = silu(gate) * up; ``return_pre`` also gives the rounded
+        (gate, up) values [*, 2N] that expert_swiglu_backward takes, else pre
+        is None.  Rows of no expert are left as they were (unspecified without
+        ``out``)."""
+        lead = self._lead("x", x)
+        x = self._check("x", x, _PRODUCT_DTYPES, lead + (None,))
+        K = x.shape[-1]
+        w = self._check("w", w, (x.dtype,), (self.num_experts, None, K))
+        N = w.shape[1]
+        if swiglu:
+            if N % 2 != 0:
+                raise ValueError(f"w has {N} rows per expert, expected gate and up halves")
+            N //= 2
+        elif return_pre:
+            raise ValueError("return_pre needs swiglu")
+        er, t = self._expert_rows(rows, x)
+        y = self._out("out", out, x.dtype, lead + (N,))
+        pre = torch.empty(lead + (2 * N,), dtype=x.dtype, device=x.device) if return_pre else None
+        ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
+        C.check(C.moedx_expert_linear(self.ctx, _ptr(x), _ptr(w), _DTYPES[x.dtype], K, N,
+                                      ctypes.byref(er), 1 if swiglu else 0, _ptr(y), _ptr(pre),
+                                      ctypes.byref(ex)))
+        self._keep(allocate_on_comm_stream, x, w, t, y, pre)
+        return y, pre, self._event(done)
+
+    def expert_linear_backward(self, d_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor, rows,
+                               out: Optional[torch.Tensor] = None,
+                               d_w: Optional[torch.Tensor] = None, d_w_dtype=None,
+                               previous_event: Optional[EventOverlap] = None,
+                               async_finish: bool = False, allocate_on_comm_stream: bool = False,
+                               no_sync: bool = False):
+        """Returns (d_x, d_w, event), the gradients of expert_linear without
+        its activation: d_x[m] = w[e]^T d_y[m] (rows of no expert left as they
+        were in ``out``) and d_w[e] = the sum of d_y[m] x[m]^T over e's rows
+        (zero without any), written to ``d_w`` (of w's dtype or fp32) or to a
+        new tensor of ``d_w_dtype`` (w's dtype by default)."""
+        lead = self._lead("x", x)
+        x = self._check("x", x, _PRODUCT_DTYPES, lead + (None,))
+        K = x.shape[-1]
+        w = self._check("w", w, (x.dtype,), (self.num_experts, None, K))
+        N = w.shape[1]
+        d_y = self._check("d_y", d_y, (x.dtype,), lead + (N,))
+        if d_w_dtype is None:
+            d_w_dtype = x.dtype if d_w is None else d_w.dtype
+        if d_w_dtype not in (x.dtype, torch.float32):
+            raise ValueError(f"d_w_dtype={d_w_dtype} must be {x.dtype} or torch.float32")
+        er, t = self._expert_rows(rows, x)
+        d_x = self._out("out", out, x.dtype, lead + (K,))
+        d_w = self._out("d_w", d_w, d_w_dtype, (self.num_experts, N, K))
+        ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
+        C.check(C.moedx_expert_linear_backward(self.ctx, _ptr(d_y), _ptr(x), _ptr(w),
+                                               _DTYPES[x.dtype], K, N, ctypes.byref(er), _ptr(d_x),
+                                               _ptr(d_w), _DTYPES[d_w_dtype], ctypes.byref(ex)))
+        self._keep(allocate_on_comm_stream, d_y, x, w, t, d_x, d_w)
+        return d_x, d_w, self._event(done)
+
+    def expert_swiglu_backward(self, d_h: torch.Tensor, pre: torch.Tensor, rows,
+                               out: Optional[torch.Tensor] = None,
+                               previous_event: Optional[EventOverlap] = None,
+                               async_finish: bool = False, allocate_on_comm_stream: bool = False,
+                               no_sync: bool = False):
+        """Returns (d_pre [*, 2N], event): the gradient of expert_linear's
+        swiglu at ``pre`` = (gate, up) for ``d_h`` [*, N]; expert_linear_backward
+        takes d_pre as its d_y.  Rows of no expert are left as they were."""
+        lead = self._lead("d_h", d_h)
+        d_h = self._check("d_h", d_h, _PRODUCT_DTYPES, lead + (None,))
+        N = d_h.shape[-1]
+        pre = self._check("pre", pre, (d_h.dtype,), lead + (2 * N,))
+        er, t = self._expert_rows(rows, d_h)
+        d_pre = self._out("out", out, d_h.dtype, lead + (2 * N,))
+        ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
+        C.check(C.moedx_expert_swiglu_backward(self.ctx, _ptr(d_h), _ptr(pre), _DTYPES[d_h.dtype],
+                                               N, ctypes.byref(er), _ptr(d_pre),
+                                               ctypes.byref(ex)))
+        self._keep(allocate_on_comm_stream, d_h, pre, t, d_pre)
+        return d_pre, self._event(done)

@@ -17,7 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoedx.so")
 
-SOURCES = ["layout.hip", "pack.hip", "combine.hip", "ll.hip", "api.cpp"]
+SOURCES = ["layout.hip", "pack.hip", "combine.hip", "ll.hip", "gate.hip",
+           "expert_rows.hip", "expert_linear.hip", "api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -18,6 +18,7 @@
 #include <new>
 #include <vector>
 
+#include "expert_launch.h"
 #include "launch.h"
 #include "moedx.h"
 
@@ -1212,6 +1213,341 @@ int moedx_ll_combine(moedx_ctx* ctx, const uint16_t* y, const int64_t* topk_idx,
                                       h->E, h->cap, out, ex.launch()));
         ctx->stats.ll_combine_launches += 1;
     }
+    return exec_end(ex);
+}
+
+// ---- router, rows in expert order, the experts' products ------------------------
+
+namespace {
+
+// exec_begin makes the ctx's device current; these calls give the caller's back.
+struct DeviceScope {
+    int before = -1;
+    DeviceScope() {
+        if (hipGetDevice(&before) != hipSuccess) before = -1;
+    }
+    ~DeviceScope() {
+        if (before >= 0) (void)hipSetDevice(before);
+    }
+};
+
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+int check_dtype(int dtype, bool f32_too) {
+    if (dtype == MOEDX_BF16 || dtype == MOEDX_F16 || (f32_too && dtype == MOEDX_F32))
+        return MOEDX_OK;
+    return fail(MOEDX_EINVAL, "unsupported dtype %d", dtype);
+}
+
+int dtype_bytes(int dtype) { return dtype == MOEDX_F32 ? 4 : 2; }
+
+int check_gate(const moedx_ctx* ctx, int dtype, int T, int K, const moedx_gate* g) {
+    if (int rc = check_dtype(dtype, true)) return rc;
+    if (T < 0 || T > (1 << 24)) return fail(MOEDX_EINVAL, "T=%d outside [0, 2^24]", T);
+    if (K < 1 || K > std::min(kMaxTopk, ctx->E))
+        return fail(MOEDX_EINVAL, "K=%d outside [1, %d]", K, std::min(kMaxTopk, ctx->E));
+    if (!g) return fail(MOEDX_EINVAL, "gate options are NULL");
+    if (g->score != MOEDX_GATE_SOFTMAX && g->score != MOEDX_GATE_SIGMOID)
+        return fail(MOEDX_EINVAL, "unknown gate score %d", g->score);
+    if (g->groups < 1 || g->groups > 64 || ctx->E % g->groups != 0)
+        return fail(MOEDX_EINVAL, "groups=%d must be in [1, 64] and divide num_experts=%d",
+                    g->groups, ctx->E);
+    if (g->groups_kept < 1 || g->groups_kept > g->groups)
+        return fail(MOEDX_EINVAL, "groups_kept=%d outside [1, %d]", g->groups_kept, g->groups);
+    if (g->bias && !aligned4(g->bias))
+        return fail(MOEDX_EINVAL, "bias must be 4-byte aligned");
+    return MOEDX_OK;
+}
+
+GateArgs gate_args(const moedx_ctx* ctx, const void* logits, int dtype, int T, int K,
+                   const moedx_gate* g) {
+    GateArgs a{};
+    a.logits = logits;
+    a.dtype = dtype;
+    a.T = T;
+    a.E = ctx->E;
+    a.K = K;
+    a.score = g->score;
+    a.groups = g->groups;
+    // with every group kept, groups restrict nothing
+    if (g->groups_kept == g->groups) a.groups = 1;
+    a.groups_kept = g->groups_kept;
+    a.renormalize = g->renormalize != 0;
+    a.scale = g->scale;
+    a.bias = g->bias;
+    return a;
+}
+
+// T tokens of K slots as pairs, and rows of H values moved by one wave per
+// (token, slice of 1024 bytes).
+int check_pairs(int T, int K) {
+    if (K < 1 || K > kMaxTopk) return fail(MOEDX_EINVAL, "K=%d outside [1, %d]", K, kMaxTopk);
+    if (T < 0 || T > (1 << 28) || (int64_t)T * K > ((int64_t)1 << 30))
+        return fail(MOEDX_EINVAL, "T=%d x K=%d exceeds 2^30 slots", T, K);
+    return MOEDX_OK;
+}
+
+int check_moves(int dtype, int T, int K, int H) {
+    if (int rc = check_dtype(dtype, true)) return rc;
+    if (int rc = check_pairs(T, K)) return rc;
+    if (H < 8 || H % 8 != 0) return fail(MOEDX_EINVAL, "H=%d must be a positive multiple of 8", H);
+    const int64_t slices = ((int64_t)H * dtype_bytes(dtype) + 1023) / 1024;
+    if ((int64_t)T * slices > ((int64_t)1 << 30))
+        return fail(MOEDX_EINVAL, "T=%d x H=%d exceeds the supported row count", T, H);
+    return MOEDX_OK;
+}
+
+int check_products(const moedx_ctx* ctx, int dtype, int K, int N, int w_rows_per_out,
+                   const moedx_expert_rows* er) {
+    if (int rc = check_dtype(dtype, false)) return rc;
+    if (K < 8 || K % 8 != 0 || K > (1 << 20))
+        return fail(MOEDX_EINVAL, "K=%d must be a positive multiple of 8 up to 2^20", K);
+    if (N < 8 || N % 8 != 0 || N > (1 << 20))
+        return fail(MOEDX_EINVAL, "N=%d must be a positive multiple of 8 up to 2^20", N);
+    if ((int64_t)w_rows_per_out * N * K * 2 >= ((int64_t)1 << 31))
+        return fail(MOEDX_EINVAL, "an expert's weights (N=%d, K=%d) exceed 2^31 bytes", N, K);
+    if (!er) return fail(MOEDX_EINVAL, "expert rows are NULL");
+    if (er->rows < 0 || er->rows > INT32_MAX)
+        return fail(MOEDX_EINVAL, "rows=%lld outside [0, 2^31)", (long long)er->rows);
+    if ((er->offsets != nullptr) == (er->counts != nullptr))
+        return fail(MOEDX_EINVAL, "exactly one of offsets and counts is given");
+    if (!aligned4(er->offsets) || !aligned4(er->counts))
+        return fail(MOEDX_EINVAL, "offsets and counts must be 4-byte aligned");
+    if (er->counts && er->rows % ctx->E != 0)
+        return fail(MOEDX_EINVAL, "rows=%lld is not a multiple of num_experts=%d",
+                    (long long)er->rows, ctx->E);
+    return MOEDX_OK;
+}
+
+ExpertRows expert_rows(const moedx_ctx* ctx, const moedx_expert_rows* er) {
+    return ExpertRows{er->offsets, er->counts, er->counts ? (int)(er->rows / ctx->E) : 0, ctx->E,
+                      er->rows};
+}
+
+}  // namespace
+
+int moedx_gate_topk(moedx_ctx* ctx, const void* logits, int dtype, int T, int K,
+                    const moedx_gate* gate, int64_t* topk_idx, float* topk_weights,
+                    const moedx_exec* exec) {
+    if (int rc = check_ctx(ctx)) return rc;
+    if (int rc = check_gate(ctx, dtype, T, K, gate)) return rc;
+    if (T > 0 && (!logits || !topk_idx || !topk_weights))
+        return fail(MOEDX_EINVAL, "NULL device pointer");
+    if (!aligned_to(logits, dtype_bytes(dtype)))
+        return fail(MOEDX_EINVAL, "logits must be aligned to their type");
+    DeviceScope scope;
+    Exec ex;
+    if (int rc = exec_begin(ctx, exec, &ex)) return rc;
+    if (T == 0)
+        HIP_OR_FAIL(ex.no_kernel());
+    else
+        HIP_OR_FAIL(launch_gate_topk(gate_args(ctx, logits, dtype, T, K, gate), topk_idx,
+                                     topk_weights, ex.launch()));
+    return exec_end(ex);
+}
+
+int moedx_gate_topk_backward(moedx_ctx* ctx, const void* logits, int dtype, int T, int K,
+                             const moedx_gate* gate, const int64_t* topk_idx,
+                             const float* d_topk_weights, void* d_logits,
+                             const moedx_exec* exec) {
+    if (int rc = check_ctx(ctx)) return rc;
+    if (int rc = check_gate(ctx, dtype, T, K, gate)) return rc;
+    if (T > 0 && (!logits || !topk_idx || !d_topk_weights || !d_logits))
+        return fail(MOEDX_EINVAL, "NULL device pointer");
+    if (!aligned_to(logits, dtype_bytes(dtype)) || !aligned_to(d_logits, dtype_bytes(dtype)))
+        return fail(MOEDX_EINVAL, "logits and d_logits must be aligned to their type");
+    DeviceScope scope;
+    Exec ex;
+    if (int rc = exec_begin(ctx, exec, &ex)) return rc;
+    if (T == 0)
+        HIP_OR_FAIL(ex.no_kernel());
+    else
+        HIP_OR_FAIL(launch_gate_topk_backward(gate_args(ctx, logits, dtype, T, K, gate), topk_idx,
+                                              d_topk_weights, d_logits, ex.launch()));
+    return exec_end(ex);
+}
+
+int moedx_expert_order_workspace_bytes(const moedx_ctx* ctx, int T, int K, size_t* bytes) {
+    if (int rc = check_ctx(ctx)) return rc;
+    if (int rc = check_pairs(T, K)) return rc;
+    if (!bytes) return fail(MOEDX_EINVAL, "bytes is NULL");
+    *bytes = align256((size_t)std::max(order_tiles((int64_t)T * K), 1) * ctx->E * 4);
+    return MOEDX_OK;
+}
+
+int moedx_expert_order(moedx_ctx* ctx, const int64_t* topk_idx, int T, int K,
+                       const moedx_handle* h, int32_t* expert_offsets, int32_t* row_of_slot,
+                       int32_t* slot_of_row, void* workspace, size_t workspace_bytes,
+                       const moedx_exec* exec) {
+    size_t need = 0;
+    if (int rc = moedx_expert_order_workspace_bytes(ctx, T, K, &need)) return rc;
+    if (h) {
+        if (h->kind != kNormal) return fail(MOEDX_EINVAL, "a normal handle is required");
+        if (h->E != ctx->E || h->R != ctx->R || h->C != ctx->C)
+            return fail(MOEDX_ESTATE, "handle was prepared on a ctx with a different E/R/C");
+        const int64_t rows = h->capacity > 0 ? h->capacity : h->n_host;
+        if (T != rows)
+            return fail(MOEDX_ESTATE, "T=%d differs from the handle's %lld receive rows", T,
+                        (long long)rows);
+        if (K != h->K) return fail(MOEDX_ESTATE, "K=%d differs from the handle's K=%d", K, h->K);
+    }
+    if (!expert_offsets || !workspace || (T > 0 && (!topk_idx || !row_of_slot || !slot_of_row)))
+        return fail(MOEDX_EINVAL, "NULL device pointer");
+    if (!aligned_to(topk_idx, 8) || !aligned4(expert_offsets) || !aligned4(row_of_slot) ||
+        !aligned4(slot_of_row))
+        return fail(MOEDX_EINVAL, "indexes must be aligned to their type");
+    if (!aligned_to(workspace, 256))
+        return fail(MOEDX_EINVAL, "workspace is not 256-byte aligned");
+    if (workspace_bytes < need)
+        return fail(MOEDX_ECAPACITY, "workspace_bytes=%zu < %zu", workspace_bytes, need);
+    DeviceScope scope;
+    Exec ex;
+    if (int rc = exec_begin(ctx, exec, &ex)) return rc;
+    OrderArgs a{};
+    if (h) {
+        if (int rc = handle_ready(h, ex.run)) return rc;
+        if (int rc = finish_pending(ctx, h, ex.run)) return rc;
+        a.rank_prefix_matrix = h->rank_prefix_matrix;
+    }
+    a.topk_idx = topk_idx;
+    a.T = T;
+    a.K = K;
+    a.E = ctx->E;
+    a.R = ctx->R;
+    a.P = ctx->P;
+    a.expert_offsets = expert_offsets;
+    a.row_of_slot = row_of_slot;
+    a.slot_of_row = slot_of_row;
+    a.tile_counts = static_cast<int32_t*>(workspace);
+    a.tiles = order_tiles((int64_t)T * K);
+    a.iters = order_iters((int64_t)T * K);
+    HIP_OR_FAIL(launch_expert_order(a, ex.launch()));
+    return exec_end(ex);
+}
+
+int moedx_expert_sort(moedx_ctx* ctx, const void* x, int dtype, int T, int K, int H,
+                      const int32_t* row_of_slot, void* rows, const moedx_exec* exec) {
+    if (int rc = check_ctx(ctx)) return rc;
+    if (int rc = check_moves(dtype, T, K, H)) return rc;
+    if (T > 0 && (!x || !row_of_slot || !rows)) return fail(MOEDX_EINVAL, "NULL device pointer");
+    if (!aligned16(x) || !aligned16(rows) || !aligned4(row_of_slot))
+        return fail(MOEDX_EINVAL, "x and rows must be 16-byte aligned");
+    DeviceScope scope;
+    Exec ex;
+    if (int rc = exec_begin(ctx, exec, &ex)) return rc;
+    if (T == 0)
+        HIP_OR_FAIL(ex.no_kernel());
+    else
+        HIP_OR_FAIL(launch_expert_sort(x, T, K, (int64_t)H * dtype_bytes(dtype), row_of_slot, rows,
+                                       ex.launch()));
+    return exec_end(ex);
+}
+
+int moedx_expert_unsort(moedx_ctx* ctx, const void* rows, int dtype, int T, int K, int H,
+                        const int32_t* row_of_slot, const float* weights, void* out,
+                        const moedx_exec* exec) {
+    if (int rc = check_ctx(ctx)) return rc;
+    if (int rc = check_moves(dtype, T, K, H)) return rc;
+    if (T > 0 && (!rows || !row_of_slot || !out)) return fail(MOEDX_EINVAL, "NULL device pointer");
+    if (!aligned16(rows) || !aligned16(out) || !aligned4(row_of_slot) || !aligned4(weights))
+        return fail(MOEDX_EINVAL, "rows and out must be 16-byte aligned");
+    DeviceScope scope;
+    Exec ex;
+    if (int rc = exec_begin(ctx, exec, &ex)) return rc;
+    if (T == 0)
+        HIP_OR_FAIL(ex.no_kernel());
+    else
+        HIP_OR_FAIL(launch_expert_unsort(rows, dtype, T, K, H, row_of_slot, weights, out,
+                                         ex.launch()));
+    return exec_end(ex);
+}
+
+int moedx_expert_unsort_backward(moedx_ctx* ctx, const void* d_out, const void* rows, int dtype,
+                                 int T, int K, int H, const int32_t* row_of_slot,
+                                 const float* weights, void* d_rows, float* d_weights,
+                                 const moedx_exec* exec) {
+    if (int rc = check_ctx(ctx)) return rc;
+    if (int rc = check_moves(dtype, T, K, H)) return rc;
+    if (T > 0 && (!d_out || !rows || !row_of_slot || !weights || !d_rows || !d_weights))
+        return fail(MOEDX_EINVAL, "NULL device pointer");
+    if (!aligned16(d_out) || !aligned16(rows) || !aligned16(d_rows) || !aligned4(row_of_slot) ||
+        !aligned4(weights) || !aligned4(d_weights))
+        return fail(MOEDX_EINVAL, "d_out, rows and d_rows must be 16-byte aligned");
+    DeviceScope scope;
+    Exec ex;
+    if (int rc = exec_begin(ctx, exec, &ex)) return rc;
+    if (T == 0)
+        HIP_OR_FAIL(ex.no_kernel());
+    else
+        HIP_OR_FAIL(launch_expert_unsort_backward(d_out, rows, dtype, T, K, H, row_of_slot, weights,
+                                                  d_rows, d_weights, ex.launch()));
+    return exec_end(ex);
+}
+
+int moedx_expert_linear(moedx_ctx* ctx, const void* x, const void* w, int dtype, int K, int N,
+                        const moedx_expert_rows* er, int swiglu, void* y, void* pre,
+                        const moedx_exec* exec) {
+    if (int rc = check_ctx(ctx)) return rc;
+    if (swiglu != 0 && swiglu != 1) return fail(MOEDX_EINVAL, "swiglu=%d must be 0 or 1", swiglu);
+    if (int rc = check_products(ctx, dtype, K, N, swiglu ? 2 : 1, er)) return rc;
+    if (pre && !swiglu) return fail(MOEDX_EINVAL, "pre is only produced with swiglu");
+    if (er->rows > 0 && (!x || !w || !y)) return fail(MOEDX_EINVAL, "NULL device pointer");
+    if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(pre))
+        return fail(MOEDX_EINVAL, "x, w, y and pre must be 16-byte aligned");
+    DeviceScope scope;
+    Exec ex;
+    if (int rc = exec_begin(ctx, exec, &ex)) return rc;
+    if (er->rows == 0)
+        HIP_OR_FAIL(ex.no_kernel());
+    else
+        HIP_OR_FAIL(launch_expert_linear(x, w, dtype, expert_rows(ctx, er), K, N, swiglu != 0, y,
+                                         pre, ex.launch()));
+    return exec_end(ex);
+}
+
+int moedx_expert_linear_backward(moedx_ctx* ctx, const void* d_y, const void* x, const void* w,
+                                 int dtype, int K, int N, const moedx_expert_rows* er, void* d_x,
+                                 void* d_w, int d_w_dtype, const moedx_exec* exec) {
+    if (int rc = check_ctx(ctx)) return rc;
+    if (int rc = check_products(ctx, dtype, K, N, 1, er)) return rc;
+    if (d_w && d_w_dtype != dtype && d_w_dtype != MOEDX_F32)
+        return fail(MOEDX_EINVAL, "d_w_dtype=%d must be the dtype or MOEDX_F32", d_w_dtype);
+    if (!d_x && !d_w) return fail(MOEDX_EINVAL, "neither d_x nor d_w is asked for");
+    if (er->rows > 0 && (!d_y || (d_x && !w) || (d_w && !x)))
+        return fail(MOEDX_EINVAL, "NULL device pointer");
+    if (!aligned16(d_y) || !aligned16(x) || !aligned16(w) || !aligned16(d_x) || !aligned16(d_w))
+        return fail(MOEDX_EINVAL, "d_y, x, w, d_x and d_w must be 16-byte aligned");
+    DeviceScope scope;
+    Exec ex;
+    if (int rc = exec_begin(ctx, exec, &ex)) return rc;
+    const ExpertRows rows = expert_rows(ctx, er);
+    const bool dx = d_x && er->rows > 0;
+    if (!dx && !d_w) HIP_OR_FAIL(ex.no_kernel());
+    if (dx)
+        HIP_OR_FAIL(launch_expert_dgrad(d_y, w, dtype, rows, K, N, d_x,
+                                        Launch{ex.run, ex.start, d_w ? nullptr : ex.stop, 0u}));
+    if (d_w)
+        HIP_OR_FAIL(launch_expert_wgrad(d_y, x, dtype, rows, K, N, d_w, d_w_dtype == MOEDX_F32,
+                                        Launch{ex.run, dx ? nullptr : ex.start, ex.stop, 0u}));
+    return exec_end(ex);
+}
+
+int moedx_expert_swiglu_backward(moedx_ctx* ctx, const void* d_h, const void* pre, int dtype, int N,
+                                 const moedx_expert_rows* er, void* d_pre,
+                                 const moedx_exec* exec) {
+    if (int rc = check_ctx(ctx)) return rc;
+    if (int rc = check_products(ctx, dtype, 8, N, 2, er)) return rc;
+    if (er->rows > 0 && (!d_h || !pre || !d_pre)) return fail(MOEDX_EINVAL, "NULL device pointer");
+    if (!aligned16(d_h) || !aligned16(pre) || !aligned16(d_pre))
+        return fail(MOEDX_EINVAL, "d_h, pre and d_pre must be 16-byte aligned");
+    DeviceScope scope;
+    Exec ex;
+    if (int rc = exec_begin(ctx, exec, &ex)) return rc;
+    if (er->rows == 0)
+        HIP_OR_FAIL(ex.no_kernel());
+    else
+        HIP_OR_FAIL(launch_swiglu_backward(d_h, pre, dtype, expert_rows(ctx, er), N, d_pre,
+                                           ex.launch()));
     return exec_end(ex);
 }
 

@@ -1,0 +1,71 @@
+// Which expert a row tile belongs to (device code).  Tiles of BM rows are
+// numbered expert by expert, an expert with c rows having ceil(c / BM) of
+// them, so a launch needs no count on the host: its grid covers the most
+// tiles that the buffer's rows can make, and workgroups past the last exit.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "expert_launch.h"
+
+namespace moedx {
+
+struct RowSpan {
+    int begin, end;
+};
+
+// Clamped to the buffer, whatever the arrays hold.
+__device__ __forceinline__ RowSpan expert_span(const ExpertRows& er, int e) {
+    if (er.offsets) {
+        const int rows = (int)er.rows;
+        const int b = min(max(er.offsets[e], 0), rows);
+        return RowSpan{b, min(max(er.offsets[e + 1], b), rows)};
+    }
+    const int b = e * er.cap;
+    return RowSpan{b, b + min(max(er.counts[e], 0), er.cap)};
+}
+
+struct RowTile {
+    int e;           // expert, or -1 past the last tile
+    int begin, end;  // the tile's rows
+};
+
+// Tile `i` (wave-uniform; every lane of the wave takes part).
+template <int BM>
+__device__ __forceinline__ RowTile find_tile(const ExpertRows& er, int i) {
+    const int lane = threadIdx.x & 63;
+    int base = 0;
+    for (int e0 = 0; e0 < er.E; e0 += 64) {
+        const int e = e0 + lane;
+        RowSpan s{0, 0};
+        if (e < er.E) s = expert_span(er, e);
+        const int t = (s.end - s.begin + BM - 1) / BM;
+        int incl = t;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(incl, d, 64);
+            if (lane >= d) incl += v;
+        }
+        const uint64_t past = __ballot(base + incl > i);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            const int begin = __builtin_amdgcn_readlane(s.begin, l);
+            const int end = __builtin_amdgcn_readlane(s.end, l);
+            const int first = base + __builtin_amdgcn_readlane(incl - t, l);
+            const int b = begin + (i - first) * BM;
+            return RowTile{e0 + l, b, min(b + BM, end)};
+        }
+        base += __builtin_amdgcn_readlane(incl, 63);
+    }
+    return RowTile{-1, 0, 0};
+}
+
+// The most tiles that `rows` rows of E experts can make.
+inline int64_t max_tiles(const ExpertRows& er, int bm) {
+    if (!er.offsets) return (int64_t)er.E * ((er.cap + bm - 1) / bm);
+    const int64_t n = er.rows / bm + er.E;
+    return n < er.rows ? n : er.rows;
+}
+
+}  // namespace moedx

@@ -425,6 +425,144 @@ MOEDX_API int moedx_ll_combine(moedx_ctx *ctx, const uint16_t *y, const int64_t 
                                const float *topk_weights, const moedx_handle *h, int H,
                                uint16_t *out, const moedx_exec *exec);
 
+/* ---- element types of the calls below ------------------------------------- */
+enum { MOEDX_BF16 = 0, MOEDX_F16 = 1, MOEDX_F32 = 2 };
+
+/* ---- router: top-k expert choice with gate weights ------------------------- */
+
+enum { MOEDX_GATE_SOFTMAX = 0, MOEDX_GATE_SIGMOID = 1 };
+
+/* How moedx_gate_topk scores and chooses, for E = the ctx's num_experts.
+ *   score        softmax over the token's logits, or the sigmoid of each.
+ *   groups       contiguous groups of E / groups experts (1 = no groups); a
+ *                group's score is the sum of its two best keys, and only the
+ *                groups_kept best groups' experts may be chosen.
+ *                groups in [1, 64], E % groups == 0, groups_kept in [1, groups].
+ *   renormalize  1: the chosen scores are divided by their sum.
+ *   scale        the weights are multiplied by it.
+ *   bias         device fp32 [E] or NULL: key = score + bias chooses (experts
+ *                and groups); the weights do not see it. */
+typedef struct moedx_gate {
+    int score;
+    int groups;
+    int groups_kept;
+    int renormalize;
+    float scale;
+    const float *bias;
+} moedx_gate;
+
+/* The K best keys of each token in descending order, ties to the lower index:
+ * topk_idx int64 [T, K] and topk_weights fp32 [T, K] (what
+ * moedx_get_dispatch_layout and moedx_dispatch take), from logits [T, E] of
+ * type `dtype`.  The choice is exact: keys are compared in fp64 where they go
+ * through exp.  An expert whose logit is -inf or NaN, or whose key is, is
+ * never chosen and counts 0 in a softmax; where fewer than K experts can be
+ * chosen, the remaining slots are -1 with weight 0.  A logit of +inf makes a
+ * softmax's weights NaN.
+ * T in [0, 2^24], K in [1, min(16, E)].  logits aligned to their type. */
+MOEDX_API int moedx_gate_topk(moedx_ctx *ctx, const void *logits, int dtype, int T, int K,
+                              const moedx_gate *gate, int64_t *topk_idx, float *topk_weights,
+                              const moedx_exec *exec);
+
+/* d_logits [T, E] (of type `dtype`) from d_topk_weights fp32 [T, K], for the
+ * choice topk_idx that moedx_gate_topk made of the same logits with the same
+ * options.  The choice itself has no gradient; empty slots add nothing. */
+MOEDX_API int moedx_gate_topk_backward(moedx_ctx *ctx, const void *logits, int dtype, int T, int K,
+                                       const moedx_gate *gate, const int64_t *topk_idx,
+                                       const float *d_topk_weights, void *d_logits,
+                                       const moedx_exec *exec);
+
+/* ---- rows in expert order ---------------------------------------------------- */
+
+/* Device bytes moedx_expert_order needs as its workspace for T tokens of K slots. */
+MOEDX_API int moedx_expert_order_workspace_bytes(const moedx_ctx *ctx, int T, int K,
+                                                 size_t *bytes);
+
+/* The filled (token, slot) pairs sorted by expert and, inside one, by token,
+ * then slot:
+ *   expert_offsets int32 [E + 1]  rows of expert e are [offsets[e], offsets[e+1])
+ *   row_of_slot    int32 [T, K]   the row of each pair, -1 for an empty slot
+ *   slot_of_row    int32 [T * K]  t * K + k of each row, -1 past offsets[E]
+ * h == NULL: topk_idx int64 [T, K] holds ids in [0, E), -1 = empty (as for
+ * moedx_get_dispatch_layout; ids outside [0, E) count as empty).
+ * h a normal handle of this ctx: topk_idx is the recv_topk_idx of its first
+ * dispatch, T the receive rows (N, or the capacity); ids are local to the
+ * row's bucket, and rows past N are empty.  No host wait in either case.
+ * workspace: device memory of at least moedx_expert_order_workspace_bytes
+ * bytes, 256-byte aligned, not shared with a call that may run at the same
+ * time.  T in [0, 2^28], K in [1, 16], T * K <= 2^30. */
+MOEDX_API int moedx_expert_order(moedx_ctx *ctx, const int64_t *topk_idx, int T, int K,
+                                 const moedx_handle *h, int32_t *expert_offsets,
+                                 int32_t *row_of_slot, int32_t *slot_of_row, void *workspace,
+                                 size_t workspace_bytes, const moedx_exec *exec);
+
+/* rows[row_of_slot[t, k]] = x[t] for every filled slot: x [T, H] and rows
+ * [T * K, H] of type `dtype`, bit-exact copies; other rows are left alone.
+ * Below, H % 8 == 0, data 16-byte aligned, buffers do not overlap, and a row
+ * index outside [0, T * K) counts as empty. */
+MOEDX_API int moedx_expert_sort(moedx_ctx *ctx, const void *x, int dtype, int T, int K, int H,
+                                const int32_t *row_of_slot, void *rows, const moedx_exec *exec);
+
+/* out[t] = sum over the filled slots, ascending k, of weights[t, k] *
+ * rows[row_of_slot[t, k]], in fp32 from +0.0f with fused multiply-adds, rounded
+ * once; weights fp32 [T, K], NULL = 1.  With weights NULL this is also the
+ * gradient of moedx_expert_sort. */
+MOEDX_API int moedx_expert_unsort(moedx_ctx *ctx, const void *rows, int dtype, int T, int K, int H,
+                                  const int32_t *row_of_slot, const float *weights, void *out,
+                                  const moedx_exec *exec);
+
+/* The gradients of moedx_expert_unsort: d_rows[row_of_slot[t, k]] = weights[t, k]
+ * * d_out[t] (other rows are left alone), d_weights[t, k] = the dot product of
+ * d_out[t] and rows[row_of_slot[t, k]] in fp32 (0 for an empty slot). */
+MOEDX_API int moedx_expert_unsort_backward(moedx_ctx *ctx, const void *d_out, const void *rows,
+                                           int dtype, int T, int K, int H,
+                                           const int32_t *row_of_slot, const float *weights,
+                                           void *d_rows, float *d_weights,
+                                           const moedx_exec *exec);
+
+/* ---- the experts' products ----------------------------------------------------- */
+
+/* Which rows of a [rows, *] buffer belong to expert e (E = the ctx's
+ * num_experts), read on the device:
+ *   offsets != NULL (counts NULL): rows [offsets[e], offsets[e + 1]), int32
+ *     [E + 1], non-decreasing (moedx_expert_order's expert_offsets);
+ *   counts != NULL (offsets NULL): the first counts[e] of the rows / E rows
+ *     from e * (rows / E), int32 [E] (moedx_ll_dispatch's recv_x and
+ *     recv_count with rows = E * cap); rows % E == 0.
+ * Both are clamped to the buffer.  Rows of no expert are neither read into a
+ * result nor written. */
+typedef struct moedx_expert_rows {
+    const int32_t *offsets;
+    const int32_t *counts;
+    int64_t rows;
+} moedx_expert_rows;
+
+/* y[m] = w[e(m)] x[m]: x [rows, K], y [rows, N], w [E, N, K], all of `dtype`
+ * (MOEDX_BF16 or MOEDX_F16), sums in fp32, one rounding.
+ * swiglu = 1: w is [E, 2N, K], gate rows then up rows; y = g / (1 + exp(-g)) * u
+ * for g = gate x, u = up x, both unrounded; pre (or NULL) receives [rows, 2N]
+ * = (g, u) rounded, which moedx_expert_swiglu_backward takes.
+ * K and N positive multiples of 8 up to 2^20, a w[e] below 2^31 bytes, rows
+ * below 2^31; data 16-byte aligned. */
+MOEDX_API int moedx_expert_linear(moedx_ctx *ctx, const void *x, const void *w, int dtype, int K,
+                                  int N, const moedx_expert_rows *er, int swiglu, void *y,
+                                  void *pre, const moedx_exec *exec);
+
+/* The gradients of y = w x: d_x[m] = w[e(m)]^T d_y[m] ([rows, K]; NULL to leave
+ * it out) and d_w[e] = the sum over e's rows of d_y[m] x[m]^T ([E, N, K], of
+ * type d_w_dtype: `dtype` or MOEDX_F32; zero for an expert without rows; NULL
+ * to leave it out; x is then not read, w not without d_x). */
+MOEDX_API int moedx_expert_linear_backward(moedx_ctx *ctx, const void *d_y, const void *x,
+                                           const void *w, int dtype, int K, int N,
+                                           const moedx_expert_rows *er, void *d_x, void *d_w,
+                                           int d_w_dtype, const moedx_exec *exec);
+
+/* d_pre [rows, 2N] = (d_g, d_u) from d_h [rows, N] and pre = (g, u) [rows, 2N]
+ * for h = g / (1 + exp(-g)) * u; N a positive multiple of 8. */
+MOEDX_API int moedx_expert_swiglu_backward(moedx_ctx *ctx, const void *d_h, const void *pre,
+                                           int dtype, int N, const moedx_expert_rows *er,
+                                           void *d_pre, const moedx_exec *exec);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,262 @@
+"""The experts' products (expert_linear and its gradients) against fp64
+products of the same inputs.  A sum of n products in fp32, in any order,
+differs by at most (n + 1) 2^-23 of the sum of their sizes (2^-23: the matrix
+instructions' own additions may truncate), and an output by half a step of its
+type more."""
+
+import pytest
+import torch
+
+from tests.gpu_common import device, make_buffer
+
+pytestmark = pytest.mark.gpu
+
+V = 2.0 ** -23
+
+
+def half_step(want, acc, dt):
+    if dt == torch.float32:
+        return torch.finfo(dt).tiny
+    return torch.finfo(dt).eps / 2 * (want.abs() + acc) + 2.0 ** -24 * (dt == torch.float16) + 1e-37
+
+
+def spans(counts, gap=0):
+    """Offsets of experts with these row counts."""
+    out = [gap]
+    for c in counts:
+        out.append(out[-1] + c)
+    return out
+
+
+def check(name, got, want, acc, dt):
+    err = (got.double() - want).abs()
+    bad = err > acc + half_step(want, acc, dt)
+    assert not bad.any(), (name, int(bad.sum()), torch.nonzero(bad)[0].tolist(),
+                           float(err[bad].max()), float(want[bad].abs().max()))
+
+
+def swiglu_reference(g, u, dg, du):
+    """silu(g) * u and its error for errors dg, du of g and u (|silu'| <= 1.1)
+    and 8 roundings of fp32 in the activation."""
+    s = g * torch.sigmoid(g)
+    h = s * u
+    acc = 1.1 * dg * (u.abs() + du) + s.abs() * du + 8 * V * h.abs()
+    return h, acc
+
+
+CASES = [
+    # counts per expert, K, N
+    ([1], 8, 8),
+    ([0, 1, 0, 0], 64, 16),
+    ([3, 0, 17, 16, 1, 33], 40, 24),
+    ([0, 0, 0], 72, 40),
+    ([65, 1, 64, 127], 136, 264),
+    ([300, 0, 129, 255, 257, 1], 328, 520),
+    ([5] * 16, 1416, 136),
+    ([700, 30], 520, 1032),
+    ([2, 2, 1, 0, 3, 1, 1, 6], 7168, 64),
+    ([1100], 128, 256),
+    ([40, 0, 90, 61, 33, 20, 70, 9], 256, 512),
+]
+TYPES = [torch.bfloat16, torch.float16]
+
+
+def make(counts, K, N, dt, dev, seed, cols):
+    g = torch.Generator(dev).manual_seed(seed)
+    off = spans(counts)
+    M = off[-1] + 5  # rows behind the last expert's
+    x = torch.randn(M, K, generator=g, device=dev).to(dt)
+    w = (torch.randn(len(counts), cols, K, generator=g, device=dev) * K ** -0.5).to(dt)
+    return off, M, x, w, g
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=lambda d: str(d)[6:])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"{len(c[0])}e{sum(c[0])}r-{c[1]}-{c[2]}")
+def test_forward(case, dt):
+    counts, K, N = case
+    dev = device()
+    E = len(counts)
+    buf = make_buffer(E, 1, 1, 1)
+    off, M, x, w, _ = make(counts, K, N, dt, dev, 1, 2 * N)
+    x[off[-1]:] = float("nan")  # never read into a result
+    rows = torch.tensor(off, dtype=torch.int32, device=dev)
+    print(f"[linear] {case} {dt}", flush=True)
+    y, none, _ = buf.expert_linear(x, w[:, :N].contiguous(), rows,
+                                   out=torch.full((M, N), 7.0, dtype=dt, device=dev))
+    assert none is None
+    h, pre, _ = buf.expert_linear(x, w, rows, swiglu=True, return_pre=True,
+                                  out=torch.full((M, N), 7.0, dtype=dt, device=dev))
+    h2, _, _ = buf.expert_linear(x, w, rows, swiglu=True)
+    assert (y[off[-1]:] == 7.0).all() and (h[off[-1]:] == 7.0).all()
+    assert torch.equal(h[:off[-1]], h2[:off[-1]])
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        if a == b:
+            continue
+        xs, ws = x[a:b].double(), w[e].double().t().contiguous()
+        p = xs @ ws
+        acc = (K + 1) * V * (xs.abs() @ ws.abs())
+        check("y", y[a:b], p[:, :N], acc[:, :N], dt)
+        check("pre", pre[a:b], p, acc, dt)
+        want, err = swiglu_reference(p[:, :N], p[:, N:], acc[:, :N], acc[:, N:])
+        check("h", h[a:b], want, err, dt)
+
+
+@pytest.mark.parametrize("wide", [False, True], ids=["same", "fp32"])
+@pytest.mark.parametrize("dt", TYPES, ids=lambda d: str(d)[6:])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"{len(c[0])}e{sum(c[0])}r-{c[1]}-{c[2]}")
+def test_backward(case, dt, wide):
+    counts, K, N = case
+    dev = device()
+    E = len(counts)
+    buf = make_buffer(E, 1, 1, 1)
+    off, M, x, w, g = make(counts, K, N, dt, dev, 2, N)
+    d_y = torch.randn(M, N, generator=g, device=dev).to(dt)
+    x[off[-1]:] = float("inf")
+    d_y[off[-1]:] = float("nan")
+    rows = torch.tensor(off, dtype=torch.int32, device=dev)
+    wt = torch.float32 if wide else dt
+    print(f"[linear backward] {case} {dt} {wt}", flush=True)
+    d_x, d_w, _ = buf.expert_linear_backward(d_y, x, w, rows, d_w_dtype=wt,
+                                             out=torch.full((M, K), 7.0, dtype=dt, device=dev))
+    assert (d_x[off[-1]:] == 7.0).all() and d_w.dtype == wt
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        if a == b:
+            assert (d_w[e] == 0).all()
+            continue
+        d, xs, ws = d_y[a:b].double(), x[a:b].double(), w[e].double()
+        check("d_x", d_x[a:b], d @ ws, (N + 1) * V * (d.abs() @ ws.abs()), dt)
+        dt_ = d.t().contiguous()
+        check("d_w", d_w[e], dt_ @ xs, (b - a + 1) * V * (dt_.abs() @ xs.abs()), wt)
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=lambda d: str(d)[6:])
+@pytest.mark.parametrize("N", [8, 24, 2056])
+def test_swiglu_backward(N, dt):
+    dev = device()
+    counts = [3, 0, 5, 1]
+    buf = make_buffer(4, 1, 1, 1)
+    off = spans(counts)
+    M = off[-1] + 3
+    g = torch.Generator(dev).manual_seed(3)
+    pre = (torch.randn(M, 2 * N, generator=g, device=dev) * 4).to(dt)
+    pre[0, :4] = torch.tensor([80.0, -80.0, 0.0, -1.2785], device=dev).to(dt)
+    d_h = torch.randn(M, N, generator=g, device=dev).to(dt)
+    rows = torch.tensor(off, dtype=torch.int32, device=dev)
+    d_pre, _ = buf.expert_swiglu_backward(d_h, pre, rows,
+                                          out=torch.full((M, 2 * N), 7.0, dtype=dt, device=dev))
+    n = off[-1]
+    assert (d_pre[n:] == 7.0).all()
+    gg, u, d = pre[:n, :N].double(), pre[:n, N:].double(), d_h[:n].double()
+    s, s1 = torch.sigmoid(gg), torch.sigmoid(-gg)
+    want = torch.cat([d * u * s * (1 + gg * s1), d * gg * s], 1)
+    # 16 roundings of each term; the two terms of d_gate may cancel
+    acc = 16 * V * torch.cat([(d * u * s).abs() * (1 + (gg * s1).abs()), (d * gg * s).abs()], 1)
+    check("d_pre", d_pre[:n], want, acc, dt)
+
+
+@pytest.mark.parametrize("cap", [1, 7, 130])
+def test_slots_with_counts(cap):
+    """[E, cap, *] buffers with counts (the low-latency layout); counts beyond
+    the capacity or below zero are clamped."""
+    dev = device()
+    E, K, N, dt = 5, 72, 40, torch.bfloat16
+    counts = [cap, 0, min(3, cap), cap + 9, -4]
+    held = [cap, 0, min(3, cap), cap, 0]
+    buf = make_buffer(E, 1, 1, 1)
+    g = torch.Generator(dev).manual_seed(4)
+    x = torch.randn(E, cap, K, generator=g, device=dev).to(dt)
+    w = (torch.randn(E, N, K, generator=g, device=dev) * K ** -0.5).to(dt)
+    d_y = torch.randn(E, cap, N, generator=g, device=dev).to(dt)
+    rows = torch.tensor(counts, dtype=torch.int32, device=dev)
+    y, _, _ = buf.expert_linear(x, w, rows, out=torch.full((E, cap, N), 7.0, dtype=dt, device=dev))
+    d_x, d_w, _ = buf.expert_linear_backward(
+        d_y, x, w, rows, out=torch.full((E, cap, K), 7.0, dtype=dt, device=dev))
+    for e in range(E):
+        c = held[e]
+        assert (y[e, c:] == 7.0).all() and (d_x[e, c:] == 7.0).all()
+        if c == 0:
+            assert (d_w[e] == 0).all()
+            continue
+        xs, ws, d = x[e, :c].double(), w[e].double(), d_y[e, :c].double()
+        wt, dtr = ws.t().contiguous(), d.t().contiguous()
+        check("y", y[e, :c], xs @ wt, (K + 1) * V * (xs.abs() @ wt.abs()), dt)
+        check("d_x", d_x[e, :c], d @ ws, (N + 1) * V * (d.abs() @ ws.abs()), dt)
+        check("d_w", d_w[e], dtr @ xs, (c + 1) * V * (dtr.abs() @ xs.abs()), dt)
+
+
+def test_offsets_are_clamped():
+    """Offsets outside the buffer, or falling, touch nothing outside it."""
+    dev = device()
+    E, K, N, M, dt = 3, 16, 16, 20, torch.bfloat16
+    buf = make_buffer(E, 1, 1, 1)
+    x = torch.ones(M, K, device=dev, dtype=dt)
+    w = torch.ones(E, N, K, device=dev, dtype=dt)
+    for off, live in (([-5, 4, 1 << 30, 1 << 30], (0, 20)), ([2, 6, 5, 9], (2, 9)),
+                      ([0, 0, 0, 0], (0, 0))):
+        y, _, _ = buf.expert_linear(x, w, torch.tensor(off, dtype=torch.int32, device=dev),
+                                    out=torch.full((M, N), 7.0, dtype=dt, device=dev))
+        want = torch.full((M, N), 7.0, dtype=dt, device=dev)
+        want[live[0]:live[1]] = K
+        assert torch.equal(y, want)
+
+
+def test_special_values_stay_in_their_rows():
+    """An infinity or NaN in one row or one expert reaches no other."""
+    dev = device()
+    E, K, N, dt = 3, 136, 72, torch.bfloat16
+    off = [0, 20, 60, 75]
+    buf = make_buffer(E, 1, 1, 1)
+    g = torch.Generator(dev).manual_seed(6)
+    x = torch.randn(75, K, generator=g, device=dev).to(dt)
+    w = torch.randn(E, N, K, generator=g, device=dev).to(dt)
+    d_y = torch.randn(75, N, generator=g, device=dev).to(dt)
+    rows = torch.tensor(off, dtype=torch.int32, device=dev)
+    clean, _, _ = buf.expert_linear(x, w, rows)
+    c_dx, c_dw, _ = buf.expert_linear_backward(d_y, x, w, rows)
+    x2, w2, d2 = x.clone(), w.clone(), d_y.clone()
+    x2[30] = float("inf")
+    w2[2] = float("nan")
+    d2[19] = float("nan")
+    y, _, _ = buf.expert_linear(x2, w2, rows)
+    same = [m for m in range(60) if m != 30]
+    assert torch.equal(y[same], clean[same])
+    assert torch.isnan(y[60:]).all() and not torch.isfinite(y[30]).any()
+    d_x, d_w, _ = buf.expert_linear_backward(d2, x2, w2, rows)
+    same = [m for m in range(60) if m != 19]
+    assert torch.equal(d_x[same], c_dx[same])
+    assert torch.isnan(d_w[0]).all() and torch.equal(d_w[2], c_dw[2])
+
+
+def test_refusals():
+    from combine_get_dispatch_layout_amd import _capi as C
+    dev = device()
+    E, K, N, dt = 4, 16, 24, torch.bfloat16
+    buf = make_buffer(E, 1, 1, 1)
+    x = torch.zeros(10, K, device=dev, dtype=dt)
+    w = torch.zeros(E, N, K, device=dev, dtype=dt)
+    off = torch.tensor([0, 2, 4, 6, 10], dtype=torch.int32, device=dev)
+    d_y = torch.zeros(10, N, device=dev, dtype=dt)
+    slots = torch.zeros(E, 3, K, device=dev, dtype=dt)
+    bad = [lambda: buf.expert_linear(x, w.half(), off), lambda: buf.expert_linear(x.float(), w.float(), off),
+           lambda: buf.expert_linear(x, w[:3], off), lambda: buf.expert_linear(x, w[:, :, :8], off),
+           lambda: buf.expert_linear(x, w, off[:4]), lambda: buf.expert_linear(x, w, off.long()),
+           lambda: buf.expert_linear(x, w, off, return_pre=True),
+           lambda: buf.expert_linear(x, w.cpu(), off), lambda: buf.expert_linear(x[0], w, off),
+           lambda: buf.expert_linear(slots, w, off), lambda: buf.expert_linear(slots[:3], w, off[:3]),
+           lambda: buf.expert_linear(x, w, off, out=torch.zeros(9, N, device=dev, dtype=dt)),
+           lambda: buf.expert_linear_backward(d_y[:9], x, w, off),
+           lambda: buf.expert_linear_backward(d_y, x, w, off, d_w_dtype=torch.float16),
+           lambda: buf.expert_linear_backward(d_y, x, w, off, d_w=w[:2]),
+           lambda: buf.expert_swiglu_backward(d_y, d_y, off)]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    odd = torch.zeros(10, 12, device=dev, dtype=dt)
+    for f in (lambda: buf.expert_linear(odd, torch.zeros(E, N, 12, device=dev, dtype=dt), off),
+              lambda: buf.expert_linear(x, torch.zeros(E, 12, K, device=dev, dtype=dt), off),
+              lambda: buf.expert_linear(x, w, off, swiglu=True)):  # halves of 12 rows
+        with pytest.raises(C.MoedxError) as e:
+            f()
+        assert e.value.code == C.MOEDX_EINVAL

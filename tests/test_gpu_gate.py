@@ -1,0 +1,228 @@
+"""The router (gate_topk and its gradient) against its definition in fp64 on
+the CPU.  The choice must be equal; a weight may differ by its fp32 roundings:
+the argument of exp is rounded once (relative error |l - max| 2^-24 of exp),
+exp and the division are within a few units, and the sum over E experts adds
+at most log2(64) + E / 64 roundings."""
+
+import pytest
+import torch
+
+from tests.gpu_common import device, make_buffer
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def reference(logits, K, score, groups, kept, renorm, scale, bias, d_w=None):
+    """(idx, weights, d_logits) in fp64, one token at a time."""
+    T, E = logits.shape
+    l = logits.double()
+    idx = torch.full((T, K), -1, dtype=torch.int64)
+    w = torch.zeros(T, K, dtype=torch.float64)
+    d = torch.zeros(T, E, dtype=torch.float64)
+    for t in range(T):
+        ok = l[t] > float("-inf")
+        if not ok.any():
+            continue
+        p = torch.zeros(E, dtype=torch.float64)
+        if score == "softmax":
+            p[ok] = torch.softmax(l[t][ok], 0)
+        else:
+            p[ok] = torch.sigmoid(l[t][ok])
+        key = p + (0.0 if bias is None else bias.double())
+        cand = [e for e in range(E) if ok[e] and key[e] > float("-inf")]
+        if groups > 1:
+            per = E // groups
+            sums = []
+            for g in range(groups):
+                best = sorted((float(key[e]) for e in cand if e // per == g), reverse=True)[:2]
+                sums.append(sum(best) if best else float("-inf"))
+            keep = sorted(range(groups), key=lambda g: (-sums[g], g))[:kept]
+            cand = [e for e in cand if e // per in keep]
+        # without a bias the logits order as the scores do, exactly
+        rank = l[t] if bias is None else key
+        cand = sorted(cand, key=lambda e: (-float(rank[e]), e))[:K]
+        n = len(cand)
+        if n == 0:
+            continue
+        c = torch.tensor(cand)
+        idx[t, :n] = c
+        if renorm:
+            s = l[t][c] if score == "softmax" else torch.nn.functional.logsigmoid(l[t][c])
+            v = torch.softmax(s, 0)
+        else:
+            v = p[c]
+        w[t, :n] = scale * v
+        if d_w is None:
+            continue
+        g = d_w[t, :n].double()
+        if renorm:
+            own = scale * v * (g - (g * v).sum())
+            if score == "sigmoid":
+                own = own * torch.sigmoid(-l[t][c])
+            d[t, c] = own
+        elif score == "sigmoid":
+            d[t, c] = scale * g * p[c] * torch.sigmoid(-l[t][c])
+        else:
+            e = torch.zeros(E, dtype=torch.float64)
+            e[c] = g
+            d[t] = scale * p * (e - (g * v).sum())
+    return idx, w, d
+
+
+def relative(logits, E):
+    """The relative error that the fp32 exps, the sum and the division allow."""
+    finite = logits[logits > float("-inf")].double()
+    span = float(finite.max() - finite.min()) if finite.numel() else 0.0
+    return (2.0 * span + 2.0 * (6 + E / 64.0) + 24.0) * U
+
+
+CASES = [
+    # T, E, K, dtype, score, groups, kept, renorm, bias, masked
+    (1, 1, 1, torch.float32, "softmax", 1, 1, False, False, 0.0),
+    (1, 256, 8, torch.float32, "sigmoid", 8, 4, True, True, 0.0),
+    (5, 16, 2, torch.bfloat16, "softmax", 1, 1, True, False, 0.3),
+    (67, 60, 6, torch.float16, "softmax", 4, 2, False, False, 0.1),
+    (129, 256, 8, torch.bfloat16, "softmax", 8, 4, False, True, 0.2),
+    (33, 64, 8, torch.bfloat16, "sigmoid", 1, 1, False, False, 0.0),
+    (33, 65, 16, torch.float32, "sigmoid", 5, 2, False, True, 0.5),
+    (7, 1024, 16, torch.float32, "softmax", 64, 3, True, True, 0.1),
+    (9, 1000, 3, torch.float16, "sigmoid", 1, 1, True, True, 0.0),
+    (3, 512, 1, torch.float32, "softmax", 2, 2, False, False, 0.9),
+    (40, 8, 8, torch.float32, "softmax", 4, 1, True, False, 0.4),
+    (40, 12, 5, torch.float32, "sigmoid", 12, 3, True, True, 0.4),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(v).replace("torch.", "") for v in c))
+def test_gate_and_gradient(case):
+    T, E, K, dt, score, groups, kept, renorm, use_bias, masked = case
+    dev = device()
+    g = torch.Generator().manual_seed(hash(case[:3]) % 1000)
+    logits = (torch.randn(T, E, generator=g) * 2.0).to(dt)
+    if masked:
+        logits[torch.rand(T, E, generator=g) < masked] = float("-inf")
+        logits[T // 2] = float("-inf")  # a token that no expert may take
+        logits[0, 0] = float("nan")
+    bias = torch.randn(E, generator=g) * 0.2 if use_bias else None
+    d_w = torch.randn(T, K, generator=g)
+    opts = dict(score=score, num_groups=groups, groups_kept=kept, renormalize=renorm, scale=2.5)
+    want_idx, want_w, want_d = reference(logits, K, score, groups, kept, renorm, 2.5, bias, d_w)
+    buf = make_buffer(E, 1, 1, T)
+    bd = None if bias is None else bias.to(dev)
+    print(f"[gate] {case}", flush=True)
+    idx, w, _ = buf.gate_topk(logits.to(dev), K, bias=bd, **opts)
+    d, _ = buf.gate_topk_backward(d_w.to(dev), logits.to(dev), idx, bias=bd, **opts)
+    assert torch.equal(idx.cpu(), want_idx)
+    rel = relative(logits, E)
+    assert ((w.cpu().double() - want_w).abs() <= rel * want_w.abs() + 1e-37).all()
+    assert (w.cpu()[want_idx < 0] == 0).all()
+    # every product of the gradient carries the weights' error; |g| and the
+    # weighted mean of g bound both terms, and the sum over K adds K roundings
+    gmax = d_w.abs().amax(1, keepdim=True).double()
+    p = want_d.new_zeros(T, E)
+    l = logits.double()
+    ok = l > float("-inf")
+    p[ok] = 1.0
+    if score == "softmax" and not renorm:
+        lm = torch.where(ok, l, -1e300)
+        p = torch.softmax(lm, 1) * ok
+    bound = 2.5 * 2 * gmax * p * (2 * rel + (K + 8) * U)
+    half = torch.finfo(dt).eps / 2
+    err = (d.cpu().double() - want_d).abs()
+    assert (err <= bound + half * (want_d.abs() + bound) + torch.finfo(dt).tiny).all()
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_gradient_by_differences(score, renorm):
+    """sum(weights * d_w) moves by d_logits * h where a logit moves by h (the
+    choice stays): central differences of the definition in fp64, whose own
+    error is O(h^2) = 1e-8."""
+    dev = device()
+    T, E, K, h = 3, 16, 4, 1e-4
+    g = torch.Generator().manual_seed(5)
+    logits = torch.stack([torch.randperm(E, generator=g) for _ in range(T)]).float() * 0.25
+    d_w = torch.randn(T, K, generator=g)
+    buf = make_buffer(E, 1, 1, T)
+    idx, _, _ = buf.gate_topk(logits.to(dev), K, score=score, renormalize=renorm, scale=1.5)
+    d, _ = buf.gate_topk_backward(d_w.to(dev), logits.to(dev), idx, score=score, renormalize=renorm,
+                                  scale=1.5)
+    d = d.cpu().double()
+    for t in range(T):
+        for e in range(E):
+            v = []
+            for s in (h, -h):
+                moved = logits.double().clone()
+                moved[t, e] += s
+                _, w, _ = reference(moved, K, score, 1, 1, renorm, 1.5, None)
+                v.append(float((w * d_w.double()).sum()))
+            assert abs((v[0] - v[1]) / (2 * h) - float(d[t, e])) < 1e-6
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_gate_extremes(dt):
+    """Ties go to the lower index; the type's lowest value is a candidate like
+    any other and renormalised weights stay finite and sum to 1."""
+    dev = device()
+    E, K = 64, 4
+    low, big = torch.finfo(dt).min, torch.finfo(dt).max
+    rows = torch.stack([torch.zeros(E), torch.full((E,), low), torch.full((E,), big),
+                        torch.full((E,), -200.0)]).to(dt)
+    rows[3, 10] = -100.0
+    buf = make_buffer(E, 1, 1, 4)
+    for score in ("softmax", "sigmoid"):
+        idx, w, _ = buf.gate_topk(rows.to(dev), K, score=score, renormalize=True)
+        idx, w = idx.cpu(), w.cpu()
+        for t in (0, 1, 2):
+            assert idx[t].tolist() == [0, 1, 2, 3]
+            assert (w[t] == 0.25).all()
+        assert idx[3].tolist() == [10, 0, 1, 2] and float(w[3, 0]) == 1.0
+        d, _ = buf.gate_topk_backward(torch.ones(4, K, device=dev), rows.to(dev), idx.to(dev),
+                                      score=score, renormalize=True)
+        assert torch.isfinite(d).all()
+
+
+def test_gate_close_scores():
+    """Scores that differ by less than an fp32 rounding are told apart: logits
+    one fp32 step apart, in every order, through a bias of zero."""
+    dev = device()
+    T, E, K = 64, 128, 8
+    g = torch.Generator().manual_seed(9)
+    ladder = torch.full((E,), 1.0)
+    for e in range(1, E):
+        ladder[e] = torch.nextafter(ladder[e - 1], torch.tensor(2.0))
+    perm = torch.stack([torch.randperm(E, generator=g) for _ in range(T)])
+    logits = ladder[perm]
+    want = torch.argsort(perm, dim=1, descending=True)[:, :K]
+    buf = make_buffer(E, 1, 1, T)
+    zero = torch.zeros(E, device=dev)
+    for score in ("softmax", "sigmoid"):
+        for bias in (None, zero):
+            idx, _, _ = buf.gate_topk(logits.to(dev), K, score=score, bias=bias)
+            assert torch.equal(idx.cpu(), want), (score, bias is None)
+
+
+def test_gate_empty_batch_and_refusals():
+    from combine_get_dispatch_layout_amd import _capi as C
+    dev = device()
+    buf = make_buffer(16, 4, 1, 8)
+    idx, w, _ = buf.gate_topk(torch.empty(0, 16, device=dev), 2)
+    assert idx.shape == (0, 2) and w.shape == (0, 2)
+    x = torch.zeros(3, 16, device=dev)
+    for bad in (dict(topk=0), dict(topk=17), dict(topk=2, num_groups=3), dict(topk=2, num_groups=0),
+                dict(topk=2, num_groups=4, groups_kept=5), dict(topk=2, num_groups=4, groups_kept=0)):
+        with pytest.raises(C.MoedxError) as e:
+            buf.gate_topk(x, **bad)
+        assert e.value.code == C.MOEDX_EINVAL
+    for args, kw in (((x[:, :8], 2), {}), ((x.double(), 2), {}), ((x.cpu(), 2), {}),
+                     ((x, 2), dict(score="relu")), ((x, 2), dict(bias=torch.zeros(8, device=dev))),
+                     ((x, 2), dict(bias=torch.zeros(16, device=dev, dtype=torch.float16)))):
+        with pytest.raises(ValueError):
+            buf.gate_topk(*args, **kw)
+    idx, w, _ = buf.gate_topk(x, 2)
+    with pytest.raises(ValueError):
+        buf.gate_topk_backward(w[:2], x, idx)
+    with pytest.raises(ValueError):
+        buf.gate_topk_backward(w, x, idx.int())
