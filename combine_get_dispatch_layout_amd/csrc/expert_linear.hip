@@ -5,126 +5,177 @@
 
 #include "expert_launch.h"
 #include "expert_map.h"
+#include "mma_tile.h"
 #include "moedx.h"
 #include "numeric.h"
+#include "xcd.h"
 
 namespace moedx {
 
 namespace {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-template <typename S>
-struct Mfma;
-template <>
-struct Mfma<__bf16> {
-    typedef __bf16 vec __attribute__((ext_vector_type(8)));
-    static __device__ __forceinline__ f32x4 mul(vec a, vec b, f32x4 c) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-    }
-};
-template <>
-struct Mfma<_Float16> {
-    typedef _Float16 vec __attribute__((ext_vector_type(8)));
-    static __device__ __forceinline__ f32x4 mul(vec a, vec b, f32x4 c) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-    }
-};
-
-// Operand values of one lane: index i (row of p, or column if kStrided), 8
-// values along the reduction from r0; zero outside [0, ni) x [0, nr).
-template <typename S, bool kStrided>
-__device__ __forceinline__ typename Mfma<S>::vec operand(const S* p, int64_t ld, int64_t i,
-                                                         int64_t ni, int64_t r0, int64_t nr) {
-    typename Mfma<S>::vec v{};
-    if (i >= ni) return v;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (r0 + j < nr) v[j] = kStrided ? p[(r0 + j) * ld + i] : p[i * ld + r0 + j];
-    return v;
-}
+// The tile shape of the three products: 256 x 256 outputs, 8 waves.
+constexpr int kBP = 256, kBQ = 256, kWP = 2, kWQ = 4;
+constexpr int kWaves = kWP * kWQ, kThreads = kWaves * 64;
+constexpr int kTP = kBP / kWP / 16, kTQ = kBQ / kWQ / 16;
+constexpr int kTileElems = kBP * kBK;  // one stage of one operand in LDS
+constexpr int kRunLog2 = 5;  // an XCD takes runs of 32 tiles: one per CU, sharing operands in its L2
+constexpr int kRowGroup = 8;  // row tiles that go through the columns together
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
-// One wave per 16 x 16 output tile; the D tile's lane holds 4 consecutive
-// contiguous-dimension outputs of one row.
+template <typename S>
+__device__ __forceinline__ void store4(S* at, const f32x4& v) {
+    typedef S vec __attribute__((ext_vector_type(4)));
+    vec o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = (S)v[i];
+    *reinterpret_cast<vec*>(at) = o;
+}
+
+// Runs f with the number of Q blocks per wave that `rows` rows need.
+template <typename F>
+__device__ __forceinline__ void with_blocks(int rows, F&& f) {
+    const int n = (rows + 16 * kWQ - 1) / (16 * kWQ);
+    if (n >= 4) f(std::integral_constant<int, 4>{});
+    else if (n == 3) f(std::integral_constant<int, 3>{});
+    else if (n == 2) f(std::integral_constant<int, 2>{});
+    else f(std::integral_constant<int, 1>{});
+}
+
+#define MOEDX_TILE_LDS(S)                        \
+    __shared__ __align__(16) S lp0[kTileElems];  \
+    __shared__ __align__(16) S lq0[kTileElems];  \
+    __shared__ __align__(16) S lp1[kTileElems];  \
+    __shared__ __align__(16) S lq1[kTileElems]
+
 template <typename S, bool kSwiglu>
-__global__ __launch_bounds__(64) void linear_kernel(const S* x, const S* w, ExpertRows er, int K,
-                                                    int N, S* y, S* pre) {
-    const RowTile tile = find_tile<16>(er, blockIdx.y);
+__global__ __launch_bounds__(kThreads, 2) void linear_kernel(const S* x, const S* w, ExpertRows er,
+                                                             int K, int N, int cols, S* y, S* pre) {
+    MOEDX_TILE_LDS(S);
+    const RowTile tile = find_block<kBQ, kRowGroup>(
+        er, xcd_run_block<kRunLog2>((int)blockIdx.x, (int)gridDim.x), cols);
     if (tile.e < 0) return;
-    const int lane = threadIdx.x, i = lane & 15, g = lane >> 4;
-    const int n0 = blockIdx.x * 16;
-    const int64_t cols = kSwiglu ? 2 * (int64_t)N : N;
-    const S* we = w + (int64_t)tile.e * cols * K;
-    f32x4 acc{0, 0, 0, 0}, up{0, 0, 0, 0};
-    for (int k0 = 0; k0 < K; k0 += 32) {
-        const auto b = operand<S, false>(x, K, (int64_t)tile.begin + i, tile.end, k0 + g * 8, K);
-        const auto a = operand<S, false>(we, K, n0 + i, N, k0 + g * 8, K);
-        acc = Mfma<S>::mul(a, b, acc);
-        if (kSwiglu) {
-            const auto u = operand<S, false>(we + (int64_t)N * K, K, n0 + i, N, k0 + g * 8, K);
-            up = Mfma<S>::mul(u, b, up);
-        }
-    }
-    const int m = tile.begin + i;
-    if (m >= tile.end) return;
-    for (int j = 0; j < 4; ++j) {
-        const int n = n0 + g * 4 + j;
-        if (n >= N) continue;
-        if (kSwiglu) {
-            y[(int64_t)m * N + n] = (S)(silu(acc[j]) * up[j]);
-            if (pre) {
-                pre[(int64_t)m * cols + n] = (S)acc[j];
-                pre[(int64_t)m * cols + N + n] = (S)up[j];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wp = wave % kWP, wq = wave / kWP;
+    const int n0 = tile.col * (kSwiglu ? kBP / 2 : kBP);
+    const S* we = w + (int64_t)tile.e * (kSwiglu ? 2 : 1) * N * K + (int64_t)n0 * K;
+    const int64_t second = kSwiglu ? (int64_t)N * K : (int64_t)(kBP / 2) * K;
+    Along<kBP, kWaves, 2> gp;
+    gp.init((int64_t)K * 2, K, wave, lane);
+    gp.half(0, we, N - n0);
+    gp.half(1, we + second, kSwiglu ? N - n0 : N - n0 - kBP / 2);
+    Along<kBQ, kWaves, 1> gq;
+    gq.init((int64_t)K * 2, K, wave, lane);
+    gq.half(0, x + (int64_t)tile.begin * K, tile.end - tile.begin);
+    with_blocks(tile.end - tile.begin, [&](auto nq) {
+        constexpr int NQ = decltype(nq)::value;
+        f32x4 acc[kTP][kTQ] = {};
+        TileLoop<S, kBP, kBQ, kWP, kWQ, NQ, decltype(gp), decltype(gq)>::run(
+            gp, gq, lp0, lq0, lp1, lq1, (K + kBK - 1) / kBK, wp, wq, wave, lane, acc);
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+            const int m = tile.begin + q_block<kWQ>(wq, j) + (lane & 15);
+            if (m >= tile.end) continue;
+            if constexpr (kSwiglu) {
+#pragma unroll
+                for (int i = 0; i < kTP / 2; ++i) {
+                    const int n = n0 + p_block<kBP, kWP>(wp, i) + 4 * (lane >> 4);
+                    if (n >= N) continue;
+                    const f32x4 g = acc[i][j], u = acc[i + kTP / 2][j];
+                    f32x4 h;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) h[r] = silu(g[r]) * u[r];
+                    store4(y + (int64_t)m * N + n, h);
+                    if (pre) {
+                        store4(pre + (int64_t)m * 2 * N + n, g);
+                        store4(pre + (int64_t)m * 2 * N + N + n, u);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kTP; ++i) {
+                    const int n = n0 + p_block<kBP, kWP>(wp, i) + 4 * (lane >> 4);
+                    if (n < N) store4(y + (int64_t)m * N + n, acc[i][j]);
+                }
             }
-        } else {
-            y[(int64_t)m * N + n] = (S)acc[j];
         }
-    }
+    });
 }
 
 template <typename S>
-__global__ __launch_bounds__(64) void dgrad_kernel(const S* d_y, const S* w, ExpertRows er, int K,
-                                                   int N, S* d_x) {
-    const RowTile tile = find_tile<16>(er, blockIdx.y);
+__global__ __launch_bounds__(kThreads, 2) void dgrad_kernel(const S* d_y, const S* w, ExpertRows er,
+                                                            int K, int N, int cols, S* d_x) {
+    MOEDX_TILE_LDS(S);
+    const RowTile tile = find_block<kBQ, kRowGroup>(
+        er, xcd_run_block<kRunLog2>((int)blockIdx.x, (int)gridDim.x), cols);
     if (tile.e < 0) return;
-    const int lane = threadIdx.x, i = lane & 15, g = lane >> 4;
-    const int k0 = blockIdx.x * 16;
-    const S* we = w + (int64_t)tile.e * N * K;
-    f32x4 acc{0, 0, 0, 0};
-    for (int n0 = 0; n0 < N; n0 += 32) {
-        const auto b = operand<S, false>(d_y, N, (int64_t)tile.begin + i, tile.end, n0 + g * 8, N);
-        const auto a = operand<S, true>(we, K, k0 + i, K, n0 + g * 8, N);
-        acc = Mfma<S>::mul(a, b, acc);
-    }
-    const int m = tile.begin + i;
-    if (m >= tile.end) return;
-    for (int j = 0; j < 4; ++j) {
-        const int k = k0 + g * 4 + j;
-        if (k < K) d_x[(int64_t)m * K + k] = (S)acc[j];
-    }
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wp = wave % kWP, wq = wave / kWP;
+    const int k0 = tile.col * kBP;
+    Across<kBP, kWaves> gp;
+    gp.init(w + (int64_t)tile.e * N * K, (int64_t)K * 2, N, k0, K, wave, lane);
+    Along<kBQ, kWaves, 1> gq;
+    gq.init((int64_t)N * 2, N, wave, lane);
+    gq.half(0, d_y + (int64_t)tile.begin * N, tile.end - tile.begin);
+    with_blocks(tile.end - tile.begin, [&](auto nq) {
+        constexpr int NQ = decltype(nq)::value;
+        f32x4 acc[kTP][kTQ] = {};
+        TileLoop<S, kBP, kBQ, kWP, kWQ, NQ, decltype(gp), decltype(gq)>::run(
+            gp, gq, lp0, lq0, lp1, lq1, (N + kBK - 1) / kBK, wp, wq, wave, lane, acc);
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+            const int m = tile.begin + q_block<kWQ>(wq, j) + (lane & 15);
+            if (m >= tile.end) continue;
+#pragma unroll
+            for (int i = 0; i < kTP; ++i) {
+                const int k = k0 + p_block<kBP, kWP>(wp, i) + 4 * (lane >> 4);
+                if (k < K) store4(d_x + (int64_t)m * K + k, acc[i][j]);
+            }
+        }
+    });
 }
 
 template <typename S, typename D>
-__global__ __launch_bounds__(64) void wgrad_kernel(const S* d_y, const S* x, ExpertRows er, int K,
-                                                   int N, D* d_w) {
-    const int e = blockIdx.z;
+__global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const S* d_y, const S* x, ExpertRows er,
+                                                            int K, int N, int cols, int rows,
+                                                            D* d_w) {
+    MOEDX_TILE_LDS(S);
+    int b = xcd_run_block<kRunLog2>((int)blockIdx.x, (int)gridDim.x);
+    const int e = b / (cols * rows);
+    b -= e * cols * rows;
+    // row tiles in groups, each through all columns
+    const int grp = b / (kRowGroup * cols);
+    b -= grp * kRowGroup * cols;
+    const int in_grp = min(kRowGroup, rows - grp * kRowGroup);
+    const int k0 = b / in_grp * kBP, n0 = (grp * kRowGroup + b % in_grp) * kBQ;
     const RowSpan s = expert_span(er, e);
-    const int lane = threadIdx.x, i = lane & 15, g = lane >> 4;
-    const int k0 = blockIdx.x * 16, n0 = blockIdx.y * 16;
-    f32x4 acc{0, 0, 0, 0};
-    for (int64_t m0 = s.begin; m0 < s.end; m0 += 32) {
-        const auto b = operand<S, true>(d_y, N, n0 + i, N, m0 + g * 8, s.end);
-        const auto a = operand<S, true>(x, K, k0 + i, K, m0 + g * 8, s.end);
-        acc = Mfma<S>::mul(a, b, acc);
-    }
-    const int n = n0 + i;
-    if (n >= N) return;
-    for (int j = 0; j < 4; ++j) {
-        const int k = k0 + g * 4 + j;
-        if (k < K) d_w[((int64_t)e * N + n) * K + k] = (D)acc[j];
-    }
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wp = wave % kWP, wq = wave / kWP;
+    const int count = s.end - s.begin;
+    Across<kBP, kWaves> gp;
+    gp.init(x + (int64_t)s.begin * K, (int64_t)K * 2, count, k0, K, wave, lane);
+    Across<kBQ, kWaves> gq;
+    gq.init(d_y + (int64_t)s.begin * N, (int64_t)N * 2, count, n0, N, wave, lane);
+    with_blocks(N - n0, [&](auto nq) {
+        constexpr int NQ = decltype(nq)::value;
+        f32x4 acc[kTP][kTQ] = {};
+        TileLoop<S, kBP, kBQ, kWP, kWQ, NQ, decltype(gp), decltype(gq)>::run(
+            gp, gq, lp0, lq0, lp1, lq1, (count + kBK - 1) / kBK, wp, wq, wave, lane, acc);
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+            const int n = n0 + q_block<kWQ>(wq, j) + (lane & 15);
+            if (n >= N) continue;
+#pragma unroll
+            for (int i = 0; i < kTP; ++i) {
+                const int k = k0 + p_block<kBP, kWP>(wp, i) + 4 * (lane >> 4);
+                if (k < K) store4(d_w + ((int64_t)e * N + n) * K + k, acc[i][j]);
+            }
+        }
+    });
 }
 
 constexpr int kActThreads = 256;
@@ -161,37 +212,42 @@ __global__ __launch_bounds__(kActThreads) void swiglu_backward_kernel(
     }
 }
 
+int tiles_of(int n, int b) { return (n + b - 1) / b; }
+
 template <typename S>
 hipError_t linear_as(const void* x, const void* w, const ExpertRows& er, int K, int N, bool swiglu,
                      void* y, void* pre, const Launch& L) {
-    const dim3 grid((N + 15) / 16, (unsigned)max_tiles(er, 16));
+    const int cols = tiles_of(N, swiglu ? kBP / 2 : kBP);
+    const dim3 grid((unsigned)(max_tiles(er, kBQ) * cols));
     const S* xs = static_cast<const S*>(x);
     const S* ws = static_cast<const S*>(w);
     if (swiglu)
-        return launch_kernel(linear_kernel<S, true>, grid, dim3(64), L, xs, ws, er, K, N,
-                             static_cast<S*>(y), static_cast<S*>(pre));
-    return launch_kernel(linear_kernel<S, false>, grid, dim3(64), L, xs, ws, er, K, N,
+        return launch_kernel(linear_kernel<S, true>, grid, dim3(kThreads), L, xs, ws, er, K, N,
+                             cols, static_cast<S*>(y), static_cast<S*>(pre));
+    return launch_kernel(linear_kernel<S, false>, grid, dim3(kThreads), L, xs, ws, er, K, N, cols,
                          static_cast<S*>(y), static_cast<S*>(pre));
 }
 
 template <typename S>
 hipError_t dgrad_as(const void* d_y, const void* w, const ExpertRows& er, int K, int N, void* d_x,
                     const Launch& L) {
-    const dim3 grid((K + 15) / 16, (unsigned)max_tiles(er, 16));
-    return launch_kernel(dgrad_kernel<S>, grid, dim3(64), L, static_cast<const S*>(d_y),
-                         static_cast<const S*>(w), er, K, N, static_cast<S*>(d_x));
+    const int cols = tiles_of(K, kBP);
+    const dim3 grid((unsigned)(max_tiles(er, kBQ) * cols));
+    return launch_kernel(dgrad_kernel<S>, grid, dim3(kThreads), L, static_cast<const S*>(d_y),
+                         static_cast<const S*>(w), er, K, N, cols, static_cast<S*>(d_x));
 }
 
 template <typename S>
 hipError_t wgrad_as(const void* d_y, const void* x, const ExpertRows& er, int K, int N, void* d_w,
                     bool f32_out, const Launch& L) {
-    const dim3 grid((K + 15) / 16, (N + 15) / 16, er.E);
+    const int cols = tiles_of(K, kBP), rows = tiles_of(N, kBQ);
+    const dim3 grid((unsigned)((int64_t)cols * rows * er.E));
     const S* ds = static_cast<const S*>(d_y);
     const S* xs = static_cast<const S*>(x);
     if (f32_out)
-        return launch_kernel(wgrad_kernel<S, float>, grid, dim3(64), L, ds, xs, er, K, N,
-                             static_cast<float*>(d_w));
-    return launch_kernel(wgrad_kernel<S, S>, grid, dim3(64), L, ds, xs, er, K, N,
+        return launch_kernel(wgrad_kernel<S, float>, grid, dim3(kThreads), L, ds, xs, er, K, N,
+                             cols, rows, static_cast<float*>(d_w));
+    return launch_kernel(wgrad_kernel<S, S>, grid, dim3(kThreads), L, ds, xs, er, K, N, cols, rows,
                          static_cast<S*>(d_w));
 }
 

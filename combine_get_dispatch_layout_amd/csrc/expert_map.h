@@ -29,11 +29,14 @@ __device__ __forceinline__ RowSpan expert_span(const ExpertRows& er, int e) {
 struct RowTile {
     int e;           // expert, or -1 past the last tile
     int begin, end;  // the tile's rows
+    int col;         // its column tile
 };
 
-// Tile `i` (wave-uniform; every lane of the wave takes part).
-template <int BM>
-__device__ __forceinline__ RowTile find_tile(const ExpertRows& er, int i) {
+// Tile `i` (wave-uniform; every lane of the wave takes part) where each expert
+// has ceil(c / BM) x cols tiles: up to kGroup row tiles go through the columns
+// together, so that tiles close in number share both operands.
+template <int BM, int kGroup>
+__device__ __forceinline__ RowTile find_block(const ExpertRows& er, int i, int cols) {
     const int lane = threadIdx.x & 63;
     int base = 0;
     for (int e0 = 0; e0 < er.E; e0 += 64) {
@@ -47,18 +50,24 @@ __device__ __forceinline__ RowTile find_tile(const ExpertRows& er, int i) {
             const int v = __shfl_up(incl, d, 64);
             if (lane >= d) incl += v;
         }
-        const uint64_t past = __ballot(base + incl > i);
+        const uint64_t past = __ballot((int64_t)(base + incl) * cols > i);
         if (past) {
             const int l = __builtin_ctzll(past);
             const int begin = __builtin_amdgcn_readlane(s.begin, l);
             const int end = __builtin_amdgcn_readlane(s.end, l);
+            const int mine = __builtin_amdgcn_readlane(t, l);
             const int first = base + __builtin_amdgcn_readlane(incl - t, l);
-            const int b = begin + (i - first) * BM;
-            return RowTile{e0 + l, b, min(b + BM, end)};
+            int local = i - first * cols;
+            const int grp = local / (kGroup * cols);
+            local -= grp * kGroup * cols;
+            const int in_grp = min(kGroup, mine - grp * kGroup);
+            const int col = local / in_grp;
+            const int b = begin + (grp * kGroup + local - col * in_grp) * BM;
+            return RowTile{e0 + l, b, min(b + BM, end), col};
         }
         base += __builtin_amdgcn_readlane(incl, 63);
     }
-    return RowTile{-1, 0, 0};
+    return RowTile{-1, 0, 0, 0};
 }
 
 // The most tiles that `rows` rows of E experts can make.
