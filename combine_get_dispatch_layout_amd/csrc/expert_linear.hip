@@ -14,11 +14,19 @@ namespace moedx {
 
 namespace {
 
-// The tile shape of the three products: 256 x 256 outputs, 8 waves.
-constexpr int kBP = 256, kBQ = 256, kWP = 2, kWQ = 4;
-constexpr int kWaves = kWP * kWQ, kThreads = kWaves * 64;
-constexpr int kTP = kBP / kWP / 16, kTQ = kBQ / kWQ / 16;
-constexpr int kTileElems = kBP * kBK;  // one stage of one operand in LDS
+// Tile shapes (mma_tile.h): forward and input gradient 256 x 256 by 8 waves,
+// weight gradient 256 x 128 by 4.
+template <int BQ_, int WQ_, int BK_>
+struct Shape {
+    static constexpr int BP = 256, BQ = BQ_, WP = 2, WQ = WQ_, BK = BK_;
+    static constexpr int kWaves = WP * WQ, kThreads = kWaves * 64;
+    static constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;
+    static __device__ __forceinline__ int p_at(int wp, int i) { return p_block<BP, WP>(wp, i); }
+    static __device__ __forceinline__ int q_at(int wq, int j) { return q_block<WQ>(wq, j); }
+};
+typedef Shape<256, 4, 64> Wide;
+typedef Shape<128, 2, 32> Narrow;
+
 constexpr int kRunLog2 = 5;  // an XCD takes runs of 32 tiles: one per CU, sharing operands in its L2
 constexpr int kRowGroup = 8;  // row tiles that go through the columns together
 
@@ -34,56 +42,52 @@ __device__ __forceinline__ void store4(S* at, const f32x4& v) {
 }
 
 // Runs f with the number of Q blocks per wave that `rows` rows need.
-template <typename F>
+template <int WQ, typename F>
 __device__ __forceinline__ void with_blocks(int rows, F&& f) {
-    const int n = (rows + 16 * kWQ - 1) / (16 * kWQ);
+    const int n = (rows + 16 * WQ - 1) / (16 * WQ);
     if (n >= 4) f(std::integral_constant<int, 4>{});
     else if (n == 3) f(std::integral_constant<int, 3>{});
     else if (n == 2) f(std::integral_constant<int, 2>{});
     else f(std::integral_constant<int, 1>{});
 }
 
-#define MOEDX_TILE_LDS(S)                        \
-    __shared__ __align__(16) S lp0[kTileElems];  \
-    __shared__ __align__(16) S lq0[kTileElems];  \
-    __shared__ __align__(16) S lp1[kTileElems];  \
-    __shared__ __align__(16) S lq1[kTileElems]
-
 template <typename S, bool kSwiglu>
-__global__ __launch_bounds__(kThreads, 2) void linear_kernel(const S* x, const S* w, ExpertRows er,
+__global__ __launch_bounds__(Wide::kThreads, 2) void linear_kernel(const S* x, const S* w, ExpertRows er,
                                                              int K, int N, int cols, S* y, S* pre) {
-    MOEDX_TILE_LDS(S);
-    const RowTile tile = find_block<kBQ, kRowGroup>(
+    typedef Wide T;
+    __shared__ __align__(16) S lp0[T::BP * T::BK], lp1[T::BP * T::BK];
+    __shared__ __align__(16) S lq0[T::BQ * T::BK], lq1[T::BQ * T::BK];
+    const RowTile tile = find_block<T::BQ, kRowGroup>(
         er, xcd_run_block<kRunLog2>((int)blockIdx.x, (int)gridDim.x), cols);
     if (tile.e < 0) return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wp = wave % kWP, wq = wave / kWP;
-    const int n0 = tile.col * (kSwiglu ? kBP / 2 : kBP);
+    const int wp = wave % T::WP, wq = wave / T::WP;
+    const int n0 = tile.col * (kSwiglu ? T::BP / 2 : T::BP);
     const S* we = w + (int64_t)tile.e * (kSwiglu ? 2 : 1) * N * K + (int64_t)n0 * K;
-    const int64_t second = kSwiglu ? (int64_t)N * K : (int64_t)(kBP / 2) * K;
-    Along<kBP, kWaves, 2> gp;
-    gp.init((int64_t)K * 2, K, wave, lane);
+    Along<T::BP, T::kWaves, T::BK, kSwiglu ? 2 : 1> gp;
+    gp.init(K * 2, K, wave, lane);
     gp.half(0, we, N - n0);
-    gp.half(1, we + second, kSwiglu ? N - n0 : N - n0 - kBP / 2);
-    Along<kBQ, kWaves, 1> gq;
-    gq.init((int64_t)K * 2, K, wave, lane);
+    if constexpr (kSwiglu) gp.half(1, we + (int64_t)N * K, N - n0);
+    Along<T::BQ, T::kWaves, T::BK, 1> gq;
+    gq.init(K * 2, K, wave, lane);
     gq.half(0, x + (int64_t)tile.begin * K, tile.end - tile.begin);
-    with_blocks(tile.end - tile.begin, [&](auto nq) {
+    with_blocks<T::WQ>(tile.end - tile.begin, [&](auto nq) {
         constexpr int NQ = decltype(nq)::value;
-        f32x4 acc[kTP][kTQ] = {};
-        TileLoop<S, kBP, kBQ, kWP, kWQ, NQ, decltype(gp), decltype(gq)>::run(
-            gp, gq, lp0, lq0, lp1, lq1, (K + kBK - 1) / kBK, wp, wq, wave, lane, acc);
+        f32x4 acc[T::TP][T::TQ] = {};
+        WholeCuLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, decltype(gp), decltype(gq)>(wp, wq, lane).run(
+            gp, gq, (lds_char*)lp0, (lds_char*)lq0, (lds_char*)lp1, (lds_char*)lq1,
+            (K + T::BK - 1) / T::BK, wave, acc);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            const int m = tile.begin + q_block<kWQ>(wq, j) + (lane & 15);
+            const int m = tile.begin + T::q_at(wq, j) + (lane & 15);
             if (m >= tile.end) continue;
             if constexpr (kSwiglu) {
 #pragma unroll
-                for (int i = 0; i < kTP / 2; ++i) {
-                    const int n = n0 + p_block<kBP, kWP>(wp, i) + 4 * (lane >> 4);
+                for (int i = 0; i < T::TP / 2; ++i) {
+                    const int n = n0 + T::p_at(wp, i) + 4 * (lane >> 4);
                     if (n >= N) continue;
-                    const f32x4 g = acc[i][j], u = acc[i + kTP / 2][j];
+                    const f32x4 g = acc[i][j], u = acc[i + T::TP / 2][j];
                     f32x4 h;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) h[r] = silu(g[r]) * u[r];
@@ -95,8 +99,8 @@ __global__ __launch_bounds__(kThreads, 2) void linear_kernel(const S* x, const S
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < kTP; ++i) {
-                    const int n = n0 + p_block<kBP, kWP>(wp, i) + 4 * (lane >> 4);
+                for (int i = 0; i < T::TP; ++i) {
+                    const int n = n0 + T::p_at(wp, i) + 4 * (lane >> 4);
                     if (n < N) store4(y + (int64_t)m * N + n, acc[i][j]);
                 }
             }
@@ -105,33 +109,36 @@ __global__ __launch_bounds__(kThreads, 2) void linear_kernel(const S* x, const S
 }
 
 template <typename S>
-__global__ __launch_bounds__(kThreads, 2) void dgrad_kernel(const S* d_y, const S* w, ExpertRows er,
+__global__ __launch_bounds__(Wide::kThreads, 2) void dgrad_kernel(const S* d_y, const S* w, ExpertRows er,
                                                             int K, int N, int cols, S* d_x) {
-    MOEDX_TILE_LDS(S);
-    const RowTile tile = find_block<kBQ, kRowGroup>(
+    typedef Wide T;
+    __shared__ __align__(16) S lp0[T::BP * T::BK], lp1[T::BP * T::BK];
+    __shared__ __align__(16) S lq0[T::BQ * T::BK], lq1[T::BQ * T::BK];
+    const RowTile tile = find_block<T::BQ, kRowGroup>(
         er, xcd_run_block<kRunLog2>((int)blockIdx.x, (int)gridDim.x), cols);
     if (tile.e < 0) return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wp = wave % kWP, wq = wave / kWP;
-    const int k0 = tile.col * kBP;
-    Across<kBP, kWaves> gp;
-    gp.init(w + (int64_t)tile.e * N * K, (int64_t)K * 2, N, k0, K, wave, lane);
-    Along<kBQ, kWaves, 1> gq;
-    gq.init((int64_t)N * 2, N, wave, lane);
+    const int wp = wave % T::WP, wq = wave / T::WP;
+    const int k0 = tile.col * T::BP;
+    Across<T::BP, T::kWaves, T::BK> gp;
+    gp.init(w + (int64_t)tile.e * N * K, K * 2, N, k0, K, wave, lane);
+    Along<T::BQ, T::kWaves, T::BK, 1> gq;
+    gq.init(N * 2, N, wave, lane);
     gq.half(0, d_y + (int64_t)tile.begin * N, tile.end - tile.begin);
-    with_blocks(tile.end - tile.begin, [&](auto nq) {
+    with_blocks<T::WQ>(tile.end - tile.begin, [&](auto nq) {
         constexpr int NQ = decltype(nq)::value;
-        f32x4 acc[kTP][kTQ] = {};
-        TileLoop<S, kBP, kBQ, kWP, kWQ, NQ, decltype(gp), decltype(gq)>::run(
-            gp, gq, lp0, lq0, lp1, lq1, (N + kBK - 1) / kBK, wp, wq, wave, lane, acc);
+        f32x4 acc[T::TP][T::TQ] = {};
+        WholeCuLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, decltype(gp), decltype(gq)>(wp, wq, lane).run(
+            gp, gq, (lds_char*)lp0, (lds_char*)lq0, (lds_char*)lp1, (lds_char*)lq1,
+            (N + T::BK - 1) / T::BK, wave, acc);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            const int m = tile.begin + q_block<kWQ>(wq, j) + (lane & 15);
+            const int m = tile.begin + T::q_at(wq, j) + (lane & 15);
             if (m >= tile.end) continue;
 #pragma unroll
-            for (int i = 0; i < kTP; ++i) {
-                const int k = k0 + p_block<kBP, kWP>(wp, i) + 4 * (lane >> 4);
+            for (int i = 0; i < T::TP; ++i) {
+                const int k = k0 + T::p_at(wp, i) + 4 * (lane >> 4);
                 if (k < K) store4(d_x + (int64_t)m * K + k, acc[i][j]);
             }
         }
@@ -139,10 +146,12 @@ __global__ __launch_bounds__(kThreads, 2) void dgrad_kernel(const S* d_y, const 
 }
 
 template <typename S, typename D>
-__global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const S* d_y, const S* x, ExpertRows er,
+__global__ __launch_bounds__(Narrow::kThreads, 2) void wgrad_kernel(const S* d_y, const S* x, ExpertRows er,
                                                             int K, int N, int cols, int rows,
                                                             D* d_w) {
-    MOEDX_TILE_LDS(S);
+    typedef Narrow T;
+    __shared__ __align__(16) S lp0[T::BP * T::BK], lp1[T::BP * T::BK], lp2[T::BP * T::BK];
+    __shared__ __align__(16) S lq0[T::BQ * T::BK], lq1[T::BQ * T::BK], lq2[T::BQ * T::BK];
     int b = xcd_run_block<kRunLog2>((int)blockIdx.x, (int)gridDim.x);
     const int e = b / (cols * rows);
     b -= e * cols * rows;
@@ -150,28 +159,30 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const S* d_y, const 
     const int grp = b / (kRowGroup * cols);
     b -= grp * kRowGroup * cols;
     const int in_grp = min(kRowGroup, rows - grp * kRowGroup);
-    const int k0 = b / in_grp * kBP, n0 = (grp * kRowGroup + b % in_grp) * kBQ;
+    const int k0 = b / in_grp * T::BP, n0 = (grp * kRowGroup + b % in_grp) * T::BQ;
     const RowSpan s = expert_span(er, e);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wp = wave % kWP, wq = wave / kWP;
+    const int wp = wave % T::WP, wq = wave / T::WP;
     const int count = s.end - s.begin;
-    Across<kBP, kWaves> gp;
-    gp.init(x + (int64_t)s.begin * K, (int64_t)K * 2, count, k0, K, wave, lane);
-    Across<kBQ, kWaves> gq;
-    gq.init(d_y + (int64_t)s.begin * N, (int64_t)N * 2, count, n0, N, wave, lane);
-    with_blocks(N - n0, [&](auto nq) {
+    Across<T::BP, T::kWaves, T::BK> gp;
+    gp.init(x + (int64_t)s.begin * K, K * 2, count, k0, K, wave, lane);
+    Across<T::BQ, T::kWaves, T::BK> gq;
+    gq.init(d_y + (int64_t)s.begin * N, N * 2, count, n0, N, wave, lane);
+    with_blocks<T::WQ>(N - n0, [&](auto nq) {
         constexpr int NQ = decltype(nq)::value;
-        f32x4 acc[kTP][kTQ] = {};
-        TileLoop<S, kBP, kBQ, kWP, kWQ, NQ, decltype(gp), decltype(gq)>::run(
-            gp, gq, lp0, lq0, lp1, lq1, (count + kBK - 1) / kBK, wp, wq, wave, lane, acc);
+        f32x4 acc[T::TP][T::TQ] = {};
+        SharedCuLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, decltype(gp), decltype(gq)>(wp, wq, lane).run(
+            gp, gq, (lds_char*)lp0, (lds_char*)lq0, (lds_char*)lp1, (lds_char*)lq1,
+            (lds_char*)lp2, (lds_char*)lq2,
+            (count + T::BK - 1) / T::BK, wave, acc);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            const int n = n0 + q_block<kWQ>(wq, j) + (lane & 15);
+            const int n = n0 + T::q_at(wq, j) + (lane & 15);
             if (n >= N) continue;
 #pragma unroll
-            for (int i = 0; i < kTP; ++i) {
-                const int k = k0 + p_block<kBP, kWP>(wp, i) + 4 * (lane >> 4);
+            for (int i = 0; i < T::TP; ++i) {
+                const int k = k0 + T::p_at(wp, i) + 4 * (lane >> 4);
                 if (k < K) store4(d_w + ((int64_t)e * N + n) * K + k, acc[i][j]);
             }
         }
@@ -217,37 +228,37 @@ int tiles_of(int n, int b) { return (n + b - 1) / b; }
 template <typename S>
 hipError_t linear_as(const void* x, const void* w, const ExpertRows& er, int K, int N, bool swiglu,
                      void* y, void* pre, const Launch& L) {
-    const int cols = tiles_of(N, swiglu ? kBP / 2 : kBP);
-    const dim3 grid((unsigned)(max_tiles(er, kBQ) * cols));
+    const int cols = tiles_of(N, swiglu ? Wide::BP / 2 : Wide::BP);
+    const dim3 grid((unsigned)(max_tiles(er, Wide::BQ) * cols));
     const S* xs = static_cast<const S*>(x);
     const S* ws = static_cast<const S*>(w);
     if (swiglu)
-        return launch_kernel(linear_kernel<S, true>, grid, dim3(kThreads), L, xs, ws, er, K, N,
+        return launch_kernel(linear_kernel<S, true>, grid, dim3(Wide::kThreads), L, xs, ws, er, K, N,
                              cols, static_cast<S*>(y), static_cast<S*>(pre));
-    return launch_kernel(linear_kernel<S, false>, grid, dim3(kThreads), L, xs, ws, er, K, N, cols,
+    return launch_kernel(linear_kernel<S, false>, grid, dim3(Wide::kThreads), L, xs, ws, er, K, N, cols,
                          static_cast<S*>(y), static_cast<S*>(pre));
 }
 
 template <typename S>
 hipError_t dgrad_as(const void* d_y, const void* w, const ExpertRows& er, int K, int N, void* d_x,
                     const Launch& L) {
-    const int cols = tiles_of(K, kBP);
-    const dim3 grid((unsigned)(max_tiles(er, kBQ) * cols));
-    return launch_kernel(dgrad_kernel<S>, grid, dim3(kThreads), L, static_cast<const S*>(d_y),
+    const int cols = tiles_of(K, Wide::BP);
+    const dim3 grid((unsigned)(max_tiles(er, Wide::BQ) * cols));
+    return launch_kernel(dgrad_kernel<S>, grid, dim3(Wide::kThreads), L, static_cast<const S*>(d_y),
                          static_cast<const S*>(w), er, K, N, cols, static_cast<S*>(d_x));
 }
 
 template <typename S>
 hipError_t wgrad_as(const void* d_y, const void* x, const ExpertRows& er, int K, int N, void* d_w,
                     bool f32_out, const Launch& L) {
-    const int cols = tiles_of(K, kBP), rows = tiles_of(N, kBQ);
+    const int cols = tiles_of(K, Narrow::BP), rows = tiles_of(N, Narrow::BQ);
     const dim3 grid((unsigned)((int64_t)cols * rows * er.E));
     const S* ds = static_cast<const S*>(d_y);
     const S* xs = static_cast<const S*>(x);
     if (f32_out)
-        return launch_kernel(wgrad_kernel<S, float>, grid, dim3(kThreads), L, ds, xs, er, K, N,
+        return launch_kernel(wgrad_kernel<S, float>, grid, dim3(Narrow::kThreads), L, ds, xs, er, K, N,
                              cols, rows, static_cast<float*>(d_w));
-    return launch_kernel(wgrad_kernel<S, S>, grid, dim3(kThreads), L, ds, xs, er, K, N, cols, rows,
+    return launch_kernel(wgrad_kernel<S, S>, grid, dim3(Narrow::kThreads), L, ds, xs, er, K, N, cols, rows,
                          static_cast<S*>(d_w));
 }
 

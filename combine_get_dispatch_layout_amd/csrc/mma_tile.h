@@ -3,24 +3,24 @@
 //   D[q, p] = sum_r P(p, r) Q(q, r)
 //
 // p is the output's contiguous dimension (BP of it per tile), q its row
-// dimension (BQ), r the reduction, taken 64 at a time.  An operand is either
-// "along" (its memory runs along r: [B rows][64 r]) or "across" (its memory
-// runs along p or q: [64 r][B columns]).  Stages of both operands go from
+// dimension (BQ), r the reduction, taken BK at a time.  An operand is either
+// "along" (its memory runs along r: [B rows][BK]) or "across" (its memory
+// runs along p or q: [BK][B columns]).  Stages of both operands go from
 // global memory straight into LDS; the buffer descriptors' range gives zeros
 // for rows past an operand's end, so ragged tiles need no branch.
 //
 // LDS holds 16-byte chunks, permuted so that the reads of a wave spread over
-// the banks.  Along: row r's chunk c sits at c ^ (r & 7), read with 16-byte
-// loads, 8 reduction values of one row per lane.  Across: row r's chunk c sits
-// at c ^ 2 f(r); the transposing LDS read hands a lane 4 reduction values of
-// one column, so a column-major operand costs no pass of its own.
+// the banks (no bank conflict is counted in any of the three products).  Along:
+// read with 16-byte loads, 8 reduction values of one row per lane.  Across: the
+// transposing LDS read hands a lane 4 reduction values of one column, so a
+// column-major operand costs no pass of its own.
 //
 // The matrix instruction is 16 x 16 x 32 with P as its A operand: a lane ends
-// up with 4 consecutive p of one q.  Two LDS buffers alternate.  A stage is
-// multiplied in two halves of 32: while the first half's products run, the
-// second half is read, then the stage after next starts loading into the
-// buffer just read, and the next stage's first half is read under the second
-// half's products.
+// up with 4 consecutive p of one q.  (32 x 32 x 16 was 6 to 14% slower here.)
+//
+// What bounds the two loops below on random data is power as much as issue: an
+// 8192^3 product that takes 934 us takes 754 us on zeros, whose clocks are
+// higher, and loops with 15% more idle matrix cycles measure the same.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -51,128 +51,170 @@ struct Mfma<_Float16> {
     }
 };
 
-constexpr int kBK = 64;  // reduction values per stage
 
+// LDS is addressed through pointers of its own address space, one offset from
+// the array's start per access: the compiler then knows which array a load
+// into LDS writes and waits only for reads of that one.
+typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) s16x8 lds_s16x8;
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* p, int64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0,
-                                             (int)(bytes > 0 ? bytes : 0), 0x00020000);
+// A value the compiler takes as it is: an address made of it stays one offset.
+__device__ __forceinline__ int opaque(int v) {
+    asm("" : "+v"(v));
+    return v;
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* p, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, max(bytes, 0),
+                                             0x00020000);
 }
 
 constexpr uint32_t kOutside = 0x80000000u;  // past any descriptor's range (below 2^31 bytes)
 
+// Both loaders keep one offset per lane; a load adds a wave-uniform step to it
+// (an offset outside the range stays outside: steps are below 2^30).
+
 // An operand along r: `halves` blocks of B / halves rows, each with its own
-// first row (a gated product's gate and up rows), ld values per row.
-template <int B, int NW, int kHalves>
+// first row (a gated product's gate and up rows).
+template <int B, int NW, int BK, int kHalves>
 struct Along {
-    static constexpr int kLoads = B / (8 * NW);  // 16-byte loads per lane and stage
-    static_assert(B % (8 * NW * kHalves) == 0, "a wave's 8 rows lie in one half");
+    static constexpr int kRow = BK * 2;                // bytes per LDS row
+    static constexpr int kRowChunks = BK / 8;
+    static constexpr int kLoadRows = 64 / kRowChunks;  // rows of one wave load
+    static constexpr int kLoads = B / (kLoadRows * NW);  // 16-byte loads per lane and stage
+    static constexpr int kFragReads = 1;  // LDS reads per block of 16 and 32 values of r
+    static_assert(B % (kLoadRows * NW * kHalves) == 0, "a wave's rows lie in one half");
     const char* base[kHalves];
     int valid[kHalves];  // rows of each half inside the operand
-    int64_t ld2;         // bytes per row
+    int ld2;             // bytes per row
     int nr;              // reduction length
-    uint32_t voff[kLoads / kHalves];
+    uint32_t voff;
     int col;             // this lane's first reduction value within a stage
 
-    __device__ __forceinline__ void init(int64_t ld_bytes, int reduction, int wave, int lane) {
+    // Rows 0, 1, ... take turns over the chunk positions, 128 bytes of LDS apart.
+    static __device__ __forceinline__ int swizzle(int row) {
+        return (BK == 64 ? row : row >> 1) & (kRowChunks - 1);
+    }
+    __device__ __forceinline__ void init(int ld_bytes, int reduction, int wave, int lane) {
         ld2 = ld_bytes;
         nr = reduction;
-        const int r = wave * 8 + (lane >> 3);
-        const int c = (lane & 7) ^ ((lane >> 3) & 7);
+        const int row = lane / kRowChunks;
+        const int c = (lane & (kRowChunks - 1)) ^ swizzle(row);
         col = c * 8;
-#pragma unroll
-        for (int j = 0; j < kLoads / kHalves; ++j)
-            voff[j] = (uint32_t)((r + j * 8 * NW) * ld2) + c * 16;
+        voff = (uint32_t)((wave * kLoadRows + row) * ld2) + c * 16;
     }
     __device__ __forceinline__ void half(int h, const void* first, int rows) {
         base[h] = static_cast<const char*>(first);
         valid[h] = min(max(rows, 0), B / kHalves);
     }
     // Stage at reduction value k0 into lds (this wave's part of it).
-    template <typename S>
-    __device__ __forceinline__ void load(S* lds, int k0, int wave) const {
-        const uint32_t out = k0 + col < nr ? 0u : kOutside;
+    __device__ __forceinline__ void load(lds_char* lds, int k0, int wave) const {
+        const uint32_t v = k0 + col < nr ? voff : kOutside;
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
-            const int64_t bytes = valid[h] * ld2 - (int64_t)k0 * 2;
-            const __amdgpu_buffer_rsrc_t rs = make_rsrc(base[h] + (int64_t)k0 * 2, bytes);
+            const __amdgpu_buffer_rsrc_t rs =
+                make_rsrc(base[h] + (int64_t)k0 * 2, valid[h] * ld2 - k0 * 2);
 #pragma unroll
             for (int j = 0; j < kLoads / kHalves; ++j) {
-                const int row = h * (B / kHalves) + (j * NW + wave) * 8;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    rs, (lds_void*)(lds + row * kBK), 16, (int)(voff[j] | out), 0, 0, 0);
+                const int row = h * (B / kHalves) + (j * NW + wave) * kLoadRows;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + row * kRow), 16,
+                                                         (int)(v + j * kLoadRows * NW * ld2), 0, 0,
+                                                         0);
             }
         }
     }
-    // Lane's 8 reduction values (half kk) of row `row` (+ lane & 15).
-    template <typename S>
-    static __device__ __forceinline__ s16x8 frag(const S* lds, int row, int kk, int lane) {
-        const int r = row + (lane & 15);
-        const int c = (kk * 4 + (lane >> 4)) ^ (r & 7);
-        return *reinterpret_cast<const s16x8*>(lds + r * kBK + c * 8);
-    }
+    // Where a lane reads: 8 reduction values (of the kk-th 32) of row `first` +
+    // (lane & 15).
+    struct At {
+        int at[BK / 32];
+        __device__ __forceinline__ void init(int first, int lane) {
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk) {
+                const int c = (kk * 4 + (lane >> 4)) ^ swizzle(lane & 15);  // first is 16 x
+                at[kk] = opaque((first + (lane & 15)) * kRow + c * 16);
+            }
+        }
+        // `off` rows further (a constant)
+        __device__ __forceinline__ s16x8 frag(const lds_char* lds, int off, int kk) const {
+            return *(const lds_s16x8*)(lds + at[kk] + off * kRow);
+        }
+    };
 };
 
-// An operand across r: 64 rows of the reduction, B columns from column c0 of
-// nc; ld values per row.
-template <int B, int NW>
+// An operand across r: BK rows of the reduction, B columns from column c0 of
+// nc.  A lane group g of 16 takes reduction values 32 kk + 8 g + 4 h + i (h = 0,
+// 1; i = 0..3); that row of the stage sits in LDS row i + 4 g + 16 h + 32 kk.  Its chunk c sits at c ^ 2 (row & 7): the 8
+// rows that half a wave's transposing read touches lie in different banks.
+template <int B, int NW, int BK>
 struct Across {
-    static constexpr int kLoads = B / (8 * NW);
-    static constexpr int kRowChunks = B / 8;           // 16-byte chunks per LDS row
+    static constexpr int kLoads = B * BK / (512 * NW);
+    static constexpr int kFragReads = 2;
+    static constexpr int kRowChunks = B / 8;              // 16-byte chunks per LDS row
     static constexpr int kRowsPerLoad = 64 / kRowChunks;  // LDS rows one wave load fills
-    static constexpr int kUnits = B / 16;              // 32-byte units per LDS row
-    static_assert(kRowChunks <= 64, "an LDS row is one wave load at most");
+    static constexpr int kStep = NW * kRowsPerLoad;       // LDS rows of one load of all waves
+
     const char* base;
-    int64_t ld2;
+    int ld2;
     int nr;
     int skip2;  // bytes before column c0
-    uint32_t voff[kLoads];
+    uint32_t voff;
 
-    static __device__ __forceinline__ int swizzle(int row) {
-        return (((row & 3) | ((row >> 1) & 12)) & (kUnits - 1)) * 2;
+    static __device__ __forceinline__ int swizzle(int lds_row) { return (lds_row & 7) * 2; }
+    // The reduction row of an LDS row.
+    static __device__ __forceinline__ constexpr int stage_row(int lds_row) {
+        return (lds_row & 3) | ((lds_row & 12) << 1) | ((lds_row & 16) >> 2) | (lds_row & 32);
     }
-    __device__ __forceinline__ void init(const void* first, int64_t ld_bytes, int reduction,
+    __device__ __forceinline__ void init(const void* first, int ld_bytes, int reduction,
                                          int c0, int nc, int wave, int lane) {
         base = static_cast<const char*>(first) + (int64_t)c0 * 2;
         ld2 = ld_bytes;
         nr = reduction;
         skip2 = c0 * 2;
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const int row = (j * NW + wave) * kRowsPerLoad + lane / kRowChunks;
-            const int c = (lane & (kRowChunks - 1)) ^ swizzle(row);
-            voff[j] = (uint32_t)(row * ld2) + c * 16;
-            if (c0 + c * 8 >= nc) voff[j] = kOutside;
-        }
+        const int row = wave * kRowsPerLoad + lane / kRowChunks;
+        const int c = (lane & (kRowChunks - 1)) ^ swizzle(row);
+        voff = c0 + c * 8 < nc ? (uint32_t)(stage_row(row) * ld2) + c * 16 : kOutside;
     }
-    template <typename S>
-    __device__ __forceinline__ void load(S* lds, int k0, int wave) const {
-        const int rows = min(nr - k0, kBK);
+    __device__ __forceinline__ void load(lds_char* lds, int k0, int wave) const {
+        const uint32_t v = k0 < nr ? voff : kOutside;
         const __amdgpu_buffer_rsrc_t rs =
-            make_rsrc(base + (int64_t)k0 * ld2, rows > 0 ? rows * ld2 - skip2 : 0);
+            make_rsrc(base + (int64_t)k0 * ld2, min(nr - k0, BK) * ld2 - skip2);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rs, (lds_void*)(lds + (j * NW + wave) * 512), 16, (int)voff[j], 0, 0, 0);
+                rs, (lds_void*)(lds + (j * NW + wave) * 1024), 16,
+                (int)(v + stage_row(j * kStep) * ld2), 0, 0, 0);
     }
-    template <typename S>
-    static __device__ __forceinline__ s16x8 frag(const S* lds, int col, int kk, int lane) {
-        s16x8 v;
+    // Where a lane reads: columns from `first`, in steps of 16.  The permutation
+    // moves 16 columns within their 128.
+    struct At {
+        int at[8];
+        __device__ __forceinline__ void init(int first, int lane) {
+            const int low = ((lane >> 4) << 2) | ((lane >> 2) & 3);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int row = kk * 32 + (lane >> 4) * 8 + h * 4 + ((lane >> 2) & 3);
-            const int c = (col / 8 + ((lane >> 1) & 1)) ^ swizzle(row);
-            const S* at = lds + row * B + c * 8 + (lane & 1) * 4;
-            const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
-            v[4 * h] = t[0];
-            v[4 * h + 1] = t[1];
-            v[4 * h + 2] = t[2];
-            v[4 * h + 3] = t[3];
+            for (int x = 0; x < 8; ++x) {
+                const int col = first + 16 * x;
+                const int c = (col / 8 + ((lane >> 1) & 1)) ^ swizzle(low);
+                at[x] = opaque(low * B * 2 + c * 16 + (lane & 1) * 8);
+            }
         }
-        return v;
-    }
+            // `off` columns further (a constant)
+        __device__ __forceinline__ s16x8 frag(const lds_char* lds, int off, int kk) const {
+            s16x8 v;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int rest = (16 * h + 32 * kk) * B * 2 + (off & ~127) * 2;
+                const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds_s16x4*)(lds + at[off / 16 & 7] + rest));
+                v[4 * h] = t[0];
+                v[4 * h + 1] = t[1];
+                v[4 * h + 2] = t[2];
+                v[4 * h + 3] = t[3];
+            }
+            return v;
+        }
+    };
 };
 
 // Waves of a tile: WP x WQ.  Wave (wp, wq) has the P blocks of 16 at
@@ -182,25 +224,112 @@ struct Across {
 // (dealt out in turn, so that a tile with few rows keeps every wave equally
 // busy and leaves out whole blocks).
 template <int BP, int WP>
-__device__ __forceinline__ int p_block(int wp, int i) {
+__device__ __forceinline__ constexpr int p_step(int i) {
     constexpr int TP = BP / WP / 16;
-    return (i / (TP / 2)) * (BP / 2) + wp * (BP / 2 / WP) + (i % (TP / 2)) * 16;
+    return (i / (TP / 2)) * (BP / 2) + (i % (TP / 2)) * 16;
+}
+template <int BP, int WP>
+__device__ __forceinline__ int p_block(int wp, int i) {
+    return wp * (BP / 2 / WP) + p_step<BP, WP>(i);
 }
 template <int WQ>
 __device__ __forceinline__ int q_block(int wq, int j) {
     return j * 16 * WQ + wq * 16;
 }
 
+// A tile by 4 waves that takes at most half of a CU's LDS and registers: two
+// workgroups share a CU, and one multiplies while the other waits at its
+// barrier or stores its tile.  Three LDS buffers of 32 reduction values rotate:
+// while stage s is multiplied, s + 1 is arriving and s + 2 is asked for.  Best
+// for operands across r and short reductions (64 experts of 512 rows, 4096 x
+// 7168 weight gradients: 2614 us, 2930 us with WholeCuLoop); an operand along r
+// is fetched in half lines, which costs the forward product 20%.
 template <typename S, int BP, int BQ, int WP, int WQ, int NQ, typename LP, typename LQ>
-struct TileLoop {
+struct SharedCuLoop {
     static constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;
+    static constexpr int kBK = 32, kBuffers = 3;
+    static constexpr int kStageLoads = LP::kLoads + LQ::kLoads;
+    typename LP::At ap;
+    typename LQ::At aq;
 
-    static __device__ __forceinline__ void frags(const S* lp, const S* lq, int kk, int wp, int wq,
-                                                 int lane, s16x8 (&p)[TP], s16x8 (&q)[TQ]) {
+    __device__ __forceinline__ SharedCuLoop(int wp, int wq, int lane) {
+        ap.init(wp * (BP / 2 / WP), lane);
+        aq.init(wq * 16, lane);
+    }
+    // Multiplies stage `it` (in lp, lq) and loads stage it + 2 into np, nq, which
+    // every wave has read.  Past the reduction's end a load leaves zeros.
+    __device__ __forceinline__ void stage(const LP& gp, const LQ& gq, const lds_char* lp,
+                                          const lds_char* lq, lds_char* np, lds_char* nq, int it,
+                                          int wave, f32x4 (&acc)[TP][TQ]) const {
+        s16x8 p[TP], q[NQ];
+        gp.load(np, (it + 2) * kBK, wave);
+        gq.load(nq, (it + 2) * kBK, wave);
 #pragma unroll
-        for (int i = 0; i < TP; ++i) p[i] = LP::frag(lp, p_block<BP, WP>(wp, i), kk, lane);
+        for (int j = 0; j < NQ; ++j) q[j] = aq.frag(lq, j * 16 * WQ, 0);
 #pragma unroll
-        for (int j = 0; j < NQ; ++j) q[j] = LQ::frag(lq, q_block<WQ>(wq, j), kk, lane);
+        for (int i = 0; i < TP; ++i) p[i] = ap.frag(lp, p_step<BP, WP>(i), 0);
+#pragma unroll
+        for (int i = 0; i < TP; ++i)
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) acc[i][j] = Mfma<S>::mul(p[i], q[j], acc[i][j]);
+        // The Q reads and two of P first, then a read and a load per P block.
+        __builtin_amdgcn_sched_group_barrier(0x100, LQ::kFragReads * NQ + 2 * LP::kFragReads, 0);
+#pragma unroll
+        for (int i = 0; i < TP; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, NQ, 0);
+            if (i < kStageLoads) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+            if (i + 2 < TP) __builtin_amdgcn_sched_group_barrier(0x100, LP::kFragReads, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // The next stage has arrived (only this stage's loads may be in flight),
+        // and this wave's reads are done: their products have been issued.
+        static_assert(kStageLoads < 16, "the wait's count has 4 bits here");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kStageLoads) : "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __device__ __forceinline__ void run(const LP& gp, const LQ& gq, lds_char* lp0, lds_char* lq0,
+                                        lds_char* lp1, lds_char* lq1, lds_char* lp2, lds_char* lq2,
+                                        int nk, int wave, f32x4 (&acc)[TP][TQ]) const {
+        if (nk <= 0) return;
+        gp.load(lp0, 0, wave);
+        gq.load(lq0, 0, wave);
+        gp.load(lp1, kBK, wave);
+        gq.load(lq1, kBK, wave);
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kStageLoads) : "memory");
+        int it = 0;
+        do {
+            stage(gp, gq, lp0, lq0, lp2, lq2, it, wave, acc);
+            stage(gp, gq, lp1, lq1, lp0, lq0, it + 1, wave, acc);
+            stage(gp, gq, lp2, lq2, lp1, lq1, it + 2, wave, acc);
+            it += kBuffers;
+        } while (it < nk);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS is left in flight
+    }
+};
+
+// A tile by 8 waves, one workgroup per CU, two LDS buffers of 64 reduction
+// values.  A stage is multiplied in two halves of 32: while the first half's
+// products run, the second half is read; past the barrier the stage after next
+// starts loading into the buffer just read, and the next stage's first half is
+// read under the second half's products.
+template <typename S, int BP, int BQ, int WP, int WQ, int NQ, typename LP, typename LQ>
+struct WholeCuLoop {
+    static constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;
+    static constexpr int kBK = 64;
+
+    typename LP::At ap;
+    typename LQ::At aq;
+
+    __device__ __forceinline__ WholeCuLoop(int wp, int wq, int lane) {
+        ap.init(wp * (BP / 2 / WP), lane);
+        aq.init(wq * 16, lane);
+    }
+    __device__ __forceinline__ void frags(const lds_char* lp, const lds_char* lq, int kk,
+                                          s16x8 (&p)[TP], s16x8 (&q)[TQ]) const {
+#pragma unroll
+        for (int i = 0; i < TP; ++i) p[i] = ap.frag(lp, p_step<BP, WP>(i), kk);
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) q[j] = aq.frag(lq, j * 16 * WQ, kk);
     }
     static __device__ __forceinline__ void products(const s16x8 (&p)[TP], const s16x8 (&q)[TQ],
                                                     f32x4 (&acc)[TP][TQ]) {
@@ -211,40 +340,74 @@ struct TileLoop {
     }
     // Stage `it` (in lp, lq; its first half already in p0, q0); the next one is
     // in np, nq.
-    static __device__ __forceinline__ void stage(const LP& gp, const LQ& gq, S* lp, S* lq,
-                                                 const S* np, const S* nq, int it, int nk, int wp,
-                                                 int wq, int wave, int lane, s16x8 (&p0)[TP],
-                                                 s16x8 (&q0)[TQ], f32x4 (&acc)[TP][TQ]) {
+    __device__ __forceinline__ void stage(const LP& gp, const LQ& gq, lds_char* lp, lds_char* lq,
+                                          const lds_char* np, const lds_char* nq, int it, int wave,
+                                          s16x8 (&p0)[TP], s16x8 (&q0)[TQ],
+                                          f32x4 (&acc)[TP][TQ]) const {
         s16x8 p1[TP], q1[TQ];
-        frags(lp, lq, 1, wp, wq, lane, p1, q1);
+        frags(lp, lq, 1, p1, q1);
         products(p0, q0, acc);
-        __syncthreads();  // this buffer is read, the next stage has arrived
-        frags(np, nq, 0, wp, wq, lane, p0, q0);
+        interleave<false>();
         __builtin_amdgcn_sched_barrier(0);
-        if (it + 2 < nk) {
-            gp.load(lp, (it + 2) * kBK, wave);
-            gq.load(lq, (it + 2) * kBK, wave);
-        }
+        __syncthreads();  // this buffer is read, the next stage has arrived
+        // past the reduction's end these fetch nothing and leave zeros
+        frags(np, nq, 0, p0, q0);
+        gp.load(lp, (it + 2) * kBK, wave);
+        gq.load(lq, (it + 2) * kBK, wave);
         products(p1, q1, acc);
+        interleave<true>();
+        __builtin_amdgcn_sched_barrier(0);
     }
-    static __device__ __forceinline__ void run(const LP& gp, const LQ& gq, S* lp0, S* lq0, S* lp1,
-                                               S* lq1, int nk, int wp, int wq, int wave, int lane,
-                                               f32x4 (&acc)[TP][TQ]) {
+    // Spreads a half's LDS reads (and a stage's loads) among its products: both
+    // waves of a SIMD leave the barrier together, and what they issue before
+    // their first product is time the matrix unit stands still.
+    template <bool kLoads>
+    static __device__ __forceinline__ void interleave() {
+        constexpr int kReads = LP::kFragReads * TP + LQ::kFragReads * NQ;
+        constexpr int kMem = kReads + (kLoads ? LP::kLoads + LQ::kLoads : 0);
+        constexpr int kPer = TP * NQ / kMem > 0 ? TP * NQ / kMem : 1;
+#pragma unroll
+        for (int i = 0; i < kReads; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
+            __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);  // products
+        }
+        if constexpr (kLoads) {
+#pragma unroll
+            for (int i = 0; i < LP::kLoads + LQ::kLoads; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);  // load
+                __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
+            }
+        }
+    }
+    __device__ __forceinline__ void run(const LP& gp, const LQ& gq, lds_char* lp0, lds_char* lq0,
+                                        lds_char* lp1, lds_char* lq1, int nk, int wave,
+                                        f32x4 (&acc)[TP][TQ]) const {
         if (nk <= 0) return;
-        gp.load(lp0, 0, wave);
-        gq.load(lq0, 0, wave);
-        __syncthreads();
-        if (nk > 1) {
+        s16x8 p0[TP], q0[TQ];
+        int it = 0;
+        if (nk & 1) {  // the pairs below start at stage 1
+            gp.load(lp0, kBK, wave);
+            gq.load(lq0, kBK, wave);
+            gp.load(lp1, 0, wave);
+            gq.load(lq1, 0, wave);
+            __syncthreads();
+            frags(lp1, lq1, 0, p0, q0);
+            stage(gp, gq, lp1, lq1, lp0, lq0, 0, wave, p0, q0, acc);
+            it = 1;
+        } else {
+            gp.load(lp0, 0, wave);
+            gq.load(lq0, 0, wave);
+            __syncthreads();
             gp.load(lp1, kBK, wave);
             gq.load(lq1, kBK, wave);
+            frags(lp0, lq0, 0, p0, q0);
         }
-        s16x8 p0[TP], q0[TQ];
-        frags(lp0, lq0, 0, wp, wq, lane, p0, q0);
-        for (int it = 0; it < nk; it += 2) {
-            stage(gp, gq, lp0, lq0, lp1, lq1, it, nk, wp, wq, wave, lane, p0, q0, acc);
-            if (it + 1 < nk)
-                stage(gp, gq, lp1, lq1, lp0, lq0, it + 1, nk, wp, wq, wave, lane, p0, q0, acc);
+        while (it < nk) {
+            stage(gp, gq, lp0, lq0, lp1, lq1, it, wave, p0, q0, acc);
+            stage(gp, gq, lp1, lq1, lp0, lq0, it + 1, wave, p0, q0, acc);
+            it += 2;
         }
+        __syncthreads();  // no load into LDS is left in flight
     }
 };
 
