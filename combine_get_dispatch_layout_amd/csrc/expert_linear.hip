@@ -108,6 +108,141 @@ __global__ __launch_bounds__(Wide::kThreads, 2) void linear_kernel(const S* x, c
     });
 }
 
+// The forward product where experts have few rows: the weights' bytes are all
+// that counts, so they go from memory straight into registers, with no LDS and
+// no barrier on the way.  A workgroup takes NP blocks of 16 weight rows (half
+// of them gate, half up rows in a gated product) and up to 32 rows of x; its 4
+// waves take turns along the reduction, 128 values each, and their sums are
+// added in LDS in wave order.  x comes from the caches.  64 experts of 4096 x
+// 7168, one row each: 602 us, the weights at 6.25 TB/s (a large copy reaches
+// 6.3); 12 rows each: 659 us.
+constexpr int kFewRows = 32, kFewBlocks = kFewRows / 16, kFewWaves = 4, kFewThreads = kFewWaves * 64;
+constexpr int kFewRunLog2 = 3;
+
+// 16 rows of an operand along r, read by the whole wave: lane l takes row
+// l & 15, reduction values 8 (l >> 4) .. + 7 of each 32; zeros outside.
+struct FewRows {
+    __amdgpu_buffer_rsrc_t rs;
+    int off;
+    __device__ __forceinline__ void init(const void* first, int rows, int K, int lane) {
+        rs = make_rsrc(first, rows * K * 2);
+        off = (lane & 15) * K * 2 + (lane >> 4) * 16;
+    }
+    __device__ __forceinline__ s16x8 load(int k, bool inside) const {
+        return __builtin_bit_cast(s16x8, __builtin_amdgcn_raw_buffer_load_b128(
+                                             rs, inside ? off + k * 2 : (int)kOutside, 0, 0));
+    }
+};
+
+// NP blocks of 16 weight rows times NQ blocks of 16 rows of x.
+template <typename S, int NP, int NQ>
+__device__ __forceinline__ void few_products(const FewRows* ws, const FewRows* xs, int K, int wave,
+                                             int lane, f32x4 (&acc)[NP][kFewBlocks]) {
+    constexpr int kU = 4, kStep = 32 * kU * kFewWaves;
+    s16x8 a[2][NP][kU], b[2][NQ][kU];
+    const int first = wave * 32 * kU, in = (lane >> 4) * 8;
+    // The scheduling barriers keep the loads of one step ahead of the products
+    // of the other.
+    const auto fetch = [&](int s, int k0) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int k = k0 + u * 32;
+            const bool inside = k + in < K;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) a[s][i][u] = ws[i].load(k, inside);
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) b[s][j][u] = xs[j].load(k, inside);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const auto multiply = [&](int s) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+                    acc[i][j] = Mfma<S>::mul(a[s][i][u], b[s][j][u], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    fetch(0, first);
+    for (int k0 = first; k0 < K; k0 += 2 * kStep) {
+        fetch(1, k0 + kStep);
+        multiply(0);
+        fetch(0, k0 + 2 * kStep);
+        multiply(1);
+    }
+}
+
+// NP: blocks of 16 weight rows; with kSwiglu the first half are gate rows.
+template <typename S, bool kSwiglu, int NP>
+__global__ __launch_bounds__(kFewThreads) void linear_few_kernel(const S* x, const S* w,
+                                                                 ExpertRows er, int K, int N,
+                                                                 int cols, S* y, S* pre) {
+    constexpr int kOut = kSwiglu ? NP / 2 : NP;  // blocks of outputs
+    __shared__ f32x4 part[kFewWaves][kFewBlocks][NP][64];
+    const RowTile tile = find_block<kFewRows, kRowGroup>(
+        er, xcd_run_block<kFewRunLog2>((int)blockIdx.x, (int)gridDim.x), cols);
+    if (tile.e < 0) return;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = tile.col * kOut * 16;
+    const S* we = w + (int64_t)tile.e * (kSwiglu ? 2 : 1) * N * K;
+    const int rows = tile.end - tile.begin;
+    FewRows ws[NP], xs[kFewBlocks];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int n = n0 + i % kOut * 16;
+        ws[i].init(we + (int64_t)(i < kOut ? n : N + n) * K, min(N - n, 16), K, lane);
+    }
+#pragma unroll
+    for (int j = 0; j < kFewBlocks; ++j)
+        xs[j].init(x + (int64_t)(tile.begin + 16 * j) * K, min(rows - 16 * j, 16), K, lane);
+    f32x4 acc[NP][kFewBlocks] = {};
+    if (rows > 16)
+        few_products<S, NP, 2>(ws, xs, K, wave, lane, acc);
+    else
+        few_products<S, NP, 1>(ws, xs, K, wave, lane, acc);
+#pragma unroll
+    for (int j = 0; j < kFewBlocks; ++j)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) part[wave][j][i][lane] = acc[i][j];
+    __syncthreads();
+    // wave j finishes block j of 16 rows
+    if (wave >= kFewBlocks) return;
+    const int m = tile.begin + wave * 16 + (lane & 15);
+    if (m >= tile.end) return;
+    f32x4 sum[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        sum[i] = part[0][wave][i][lane];
+#pragma unroll
+        for (int v = 1; v < kFewWaves; ++v) {
+            const f32x4 a = part[v][wave][i][lane];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum[i][r] += a[r];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kOut; ++i) {
+        const int n = n0 + i * 16 + 4 * (lane >> 4);
+        if (n >= N) return;
+        if constexpr (kSwiglu) {
+            const f32x4 g = sum[i], u = sum[kOut + i];
+            f32x4 h;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) h[r] = silu(g[r]) * u[r];
+            store4(y + (int64_t)m * N + n, h);
+            if (pre) {
+                store4(pre + (int64_t)m * 2 * N + n, g);
+                store4(pre + (int64_t)m * 2 * N + N + n, u);
+            }
+        } else {
+            store4(y + (int64_t)m * N + n, sum[i]);
+        }
+    }
+}
+
 template <typename S>
 __global__ __launch_bounds__(Wide::kThreads, 2) void dgrad_kernel(const S* d_y, const S* w, ExpertRows er,
                                                             int K, int N, int cols, S* d_x) {
@@ -225,13 +360,34 @@ __global__ __launch_bounds__(kActThreads) void swiglu_backward_kernel(
 
 int tiles_of(int n, int b) { return (n + b - 1) / b; }
 
+// Rows an expert is likely to have, from what the host knows.  A capacity
+// buffer holds at most cap tokens, each with a few experts: 8 are taken, the
+// top-k of the wide routings (more only moves where the kernels change).
+int64_t expected_rows(const ExpertRows& er) {
+    if (er.offsets) return er.rows / er.E;
+    return er.E > 8 ? (int64_t)er.cap * 8 / er.E : er.cap;
+}
+
 template <typename S>
 hipError_t linear_as(const void* x, const void* w, const ExpertRows& er, int K, int N, bool swiglu,
                      void* y, void* pre, const Launch& L) {
-    const int cols = tiles_of(N, swiglu ? Wide::BP / 2 : Wide::BP);
-    const dim3 grid((unsigned)(max_tiles(er, Wide::BQ) * cols));
     const S* xs = static_cast<const S*>(x);
     const S* ws = static_cast<const S*>(w);
+    // 64 experts, 7168 -> 4096, us at 1 / 12 / 24 / 40 rows each: 2 blocks 602 /
+    // 659 / 821 / 988, 4 blocks 629 / 644 / 695 / 765, tiles 731 / 721 / 727 / 740.
+    // Fewer columns per workgroup also means more workgroups for a few experts.
+    const int64_t likely = expected_rows(er);
+    if (likely <= 32) {
+        const int np = likely <= 16 ? 2 : 4;
+        const int cols = tiles_of(N, swiglu ? np * 8 : np * 16);
+        const dim3 grid((unsigned)(max_tiles(er, kFewRows) * cols));
+        const auto two = swiglu ? linear_few_kernel<S, true, 2> : linear_few_kernel<S, false, 2>;
+        const auto four = swiglu ? linear_few_kernel<S, true, 4> : linear_few_kernel<S, false, 4>;
+        return launch_kernel(np == 2 ? two : four, grid, dim3(kFewThreads), L, xs, ws, er, K, N,
+                             cols, static_cast<S*>(y), static_cast<S*>(pre));
+    }
+    const int cols = tiles_of(N, swiglu ? Wide::BP / 2 : Wide::BP);
+    const dim3 grid((unsigned)(max_tiles(er, Wide::BQ) * cols));
     if (swiglu)
         return launch_kernel(linear_kernel<S, true>, grid, dim3(Wide::kThreads), L, xs, ws, er, K, N,
                              cols, static_cast<S*>(y), static_cast<S*>(pre));

@@ -35,8 +35,8 @@ struct RowTile {
 // Tile `i` (wave-uniform; every lane of the wave takes part) where each expert
 // has ceil(c / BM) x cols tiles: up to kGroup row tiles go through the columns
 // together, so that tiles close in number share both operands.  An expert's
-// rows are dealt evenly to its tiles, in steps of 64: two full tiles and one
-// of 20 rows would take longer than three of 192.
+// rows are dealt evenly to its tiles, in steps of 64 (16 for small tiles): two
+// full tiles and one of 20 rows would take longer than three of 192.
 template <int BM, int kGroup>
 __device__ __forceinline__ RowTile find_block(const ExpertRows& er, int i, int cols) {
     const int lane = threadIdx.x & 63;
@@ -64,7 +64,8 @@ __device__ __forceinline__ RowTile find_block(const ExpertRows& er, int i, int c
             local -= grp * kGroup * cols;
             const int in_grp = min(kGroup, mine - grp * kGroup);
             const int col = local / in_grp;
-            const int step = ((end - begin + 64 * mine - 1) / (64 * mine)) * 64;
+            constexpr int kUnit = BM < 64 ? 16 : 64;  // divides BM, so step <= BM
+            const int step = ((end - begin + kUnit * mine - 1) / (kUnit * mine)) * kUnit;
             const int b = begin + (grp * kGroup + local - col * in_grp) * step;
             return RowTile{e0 + l, b, min(b + step, end), col};
         }

@@ -57,6 +57,8 @@ CASES = [
     ([2, 2, 1, 0, 3, 1, 1, 6], 7168, 64),
     ([1100], 128, 256),
     ([40, 0, 90, 61, 33, 20, 70, 9], 256, 512),
+    ([20, 33, 64, 0, 31, 17], 520, 72),
+    ([16, 31, 1, 47], 4104, 48),
 ]
 TYPES = [torch.bfloat16, torch.float16]
 
