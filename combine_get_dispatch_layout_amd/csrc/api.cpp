@@ -1272,6 +1272,7 @@ GateArgs gate_args(const moedx_ctx* ctx, const void* logits, int dtype, int T, i
     // with every group kept, groups restrict nothing
     if (g->groups_kept == g->groups) a.groups = 1;
     a.groups_kept = g->groups_kept;
+    a.per_div = make_fastdiv((uint32_t)(ctx->E / a.groups));
     a.renormalize = g->renormalize != 0;
     a.scale = g->scale;
     a.bias = g->bias;

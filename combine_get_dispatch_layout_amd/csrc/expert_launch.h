@@ -22,6 +22,7 @@ struct GateArgs {
     int renormalize;
     float scale;
     const float* bias;   // [E] or null; selection only
+    FastDiv per_div;     // by the experts of a group
 };
 
 hipError_t launch_gate_topk(const GateArgs& a, int64_t* topk_idx, float* topk_weights,
@@ -32,9 +33,10 @@ hipError_t launch_gate_topk_backward(const GateArgs& a, const int64_t* topk_idx,
 
 // ---- rows in expert order -----------------------------------------------------
 
-// Pairs (token, slot) are counted and ranked in tiles of kOrderTile * iters.
+// Pairs (token, slot) are counted and ranked in tiles of kOrderTile * iters,
+// at most kOrderMaxTiles of them: every ranking workgroup reads all counts.
 constexpr int kOrderTile = 1024;
-constexpr int kOrderMaxTiles = 1024;
+constexpr int kOrderMaxTiles = 128;
 
 struct OrderArgs {
     const int64_t* topk_idx;  // [T, K]

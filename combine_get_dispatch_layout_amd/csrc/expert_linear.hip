@@ -343,9 +343,9 @@ __global__ __launch_bounds__(kActThreads) void swiglu_backward_kernel(
     if (!live) return;
     for (int c = threadIdx.x; c < chunks; c += kActThreads) {
         float d[C], g[C], u[C];
-        chunk_to_f32<S>(d_h[row * chunks + c], d);
-        chunk_to_f32<S>(pre[row * 2 * chunks + c], g);
-        chunk_to_f32<S>(pre[row * 2 * chunks + chunks + c], u);
+        chunk_to_f32<S>(__builtin_nontemporal_load(d_h + row * chunks + c), d);
+        chunk_to_f32<S>(__builtin_nontemporal_load(pre + row * 2 * chunks + c), g);
+        chunk_to_f32<S>(__builtin_nontemporal_load(pre + row * 2 * chunks + chunks + c), u);
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const float s = 1.0f / (1.0f + expf(-g[i]));

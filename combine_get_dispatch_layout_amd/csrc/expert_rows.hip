@@ -4,16 +4,21 @@
 // A pair p = t * K + k is a filled slot of topk_idx.  In expert order the
 // pairs are sorted by expert and, inside one, by p:
 //   row(p) = offsets[e(p)] + #{p' < p : e(p') = e(p)}.
-// The order is a counting sort: every tile of pairs counts its experts, one
-// workgroup turns the counts into prefixes, every tile ranks its pairs.  Ranks
+// The order is a counting sort in two launches (one for up to 1024 pairs):
+// every tile of pairs counts its experts; then every tile sums the counts it
+// needs, all experts' totals and its own prefix, and ranks its pairs.  Ranks
 // come from wave ballots (the lanes that hold the same expert), not from
 // atomics, so the order is the same on every run.
+//
+// The moves are bound by memory.  Rows are streamed past the caches (every
+// one is read and written once): of 16-byte chunks, one wave per token and 64.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "expert_launch.h"
 #include "moedx.h"
 #include "numeric.h"
+#include "xcd.h"
 
 namespace moedx {
 
@@ -51,97 +56,139 @@ __device__ __forceinline__ uint64_t same_lanes(int e, int bits) {
     return m;
 }
 
+constexpr int kOrderUnroll = kOrderTile / kOrderThreads;
+
 __global__ __launch_bounds__(kOrderThreads) void order_count_kernel(OrderArgs a) {
     __shared__ int32_t hist[kMaxExperts];
     __shared__ int32_t prefix[kMaxRanks];
     const int64_t pairs = (int64_t)a.T * a.K;
-    const int64_t tile = (int64_t)kOrderTile * a.iters;
     load_prefix(a, prefix);
     for (int e = threadIdx.x; e < a.E; e += kOrderThreads) hist[e] = 0;
     __syncthreads();
-    const int64_t b = blockIdx.x * tile;
-    for (int64_t i = b + threadIdx.x; i < b + tile; i += kOrderThreads) {
-        const int e = pair_expert(a, prefix, i, pairs);
-        if (e >= 0) atomicAdd(&hist[e], 1);  // a sum of ones: any order gives it
+    for (int it = 0; it < a.iters; ++it) {
+        const int64_t b = ((int64_t)blockIdx.x * a.iters + it) * kOrderTile + threadIdx.x;
+        int e[kOrderUnroll];
+#pragma unroll
+        for (int u = 0; u < kOrderUnroll; ++u)
+            e[u] = pair_expert(a, prefix, b + u * kOrderThreads, pairs);
+#pragma unroll
+        for (int u = 0; u < kOrderUnroll; ++u)
+            if (e[u] >= 0) atomicAdd(&hist[e[u]], 1);  // a sum of ones: any order gives it
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += kOrderThreads)
         a.tile_counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
 }
 
-// One workgroup, thread e per expert: counts become exclusive prefixes over
-// the tiles plus the expert's offset.
-__global__ __launch_bounds__(kMaxExperts) void order_scan_kernel(OrderArgs a) {
-    __shared__ int32_t total[kMaxExperts];
-    const int e = threadIdx.x;
-    int sum = 0;
-    if (e < a.E)
-        for (int t = 0; t < a.tiles; ++t) sum += a.tile_counts[(int64_t)t * a.E + e];
-    total[e] = sum;
+// Exclusive prefix of v over the workgroup's threads; *total gets the sum.
+__device__ __forceinline__ int block_prefix(int v, int32_t* wave_sums, int* total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int incl = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(incl, d, 64);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 63) wave_sums[wave] = incl;
     __syncthreads();
-    for (int d = 1; d < kMaxExperts; d <<= 1) {
-        const int v = e >= d ? total[e - d] : 0;
-        __syncthreads();
-        total[e] += v;
-        __syncthreads();
+    int before = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kOrderWaves; ++w) {
+        before += w < wave ? wave_sums[w] : 0;
+        sum += wave_sums[w];
     }
-    if (e >= a.E) return;
-    int at = total[e] - sum;
-    a.expert_offsets[e] = at;
-    if (e == a.E - 1) a.expert_offsets[a.E] = total[e];
-    for (int t = 0; t < a.tiles; ++t) {
-        int32_t* c = &a.tile_counts[(int64_t)t * a.E + e];
-        const int n = *c;
-        *c = at;
-        at += n;
-    }
+    *total = sum;
+    return before + incl - v;
 }
 
 // Waves take contiguous quarters of the tile, so that ranks ascend with p.
+// A wave's lane holds 4 pairs, 64 apart, per kOrderTile pairs of the tile.
 __global__ __launch_bounds__(kOrderThreads) void order_rank_kernel(OrderArgs a, int bits) {
+    constexpr int kPer = kMaxExperts / kOrderThreads;  // experts t, t + 256, ... of thread t
     __shared__ int32_t base[kOrderWaves][kMaxExperts];
     __shared__ int32_t prefix[kMaxRanks];
+    __shared__ int32_t wave_sums[kOrderWaves];
     const int64_t pairs = (int64_t)a.T * a.K;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t span = (int64_t)kOrderTile / kOrderWaves * a.iters;
-    const int64_t b = ((int64_t)blockIdx.x * kOrderWaves + wave) * span;
+    const int64_t b = ((int64_t)blockIdx.x * kOrderWaves + wave) * span + lane;
     load_prefix(a, prefix);
     for (int e = threadIdx.x; e < kOrderWaves * kMaxExperts; e += kOrderThreads)
         (&base[0][0])[e] = 0;
     __syncthreads();
-    for (int64_t i = b + lane; i < b + span; i += 64) {
-        const int e = pair_expert(a, prefix, i, pairs);
-        if (e >= 0) atomicAdd(&base[wave][e], 1);
+    int e[kOrderUnroll];
+    for (int it = 0; it < a.iters; ++it) {
+        const int64_t i = b + (int64_t)it * (64 * kOrderUnroll);
+#pragma unroll
+        for (int u = 0; u < kOrderUnroll; ++u) e[u] = pair_expert(a, prefix, i + u * 64, pairs);
+#pragma unroll
+        for (int u = 0; u < kOrderUnroll; ++u)
+            if (e[u] >= 0) atomicAdd(&base[wave][e[u]], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kOrderThreads) {
-        int at = a.tile_counts[(int64_t)blockIdx.x * a.E + e];
+    // Totals over all tiles, and over those before this one.
+    int all[kPer], mine[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int x = j * kOrderThreads + threadIdx.x;
+        all[j] = mine[j] = 0;
+        if (a.tiles == 1) {  // no counts were taken: this tile's are all
+            for (int w = 0; w < kOrderWaves; ++w) all[j] += base[w][x];
+        } else if (x < a.E) {
+#pragma unroll 16
+            for (int t = 0; t < a.tiles; ++t) {
+                const int c = a.tile_counts[(int64_t)t * a.E + x];
+                all[j] += c;
+                mine[j] += t < (int)blockIdx.x ? c : 0;
+            }
+        }
+    }
+    int filled = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        if (j * kOrderThreads >= a.E) break;
+        const int x = j * kOrderThreads + threadIdx.x;
+        int layer;
+        const int at = filled + block_prefix(all[j], wave_sums, &layer);
+        filled += layer;
+        if (blockIdx.x == 0 && x < a.E) a.expert_offsets[x] = at;
+        int p = at + mine[j];
         for (int w = 0; w < kOrderWaves; ++w) {
-            const int n = base[w][e];
-            base[w][e] = at;
-            at += n;
+            const int n = base[w][x];
+            base[w][x] = p;
+            p += n;
+        }
+        __syncthreads();
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.expert_offsets[a.E] = filled;
+    for (int it = 0; it < a.iters; ++it) {
+        const int64_t i0 = b + (int64_t)it * (64 * kOrderUnroll);
+        if (a.iters > 1) {  // else they are at hand
+#pragma unroll
+            for (int u = 0; u < kOrderUnroll; ++u) e[u] = pair_expert(a, prefix, i0 + u * 64, pairs);
+        }
+#pragma unroll
+        for (int u = 0; u < kOrderUnroll; ++u) {
+            const int64_t i = i0 + u * 64;
+            const uint64_t same = same_lanes(e[u], bits) & __ballot(e[u] >= 0);
+            int row = -1;
+            if (e[u] >= 0) row = base[wave][e[u]] + __popcll(same & ((1ull << lane) - 1));
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            // the last of them moves the expert on
+            if (e[u] >= 0 && (same >> lane) == 1ull) base[wave][e[u]] = row + 1;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (i < pairs) {
+                a.row_of_slot[i] = row;
+                if (row >= 0) a.slot_of_row[row] = (int32_t)i;
+                if (i >= filled) a.slot_of_row[i] = -1;
+            }
         }
     }
-    __syncthreads();
-    const int filled = a.expert_offsets[a.E];
-    for (int64_t i0 = b; i0 < b + span; i0 += 64) {
-        const int64_t i = i0 + lane;
-        const int e = pair_expert(a, prefix, i, pairs);
-        const uint64_t same = same_lanes(e, bits) & __ballot(e >= 0);
-        int row = -1;
-        if (e >= 0) {
-            const uint64_t below = same & ((1ull << lane) - 1);
-            row = base[wave][e] + __popcll(below);
-        }
-        __builtin_amdgcn_wave_barrier();
-        if (e >= 0 && (same >> lane) == 1ull) base[wave][e] = row + 1;  // the last of them
-        __builtin_amdgcn_wave_barrier();
-        if (i < pairs) {
-            a.row_of_slot[i] = row;
-            if (row >= 0) a.slot_of_row[row] = (int32_t)i;
-            if (i >= filled) a.slot_of_row[i] = -1;
-        }
-    }
+}
+
+// No pairs at all: every offset is zero.
+__global__ __launch_bounds__(kOrderThreads) void order_empty_kernel(OrderArgs a) {
+    for (int e = threadIdx.x; e <= a.E; e += kOrderThreads) a.expert_offsets[e] = 0;
 }
 
 // One wave per (token, slice of 64 chunks): the chunk is read once and stored
@@ -157,29 +204,61 @@ __global__ __launch_bounds__(kRowThreads) void expert_sort_kernel(
     int row = -1;
     if (lane < K) row = row_of_slot[(int64_t)t * K + lane];
     u32x4_t v{};
-    if (c < chunks) v = x[(int64_t)t * chunks + c];
+    if (c < chunks) v = __builtin_nontemporal_load(x + (int64_t)t * chunks + c);
     uint64_t m = __ballot(row >= 0 && row < n_rows);
     while (m) {
         const int k = __builtin_ctzll(m);
         m &= m - 1;
         const int64_t r = __builtin_amdgcn_readlane(row, k);
-        if (c < chunks) rows[r * chunks + c] = v;
+        if (c < chunks) __builtin_nontemporal_store(v, rows + r * chunks + c);
+    }
+}
+
+// The next NB filled slots of *m: all their chunks are loaded, then added.
+template <typename S, int NB>
+__device__ __forceinline__ void unsort_batch(const u32x4_t* __restrict__ rows, int chunks, int c,
+                                             int row, float w, uint64_t* m,
+                                             float (&acc)[Chunk<S>::kN]) {
+    constexpr int N = Chunk<S>::kN;
+    u32x4_t v[NB];
+    float wt[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int k = __builtin_ctzll(*m);
+        *m &= *m - 1;
+        const int64_t r = __builtin_amdgcn_readlane(row, k);
+        wt[b] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), k));
+        v[b] = __builtin_nontemporal_load(rows + r * chunks + c);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        float f[N];
+        chunk_to_f32<S>(v[b], f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = fmaf(wt[b], f[i], acc[i]);
     }
 }
 
 // One wave per (token, slice): out = sum over the filled slots, in ascending
-// slot order, of weight * row, in fp32 from +0; one rounding.
+// slot order, of weight * row, in fp32 from +0; one rounding.  Workgroups go to
+// the XCDs in short runs, so that a token's slots and weights stay in one L2.
+constexpr int kUnsortRunLog2 = 4;
+
 template <typename S>
 __global__ __launch_bounds__(kRowThreads) void expert_unsort_kernel(
     const u32x4_t* __restrict__ rows, int T, int K, int chunks, int64_t n_rows,
     const int32_t* __restrict__ row_of_slot, const float* __restrict__ weights,
     u32x4_t* __restrict__ out, RowSplit rs) {
     constexpr int N = Chunk<S>::kN;
-    int t, part;
-    row_part(rs, &t, &part);
-    if (t >= T) return;
     const int lane = threadIdx.x & 63;
-    const int c = part * 64 + lane;
+    const int wv = __builtin_amdgcn_readfirstlane(
+        xcd_run_block<kUnsortRunLog2>((int)blockIdx.x, (int)gridDim.x) * kRowWavesPerBlock +
+        (int)(threadIdx.x >> 6));
+    const int t = (int)rs.div.div((uint32_t)wv);
+    if (t >= T) return;
+    const int c = (wv - t * rs.split) * 64 + lane;
+    const int at = min(c, chunks - 1);  // lanes past the row's end store nothing
     int row = -1;
     float w = 1.0f;
     if (lane < K) {
@@ -190,23 +269,16 @@ __global__ __launch_bounds__(kRowThreads) void expert_unsort_kernel(
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.0f;
     uint64_t m = __ballot(row >= 0 && row < n_rows);
-    while (m) {
-        const int k = __builtin_ctzll(m);
-        m &= m - 1;
-        const int64_t r = __builtin_amdgcn_readlane(row, k);
-        const float wk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), k));
-        if (c < chunks) {
-            float f[N];
-            chunk_to_f32<S>(rows[r * chunks + c], f);
-#pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = fmaf(wk, f[i], acc[i]);
-        }
-    }
-    if (c < chunks) out[(int64_t)t * chunks + c] = chunk_from_f32<S>(acc);
+    while (__popcll(m) >= 4) unsort_batch<S, 4>(rows, chunks, at, row, w, &m, acc);
+    if (__popcll(m) >= 2) unsort_batch<S, 2>(rows, chunks, at, row, w, &m, acc);
+    if (m) unsort_batch<S, 1>(rows, chunks, at, row, w, &m, acc);
+    if (c < chunks)
+        __builtin_nontemporal_store(chunk_from_f32<S>(acc), out + (int64_t)t * chunks + c);
 }
 
-// One workgroup per token: d_rows[row] = w * d_out and the dot product of
-// d_out with the row, which is read in the same pass.
+// One workgroup per token: a chunk of d_out is read once and held while the
+// chunks of the token's rows pass, four at a time: their products go into one
+// sum per filled slot, and weight * d_out to their gradients.
 constexpr int kBackThreads = 256;
 
 template <typename S>
@@ -218,30 +290,63 @@ __global__ __launch_bounds__(kBackThreads) void expert_unsort_backward_kernel(
     __shared__ float part[kBackThreads / 64][kMaxTopk];
     const int t = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int k = 0; k < K; ++k) {
-        const int64_t r = row_of_slot[(int64_t)t * K + k];
-        float dot = 0.0f;
-        if (r >= 0 && r < n_rows) {
-            const float w = weights[(int64_t)t * K + k];
-            for (int c = threadIdx.x; c < chunks; c += kBackThreads) {
-                float d[N], y[N];
-                chunk_to_f32<S>(d_out[(int64_t)t * chunks + c], d);
-                chunk_to_f32<S>(rows[r * chunks + c], y);
+    int row = -1;
+    float w = 0.0f;
+    if (lane < K) {
+        row = row_of_slot[(int64_t)t * K + lane];
+        w = weights[(int64_t)t * K + lane];
+    }
+    const uint64_t filled = __ballot(row >= 0 && row < n_rows);
+    float dot[kMaxTopk];  // of the b-th filled slot
+#pragma unroll
+    for (int b = 0; b < kMaxTopk; ++b) dot[b] = 0.0f;
+    for (int c = threadIdx.x; c < chunks; c += kBackThreads) {
+        float d[N];
+        chunk_to_f32<S>(__builtin_nontemporal_load(d_out + (int64_t)t * chunks + c), d);
+        uint64_t m = filled;
+#pragma unroll
+        for (int b0 = 0; b0 < kMaxTopk; b0 += 4) {
+            if (m == 0) break;
+            int64_t at[4];
+            float wt[4];
+            u32x4_t v[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int k = m ? __builtin_ctzll(m) : 0;
+                const bool has = m != 0;
+                m &= m - 1;
+                wt[b] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), k));
+                at[b] = has ? (int64_t)__builtin_amdgcn_readlane(row, k) * chunks + c : -1;
+                if (has) v[b] = __builtin_nontemporal_load(rows + at[b]);
+            }
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if (at[b] < 0) break;
+                float y[N], g[N];
+                chunk_to_f32<S>(v[b], y);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    dot = fmaf(d[i], y[i], dot);
-                    d[i] *= w;
+                    dot[b0 + b] = fmaf(d[i], y[i], dot[b0 + b]);
+                    g[i] = d[i] * wt[b];
                 }
-                d_rows[r * chunks + c] = chunk_from_f32<S>(d);
+                __builtin_nontemporal_store(chunk_from_f32<S>(g), d_rows + at[b]);
             }
         }
-        dot = wave_sum(dot);
-        if (lane == 0) part[wave][k] = dot;
+    }
+    uint64_t m = filled;
+#pragma unroll
+    for (int b = 0; b < kMaxTopk; ++b) {
+        if (m == 0) break;
+        const int k = __builtin_ctzll(m);
+        m &= m - 1;
+        const float s = wave_sum(dot[b]);
+        if (lane == 0) part[wave][k] = s;
     }
     __syncthreads();
     if ((int)threadIdx.x < K) {
         float s = 0.0f;
-        for (int i = 0; i < kBackThreads / 64; ++i) s += part[i][threadIdx.x];
+        if ((filled >> threadIdx.x) & 1)
+            for (int i = 0; i < kBackThreads / 64; ++i) s += part[i][threadIdx.x];
         d_weights[(int64_t)t * K + threadIdx.x] = s;
     }
 }
@@ -249,16 +354,18 @@ __global__ __launch_bounds__(kBackThreads) void expert_unsort_backward_kernel(
 }  // namespace
 
 hipError_t launch_expert_order(const OrderArgs& a, const Launch& L) {
-    const Launch first{L.stream, L.start, nullptr, 0u}, mid{L.stream, nullptr, nullptr, 0u},
-        last{L.stream, nullptr, L.stop, 0u};
-    hipError_t e = hipSuccess;
-    if (a.tiles > 0) e = launch_kernel(order_count_kernel, dim3(a.tiles), dim3(kOrderThreads), first, a);
-    if (e == hipSuccess)
-        e = launch_kernel(order_scan_kernel, dim3(1), dim3(kMaxExperts), a.tiles > 0 ? mid : L, a);
-    if (e != hipSuccess || a.tiles == 0) return e;
+    if (a.tiles == 0)
+        return launch_kernel(order_empty_kernel, dim3(1), dim3(kOrderThreads), L, a);
     int bits = 0;
     while ((1 << bits) < a.E) ++bits;
-    return launch_kernel(order_rank_kernel, dim3(a.tiles), dim3(kOrderThreads), last, a, bits);
+    const bool counted = a.tiles > 1;
+    if (counted) {
+        const hipError_t e = launch_kernel(order_count_kernel, dim3(a.tiles), dim3(kOrderThreads),
+                                           Launch{L.stream, L.start, nullptr, 0u}, a);
+        if (e != hipSuccess) return e;
+    }
+    return launch_kernel(order_rank_kernel, dim3(a.tiles), dim3(kOrderThreads),
+                         Launch{L.stream, counted ? nullptr : L.start, L.stop, 0u}, a, bits);
 }
 
 hipError_t launch_expert_sort(const void* x, int T, int K, int64_t row_bytes,

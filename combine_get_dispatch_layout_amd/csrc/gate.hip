@@ -12,8 +12,11 @@
 // wherever they go through exp, and the logits themselves (exact, and in the
 // same order) when there is neither bias nor group.  The weights are fp32.
 //
-// One wavefront per token: lane l holds experts l, l + 64, ...; the K rounds
-// are wave-wide maxima.
+// One wavefront per token: lane l holds experts l NV .. l NV + NV - 1 in
+// registers (one vector load where E allows it).  A round takes the wave-wide
+// maximum of the keys as unsigned integers that order like them (0 = cannot be
+// chosen), then the first lane that holds it.  What bounds it is that chain of
+// rounds, not the logits' bytes.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -37,31 +40,36 @@ __device__ __forceinline__ float log_sigmoid(float l) {
 }
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
-// Wave-wide best (largest key, then lowest index).
-template <typename Key>
-__device__ __forceinline__ void wave_best(Key& key, int& idx) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-        const Key k = __shfl_xor(key, d, 64);
-        const int i = __shfl_xor(idx, d, 64);
-        if (k > key || (k == key && i < idx)) {
-            key = k;
-            idx = i;
-        }
-    }
+// Unsigned integers in the order of the values; +0 and -0 are alike.
+__device__ __forceinline__ uint32_t ordered(float v) {
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ uint64_t ordered(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);
+    return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
 }
 
-// The token's logits, l[j] of expert lane + 64 j; NaN counts as -inf.
+// The token's logits, l[j] of expert lane * NV + j; NaN counts as -inf, and
+// past the last expert there is -inf.  `vec`: E is a multiple of NV and rows
+// are aligned to NV values.
 template <typename S, int NV>
-__device__ __forceinline__ void load_logits(const S* logits, int E, int t, int lane,
+__device__ __forceinline__ void load_logits(const S* logits, int E, int t, int lane, bool vec,
                                             float (&l)[NV]) {
     const S* row = logits + (int64_t)t * E;
+    const int e0 = lane * NV;
+    if (vec) {
+        typedef S vals __attribute__((ext_vector_type(NV)));
+        vals v{};
+        if (e0 < E) v = *reinterpret_cast<const vals*>(row + e0);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int e = lane + 64 * j;
-        const float v = e < E ? (float)row[e] : kNegInf;
-        l[j] = v >= kNegInf ? v : kNegInf;
+        for (int j = 0; j < NV; ++j) l[j] = e0 < E ? (float)v[j] : kNegInf;
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) l[j] = e0 + j < E ? (float)row[e0 + j] : kNegInf;
     }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) l[j] = l[j] >= kNegInf ? l[j] : kNegInf;
 }
 
 template <int NV>
@@ -80,102 +88,139 @@ __device__ __forceinline__ float exp_sum(const float (&l)[NV], float m) {
     return wave_sum(z);
 }
 
-// Key: float (the logits are the keys) or double.
+// The sum of the two best of (one, two), each -inf when there is none.
+__device__ __forceinline__ double pair_score(double one, double two) {
+    return one > -INFINITY ? one + (two > -INFINITY ? two : 0.0) : -INFINITY;
+}
+
+// Drops the keys outside the groups_kept best groups.  staged: 64 * NV values
+// of this wave in LDS.
+template <int NV>
+__device__ __forceinline__ void keep_groups(const GateArgs& a, int lane, double* staged,
+                                            double (&key)[NV]) {
+    const int per = a.E / a.groups;
+    const int span = per / NV;  // lanes of a group, when it fills whole lanes
+    double gs = -INFINITY;      // lane g < groups: the group's score
+    if (per % NV == 0 && (span & (span - 1)) == 0 && span <= 64) {
+        double one = key[0], two = -INFINITY;
+#pragma unroll
+        for (int j = 1; j < NV; ++j) {
+            two = fmax(two, fmin(one, key[j]));
+            one = fmax(one, key[j]);
+        }
+        for (int d = 1; d < span; d <<= 1) {
+            const double o1 = __shfl_xor(one, d, 64), o2 = __shfl_xor(two, d, 64);
+            two = fmax(fmin(one, o1), fmax(two, o2));
+            one = fmax(one, o1);
+        }
+        const double score = pair_score(one, two);
+        gs = __shfl(score, lane * span & 63, 64);
+        if (lane >= a.groups) gs = -INFINITY;
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) staged[lane * NV + j] = key[j];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        double one = -INFINITY, two = -INFINITY;
+        if (lane < a.groups) {
+            for (int i = 0; i < per; ++i) {
+                const double v = staged[lane * per + i];
+                two = fmax(two, fmin(one, v));
+                one = fmax(one, v);
+            }
+            gs = pair_score(one, two);
+        }
+    }
+    const uint64_t mine = ordered(gs);
+    int better = 0;
+    for (int g = 0; g < a.groups; ++g) {
+        const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)mine, g);
+        const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(mine >> 32), g);
+        const uint64_t o = ((uint64_t)hi << 32) | lo;
+        better += (o > mine || (o == mine && g < lane)) ? 1 : 0;
+    }
+    const uint64_t keep = __ballot(lane < a.groups && better < a.groups_kept);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int g = (int)a.per_div.div((uint32_t)(lane * NV + j));
+        if (g >= 64 || !((keep >> g) & 1)) key[j] = -INFINITY;
+    }
+}
+
+// Key: uint32_t where the logits are the keys, uint64_t where scores are.
 template <typename S, int NV, typename Key>
-__global__ __launch_bounds__(kGateThreads) void gate_topk_kernel(GateArgs a,
+__global__ __launch_bounds__(kGateThreads) void gate_topk_kernel(GateArgs a, bool vec,
                                                                  int64_t* __restrict__ topk_idx,
                                                                  float* __restrict__ topk_weights) {
-    constexpr bool kExact = sizeof(Key) == 8;
-    __shared__ Key staged[kExact ? kGateWaves * NV * 64 : 1];
+    constexpr bool kScores = sizeof(Key) == 8;
+    __shared__ double staged[kScores ? kGateWaves * NV * 64 : 1];
     const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t = blockIdx.x * kGateWaves + wave;
     if (t >= a.T) return;
     float l[NV];
-    load_logits<S, NV>(static_cast<const S*>(a.logits), a.E, t, lane, l);
+    load_logits<S, NV>(static_cast<const S*>(a.logits), a.E, t, lane, vec, l);
     const bool softmax = a.score == MOEDX_GATE_SOFTMAX;
-    const float m = row_max(l);
-    const float z = softmax ? exp_sum(l, m) : 1.0f;
 
-    const Key none = (Key)kNegInf;
+    float m = 0.0f;
     Key key[NV];
-    if constexpr (!kExact) {
+    if constexpr (!kScores) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) key[j] = l[j];
+        for (int j = 0; j < NV; ++j) key[j] = l[j] > kNegInf ? ordered(l[j]) : 0u;
+        if (softmax && !a.renormalize) m = row_max(l);
     } else {
-        double zd = 0.0;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            key[j] = softmax ? exp((double)l[j] - (double)m) : 1.0 / (1.0 + exp(-(double)l[j]));
-            if (!(l[j] > kNegInf)) key[j] = 0.0;
-            zd += key[j];
-        }
+        double s[NV];
         if (softmax) {
-#pragma unroll
-            for (int d = 32; d >= 1; d >>= 1) zd += __shfl_xor(zd, d, 64);
-        }
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int e = lane + 64 * j;
-            if (softmax) key[j] /= zd;
-            if (a.bias && e < a.E) key[j] += (double)a.bias[e];
-            if (!(l[j] > kNegInf) || !(key[j] > none)) key[j] = none;
-        }
-        if (a.groups > 1) {
-            Key* mine = staged + wave * NV * 64;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) mine[lane + 64 * j] = key[j];
-            __builtin_amdgcn_wave_barrier();
-            // lane g < groups: the sum of the group's two best keys
-            const int per = a.E / a.groups;
-            Key one = none, two = none;
-            if (lane < a.groups) {
-                for (int i = 0; i < per; ++i) {
-                    const Key v = mine[lane * per + i];
-                    two = fmax(two, fmin(one, v));
-                    one = fmax(one, v);
-                }
-            }
-            const Key gs = one > none ? one + (two > none ? two : 0.0) : none;
-            int better = 0;
-            for (int g = 0; g < a.groups; ++g) {
-                const Key o = __shfl(gs, g, 64);
-                better += (o > gs || (o == gs && g < lane)) ? 1 : 0;
-            }
-            const uint64_t keep = __ballot(lane < a.groups && better < a.groups_kept);
+            m = row_max(l);
+            double z = 0.0;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int e = lane + 64 * j;
-                if (e < a.E && !((keep >> (e / per)) & 1)) key[j] = none;
+                s[j] = l[j] > kNegInf ? exp((double)l[j] - (double)m) : 0.0;
+                z += s[j];
             }
+            z = wave_sum(z);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) s[j] /= z;
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) s[j] = 1.0 / (1.0 + exp(-(double)l[j]));
         }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int e = lane * NV + j;
+            if (a.bias && e < a.E) s[j] += (double)a.bias[e];
+            if (!(l[j] > kNegInf) || !(s[j] > -INFINITY)) s[j] = -INFINITY;
+        }
+        if (a.groups > 1) keep_groups<NV>(a, lane, staged + wave * NV * 64, s);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) key[j] = s[j] > -INFINITY ? ordered(s[j]) : 0ull;
     }
 
     // K rounds; lane k keeps the k-th choice and its logit.
     int mine_idx = -1;
     float mine_l = kNegInf;
     for (int k = 0; k < a.K; ++k) {
-        Key best = none;
-        int at = 1 << 30;
+        Key best = key[0];
+        int at = 0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 1; j < NV; ++j)
             if (key[j] > best) {
                 best = key[j];
-                at = lane + 64 * j;
+                at = j;
             }
-        wave_best(best, at);
-        if (!(best > none)) break;
+        const Key top = wave_max(best);
+        if (top == 0) break;
+        const int from = __builtin_ctzll(__ballot(best == top));
+        const int j0 = __builtin_amdgcn_readlane(at, from);
         float lv = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (at == lane + 64 * j) {
-                key[j] = none;
+        for (int j = 0; j < NV; ++j)
+            if (j == j0) {
                 lv = l[j];
+                if (lane == from) key[j] = 0;
             }
-        }
-        lv = __shfl(lv, at & 63, 64);
+        lv = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lv), from));
         if (lane == k) {
-            mine_idx = at;
+            mine_idx = from * NV + j0;
             mine_l = lv;
         }
     }
@@ -188,8 +233,11 @@ __global__ __launch_bounds__(kGateThreads) void gate_topk_kernel(GateArgs a,
         const float x = have ? expf(s - top) : 0.0f;
         const float total = wave_sum(x);
         w = have ? x / total : 0.0f;
+    } else if (softmax) {
+        const float z = exp_sum(l, m);
+        w = have ? expf(mine_l - m) / z : 0.0f;
     } else if (have) {
-        w = softmax ? expf(mine_l - m) / z : sigmoid(mine_l);
+        w = sigmoid(mine_l);
     }
     if (lane < a.K) {
         topk_idx[(int64_t)t * a.K + lane] = mine_idx;
@@ -199,14 +247,14 @@ __global__ __launch_bounds__(kGateThreads) void gate_topk_kernel(GateArgs a,
 
 template <typename S, int NV>
 __global__ __launch_bounds__(kGateThreads) void gate_topk_backward_kernel(
-    GateArgs a, const int64_t* __restrict__ topk_idx, const float* __restrict__ d_topk_weights,
+    GateArgs a, bool vec, const int64_t* __restrict__ topk_idx, const float* __restrict__ d_topk_weights,
     S* __restrict__ d_logits) {
     const int lane = threadIdx.x & 63;
-    const int t = blockIdx.x * kGateWaves + (threadIdx.x >> 6);
+    const int t = blockIdx.x * kGateWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (t >= a.T) return;
     const S* logits = static_cast<const S*>(a.logits);
     float l[NV];
-    load_logits<S, NV>(logits, a.E, t, lane, l);
+    load_logits<S, NV>(logits, a.E, t, lane, vec, l);
     const bool softmax = a.score == MOEDX_GATE_SOFTMAX;
 
     // lane k: the k-th choice, its logit and its incoming gradient
@@ -252,33 +300,50 @@ __global__ __launch_bounds__(kGateThreads) void gate_topk_backward_kernel(
         const int e = __builtin_amdgcn_readlane(idx, k);
         const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(own), k));
 #pragma unroll
-        for (int j = 0; j < NV; ++j) d[j] += e == lane + 64 * j ? v : 0.0f;
+        for (int j = 0; j < NV; ++j) d[j] += e == lane * NV + j ? v : 0.0f;
     }
-    S* out = d_logits + (int64_t)t * a.E;
+    if (dense) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int e = lane + 64 * j;
-        if (e >= a.E) continue;
-        float v = d[j];
-        if (dense) v = l[j] > kNegInf ? a.scale * (expf(l[j] - m) / z) * (v - dot) : 0.0f;
-        out[e] = (S)v;
+        for (int j = 0; j < NV; ++j)
+            d[j] = l[j] > kNegInf ? a.scale * (expf(l[j] - m) / z) * (d[j] - dot) : 0.0f;
     }
+    S* out = d_logits + (int64_t)t * a.E + lane * NV;
+    if (vec) {
+        typedef S vals __attribute__((ext_vector_type(NV)));
+        vals v;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) v[j] = (S)d[j];
+        if (lane * NV < a.E) *reinterpret_cast<vals*>(out) = v;
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (lane * NV + j < a.E) out[j] = (S)d[j];
+    }
+}
+
+// Whether rows can be moved NV values at a time (16 bytes at most).
+template <typename S, int NV>
+bool vector_rows(const GateArgs& a, const void* other) {
+    constexpr uintptr_t kBytes = sizeof(S) * NV < 16 ? sizeof(S) * NV : 16;
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(other);
+    return a.E % NV == 0 && (p | (a.E * sizeof(S))) % kBytes == 0;
 }
 
 template <typename S, int NV>
 hipError_t launch_gate_nv(const GateArgs& a, int64_t* idx, float* w, const Launch& L) {
     const dim3 grid((a.T + kGateWaves - 1) / kGateWaves), block(kGateThreads);
+    const bool vec = vector_rows<S, NV>(a, nullptr);
     if (a.bias == nullptr && a.groups <= 1)
-        return launch_kernel(gate_topk_kernel<S, NV, float>, grid, block, L, a, idx, w);
-    return launch_kernel(gate_topk_kernel<S, NV, double>, grid, block, L, a, idx, w);
+        return launch_kernel(gate_topk_kernel<S, NV, uint32_t>, grid, block, L, a, vec, idx, w);
+    return launch_kernel(gate_topk_kernel<S, NV, uint64_t>, grid, block, L, a, vec, idx, w);
 }
 
 template <typename S, int NV>
 hipError_t launch_gate_bwd_nv(const GateArgs& a, const int64_t* idx, const float* dw, void* dl,
                               const Launch& L) {
     const dim3 grid((a.T + kGateWaves - 1) / kGateWaves), block(kGateThreads);
-    return launch_kernel(gate_topk_backward_kernel<S, NV>, grid, block, L, a, idx, dw,
-                         static_cast<S*>(dl));
+    return launch_kernel(gate_topk_backward_kernel<S, NV>, grid, block, L, a,
+                         vector_rows<S, NV>(a, dl), idx, dw, static_cast<S*>(dl));
 }
 
 template <typename F>

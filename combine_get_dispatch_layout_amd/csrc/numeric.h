@@ -33,17 +33,74 @@ __device__ __forceinline__ u32x4_t chunk_from_f32(const float (&f)[Chunk<S>::kN]
     return __builtin_bit_cast(u32x4_t, v);
 }
 
-// Sum over the 64 lanes of a wave, in a fixed order; every lane gets it.
+// Reductions over the 64 lanes of a wave by lane-shifted operands (no LDS
+// traffic): rows of 16 first, then across rows; lane 63 holds the result,
+// which every lane gets.  The order is fixed.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ int dpp(int old, int v) {
+    return __builtin_amdgcn_update_dpp(old, v, kCtrl, kRows, 0xf, false);
+}
+
+#define MOEDX_DPP_STEPS(step) \
+    step(0x111, 0xf);         \
+    step(0x112, 0xf);         \
+    step(0x114, 0xf);         \
+    step(0x118, 0xf);         \
+    step(0x142, 0xa);         \
+    step(0x143, 0xc)
+
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-    return v;
+#define MOEDX_STEP(c, r) v += __int_as_float(dpp<c, r>(0, __float_as_int(v)))
+    MOEDX_DPP_STEPS(MOEDX_STEP);
+#undef MOEDX_STEP
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#define MOEDX_STEP(c, r)                                                       \
+    {                                                                          \
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);                    \
+        const uint32_t lo = (uint32_t)dpp<c, r>(0, (int)(uint32_t)b);          \
+        const uint32_t hi = (uint32_t)dpp<c, r>(0, (int)(uint32_t)(b >> 32));  \
+        v += __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);            \
+    }
+    MOEDX_DPP_STEPS(MOEDX_STEP);
+#undef MOEDX_STEP
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#define MOEDX_STEP(c, r) v = max(v, (uint32_t)dpp<c, r>((int)v, (int)v))
+    MOEDX_DPP_STEPS(MOEDX_STEP);
+#undef MOEDX_STEP
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+#define MOEDX_STEP(c, r)                                                                 \
+    {                                                                                    \
+        const uint32_t lo = (uint32_t)dpp<c, r>((int)(uint32_t)v, (int)(uint32_t)v);     \
+        const uint32_t hi =                                                              \
+            (uint32_t)dpp<c, r>((int)(uint32_t)(v >> 32), (int)(uint32_t)(v >> 32));     \
+        const uint64_t o = ((uint64_t)hi << 32) | lo;                                    \
+        v = o > v ? o : v;                                                               \
+    }
+    MOEDX_DPP_STEPS(MOEDX_STEP);
+#undef MOEDX_STEP
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, 63);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), 63);
+    return ((uint64_t)hi << 32) | lo;
 }
 
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-    return v;
+#define MOEDX_STEP(c, r) \
+    v = fmaxf(v, __int_as_float(dpp<c, r>(__float_as_int(v), __float_as_int(v))))
+    MOEDX_DPP_STEPS(MOEDX_STEP);
+#undef MOEDX_STEP
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
 }  // namespace moedx
