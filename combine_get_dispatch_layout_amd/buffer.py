@@ -32,6 +32,19 @@ def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _addr(t: Optional[torch.Tensor]):
+    """_ptr as a plain int (or None)."""
+    if t is None:
+        return None
+    return t.data_ptr() or (t.untyped_storage().data_ptr() or None)
+
+
+# The handle of a device's current stream: torch's own accessor for callers of
+# raw kernels where it has one (a tenth of the Stream object's cost).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 # Releases that must wait until no stream capture is running.  Destroying a
 # context synchronises its stream and frees device and pinned memory, and an
 # event destroy is not a capturable call either; any of them during a capture
@@ -211,6 +224,9 @@ class Buffer:
         # on it when such a tensor is freed, possibly after this Buffer is gone.
         self._ctx_stream = torch.cuda.Stream(device=self.device)
         C.check(C.moedx_ctx_set_stream(self.ctx, self._ctx_stream.cuda_stream))
+        self._torch_device = torch.device("cuda", self.device)
+        self._index = self._torch_device.index
+        self._order_size = (None, None, 0)  # the last expert_order's T, K and workspace bytes
 
     _destroy = staticmethod(C.moedx_destroy)
     _release = staticmethod(_release)
@@ -511,13 +527,19 @@ class Buffer:
         `shape` (None = any size); made contiguous."""
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a tensor")
-        if t.device != self._torch_device:
+        if not t.is_cuda or t.get_device() != self._index:
             raise ValueError(f"{name} is on {t.device}, the Buffer on {self._torch_device}")
         if t.dtype not in dtypes:
             raise ValueError(f"{name} has dtype {t.dtype}, expected one of {list(dtypes)}")
-        if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        return t.contiguous()
+        got = t.shape
+        bad = len(got) != len(shape)
+        if not bad:
+            for n, m in zip(shape, got):
+                if n is not None and n != m:
+                    bad = True
+        if bad:
+            raise ValueError(f"{name} has shape {tuple(got)}, expected {tuple(shape)}")
+        return t if t.is_contiguous() else t.contiguous()
 
     def _out(self, name: str, out, dtype, shape) -> torch.Tensor:
         """`out` checked (it must be contiguous), or a new tensor."""
@@ -527,10 +549,6 @@ class Buffer:
             raise ValueError(f"{name} must be contiguous")
         return out
 
-    @property
-    def _torch_device(self) -> "torch.device":
-        return torch.device("cuda", self.device)
-
     def _exec_here(self, previous_event, async_finish, allocate_on_comm_stream, no_sync):
         """As _exec, on the current stream of this Buffer's device."""
         if _deferred:
@@ -538,9 +556,14 @@ class Buffer:
         done = ctypes.c_void_p() if async_finish else None
         flags = (C.MOEDX_ON_CTX_STREAM if allocate_on_comm_stream else 0) | (
             C.MOEDX_ASYNC if no_sync else 0)
-        prev = previous_event.event if previous_event is not None else None
-        stream = torch.cuda.current_stream(self.device).cuda_stream
-        return C.make_exec(stream, prev, done, flags), done
+        ex = C.moedx_exec()  # zeroed
+        ex.stream = _raw_stream(self._index)
+        ex.flags = flags
+        if previous_event is not None:
+            ex.prev = previous_event.event
+        if done is not None:
+            ex.done = ctypes.addressof(done)
+        return ex, done
 
     def _gate_options(self, score, num_groups, groups_kept, renormalize, scale, bias):
         if score not in _SCORES:
@@ -549,7 +572,7 @@ class Buffer:
             bias = self._check("bias", bias, (torch.float32,), (self.num_experts,))
         return C.moedx_gate(_SCORES[score], num_groups,
                             num_groups if groups_kept is None else groups_kept,
-                            1 if renormalize else 0, scale, _ptr(bias)), bias
+                            1 if renormalize else 0, scale, _addr(bias)), bias
 
     def gate_topk(self, logits: torch.Tensor, topk: int, score: str = "softmax",
                   num_groups: int = 1, groups_kept: Optional[int] = None,
@@ -569,12 +592,12 @@ class Buffer:
         logits = self._check("logits", logits, _DTYPES, (None, self.num_experts))
         T = logits.shape[0]
         opts, bias = self._gate_options(score, num_groups, groups_kept, renormalize, scale, bias)
-        dev = logits.device
+        dev = self._torch_device
         idx = torch.empty(T, max(topk, 0), dtype=torch.int64, device=dev)
         w = torch.empty(T, max(topk, 0), dtype=torch.float32, device=dev)
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
-        C.check(C.moedx_gate_topk(self.ctx, _ptr(logits), _DTYPES[logits.dtype], T, topk,
-                                  ctypes.byref(opts), _ptr(idx), _ptr(w), ctypes.byref(ex)))
+        C.check(C.moedx_gate_topk(self.ctx, _addr(logits), _DTYPES[logits.dtype], T, topk,
+                                  ctypes.byref(opts), _addr(idx), _addr(w), ctypes.byref(ex)))
         self._keep(allocate_on_comm_stream, logits, bias, idx, w)
         return idx, w, self._event(done)
 
@@ -596,8 +619,8 @@ class Buffer:
         opts, bias = self._gate_options(score, num_groups, groups_kept, renormalize, scale, bias)
         d = torch.empty_like(logits)
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
-        C.check(C.moedx_gate_topk_backward(self.ctx, _ptr(logits), _DTYPES[logits.dtype], T, K,
-                                           ctypes.byref(opts), _ptr(topk_idx), _ptr(dw), _ptr(d),
+        C.check(C.moedx_gate_topk_backward(self.ctx, _addr(logits), _DTYPES[logits.dtype], T, K,
+                                           ctypes.byref(opts), _addr(topk_idx), _addr(dw), _addr(d),
                                            ctypes.byref(ex)))
         self._keep(allocate_on_comm_stream, logits, bias, topk_idx, dw, d)
         return d, self._event(done)
@@ -612,17 +635,20 @@ class Buffer:
         read on the host."""
         topk_idx = self._check("topk_idx", topk_idx, (torch.int64,), (None, None))
         T, K = topk_idx.shape
-        nbytes = ctypes.c_size_t()
-        C.check(C.moedx_expert_order_workspace_bytes(self.ctx, T, K, ctypes.byref(nbytes)))
-        dev = topk_idx.device
+        if self._order_size[:2] != (T, K):
+            nbytes = ctypes.c_size_t()
+            C.check(C.moedx_expert_order_workspace_bytes(self.ctx, T, K, ctypes.byref(nbytes)))
+            self._order_size = (T, K, nbytes.value)
+        nbytes = self._order_size[2]
+        dev = self._torch_device
         offsets = torch.empty(self.num_experts + 1, dtype=torch.int32, device=dev)
         row_of_slot = torch.empty(T, K, dtype=torch.int32, device=dev)
         slot_of_row = torch.empty(T * K, dtype=torch.int32, device=dev)
-        ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
-        C.check(C.moedx_expert_order(self.ctx, _ptr(topk_idx), T, K,
-                                     handle.ptr if handle is not None else None, _ptr(offsets),
-                                     _ptr(row_of_slot), _ptr(slot_of_row), _ptr(ws), nbytes.value,
+        C.check(C.moedx_expert_order(self.ctx, _addr(topk_idx), T, K,
+                                     handle.ptr if handle is not None else None, _addr(offsets),
+                                     _addr(row_of_slot), _addr(slot_of_row), _addr(ws), nbytes,
                                      ctypes.byref(ex)))
         self._keep(allocate_on_comm_stream, topk_idx, offsets, row_of_slot, slot_of_row, ws,
                    handle.workspace if handle is not None else None)
@@ -640,8 +666,8 @@ class Buffer:
         ros = self._check("row_of_slot", order.row_of_slot, (torch.int32,), (T, K))
         rows = self._out("out", out, x.dtype, (T * K, H))
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
-        C.check(C.moedx_expert_sort(self.ctx, _ptr(x), _DTYPES[x.dtype], T, K, H, _ptr(ros),
-                                    _ptr(rows), ctypes.byref(ex)))
+        C.check(C.moedx_expert_sort(self.ctx, _addr(x), _DTYPES[x.dtype], T, K, H, _addr(ros),
+                                    _addr(rows), ctypes.byref(ex)))
         self._keep(allocate_on_comm_stream, x, ros, rows)
         return rows, self._event(done)
 
@@ -661,8 +687,8 @@ class Buffer:
                                                           (torch.float32,), (T, K))
         out = self._out("out", out, rows.dtype, (T, H))
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
-        C.check(C.moedx_expert_unsort(self.ctx, _ptr(rows), _DTYPES[rows.dtype], T, K, H,
-                                      _ptr(ros), _ptr(w), _ptr(out), ctypes.byref(ex)))
+        C.check(C.moedx_expert_unsort(self.ctx, _addr(rows), _DTYPES[rows.dtype], T, K, H,
+                                      _addr(ros), _addr(w), _addr(out), ctypes.byref(ex)))
         self._keep(allocate_on_comm_stream, rows, ros, w, out)
         return out, self._event(done)
 
@@ -693,9 +719,9 @@ class Buffer:
         d_rows = self._out("out", out, rows.dtype, (T * K, H))
         d_w = torch.empty(T, K, dtype=torch.float32, device=rows.device)
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
-        C.check(C.moedx_expert_unsort_backward(self.ctx, _ptr(d_out), _ptr(rows),
-                                               _DTYPES[rows.dtype], T, K, H, _ptr(ros), _ptr(w),
-                                               _ptr(d_rows), _ptr(d_w), ctypes.byref(ex)))
+        C.check(C.moedx_expert_unsort_backward(self.ctx, _addr(d_out), _addr(rows),
+                                               _DTYPES[rows.dtype], T, K, H, _addr(ros), _addr(w),
+                                               _addr(d_rows), _addr(d_w), ctypes.byref(ex)))
         self._keep(allocate_on_comm_stream, d_out, rows, ros, w, d_rows, d_w)
         return d_rows, d_w, self._event(done)
 
@@ -706,9 +732,9 @@ class Buffer:
         t = rows.expert_offsets if isinstance(rows, ExpertOrder) else rows
         if x.dim() == 3:
             t = self._check("recv_count", t, (torch.int32,), (E,))
-            return C.moedx_expert_rows(None, _ptr(t), x.shape[0] * x.shape[1]), t
+            return C.moedx_expert_rows(None, _addr(t), x.shape[0] * x.shape[1]), t
         t = self._check("expert_offsets", t, (torch.int32,), (E + 1,))
-        return C.moedx_expert_rows(_ptr(t), None, x.shape[0]), t
+        return C.moedx_expert_rows(_addr(t), None, x.shape[0]), t
 
     def _lead(self, name: str, x) -> tuple:
         """Leading dimensions of a row buffer: (M,) or (E, cap)."""
@@ -746,8 +772,8 @@ class Buffer:
         y = self._out("out", out, x.dtype, lead + (N,))
         pre = torch.empty(lead + (2 * N,), dtype=x.dtype, device=x.device) if return_pre else None
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
-        C.check(C.moedx_expert_linear(self.ctx, _ptr(x), _ptr(w), _DTYPES[x.dtype], K, N,
-                                      ctypes.byref(er), 1 if swiglu else 0, _ptr(y), _ptr(pre),
+        C.check(C.moedx_expert_linear(self.ctx, _addr(x), _addr(w), _DTYPES[x.dtype], K, N,
+                                      ctypes.byref(er), 1 if swiglu else 0, _addr(y), _addr(pre),
                                       ctypes.byref(ex)))
         self._keep(allocate_on_comm_stream, x, w, t, y, pre)
         return y, pre, self._event(done)
@@ -777,9 +803,9 @@ class Buffer:
         d_x = self._out("out", out, x.dtype, lead + (K,))
         d_w = self._out("d_w", d_w, d_w_dtype, (self.num_experts, N, K))
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
-        C.check(C.moedx_expert_linear_backward(self.ctx, _ptr(d_y), _ptr(x), _ptr(w),
-                                               _DTYPES[x.dtype], K, N, ctypes.byref(er), _ptr(d_x),
-                                               _ptr(d_w), _DTYPES[d_w_dtype], ctypes.byref(ex)))
+        C.check(C.moedx_expert_linear_backward(self.ctx, _addr(d_y), _addr(x), _addr(w),
+                                               _DTYPES[x.dtype], K, N, ctypes.byref(er), _addr(d_x),
+                                               _addr(d_w), _DTYPES[d_w_dtype], ctypes.byref(ex)))
         self._keep(allocate_on_comm_stream, d_y, x, w, t, d_x, d_w)
         return d_x, d_w, self._event(done)
 
@@ -798,8 +824,8 @@ class Buffer:
         er, t = self._expert_rows(rows, d_h)
         d_pre = self._out("out", out, d_h.dtype, lead + (2 * N,))
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
-        C.check(C.moedx_expert_swiglu_backward(self.ctx, _ptr(d_h), _ptr(pre), _DTYPES[d_h.dtype],
-                                               N, ctypes.byref(er), _ptr(d_pre),
+        C.check(C.moedx_expert_swiglu_backward(self.ctx, _addr(d_h), _addr(pre), _DTYPES[d_h.dtype],
+                                               N, ctypes.byref(er), _addr(d_pre),
                                                ctypes.byref(ex)))
         self._keep(allocate_on_comm_stream, d_h, pre, t, d_pre)
         return d_pre, self._event(done)

@@ -192,7 +192,14 @@ __global__ __launch_bounds__(kOrderThreads) void order_empty_kernel(OrderArgs a)
 }
 
 // One wave per (token, slice of 64 chunks): the chunk is read once and stored
-// to every row of the token.
+// to every row of the token.  The stores stay in the caches for the product
+// that reads the rows next (4096 x 7168 to half of 8 slots: 46 us, 55 us with
+// streaming stores), and LDS that nothing touches keeps it to 6 workgroups per
+// CU: more rows in flight spread over more of memory (8191 x 7168 to 8 skewed
+// slots: 182 us at 4 to 6, 193 at 7, 198 without; 2 to 14 chunks per lane 195
+// to 205).
+constexpr int kSortWorkgroupsPerCu = 6;
+
 __global__ __launch_bounds__(kRowThreads) void expert_sort_kernel(
     const u32x4_t* __restrict__ x, int T, int K, int chunks, int64_t n_rows,
     const int32_t* __restrict__ row_of_slot, u32x4_t* __restrict__ rows, RowSplit rs) {
@@ -203,14 +210,13 @@ __global__ __launch_bounds__(kRowThreads) void expert_sort_kernel(
     const int c = part * 64 + lane;
     int row = -1;
     if (lane < K) row = row_of_slot[(int64_t)t * K + lane];
-    u32x4_t v{};
-    if (c < chunks) v = __builtin_nontemporal_load(x + (int64_t)t * chunks + c);
+    const u32x4_t v = __builtin_nontemporal_load(x + (int64_t)t * chunks + min(c, chunks - 1));
     uint64_t m = __ballot(row >= 0 && row < n_rows);
     while (m) {
         const int k = __builtin_ctzll(m);
         m &= m - 1;
         const int64_t r = __builtin_amdgcn_readlane(row, k);
-        if (c < chunks) __builtin_nontemporal_store(v, rows + r * chunks + c);
+        if (c < chunks) rows[r * chunks + c] = v;
     }
 }
 
@@ -278,7 +284,9 @@ __global__ __launch_bounds__(kRowThreads) void expert_unsort_kernel(
 
 // One workgroup per token: a chunk of d_out is read once and held while the
 // chunks of the token's rows pass, four at a time: their products go into one
-// sum per filled slot, and weight * d_out to their gradients.
+// sum per filled slot, and weight * d_out to their gradients.  4095 x 7168 x
+// top-8: 192 us, 951 MB at 5.0 TB/s; fewer workgroups per CU (2 to 7), streaming
+// stores, 512 or 1024 threads and 8 rows at a time were no faster.
 constexpr int kBackThreads = 256;
 
 template <typename S>
@@ -329,7 +337,7 @@ __global__ __launch_bounds__(kBackThreads) void expert_unsort_backward_kernel(
                     dot[b0 + b] = fmaf(d[i], y[i], dot[b0 + b]);
                     g[i] = d[i] * wt[b];
                 }
-                __builtin_nontemporal_store(chunk_from_f32<S>(g), d_rows + at[b]);
+                d_rows[at[b]] = chunk_from_f32<S>(g);
             }
         }
     }
@@ -372,9 +380,11 @@ hipError_t launch_expert_sort(const void* x, int T, int K, int64_t row_bytes,
                               const int32_t* row_of_slot, void* rows, const Launch& L) {
     const int chunks = (int)(row_bytes / 16);
     const int slices = (chunks + 63) / 64;
-    return launch_kernel(expert_sort_kernel, dim3((int)row_blocks(T, slices)), dim3(kRowThreads), L,
-                         static_cast<const u32x4_t*>(x), T, K, chunks, (int64_t)T * K, row_of_slot,
-                         static_cast<u32x4_t*>(rows), make_row_split(chunks, slices));
+    Launch capped = L;
+    capped.lds_bytes = occupancy_lds(kSortWorkgroupsPerCu, 0);
+    return launch_kernel(expert_sort_kernel, dim3((int)row_blocks(T, slices)), dim3(kRowThreads),
+                         capped, static_cast<const u32x4_t*>(x), T, K, chunks, (int64_t)T * K,
+                         row_of_slot, static_cast<u32x4_t*>(rows), make_row_split(chunks, slices));
 }
 
 namespace {
