@@ -16,16 +16,17 @@ namespace {
 
 // Tile shapes (mma_tile.h): forward and input gradient 256 x 256 by 8 waves,
 // weight gradient 256 x 128 by 4.
-template <int BQ_, int WQ_, int BK_>
+template <int BP_, int BQ_, int WQ_, int BK_>
 struct Shape {
-    static constexpr int BP = 256, BQ = BQ_, WP = 2, WQ = WQ_, BK = BK_;
+    static constexpr int BP = BP_, BQ = BQ_, WP = 2, WQ = WQ_, BK = BK_;
     static constexpr int kWaves = WP * WQ, kThreads = kWaves * 64;
     static constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;
     static __device__ __forceinline__ int p_at(int wp, int i) { return p_block<BP, WP>(wp, i); }
     static __device__ __forceinline__ int q_at(int wq, int j) { return q_block<WQ>(wq, j); }
 };
-typedef Shape<256, 4, 64> Wide;
-typedef Shape<128, 2, 32> Narrow;
+typedef Shape<256, 256, 4, 64> Wide;
+typedef Shape<256, 128, 2, 32> Narrow;
+typedef Shape<128, 128, 2, 64> Small;
 
 constexpr int kRunLog2 = 5;  // an XCD takes runs of 32 tiles: one per CU, sharing operands in its L2
 constexpr int kRowGroup = 8;  // row tiles that go through the columns together
@@ -41,6 +42,43 @@ __device__ __forceinline__ void store4(S* at, const f32x4& v) {
     *reinterpret_cast<vec*>(at) = o;
 }
 
+// Outputs of two neighbouring blocks of 16: the lane groups trade halves, so
+// that each lane holds 8 consecutive outputs (16 bytes) and a row's 32 outputs
+// are 64 contiguous bytes.  They start pair_at(lane) outputs into the blocks.
+template <typename S>
+__device__ __forceinline__ u32x4_t pack_pair(const f32x4& a, const f32x4& b) {
+    typedef S vec __attribute__((ext_vector_type(4)));
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    vec va, vb;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        va[i] = (S)a[i];
+        vb[i] = (S)b[i];
+    }
+    const u32x2 ua = __builtin_bit_cast(u32x2, va), ub = __builtin_bit_cast(u32x2, vb);
+    // swaps the odd rows of 16 lanes of one operand with the even ones of the other
+    const auto lo = __builtin_amdgcn_permlane16_swap(ua[0], ub[0], false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(ua[1], ub[1], false, false);
+    return u32x4_t{lo[0], hi[0], lo[1], hi[1]};
+}
+__device__ __forceinline__ int pair_at(int lane) {
+    return ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+}
+template <typename S>
+__device__ __forceinline__ void store8(S* at, u32x4_t v) {
+    *reinterpret_cast<u32x4_t*>(at) = v;
+}
+
+// One of n starting points for tile i, scattered (a multiplicative hash).  Rows
+// a multiple of 4 KiB apart start on the same memory channels, and so do
+// workgroups that all begin at the reduction's start; where a weight row is
+// read by one workgroup only, each may begin elsewhere.  64 experts of 12 rows,
+// 4096 -> 4096: 454 us from the start, 366 us scattered.  Where several row
+// tiles share the weights, it would cost them the sharing.
+__device__ __forceinline__ int scattered(int i, int n) {
+    return (int)__umulhi((uint32_t)i * 2654435761u, (uint32_t)n);
+}
+
 // Runs f with the number of Q blocks per wave that `rows` rows need.
 template <int WQ, typename F>
 __device__ __forceinline__ void with_blocks(int rows, F&& f) {
@@ -51,14 +89,14 @@ __device__ __forceinline__ void with_blocks(int rows, F&& f) {
     else f(std::integral_constant<int, 1>{});
 }
 
-template <typename S, bool kSwiglu>
-__global__ __launch_bounds__(Wide::kThreads, 2) void linear_kernel(const S* x, const S* w, ExpertRows er,
-                                                             int K, int N, int cols, S* y, S* pre) {
-    typedef Wide T;
+template <typename S, bool kSwiglu, typename T>
+__global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(const S* x, const S* w, ExpertRows er,
+                                                             int K, int N, int cols, S* y, S* pre,
+                                                                bool rotate) {
     __shared__ __align__(16) S lp0[T::BP * T::BK], lp1[T::BP * T::BK];
     __shared__ __align__(16) S lq0[T::BQ * T::BK], lq1[T::BQ * T::BK];
-    const RowTile tile = find_block<T::BQ, kRowGroup>(
-        er, xcd_run_block<kRunLog2>((int)blockIdx.x, (int)gridDim.x), cols);
+    const int blk = xcd_run_block<kRunLog2>((int)blockIdx.x, (int)gridDim.x);
+    const RowTile tile = find_block<T::BQ, kRowGroup>(er, blk, cols);
     if (tile.e < 0) return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -75,33 +113,44 @@ __global__ __launch_bounds__(Wide::kThreads, 2) void linear_kernel(const S* x, c
     with_blocks<T::WQ>(tile.end - tile.begin, [&](auto nq) {
         constexpr int NQ = decltype(nq)::value;
         f32x4 acc[T::TP][T::TQ] = {};
-        WholeCuLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, decltype(gp), decltype(gq)>(wp, wq, lane).run(
-            gp, gq, (lds_char*)lp0, (lds_char*)lq0, (lds_char*)lp1, (lds_char*)lq1,
-            (K + T::BK - 1) / T::BK, wave, acc);
+        const int nk = (K + T::BK - 1) / T::BK;
+        WholeCuLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, decltype(gp), decltype(gq)>(
+            wp, wq, lane, rotate ? scattered(blk, nk) : 0, nk)
+            .run(gp, gq, (lds_char*)lp0, (lds_char*)lq0, (lds_char*)lp1, (lds_char*)lq1, wave, acc);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
             const int m = tile.begin + T::q_at(wq, j) + (lane & 15);
-            if (m >= tile.end) continue;
+            const bool row = m < tile.end;
+            S* const ym = y + (int64_t)m * N;
             if constexpr (kSwiglu) {
+                S* const gm = pre + (int64_t)m * 2 * N;
 #pragma unroll
-                for (int i = 0; i < T::TP / 2; ++i) {
-                    const int n = n0 + T::p_at(wp, i) + 4 * (lane >> 4);
-                    if (n >= N) continue;
-                    const f32x4 g = acc[i][j], u = acc[i + T::TP / 2][j];
-                    f32x4 h;
+                for (int i = 0; i < T::TP / 2; i += 2) {
+                    const int n = n0 + T::p_at(wp, i) + pair_at(lane);
+                    const f32x4 g[2] = {acc[i][j], acc[i + 1][j]};
+                    const f32x4 u[2] = {acc[i + T::TP / 2][j], acc[i + 1 + T::TP / 2][j]};
+                    f32x4 h[2];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) h[r] = silu(g[r]) * u[r];
-                    store4(y + (int64_t)m * N + n, h);
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) h[b][r] = silu(g[b][r]) * u[b][r];
+                    const bool in = row && n < N;
+                    const u32x4_t hv = pack_pair<S>(h[0], h[1]);
+                    if (in) store8(ym + n, hv);
                     if (pre) {
-                        store4(pre + (int64_t)m * 2 * N + n, g);
-                        store4(pre + (int64_t)m * 2 * N + N + n, u);
+                        const u32x4_t gv = pack_pair<S>(g[0], g[1]), uv = pack_pair<S>(u[0], u[1]);
+                        if (in) {
+                            store8(gm + n, gv);
+                            store8(gm + N + n, uv);
+                        }
                     }
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < T::TP; ++i) {
-                    const int n = n0 + T::p_at(wp, i) + 4 * (lane >> 4);
-                    if (n < N) store4(y + (int64_t)m * N + n, acc[i][j]);
+                for (int i = 0; i < T::TP; i += 2) {
+                    const int n = n0 + T::p_at(wp, i) + pair_at(lane);
+                    const u32x4_t v = pack_pair<S>(acc[i][j], acc[i + 1][j]);
+                    if (row && n < N) store8(ym + n, v);
                 }
             }
         }
@@ -110,13 +159,15 @@ __global__ __launch_bounds__(Wide::kThreads, 2) void linear_kernel(const S* x, c
 
 // The forward product where experts have few rows: the weights' bytes are all
 // that counts, so they go from memory straight into registers, with no LDS and
-// no barrier on the way.  A workgroup takes NP blocks of 16 weight rows (half
-// of them gate, half up rows in a gated product) and up to 32 rows of x; its 4
+// no barrier on the way.  A workgroup takes 32 weight rows (16 gate
+// and 16 up rows in a gated product) and up to 32 rows of x; its 4
 // waves take turns along the reduction, 128 values each, and their sums are
 // added in LDS in wave order.  x comes from the caches.  64 experts of 4096 x
 // 7168, one row each: 602 us, the weights at 6.25 TB/s (a large copy reaches
 // 6.3); 12 rows each: 659 us.
-constexpr int kFewRows = 32, kFewBlocks = kFewRows / 16, kFewWaves = 4, kFewThreads = kFewWaves * 64;
+constexpr int kFewP = 2;  // blocks of 16 weight rows
+constexpr int kFewRows = 32, kFewBlocks = kFewRows / 16, kFewWaves = 4, kFewThreads = kFewWaves * 64,
+              kFewStep = 128 * kFewWaves;
 constexpr int kFewRunLog2 = 3;
 
 // 16 rows of an operand along r, read by the whole wave: lane l takes row
@@ -134,22 +185,28 @@ struct FewRows {
     }
 };
 
-// NP blocks of 16 weight rows times NQ blocks of 16 rows of x.
-template <typename S, int NP, int NQ>
-__device__ __forceinline__ void few_products(const FewRows* ws, const FewRows* xs, int K, int wave,
-                                             int lane, f32x4 (&acc)[NP][kFewBlocks]) {
-    constexpr int kU = 4, kStep = 32 * kU * kFewWaves;
-    s16x8 a[2][NP][kU], b[2][NQ][kU];
-    const int first = wave * 32 * kU, in = (lane >> 4) * 8;
-    // The scheduling barriers keep the loads of one step ahead of the products
-    // of the other.
-    const auto fetch = [&](int s, int k0) {
+// Two blocks of 16 weight rows times NQ blocks of 16 rows of x.
+template <typename S, int NQ>
+__device__ __forceinline__ void few_products(const FewRows* ws, const FewRows* xs, int K, int shift,
+                                             int wave, int lane, f32x4 (&acc)[kFewP][kFewBlocks]) {
+    constexpr int kU = 4, kStep = kFewStep;
+    static_assert(kStep == 32 * kU * kFewWaves, "a step of all waves");
+    const int steps = (K + kStep - 1) / kStep;
+    s16x8 a[2][kFewP][kU], b[2][NQ][kU];
+    const int in = (lane >> 4) * 8;
+    // Steps go around the reduction from `shift` on; past the last one nothing
+    // is read.  The scheduling barriers keep the loads of one step ahead of the
+    // products of the other.
+    const auto fetch = [&](int s, int step) {
+        int at = step + shift;
+        at -= at >= steps ? steps : 0;
+        const int k0 = step < steps ? at * kStep + wave * 32 * kU : K;
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int k = k0 + u * 32;
             const bool inside = k + in < K;
 #pragma unroll
-            for (int i = 0; i < NP; ++i) a[s][i][u] = ws[i].load(k, inside);
+            for (int i = 0; i < kFewP; ++i) a[s][i][u] = ws[i].load(k, inside);
 #pragma unroll
             for (int j = 0; j < NQ; ++j) b[s][j][u] = xs[j].load(k, inside);
         }
@@ -161,60 +218,60 @@ __device__ __forceinline__ void few_products(const FewRows* ws, const FewRows* x
 #pragma unroll
             for (int j = 0; j < NQ; ++j)
 #pragma unroll
-                for (int i = 0; i < NP; ++i)
+                for (int i = 0; i < kFewP; ++i)
                     acc[i][j] = Mfma<S>::mul(a[s][i][u], b[s][j][u], acc[i][j]);
         __builtin_amdgcn_sched_barrier(0);
     };
-    fetch(0, first);
-    for (int k0 = first; k0 < K; k0 += 2 * kStep) {
-        fetch(1, k0 + kStep);
+    fetch(0, 0);
+    for (int step = 0; step < steps; step += 2) {
+        fetch(1, step + 1);
         multiply(0);
-        fetch(0, k0 + 2 * kStep);
+        fetch(0, step + 2);
         multiply(1);
     }
 }
 
-// NP: blocks of 16 weight rows; with kSwiglu the first half are gate rows.
-template <typename S, bool kSwiglu, int NP>
+template <typename S, bool kSwiglu>
 __global__ __launch_bounds__(kFewThreads) void linear_few_kernel(const S* x, const S* w,
                                                                  ExpertRows er, int K, int N,
-                                                                 int cols, S* y, S* pre) {
-    constexpr int kOut = kSwiglu ? NP / 2 : NP;  // blocks of outputs
-    __shared__ f32x4 part[kFewWaves][kFewBlocks][NP][64];
-    const RowTile tile = find_block<kFewRows, kRowGroup>(
-        er, xcd_run_block<kFewRunLog2>((int)blockIdx.x, (int)gridDim.x), cols);
+                                                                 int cols, S* y, S* pre, bool rotate) {
+    constexpr int kOut = kSwiglu ? kFewP / 2 : kFewP;  // blocks of outputs
+    __shared__ f32x4 part[kFewWaves][kFewBlocks][kFewP][64];
+    const int blk = xcd_run_block<kFewRunLog2>((int)blockIdx.x, (int)gridDim.x);
+    const RowTile tile = find_block<kFewRows, kRowGroup>(er, blk, cols);
     if (tile.e < 0) return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = tile.col * kOut * 16;
     const S* we = w + (int64_t)tile.e * (kSwiglu ? 2 : 1) * N * K;
     const int rows = tile.end - tile.begin;
-    FewRows ws[NP], xs[kFewBlocks];
+    FewRows ws[kFewP], xs[kFewBlocks];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
+    for (int i = 0; i < kFewP; ++i) {
         const int n = n0 + i % kOut * 16;
         ws[i].init(we + (int64_t)(i < kOut ? n : N + n) * K, min(N - n, 16), K, lane);
     }
 #pragma unroll
     for (int j = 0; j < kFewBlocks; ++j)
         xs[j].init(x + (int64_t)(tile.begin + 16 * j) * K, min(rows - 16 * j, 16), K, lane);
-    f32x4 acc[NP][kFewBlocks] = {};
+    f32x4 acc[kFewP][kFewBlocks] = {};
+    const int shift = rotate ? scattered(blk, (K + kFewStep - 1) / kFewStep) : 0;
     if (rows > 16)
-        few_products<S, NP, 2>(ws, xs, K, wave, lane, acc);
+        few_products<S, 2>(ws, xs, K, shift, wave, lane, acc);
     else
-        few_products<S, NP, 1>(ws, xs, K, wave, lane, acc);
+        few_products<S, 1>(ws, xs, K, shift, wave, lane, acc);
 #pragma unroll
     for (int j = 0; j < kFewBlocks; ++j)
 #pragma unroll
-        for (int i = 0; i < NP; ++i) part[wave][j][i][lane] = acc[i][j];
+        for (int i = 0; i < kFewP; ++i) part[wave][j][i][lane] = acc[i][j];
     __syncthreads();
     // wave j finishes block j of 16 rows
     if (wave >= kFewBlocks) return;
     const int m = tile.begin + wave * 16 + (lane & 15);
     if (m >= tile.end) return;
-    f32x4 sum[NP];
+    f32x4 sum[kFewP];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
+    for (int i = 0; i < kFewP; ++i) {
         sum[i] = part[0][wave][i][lane];
 #pragma unroll
         for (int v = 1; v < kFewWaves; ++v) {
@@ -243,10 +300,9 @@ __global__ __launch_bounds__(kFewThreads) void linear_few_kernel(const S* x, con
     }
 }
 
-template <typename S>
-__global__ __launch_bounds__(Wide::kThreads, 2) void dgrad_kernel(const S* d_y, const S* w, ExpertRows er,
+template <typename S, typename T>
+__global__ __launch_bounds__(T::kThreads, 2) void dgrad_kernel(const S* d_y, const S* w, ExpertRows er,
                                                             int K, int N, int cols, S* d_x) {
-    typedef Wide T;
     __shared__ __align__(16) S lp0[T::BP * T::BK], lp1[T::BP * T::BK];
     __shared__ __align__(16) S lq0[T::BQ * T::BK], lq1[T::BQ * T::BK];
     const RowTile tile = find_block<T::BQ, kRowGroup>(
@@ -264,17 +320,17 @@ __global__ __launch_bounds__(Wide::kThreads, 2) void dgrad_kernel(const S* d_y, 
     with_blocks<T::WQ>(tile.end - tile.begin, [&](auto nq) {
         constexpr int NQ = decltype(nq)::value;
         f32x4 acc[T::TP][T::TQ] = {};
-        WholeCuLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, decltype(gp), decltype(gq)>(wp, wq, lane).run(
-            gp, gq, (lds_char*)lp0, (lds_char*)lq0, (lds_char*)lp1, (lds_char*)lq1,
-            (N + T::BK - 1) / T::BK, wave, acc);
+        WholeCuLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, decltype(gp), decltype(gq)>(
+            wp, wq, lane, 0, (N + T::BK - 1) / T::BK)
+            .run(gp, gq, (lds_char*)lp0, (lds_char*)lq0, (lds_char*)lp1, (lds_char*)lq1, wave, acc);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
             const int m = tile.begin + T::q_at(wq, j) + (lane & 15);
-            if (m >= tile.end) continue;
 #pragma unroll
-            for (int i = 0; i < T::TP; ++i) {
-                const int k = k0 + T::p_at(wp, i) + 4 * (lane >> 4);
-                if (k < K) store4(d_x + (int64_t)m * K + k, acc[i][j]);
+            for (int i = 0; i < T::TP; i += 2) {
+                const int k = k0 + T::p_at(wp, i) + pair_at(lane);
+                const u32x4_t v = pack_pair<S>(acc[i][j], acc[i + 1][j]);
+                if (m < tile.end && k < K) store8(d_x + (int64_t)m * K + k, v);
             }
         }
     });
@@ -314,11 +370,20 @@ __global__ __launch_bounds__(Narrow::kThreads, 2) void wgrad_kernel(const S* d_y
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
             const int n = n0 + T::q_at(wq, j) + (lane & 15);
-            if (n >= N) continue;
+            D* const row = d_w + ((int64_t)e * N + n) * K;
+            if constexpr (sizeof(D) == 2) {
 #pragma unroll
-            for (int i = 0; i < T::TP; ++i) {
-                const int k = k0 + T::p_at(wp, i) + 4 * (lane >> 4);
-                if (k < K) store4(d_w + ((int64_t)e * N + n) * K + k, acc[i][j]);
+                for (int i = 0; i < T::TP; i += 2) {
+                    const int k = k0 + T::p_at(wp, i) + pair_at(lane);
+                    const u32x4_t v = pack_pair<D>(acc[i][j], acc[i + 1][j]);
+                    if (n < N && k < K) store8(row + k, v);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < T::TP; ++i) {
+                    const int k = k0 + T::p_at(wp, i) + 4 * (lane >> 4);
+                    if (n < N && k < K) store4(row + k, acc[i][j]);
+                }
             }
         }
     });
@@ -368,40 +433,69 @@ int64_t expected_rows(const ExpertRows& er) {
     return er.E > 8 ? (int64_t)er.cap * 8 / er.E : er.cap;
 }
 
+// Whether experts that likely have `likely` rows are better served by tiles of
+// 128 x 128, two workgroups per CU: up to 120 rows, where the weights' bytes
+// count (64 experts, 7168 -> 4096, 128 x 128 against 256 x 256: 615 and 740 us
+// at 12 rows, 656 and 765 at 64, 756 and 822 at 128, 1103 and 903 at 192), and
+// where 256 x 256 would leave CUs without a tile (8 experts of 256 rows, 4096 ->
+// 2048: 56 and 83 us; of 512 rows, 4096 -> 4096, 256 tiles: 157 and 128).
+bool small_tiles(const ExpertRows& er, int64_t likely, int out) {
+    const int64_t rows = er.offsets ? er.rows : likely * er.E;
+    const int64_t tiles = (rows + Wide::BQ - 1) / Wide::BQ * tiles_of(out, Wide::BP);
+    return likely <= 120 || tiles < 256;
+}
+
+// Whether workgroups start at scattered places of the reduction (`scattered`).
+bool rotates(int64_t likely, int reduction) { return likely <= 120 && reduction % 2048 == 0; }
+
+template <typename S, typename T>
+hipError_t linear_tiles(const S* x, const S* w, const ExpertRows& er, int K, int N, bool swiglu,
+                        bool rotate, S* y, S* pre, const Launch& L) {
+    const int cols = tiles_of(N, swiglu ? T::BP / 2 : T::BP);
+    const dim3 grid((unsigned)(max_tiles(er, T::BQ) * cols));
+    return launch_kernel(swiglu ? linear_kernel<S, true, T> : linear_kernel<S, false, T>, grid,
+                         dim3(T::kThreads), L, x, w, er, K, N, cols, y, pre, rotate);
+}
+
 template <typename S>
 hipError_t linear_as(const void* x, const void* w, const ExpertRows& er, int K, int N, bool swiglu,
                      void* y, void* pre, const Launch& L) {
     const S* xs = static_cast<const S*>(x);
     const S* ws = static_cast<const S*>(w);
-    // 64 experts, 7168 -> 4096, us at 1 / 12 / 24 / 40 rows each: 2 blocks 602 /
-    // 659 / 821 / 988, 4 blocks 629 / 644 / 695 / 765, tiles 731 / 721 / 727 / 740.
-    // Fewer columns per workgroup also means more workgroups for a few experts.
+    S* ys = static_cast<S*>(y);
+    S* ps = static_cast<S*>(pre);
     const int64_t likely = expected_rows(er);
-    if (likely <= 32) {
-        const int np = likely <= 16 ? 2 : 4;
-        const int cols = tiles_of(N, swiglu ? np * 8 : np * 16);
+    const bool rotate = rotates(likely, K);
+    // A few rows, or a few experts' rows: 8 of 64 experts with one row each,
+    // 7168 -> 4096: 79 us, 128 x 128 tiles 113; 8 rows each in all 64: 620 and 611.
+    if (likely <= 8) {
+        const int cols = tiles_of(N, swiglu ? 16 : 32);
         const dim3 grid((unsigned)(max_tiles(er, kFewRows) * cols));
-        const auto two = swiglu ? linear_few_kernel<S, true, 2> : linear_few_kernel<S, false, 2>;
-        const auto four = swiglu ? linear_few_kernel<S, true, 4> : linear_few_kernel<S, false, 4>;
-        return launch_kernel(np == 2 ? two : four, grid, dim3(kFewThreads), L, xs, ws, er, K, N,
-                             cols, static_cast<S*>(y), static_cast<S*>(pre));
+        return launch_kernel(swiglu ? linear_few_kernel<S, true> : linear_few_kernel<S, false>,
+                             grid, dim3(kFewThreads), L, xs, ws, er, K, N, cols, ys, ps, rotate);
     }
-    const int cols = tiles_of(N, swiglu ? Wide::BP / 2 : Wide::BP);
-    const dim3 grid((unsigned)(max_tiles(er, Wide::BQ) * cols));
-    if (swiglu)
-        return launch_kernel(linear_kernel<S, true>, grid, dim3(Wide::kThreads), L, xs, ws, er, K, N,
-                             cols, static_cast<S*>(y), static_cast<S*>(pre));
-    return launch_kernel(linear_kernel<S, false>, grid, dim3(Wide::kThreads), L, xs, ws, er, K, N, cols,
-                         static_cast<S*>(y), static_cast<S*>(pre));
+    if (small_tiles(er, likely, swiglu ? 2 * N : N))
+        return linear_tiles<S, Small>(xs, ws, er, K, N, swiglu, rotate, ys, ps, L);
+    return linear_tiles<S, Wide>(xs, ws, er, K, N, swiglu, false, ys, ps, L);
+}
+
+template <typename S, typename T>
+hipError_t dgrad_tiles(const S* d_y, const S* w, const ExpertRows& er, int K, int N, S* d_x,
+                       const Launch& L) {
+    const int cols = tiles_of(K, T::BP);
+    const dim3 grid((unsigned)(max_tiles(er, T::BQ) * cols));
+    return launch_kernel(dgrad_kernel<S, T>, grid, dim3(T::kThreads), L, d_y, w, er, K, N, cols,
+                         d_x);
 }
 
 template <typename S>
 hipError_t dgrad_as(const void* d_y, const void* w, const ExpertRows& er, int K, int N, void* d_x,
                     const Launch& L) {
-    const int cols = tiles_of(K, Wide::BP);
-    const dim3 grid((unsigned)(max_tiles(er, Wide::BQ) * cols));
-    return launch_kernel(dgrad_kernel<S>, grid, dim3(Wide::kThreads), L, static_cast<const S*>(d_y),
-                         static_cast<const S*>(w), er, K, N, cols, static_cast<S*>(d_x));
+    const S* ds = static_cast<const S*>(d_y);
+    const S* ws = static_cast<const S*>(w);
+    if (small_tiles(er, expected_rows(er), K))
+        return dgrad_tiles<S, Small>(ds, ws, er, K, N, static_cast<S*>(d_x), L);
+    return dgrad_tiles<S, Wide>(ds, ws, er, K, N, static_cast<S*>(d_x), L);
 }
 
 template <typename S>

@@ -319,10 +319,20 @@ struct WholeCuLoop {
 
     typename LP::At ap;
     typename LQ::At aq;
+    int shift, stages;
 
-    __device__ __forceinline__ WholeCuLoop(int wp, int wq, int lane) {
+    // Stages are taken from `first_stage` on, around the reduction.
+    __device__ __forceinline__ WholeCuLoop(int wp, int wq, int lane, int first_stage, int nk)
+        : shift(first_stage), stages(nk) {
         ap.init(wp * (BP / 2 / WP), lane);
         aq.init(wq * 16, lane);
+    }
+    __device__ __forceinline__ void load(const LP& gp, const LQ& gq, lds_char* lp, lds_char* lq,
+                                         int it, int wave) const {
+        int s = it + shift;
+        s -= s >= stages ? stages : 0;
+        gp.load(lp, s * kBK, wave);
+        gq.load(lq, s * kBK, wave);
     }
     __device__ __forceinline__ void frags(const lds_char* lp, const lds_char* lq, int kk,
                                           s16x8 (&p)[TP], s16x8 (&q)[TQ]) const {
@@ -350,10 +360,9 @@ struct WholeCuLoop {
         interleave<false>();
         __builtin_amdgcn_sched_barrier(0);
         __syncthreads();  // this buffer is read, the next stage has arrived
-        // past the reduction's end these fetch nothing and leave zeros
+        // past the last stage: what is fetched goes unused
         frags(np, nq, 0, p0, q0);
-        gp.load(lp, (it + 2) * kBK, wave);
-        gq.load(lq, (it + 2) * kBK, wave);
+        load(gp, gq, lp, lq, it + 2, wave);
         products(p1, q1, acc);
         interleave<true>();
         __builtin_amdgcn_sched_barrier(0);
@@ -380,26 +389,23 @@ struct WholeCuLoop {
         }
     }
     __device__ __forceinline__ void run(const LP& gp, const LQ& gq, lds_char* lp0, lds_char* lq0,
-                                        lds_char* lp1, lds_char* lq1, int nk, int wave,
+                                        lds_char* lp1, lds_char* lq1, int wave,
                                         f32x4 (&acc)[TP][TQ]) const {
+        const int nk = stages;
         if (nk <= 0) return;
         s16x8 p0[TP], q0[TQ];
         int it = 0;
         if (nk & 1) {  // the pairs below start at stage 1
-            gp.load(lp0, kBK, wave);
-            gq.load(lq0, kBK, wave);
-            gp.load(lp1, 0, wave);
-            gq.load(lq1, 0, wave);
+            load(gp, gq, lp0, lq0, 1, wave);
+            load(gp, gq, lp1, lq1, 0, wave);
             __syncthreads();
             frags(lp1, lq1, 0, p0, q0);
             stage(gp, gq, lp1, lq1, lp0, lq0, 0, wave, p0, q0, acc);
             it = 1;
         } else {
-            gp.load(lp0, 0, wave);
-            gq.load(lq0, 0, wave);
+            load(gp, gq, lp0, lq0, 0, wave);
             __syncthreads();
-            gp.load(lp1, kBK, wave);
-            gq.load(lq1, kBK, wave);
+            load(gp, gq, lp1, lq1, 1, wave);
             frags(lp0, lq0, 0, p0, q0);
         }
         while (it < nk) {
