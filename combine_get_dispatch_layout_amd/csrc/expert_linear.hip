@@ -16,17 +16,18 @@ namespace {
 
 // Tile shapes (mma_tile.h): forward and input gradient 256 x 256 by 8 waves,
 // weight gradient 256 x 128 by 4.
-template <int BP_, int BQ_, int WQ_, int BK_>
+template <int BP_, int BQ_, int WQ_, int BK_, int kP_, int kQ_>
 struct Shape {
     static constexpr int BP = BP_, BQ = BQ_, WP = 2, WQ = WQ_, BK = BK_;
+    static constexpr int kP = kP_, kQ = kQ_;  // stages of either operand in LDS
     static constexpr int kWaves = WP * WQ, kThreads = kWaves * 64;
     static constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;
     static __device__ __forceinline__ int p_at(int wp, int i) { return p_block<BP, WP>(wp, i); }
     static __device__ __forceinline__ int q_at(int wq, int j) { return q_block<WQ>(wq, j); }
 };
-typedef Shape<256, 256, 4, 64> Wide;
-typedef Shape<256, 128, 2, 32> Narrow;
-typedef Shape<128, 128, 2, 64> Small;
+typedef Shape<256, 256, 4, 64, 3, 2> Wide;
+typedef Shape<256, 128, 2, 32, 3, 3> Narrow;
+typedef Shape<128, 128, 2, 64, 2, 2> Small;
 
 constexpr int kRunLog2 = 5;  // an XCD takes runs of 32 tiles: one per CU, sharing operands in its L2
 constexpr int kRowGroup = 8;  // row tiles that go through the columns together
@@ -93,8 +94,8 @@ template <typename S, bool kSwiglu, typename T>
 __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(const S* x, const S* w, ExpertRows er,
                                                              int K, int N, int cols, S* y, S* pre,
                                                                 bool rotate) {
-    __shared__ __align__(16) S lp0[T::BP * T::BK], lp1[T::BP * T::BK];
-    __shared__ __align__(16) S lq0[T::BQ * T::BK], lq1[T::BQ * T::BK];
+    __shared__ __align__(16) S lp[T::kP * T::BP * T::BK];
+    __shared__ __align__(16) S lq[T::kQ * T::BQ * T::BK];
     const int blk = xcd_run_block<kRunLog2>((int)blockIdx.x, (int)gridDim.x);
     const RowTile tile = find_block<T::BQ, kRowGroup>(er, blk, cols);
     if (tile.e < 0) return;
@@ -114,9 +115,9 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(const S* x, cons
         constexpr int NQ = decltype(nq)::value;
         f32x4 acc[T::TP][T::TQ] = {};
         const int nk = (K + T::BK - 1) / T::BK;
-        WholeCuLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, decltype(gp), decltype(gq)>(
+        RingLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, T::kP, T::kQ, decltype(gp), decltype(gq)>(
             wp, wq, lane, rotate ? scattered(blk, nk) : 0, nk)
-            .run(gp, gq, (lds_char*)lp0, (lds_char*)lq0, (lds_char*)lp1, (lds_char*)lq1, wave, acc);
+            .run(gp, gq, (lds_char*)lp, (lds_char*)lq, wave, acc);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
             const int m = tile.begin + T::q_at(wq, j) + (lane & 15);
@@ -303,8 +304,8 @@ __global__ __launch_bounds__(kFewThreads) void linear_few_kernel(const S* x, con
 template <typename S, typename T>
 __global__ __launch_bounds__(T::kThreads, 2) void dgrad_kernel(const S* d_y, const S* w, ExpertRows er,
                                                             int K, int N, int cols, S* d_x) {
-    __shared__ __align__(16) S lp0[T::BP * T::BK], lp1[T::BP * T::BK];
-    __shared__ __align__(16) S lq0[T::BQ * T::BK], lq1[T::BQ * T::BK];
+    __shared__ __align__(16) S lp[T::kP * T::BP * T::BK];
+    __shared__ __align__(16) S lq[T::kQ * T::BQ * T::BK];
     const RowTile tile = find_block<T::BQ, kRowGroup>(
         er, xcd_run_block<kRunLog2>((int)blockIdx.x, (int)gridDim.x), cols);
     if (tile.e < 0) return;
@@ -320,9 +321,9 @@ __global__ __launch_bounds__(T::kThreads, 2) void dgrad_kernel(const S* d_y, con
     with_blocks<T::WQ>(tile.end - tile.begin, [&](auto nq) {
         constexpr int NQ = decltype(nq)::value;
         f32x4 acc[T::TP][T::TQ] = {};
-        WholeCuLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, decltype(gp), decltype(gq)>(
+        RingLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, T::kP, T::kQ, decltype(gp), decltype(gq)>(
             wp, wq, lane, 0, (N + T::BK - 1) / T::BK)
-            .run(gp, gq, (lds_char*)lp0, (lds_char*)lq0, (lds_char*)lp1, (lds_char*)lq1, wave, acc);
+            .run(gp, gq, (lds_char*)lp, (lds_char*)lq, wave, acc);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
             const int m = tile.begin + T::q_at(wq, j) + (lane & 15);

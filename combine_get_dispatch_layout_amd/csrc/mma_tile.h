@@ -307,32 +307,36 @@ struct SharedCuLoop {
     }
 };
 
-// A tile by 8 waves, one workgroup per CU, two LDS buffers of 64 reduction
-// values.  A stage is multiplied in two halves of 32: while the first half's
-// products run, the second half is read; past the barrier the stage after next
-// starts loading into the buffer just read, and the next stage's first half is
-// read under the second half's products.
-template <typename S, int BP, int BQ, int WP, int WQ, int NQ, typename LP, typename LQ>
-struct WholeCuLoop {
+// A tile whose operands' stages of 64 reduction values go around rings of LDS
+// buffers, kP of them for P and kQ for Q.  A stage is multiplied in two halves
+// of 32: while the first half's products run, the second half is read; past the
+// barrier the stages kP and kQ further start loading into the buffers just
+// read, and the next stage's first half is read under the second half's
+// products.
+//
+// `stage` is told (restrict) that the buffers it reads are not the ones it
+// loads into: the compiler then puts no wait of its own before an LDS read, and
+// the one before the barrier is exact.
+template <typename S, int BP, int BQ, int WP, int WQ, int NQ, int kP, int kQ, typename LP,
+          typename LQ>
+struct RingLoop {
     static constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;
     static constexpr int kBK = 64;
-
+    static constexpr int kPBytes = BP * kBK * 2, kQBytes = BQ * kBK * 2;
+    static_assert(kP >= kQ && kQ >= 2, "P is loaded at least as far ahead as Q");
     typename LP::At ap;
     typename LQ::At aq;
     int shift, stages;
 
     // Stages are taken from `first_stage` on, around the reduction.
-    __device__ __forceinline__ WholeCuLoop(int wp, int wq, int lane, int first_stage, int nk)
+    __device__ __forceinline__ RingLoop(int wp, int wq, int lane, int first_stage, int nk)
         : shift(first_stage), stages(nk) {
         ap.init(wp * (BP / 2 / WP), lane);
         aq.init(wq * 16, lane);
     }
-    __device__ __forceinline__ void load(const LP& gp, const LQ& gq, lds_char* lp, lds_char* lq,
-                                         int it, int wave) const {
-        int s = it + shift;
-        s -= s >= stages ? stages : 0;
-        gp.load(lp, s * kBK, wave);
-        gq.load(lq, s * kBK, wave);
+    __device__ __forceinline__ int place(int it) const {
+        const int s = it + shift;
+        return (s - (s >= stages ? stages : 0)) * kBK;
     }
     __device__ __forceinline__ void frags(const lds_char* lp, const lds_char* lq, int kk,
                                           s16x8 (&p)[TP], s16x8 (&q)[TQ]) const {
@@ -348,21 +352,30 @@ struct WholeCuLoop {
 #pragma unroll
             for (int i = 0; i < TP; ++i) acc[i][j] = Mfma<S>::mul(p[i], q[j], acc[i][j]);
     }
-    // Stage `it` (in lp, lq; its first half already in p0, q0); the next one is
-    // in np, nq.
-    __device__ __forceinline__ void stage(const LP& gp, const LQ& gq, lds_char* lp, lds_char* lq,
-                                          const lds_char* np, const lds_char* nq, int it, int wave,
-                                          s16x8 (&p0)[TP], s16x8 (&q0)[TQ],
+    // The first half's products (operands in p0, q0) while the second half is
+    // read from rp, rq.
+    __device__ __forceinline__ void first(const lds_char* rp, const lds_char* rq,
+                                          const s16x8 (&p0)[TP], const s16x8 (&q0)[TQ],
+                                          s16x8 (&p1)[TP], s16x8 (&q1)[TQ],
                                           f32x4 (&acc)[TP][TQ]) const {
-        s16x8 p1[TP], q1[TQ];
-        frags(lp, lq, 1, p1, q1);
+        frags(rp, rq, 1, p1, q1);
         products(p0, q0, acc);
         interleave<false>();
         __builtin_amdgcn_sched_barrier(0);
-        __syncthreads();  // this buffer is read, the next stage has arrived
-        // past the last stage: what is fetched goes unused
-        frags(np, nq, 0, p0, q0);
-        load(gp, gq, lp, lq, it + 2, wave);
+    }
+    // The second half's products while the next stage's first half is read from
+    // rp, rq and further stages load into wp, wq.  Past the last stage what is
+    // fetched and read goes unused.
+    __device__ __forceinline__ void second(const LP& gp, const LQ& gq,
+                                           const lds_char* __restrict rp,
+                                           const lds_char* __restrict rq,
+                                           lds_char* __restrict wp, lds_char* __restrict wq, int it,
+                                           int wave, s16x8 (&p0)[TP], s16x8 (&q0)[TQ],
+                                           const s16x8 (&p1)[TP], const s16x8 (&q1)[TQ],
+                                           f32x4 (&acc)[TP][TQ]) const {
+        frags(rp, rq, 0, p0, q0);
+        gq.load(wq, place(it + kQ), wave);
+        gp.load(wp, place(it + kP), wave);
         products(p1, q1, acc);
         interleave<true>();
         __builtin_amdgcn_sched_barrier(0);
@@ -377,7 +390,7 @@ struct WholeCuLoop {
         constexpr int kPer = TP * NQ / kMem > 0 ? TP * NQ / kMem : 1;
 #pragma unroll
         for (int i = 0; i < kReads; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // LDS read
             __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);  // products
         }
         if constexpr (kLoads) {
@@ -388,32 +401,36 @@ struct WholeCuLoop {
             }
         }
     }
-    __device__ __forceinline__ void run(const LP& gp, const LQ& gq, lds_char* lp0, lds_char* lq0,
-                                        lds_char* lp1, lds_char* lq1, int wave,
-                                        f32x4 (&acc)[TP][TQ]) const {
-        const int nk = stages;
-        if (nk <= 0) return;
-        s16x8 p0[TP], q0[TQ];
-        int it = 0;
-        if (nk & 1) {  // the pairs below start at stage 1
-            load(gp, gq, lp0, lq0, 1, wave);
-            load(gp, gq, lp1, lq1, 0, wave);
-            __syncthreads();
-            frags(lp1, lq1, 0, p0, q0);
-            stage(gp, gq, lp1, lq1, lp0, lq0, 0, wave, p0, q0, acc);
-            it = 1;
-        } else {
-            load(gp, gq, lp0, lq0, 0, wave);
-            __syncthreads();
-            load(gp, gq, lp1, lq1, 1, wave);
-            frags(lp0, lq0, 0, p0, q0);
+    template <int kInFlight>
+    static __device__ __forceinline__ void barrier() {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kInFlight) : "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __device__ __forceinline__ void run(const LP& gp, const LQ& gq, lds_char* lp, lds_char* lq,
+                                        int wave, f32x4 (&acc)[TP][TQ]) const {
+        if (stages <= 0) return;
+        // in the order in which they are needed
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            if (i < kQ) gq.load(lq + i * kQBytes, place(i), wave);
+            gp.load(lp + i * kPBytes, place(i), wave);
         }
-        while (it < nk) {
-            stage(gp, gq, lp0, lq0, lp1, lq1, it, wave, p0, q0, acc);
-            stage(gp, gq, lp1, lq1, lp0, lq0, it + 1, wave, p0, q0, acc);
-            it += 2;
+        constexpr int kAhead = (kP - kQ) * LP::kLoads;  // loads of later stages, at a barrier
+        barrier<(kP - 1) * LP::kLoads + (kQ - 1) * LQ::kLoads>();
+        s16x8 p0[TP], q0[TQ], p1[TP], q1[TQ];
+        frags(lp, lq, 0, p0, q0);
+        int pb = 0, qb = 0;
+        for (int it = 0; it < stages; ++it) {
+            lds_char* const rp = lp + pb * kPBytes;
+            lds_char* const rq = lq + qb * kQBytes;
+            pb = pb + 1 == kP ? 0 : pb + 1;
+            qb = qb + 1 == kQ ? 0 : qb + 1;
+            first(rp, rq, p0, q0, p1, q1, acc);
+            barrier<kAhead>();
+            second(gp, gq, lp + pb * kPBytes, lq + qb * kQBytes, rp, rq, it, wave, p0, q0, p1, q1,
+                   acc);
         }
-        __syncthreads();  // no load into LDS is left in flight
+        barrier<0>();  // no load into LDS is left in flight
     }
 };
 
