@@ -256,14 +256,28 @@ struct SharedCuLoop {
         ap.init(wp * (BP / 2 / WP), lane);
         aq.init(wq * 16, lane);
     }
+    __device__ __forceinline__ void load(const LP& gp, const LQ& gq, lds_char* lp, lds_char* lq,
+                                         int it, int wave) const {
+        gp.load(lp, it * kBK, wave);
+        gq.load(lq, it * kBK, wave);
+    }
+    // Waits until only the last stage's loads are in flight and meets the other
+    // waves.  The wait is the compiler's own instruction, so that it knows which
+    // buffers have arrived and adds no wait before their reads.
+    static __device__ __forceinline__ void arrive() {
+        static_assert(kStageLoads < 16, "the wait's count has 4 bits here");
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(kStageLoads | 0x70);  // vmcnt, no expcnt, lgkmcnt 0
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
     // Multiplies stage `it` (in lp, lq) and loads stage it + 2 into np, nq, which
     // every wave has read.  Past the reduction's end a load leaves zeros.
     __device__ __forceinline__ void stage(const LP& gp, const LQ& gq, const lds_char* lp,
                                           const lds_char* lq, lds_char* np, lds_char* nq, int it,
                                           int wave, f32x4 (&acc)[TP][TQ]) const {
         s16x8 p[TP], q[NQ];
-        gp.load(np, (it + 2) * kBK, wave);
-        gq.load(nq, (it + 2) * kBK, wave);
+        load(gp, gq, np, nq, it + 2, wave);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) q[j] = aq.frag(lq, j * 16 * WQ, 0);
 #pragma unroll
@@ -283,26 +297,41 @@ struct SharedCuLoop {
         __builtin_amdgcn_sched_barrier(0);
         // The next stage has arrived (only this stage's loads may be in flight),
         // and this wave's reads are done: their products have been issued.
-        static_assert(kStageLoads < 16, "the wait's count has 4 bits here");
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kStageLoads) : "memory");
-        __builtin_amdgcn_sched_barrier(0);
+        arrive();
     }
     __device__ __forceinline__ void run(const LP& gp, const LQ& gq, lds_char* lp0, lds_char* lq0,
                                         lds_char* lp1, lds_char* lq1, lds_char* lp2, lds_char* lq2,
                                         int nk, int wave, f32x4 (&acc)[TP][TQ]) const {
         if (nk <= 0) return;
-        gp.load(lp0, 0, wave);
-        gq.load(lq0, 0, wave);
-        gp.load(lp1, kBK, wave);
-        gq.load(lq1, kBK, wave);
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kStageLoads) : "memory");
+        // The stages past a multiple of three go first, in the last buffers, so
+        // that the loop always starts at buffer 0.
+        const int odd = nk % kBuffers;
+        if (odd == 0) {
+            load(gp, gq, lp0, lq0, 0, wave);
+            load(gp, gq, lp1, lq1, 1, wave);
+        } else if (odd == 1) {
+            load(gp, gq, lp2, lq2, 0, wave);
+            load(gp, gq, lp0, lq0, 1, wave);
+        } else {
+            load(gp, gq, lp1, lq1, 0, wave);
+            load(gp, gq, lp2, lq2, 1, wave);
+        }
+        arrive();
         int it = 0;
-        do {
+        if (odd == 2) {
+            stage(gp, gq, lp1, lq1, lp0, lq0, it, wave, acc);
+            ++it;
+        }
+        if (odd != 0) {
+            stage(gp, gq, lp2, lq2, lp1, lq1, it, wave, acc);
+            ++it;
+        }
+        while (it < nk) {
             stage(gp, gq, lp0, lq0, lp2, lq2, it, wave, acc);
             stage(gp, gq, lp1, lq1, lp0, lq0, it + 1, wave, acc);
             stage(gp, gq, lp2, lq2, lp1, lq1, it + 2, wave, acc);
             it += kBuffers;
-        } while (it < nk);
+        }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS is left in flight
     }
 };
@@ -388,6 +417,7 @@ struct RingLoop {
         constexpr int kReads = LP::kFragReads * TP + LQ::kFragReads * NQ;
         constexpr int kMem = kReads + (kLoads ? LP::kLoads + LQ::kLoads : 0);
         constexpr int kPer = TP * NQ / kMem > 0 ? TP * NQ / kMem : 1;
+        __builtin_amdgcn_sched_group_barrier(0x002, 12, 0);  // addresses
 #pragma unroll
         for (int i = 0; i < kReads; ++i) {
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // LDS read
