@@ -12,11 +12,15 @@
 // wherever they go through exp, and the logits themselves (exact, and in the
 // same order) when there is neither bias nor group.  The weights are fp32.
 //
-// One wavefront per token: lane l holds experts l NV .. l NV + NV - 1 in
-// registers (one vector load where E allows it).  A round takes the wave-wide
-// maximum of the keys as unsigned integers that order like them (0 = cannot be
-// chosen), then the first lane that holds it.  What bounds it is that chain of
-// rounds, not the logits' bytes.
+// Where scores are the keys, one wavefront takes a token: lane l holds experts
+// l NV .. l NV + NV - 1 in registers (one vector load where E allows it).  A
+// round takes the wave-wide maximum of the keys as unsigned integers that order
+// like them (0 = cannot be chosen), then the first lane that holds it.  Where
+// the logits are, and in the gradient, a row of 16 lanes takes a token (up to
+// 256 experts): a key is the ordered logit with the expert's number below it,
+// so keys differ, a maximum names its expert, and ties go to the lower one by
+// themselves.  What bounds these kernels is the instructions of the rounds and
+// exps, not the logits' bytes.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -73,7 +77,7 @@ __device__ __forceinline__ void load_logits(const S* logits, int E, int t, int l
 }
 
 template <int NV>
-__device__ __forceinline__ float row_max(const float (&l)[NV]) {
+__device__ __forceinline__ float token_max(const float (&l)[NV]) {
     float m = l[0];
 #pragma unroll
     for (int j = 1; j < NV; ++j) m = fmaxf(m, l[j]);
@@ -166,11 +170,11 @@ __global__ __launch_bounds__(kGateThreads) void gate_topk_kernel(GateArgs a, boo
     if constexpr (!kScores) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) key[j] = l[j] > kNegInf ? ordered(l[j]) : 0u;
-        if (softmax && !a.renormalize) m = row_max(l);
+        if (softmax && !a.renormalize) m = token_max(l);
     } else {
         double s[NV];
         if (softmax) {
-            m = row_max(l);
+            m = token_max(l);
             double z = 0.0;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
@@ -285,7 +289,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_topk_backward_kernel(
         if (!softmax) own *= sigmoid(-lk);
         if (!have) own = 0.0f;
     } else if (softmax) {
-        m = row_max(l);
+        m = token_max(l);
         z = exp_sum(l, m);
         const float p = have ? expf(lk - m) / z : 0.0f;
         dot = wave_sum(have ? g * p : 0.0f);
@@ -321,6 +325,177 @@ __global__ __launch_bounds__(kGateThreads) void gate_topk_backward_kernel(
     }
 }
 
+// ---- a token per row of 16 lanes ------------------------------------------------
+
+constexpr int kRowTokens = kGateThreads / 16;  // tokens of a workgroup
+
+// A logit's key: ordered, and below it ~expert; 0 = cannot be chosen.
+template <typename S>
+struct LogitKey;
+template <>
+struct LogitKey<float> {
+    typedef uint64_t type;
+    static __device__ __forceinline__ type make(float l, int e) {
+        return ((uint64_t)ordered(l) << 32) | (uint32_t)~e;
+    }
+    static __device__ __forceinline__ int expert(type k) { return (int)~(uint32_t)k; }
+    static __device__ __forceinline__ float logit(type k) {
+        const uint32_t o = (uint32_t)(k >> 32);
+        return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
+    }
+};
+template <typename S>
+struct LogitKey16 {  // 16-bit logits: their own bits suffice
+    typedef uint32_t type;
+    static __device__ __forceinline__ type make(float l, int e) {
+        const uint32_t u = __builtin_bit_cast(uint16_t, (S)(l + 0.0f));
+        const uint32_t o = u ^ ((u >> 15) ? 0xffffu : 0x8000u);
+        return (o << 16) | (~e & 0xffff);
+    }
+    static __device__ __forceinline__ int expert(type k) { return (int)(~k & 0xffff); }
+    static __device__ __forceinline__ float logit(type k) {
+        const uint32_t o = k >> 16;
+        return (float)__builtin_bit_cast(S, (uint16_t)(o ^ ((o >> 15) ? 0x8000u : 0xffffu)));
+    }
+};
+template <>
+struct LogitKey<__bf16> : LogitKey16<__bf16> {};
+template <>
+struct LogitKey<_Float16> : LogitKey16<_Float16> {};
+
+template <int NV>
+__device__ __forceinline__ float row_exp_sum(const float (&l)[NV], float m) {
+    float z = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) z += l[j] > kNegInf ? exp_neg(l[j] - m) : 0.0f;
+    return row_sum(z);
+}
+
+// The renormalised weight (before scale) of a row's lane that holds a chosen
+// logit l: a softmax over the chosen (log) scores, never 0 / 0.
+__device__ __forceinline__ float row_share(bool have, bool softmax, float l) {
+    const float s = !have ? kNegInf : softmax ? l : log_sigmoid(l);
+    const float top = row_max(s);  // by every lane of the row
+    const float x = have ? expf(s - top) : 0.0f;
+    const float total = row_sum(x);
+    return have ? x / total : 0.0f;
+}
+
+template <typename S, int NV>
+__global__ __launch_bounds__(kGateThreads) void gate_rows_kernel(GateArgs a, bool vec,
+                                                                 int64_t* __restrict__ topk_idx,
+                                                                 float* __restrict__ topk_weights) {
+    typedef LogitKey<S> Key;
+    const int lane = threadIdx.x & 15;
+    const int t = blockIdx.x * kRowTokens + (threadIdx.x >> 4);
+    float l[NV];
+    load_logits<S, NV>(static_cast<const S*>(a.logits), a.E, min(t, a.T - 1), lane, vec, l);
+    typename Key::type key[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) key[j] = l[j] > kNegInf ? Key::make(l[j], lane * NV + j) : 0;
+    const bool softmax = a.score == MOEDX_GATE_SOFTMAX;
+    // lane k keeps the k-th choice and its logit
+    int mine = -1;
+    float mine_l = kNegInf, m = 0.0f;
+    for (int k = 0; k < a.K; ++k) {
+        typename Key::type top = key[0];
+#pragma unroll
+        for (int j = 1; j < NV; ++j) top = key[j] > top ? key[j] : top;
+        top = row_max(top);
+        const float lv = Key::logit(top);
+        if (lane == k && top != 0) {
+            mine = Key::expert(top);
+            mine_l = lv;
+        }
+        if (k == 0) m = top != 0 ? lv : 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) key[j] = key[j] == top ? 0 : key[j];
+    }
+    const bool have = mine >= 0;
+    float w;
+    if (a.renormalize)
+        w = row_share(have, softmax, mine_l);
+    else if (softmax)
+        w = expf(mine_l - m) / row_exp_sum(l, m);
+    else
+        w = sigmoid(mine_l);
+    if (lane < a.K && t < a.T) {
+        topk_idx[(int64_t)t * a.K + lane] = mine;
+        topk_weights[(int64_t)t * a.K + lane] = have ? a.scale * w : 0.0f;
+    }
+}
+
+template <typename S, int NV>
+__global__ __launch_bounds__(kGateThreads) void gate_rows_backward_kernel(
+    GateArgs a, bool vec, const int64_t* __restrict__ topk_idx,
+    const float* __restrict__ d_topk_weights, S* __restrict__ d_logits) {
+    __shared__ __align__(16) float spread[kRowTokens][16 * NV];
+    const int lane = threadIdx.x & 15, slot = threadIdx.x >> 4;
+    const int t = min((int)blockIdx.x * kRowTokens + slot, a.T - 1);
+    const S* logits = static_cast<const S*>(a.logits);
+    const bool softmax = a.score == MOEDX_GATE_SOFTMAX;
+    const bool dense = softmax && !a.renormalize;
+    float l[NV];
+    if (dense) load_logits<S, NV>(logits, a.E, t, lane, vec, l);
+    // lane k: the k-th choice, its logit and its incoming gradient
+    int idx = -1;
+    float g = 0.0f, lk = kNegInf;
+    if (lane < a.K) {
+        const int64_t i = topk_idx[(int64_t)t * a.K + lane];
+        if (i >= 0 && i < a.E) {
+            idx = (int)i;
+            g = d_topk_weights[(int64_t)t * a.K + lane];
+            const float v = (float)logits[(int64_t)t * a.E + idx];
+            lk = v >= kNegInf ? v : kNegInf;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) spread[slot][lane * NV + j] = 0.0f;
+    const bool have = idx >= 0 && lk > kNegInf;
+    float own = 0.0f;            // gradient added at the chosen expert
+    float m = 0.0f, z = 1.0f, dot = 0.0f;
+    if (a.renormalize) {
+        const float v = row_share(have, softmax, lk);
+        const float gv = row_sum(have ? g * v : 0.0f);
+        own = a.scale * v * (g - gv);
+        if (!softmax) own *= sigmoid(-lk);
+    } else if (softmax) {  // p_j * scale * (g_j - dot) for every expert j
+        m = l[0];
+#pragma unroll
+        for (int j = 1; j < NV; ++j) m = fmaxf(m, l[j]);
+        m = row_max(m);
+        z = row_exp_sum(l, m);
+        dot = row_sum(have ? g * (expf(lk - m) / z) : 0.0f);
+        own = g;
+    } else {
+        own = a.scale * g * sigmoid(lk) * sigmoid(-lk);
+    }
+    // the row's lanes are of one wave, whose LDS accesses keep their order
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (have) atomicAdd(&spread[slot][idx], own);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const float per_z = a.scale / z;
+    float d[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        d[j] = spread[slot][lane * NV + j];
+        if (dense) d[j] = l[j] > kNegInf ? exp_neg(l[j] - m) * per_z * (d[j] - dot) : 0.0f;
+    }
+    if ((int)blockIdx.x * kRowTokens + slot >= a.T) return;
+    S* out = d_logits + (int64_t)t * a.E + lane * NV;
+    if (vec) {
+        typedef S vals __attribute__((ext_vector_type(NV)));
+        vals v;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) v[j] = (S)d[j];
+        if (lane * NV < a.E) *reinterpret_cast<vals*>(out) = v;
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (lane * NV + j < a.E) out[j] = (S)d[j];
+    }
+}
+
 // Whether rows can be moved NV values at a time (16 bytes at most).
 template <typename S, int NV>
 bool vector_rows(const GateArgs& a, const void* other) {
@@ -329,50 +504,71 @@ bool vector_rows(const GateArgs& a, const void* other) {
     return a.E % NV == 0 && (p | (a.E * sizeof(S))) % kBytes == 0;
 }
 
-template <typename S, int NV>
-hipError_t launch_gate_nv(const GateArgs& a, int64_t* idx, float* w, const Launch& L) {
-    const dim3 grid((a.T + kGateWaves - 1) / kGateWaves), block(kGateThreads);
-    const bool vec = vector_rows<S, NV>(a, nullptr);
-    if (a.bias == nullptr && a.groups <= 1)
-        return launch_kernel(gate_topk_kernel<S, NV, uint32_t>, grid, block, L, a, vec, idx, w);
-    return launch_kernel(gate_topk_kernel<S, NV, uint64_t>, grid, block, L, a, vec, idx, w);
-}
-
-template <typename S, int NV>
-hipError_t launch_gate_bwd_nv(const GateArgs& a, const int64_t* idx, const float* dw, void* dl,
-                              const Launch& L) {
-    const dim3 grid((a.T + kGateWaves - 1) / kGateWaves), block(kGateThreads);
-    return launch_kernel(gate_topk_backward_kernel<S, NV>, grid, block, L, a,
-                         vector_rows<S, NV>(a, dl), idx, dw, static_cast<S*>(dl));
-}
-
-template <typename F>
-hipError_t by_width(int E, F&& f) {
-    const int nv = (E + 63) / 64;
-    if (nv <= 1) return f(std::integral_constant<int, 1>{});
-    if (nv <= 2) return f(std::integral_constant<int, 2>{});
-    if (nv <= 4) return f(std::integral_constant<int, 4>{});
+// Calls f with NV, a power of two, such that `lanes` lanes of NV hold E experts.
+template <int kLeast = 1, typename F>
+hipError_t by_width(int E, int lanes, F&& f) {
+    const int nv = (E + lanes - 1) / lanes;
+    if constexpr (kLeast <= 1)
+        if (nv <= 1) return f(std::integral_constant<int, 1>{});
+    if constexpr (kLeast <= 2)
+        if (nv <= 2) return f(std::integral_constant<int, 2>{});
+    if constexpr (kLeast <= 4)
+        if (nv <= 4) return f(std::integral_constant<int, 4>{});
     if (nv <= 8) return f(std::integral_constant<int, 8>{});
     return f(std::integral_constant<int, 16>{});
+}
+
+constexpr int kRowExperts = 256;  // a row of 16 lanes holds them
+
+template <typename S>
+hipError_t gate_as(const GateArgs& a, int64_t* idx, float* w, const Launch& L) {
+    const dim3 waves((a.T + kGateWaves - 1) / kGateWaves), block(kGateThreads);
+    if (a.bias != nullptr || a.groups > 1)
+        return by_width(a.E, 64, [&](auto nv) {
+            return launch_kernel(gate_topk_kernel<S, nv(), uint64_t>, waves, block, L, a,
+                                 vector_rows<S, nv()>(a, nullptr), idx, w);
+        });
+    if (a.E > kRowExperts)
+        return by_width<8>(a.E, 64, [&](auto nv) {
+            return launch_kernel(gate_topk_kernel<S, nv(), uint32_t>, waves, block, L, a,
+                                 vector_rows<S, nv()>(a, nullptr), idx, w);
+        });
+    return by_width(a.E, 16, [&](auto nv) {
+        return launch_kernel(gate_rows_kernel<S, nv()>, dim3((a.T + kRowTokens - 1) / kRowTokens),
+                             block, L, a, vector_rows<S, nv()>(a, nullptr), idx, w);
+    });
+}
+
+template <typename S>
+hipError_t gate_backward_as(const GateArgs& a, const int64_t* idx, const float* dw, void* dl,
+                            const Launch& L) {
+    const dim3 waves((a.T + kGateWaves - 1) / kGateWaves), block(kGateThreads);
+    S* out = static_cast<S*>(dl);
+    if (a.E > kRowExperts)
+        return by_width<8>(a.E, 64, [&](auto nv) {
+            return launch_kernel(gate_topk_backward_kernel<S, nv()>, waves, block, L, a,
+                                 vector_rows<S, nv()>(a, dl), idx, dw, out);
+        });
+    return by_width(a.E, 16, [&](auto nv) {
+        return launch_kernel(gate_rows_backward_kernel<S, nv()>,
+                             dim3((a.T + kRowTokens - 1) / kRowTokens), block, L, a,
+                             vector_rows<S, nv()>(a, dl), idx, dw, out);
+    });
 }
 
 }  // namespace
 
 hipError_t launch_gate_topk(const GateArgs& a, int64_t* idx, float* w, const Launch& L) {
-    return by_width(a.E, [&](auto nv) {
-        if (a.dtype == MOEDX_F32) return launch_gate_nv<float, nv()>(a, idx, w, L);
-        if (a.dtype == MOEDX_F16) return launch_gate_nv<_Float16, nv()>(a, idx, w, L);
-        return launch_gate_nv<__bf16, nv()>(a, idx, w, L);
-    });
+    if (a.dtype == MOEDX_F32) return gate_as<float>(a, idx, w, L);
+    if (a.dtype == MOEDX_F16) return gate_as<_Float16>(a, idx, w, L);
+    return gate_as<__bf16>(a, idx, w, L);
 }
 
 hipError_t launch_gate_topk_backward(const GateArgs& a, const int64_t* idx, const float* dw,
                                      void* dl, const Launch& L) {
-    return by_width(a.E, [&](auto nv) {
-        if (a.dtype == MOEDX_F32) return launch_gate_bwd_nv<float, nv()>(a, idx, dw, dl, L);
-        if (a.dtype == MOEDX_F16) return launch_gate_bwd_nv<_Float16, nv()>(a, idx, dw, dl, L);
-        return launch_gate_bwd_nv<__bf16, nv()>(a, idx, dw, dl, L);
-    });
+    if (a.dtype == MOEDX_F32) return gate_backward_as<float>(a, idx, dw, dl, L);
+    if (a.dtype == MOEDX_F16) return gate_backward_as<_Float16>(a, idx, dw, dl, L);
+    return gate_backward_as<__bf16>(a, idx, dw, dl, L);
 }
 
 }  // namespace moedx

@@ -103,4 +103,59 @@ __device__ __forceinline__ float wave_max(float v) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
+// The same over the 16 lanes of a row, by rotations: every lane ends with the
+// same bits.
+#define MOEDX_ROR_STEPS(step) \
+    step(0x128);              \
+    step(0x124);              \
+    step(0x122);              \
+    step(0x121)
+
+__device__ __forceinline__ float row_sum(float v) {
+#define MOEDX_STEP(c) v += __int_as_float(dpp<c, 0xf>(0, __float_as_int(v)))
+    MOEDX_ROR_STEPS(MOEDX_STEP);
+#undef MOEDX_STEP
+    return v;
+}
+
+__device__ __forceinline__ float row_max(float v) {
+#define MOEDX_STEP(c) v = fmaxf(v, __int_as_float(dpp<c, 0xf>(0, __float_as_int(v))))
+    MOEDX_ROR_STEPS(MOEDX_STEP);
+#undef MOEDX_STEP
+    return v;
+}
+
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+#define MOEDX_STEP(c) v = max(v, (uint32_t)dpp<c, 0xf>(0, (int)v))
+    MOEDX_ROR_STEPS(MOEDX_STEP);
+#undef MOEDX_STEP
+    return v;
+}
+
+__device__ __forceinline__ uint64_t row_max(uint64_t v) {
+#define MOEDX_STEP(c)                                                         \
+    {                                                                         \
+        const uint32_t lo = (uint32_t)dpp<c, 0xf>(0, (int)(uint32_t)v);       \
+        const uint32_t hi = (uint32_t)dpp<c, 0xf>(0, (int)(uint32_t)(v >> 32)); \
+        const uint64_t o = ((uint64_t)hi << 32) | lo;                         \
+        v = o > v ? o : v;                                                    \
+    }
+    MOEDX_ROR_STEPS(MOEDX_STEP);
+#undef MOEDX_STEP
+    return v;
+}
+
+// exp(x) for x <= 0 to about an fp32 rounding: x log2 e as a rounded product
+// and its remainder, the hardware's 2^t, and 1 + r ln 2 for the remainder.
+// Below the normal range (x < -87.3) the result is 0.
+__device__ __forceinline__ float exp_neg(float x) {
+    constexpr float kLog2e = 1.44269504088896341f;
+    constexpr float kLog2eLow = (float)(1.44269504088896341 - (double)kLog2e);
+    x = fmaxf(x, -150.0f);
+    const float t = x * kLog2e;
+    const float r = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, r * 0.693147180559945f, e);
+}
+
 }  // namespace moedx
