@@ -289,6 +289,38 @@ __global__ __launch_bounds__(kRowThreads) void expert_unsort_kernel(
 // stores, 512 or 1024 threads and 8 rows at a time were no faster.
 constexpr int kBackThreads = 256;
 
+// NB filled slots from the lowest of *m on, at one chunk.
+template <typename S, int NB>
+__device__ __forceinline__ void back_batch(const u32x4_t* __restrict__ rows,
+                                           u32x4_t* __restrict__ d_rows, int chunks, int c, int row,
+                                           float w, uint64_t* m, const float (&d)[Chunk<S>::kN],
+                                           float* dot) {
+    constexpr int N = Chunk<S>::kN;
+    int64_t at[NB];
+    float wt[NB];
+    u32x4_t v[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int k = __builtin_ctzll(*m);
+        *m &= *m - 1;
+        wt[b] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), k));
+        at[b] = (int64_t)__builtin_amdgcn_readlane(row, k) * chunks + c;
+        v[b] = __builtin_nontemporal_load(rows + at[b]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        float y[N], g[N];
+        chunk_to_f32<S>(v[b], y);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            dot[b] = fmaf(d[i], y[i], dot[b]);
+            g[i] = d[i] * wt[b];
+        }
+        d_rows[at[b]] = chunk_from_f32<S>(g);
+    }
+}
+
 template <typename S>
 __global__ __launch_bounds__(kBackThreads) void expert_unsort_backward_kernel(
     const u32x4_t* __restrict__ d_out, const u32x4_t* __restrict__ rows, int K, int chunks,
@@ -313,32 +345,16 @@ __global__ __launch_bounds__(kBackThreads) void expert_unsort_backward_kernel(
         chunk_to_f32<S>(__builtin_nontemporal_load(d_out + (int64_t)t * chunks + c), d);
         uint64_t m = filled;
 #pragma unroll
-        for (int b0 = 0; b0 < kMaxTopk; b0 += 4) {
-            if (m == 0) break;
-            int64_t at[4];
-            float wt[4];
-            u32x4_t v[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int k = m ? __builtin_ctzll(m) : 0;
-                const bool has = m != 0;
-                m &= m - 1;
-                wt[b] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), k));
-                at[b] = has ? (int64_t)__builtin_amdgcn_readlane(row, k) * chunks + c : -1;
-                if (has) v[b] = __builtin_nontemporal_load(rows + at[b]);
+        for (int b = 0; b < kMaxTopk; b += 4) {
+            const int left = __popcll(m);
+            if (left >= 4) {
+                back_batch<S, 4>(rows, d_rows, chunks, c, row, w, &m, d, dot + b);
+                continue;
             }
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (at[b] < 0) break;
-                float y[N], g[N];
-                chunk_to_f32<S>(v[b], y);
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    dot[b0 + b] = fmaf(d[i], y[i], dot[b0 + b]);
-                    g[i] = d[i] * wt[b];
-                }
-                d_rows[at[b]] = chunk_from_f32<S>(g);
-            }
+            if (left >= 2) back_batch<S, 2>(rows, d_rows, chunks, c, row, w, &m, d, dot + b);
+            if (left == 3) back_batch<S, 1>(rows, d_rows, chunks, c, row, w, &m, d, dot + b + 2);
+            if (left == 1) back_batch<S, 1>(rows, d_rows, chunks, c, row, w, &m, d, dot + b);
+            break;
         }
     }
     uint64_t m = filled;
