@@ -134,7 +134,7 @@ SIGNATURES = {
     "moedx_expert_order": (_I, [_P, _P, _I, _I, _P, _P, _P, _P, _P, _SZ, _EX]),
     "moedx_expert_sort": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _EX]),
     "moedx_expert_unsort": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _EX]),
-    "moedx_expert_unsort_backward": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _EX]),
+    "moedx_expert_unsort_backward": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _EX]),
     "moedx_expert_linear": (_I, [_P, _P, _P, _I, _I, _I, _ROWS, _I, _P, _P, _EX]),
     "moedx_expert_linear_backward": (_I, [_P, _P, _P, _P, _I, _I, _I, _ROWS, _P, _P, _I, _EX]),
     "moedx_expert_swiglu_backward": (_I, [_P, _P, _P, _I, _I, _ROWS, _P, _EX]),

@@ -715,14 +715,16 @@ class Buffer:
         H = rows.shape[1]
         d_out = self._check("d_out", d_out, (rows.dtype,), (T, H))
         ros = self._check("row_of_slot", order.row_of_slot, (torch.int32,), (T, K))
+        sor = self._check("slot_of_row", order.slot_of_row, (torch.int32,), (T * K,))
         w = self._check("topk_weights", topk_weights, (torch.float32,), (T, K))
         d_rows = self._out("out", out, rows.dtype, (T * K, H))
         d_w = torch.empty(T, K, dtype=torch.float32, device=rows.device)
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
         C.check(C.moedx_expert_unsort_backward(self.ctx, _addr(d_out), _addr(rows),
-                                               _DTYPES[rows.dtype], T, K, H, _addr(ros), _addr(w),
-                                               _addr(d_rows), _addr(d_w), ctypes.byref(ex)))
-        self._keep(allocate_on_comm_stream, d_out, rows, ros, w, d_rows, d_w)
+                                               _DTYPES[rows.dtype], T, K, H, _addr(ros), _addr(sor),
+                                               _addr(w), _addr(d_rows), _addr(d_w),
+                                               ctypes.byref(ex)))
+        self._keep(allocate_on_comm_stream, d_out, rows, ros, sor, w, d_rows, d_w)
         return d_rows, d_w, self._event(done)
 
     def _expert_rows(self, rows, x: torch.Tensor):

@@ -1465,14 +1465,15 @@ int moedx_expert_unsort(moedx_ctx* ctx, const void* rows, int dtype, int T, int 
 
 int moedx_expert_unsort_backward(moedx_ctx* ctx, const void* d_out, const void* rows, int dtype,
                                  int T, int K, int H, const int32_t* row_of_slot,
-                                 const float* weights, void* d_rows, float* d_weights,
-                                 const moedx_exec* exec) {
+                                 const int32_t* slot_of_row, const float* weights, void* d_rows,
+                                 float* d_weights, const moedx_exec* exec) {
     if (int rc = check_ctx(ctx)) return rc;
     if (int rc = check_moves(dtype, T, K, H)) return rc;
-    if (T > 0 && (!d_out || !rows || !row_of_slot || !weights || !d_rows || !d_weights))
+    if (T > 0 && (!d_out || !rows || !row_of_slot || !slot_of_row || !weights || !d_rows ||
+                  !d_weights))
         return fail(MOEDX_EINVAL, "NULL device pointer");
     if (!aligned16(d_out) || !aligned16(rows) || !aligned16(d_rows) || !aligned4(row_of_slot) ||
-        !aligned4(weights) || !aligned4(d_weights))
+        !aligned4(slot_of_row) || !aligned4(weights) || !aligned4(d_weights))
         return fail(MOEDX_EINVAL, "d_out, rows and d_rows must be 16-byte aligned");
     DeviceScope scope;
     Exec ex;
@@ -1480,8 +1481,9 @@ int moedx_expert_unsort_backward(moedx_ctx* ctx, const void* d_out, const void* 
     if (T == 0)
         HIP_OR_FAIL(ex.no_kernel());
     else
-        HIP_OR_FAIL(launch_expert_unsort_backward(d_out, rows, dtype, T, K, H, row_of_slot, weights,
-                                                  d_rows, d_weights, ex.launch()));
+        HIP_OR_FAIL(launch_expert_unsort_backward(d_out, rows, dtype, T, K, H, row_of_slot,
+                                                  slot_of_row, weights, d_rows, d_weights,
+                                                  ex.launch()));
     return exec_end(ex);
 }
 

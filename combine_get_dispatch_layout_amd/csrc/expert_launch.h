@@ -70,8 +70,8 @@ hipError_t launch_expert_unsort(const void* rows, int dtype, int T, int K, int H
                                 const Launch& L);
 hipError_t launch_expert_unsort_backward(const void* d_out, const void* rows, int dtype, int T,
                                          int K, int H, const int32_t* row_of_slot,
-                                         const float* weights, void* d_rows, float* d_weights,
-                                         const Launch& L);
+                                         const int32_t* slot_of_row, const float* weights,
+                                         void* d_rows, float* d_weights, const Launch& L);
 
 // ---- the experts' products ----------------------------------------------------
 

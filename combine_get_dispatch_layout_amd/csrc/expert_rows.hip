@@ -282,97 +282,57 @@ __global__ __launch_bounds__(kRowThreads) void expert_unsort_kernel(
         __builtin_nontemporal_store(chunk_from_f32<S>(acc), out + (int64_t)t * chunks + c);
 }
 
-// One workgroup per token: a chunk of d_out is read once and held while the
-// chunks of the token's rows pass, four at a time: their products go into one
-// sum per filled slot, and weight * d_out to their gradients.  4095 x 7168 x
-// top-8: 192 us, 951 MB at 5.0 TB/s; fewer workgroups per CU (2 to 7), streaming
-// stores, 512 or 1024 threads and 8 rows at a time were no faster.
-constexpr int kBackThreads = 256;
-
-// NB filled slots from the lowest of *m on, at one chunk.
-template <typename S, int NB>
-__device__ __forceinline__ void back_batch(const u32x4_t* __restrict__ rows,
-                                           u32x4_t* __restrict__ d_rows, int chunks, int c, int row,
-                                           float w, uint64_t* m, const float (&d)[Chunk<S>::kN],
-                                           float* dot) {
-    constexpr int N = Chunk<S>::kN;
-    int64_t at[NB];
-    float wt[NB];
-    u32x4_t v[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const int k = __builtin_ctzll(*m);
-        *m &= *m - 1;
-        wt[b] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), k));
-        at[b] = (int64_t)__builtin_amdgcn_readlane(row, k) * chunks + c;
-        v[b] = __builtin_nontemporal_load(rows + at[b]);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        float y[N], g[N];
-        chunk_to_f32<S>(v[b], y);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            dot[b] = fmaf(d[i], y[i], dot[b]);
-            g[i] = d[i] * wt[b];
-        }
-        d_rows[at[b]] = chunk_from_f32<S>(g);
-    }
-}
+// One wave per row, in row order: the row and its gradient pass as two
+// streams, and its token's d_out comes from the caches after the first of the
+// token's rows; the dot product ends in the wave.  16384 x 4096 x top-6: 1.75
+// GB in 334 us (5.2 TB/s); by token, with d_out held and the rows gathered, 346
+// us, and with cached instead of streaming stores 343 us.  (All-zero data takes
+// 290 us: what memory reaches depends on the bits.)
+constexpr int kBackChunks = 4;  // chunks of 64 lanes whose loads go out together
 
 template <typename S>
-__global__ __launch_bounds__(kBackThreads) void expert_unsort_backward_kernel(
-    const u32x4_t* __restrict__ d_out, const u32x4_t* __restrict__ rows, int K, int chunks,
-    int64_t n_rows, const int32_t* __restrict__ row_of_slot, const float* __restrict__ weights,
+__global__ __launch_bounds__(kRowThreads) void expert_unsort_backward_kernel(
+    const u32x4_t* __restrict__ d_out, const u32x4_t* __restrict__ rows, int K, FastDiv by_k,
+    int chunks, int n_rows, const int32_t* __restrict__ row_of_slot,
+    const int32_t* __restrict__ slot_of_row, const float* __restrict__ weights,
     u32x4_t* __restrict__ d_rows, float* __restrict__ d_weights) {
-    constexpr int N = Chunk<S>::kN;
-    __shared__ float part[kBackThreads / 64][kMaxTopk];
-    const int t = blockIdx.x;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int row = -1;
-    float w = 0.0f;
-    if (lane < K) {
-        row = row_of_slot[(int64_t)t * K + lane];
-        w = weights[(int64_t)t * K + lane];
-    }
-    const uint64_t filled = __ballot(row >= 0 && row < n_rows);
-    float dot[kMaxTopk];  // of the b-th filled slot
+    constexpr int N = Chunk<S>::kN, C = kBackChunks;
+    const int r = row_wave();
+    if (r >= n_rows) return;
+    const int lane = threadIdx.x & 63;
+    // pair r, if its slot is empty, has no row to get its gradient from
+    if (lane == 0 && row_of_slot[r] < 0) d_weights[r] = 0.0f;
+    const int slot = slot_of_row[r];
+    if (slot < 0 || slot >= n_rows) return;
+    const float w = weights[slot];
+    const u32x4_t* d0 = d_out + (int64_t)by_k.div((uint32_t)slot) * chunks;
+    const u32x4_t* y0 = rows + (int64_t)r * chunks;
+    u32x4_t* g0 = d_rows + (int64_t)r * chunks;
+    float dot = 0.0f;
+    for (int c0 = lane; c0 < chunks; c0 += 64 * C) {
+        u32x4_t dv[C], yv[C];
 #pragma unroll
-    for (int b = 0; b < kMaxTopk; ++b) dot[b] = 0.0f;
-    for (int c = threadIdx.x; c < chunks; c += kBackThreads) {
-        float d[N];
-        chunk_to_f32<S>(__builtin_nontemporal_load(d_out + (int64_t)t * chunks + c), d);
-        uint64_t m = filled;
+        for (int i = 0; i < C; ++i) {
+            const int c = min(c0 + 64 * i, chunks - 1);
+            yv[i] = __builtin_nontemporal_load(y0 + c);
+            dv[i] = d0[c];
+        }
 #pragma unroll
-        for (int b = 0; b < kMaxTopk; b += 4) {
-            const int left = __popcll(m);
-            if (left >= 4) {
-                back_batch<S, 4>(rows, d_rows, chunks, c, row, w, &m, d, dot + b);
-                continue;
+        for (int i = 0; i < C; ++i) {
+            if (c0 + 64 * i >= chunks) break;
+            float d[N], y[N];
+            chunk_to_f32<S>(dv[i], d);
+            chunk_to_f32<S>(yv[i], y);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                dot = fmaf(d[j], y[j], dot);
+                d[j] *= w;
             }
-            if (left >= 2) back_batch<S, 2>(rows, d_rows, chunks, c, row, w, &m, d, dot + b);
-            if (left == 3) back_batch<S, 1>(rows, d_rows, chunks, c, row, w, &m, d, dot + b + 2);
-            if (left == 1) back_batch<S, 1>(rows, d_rows, chunks, c, row, w, &m, d, dot + b);
-            break;
+            __builtin_nontemporal_store(chunk_from_f32<S>(d), g0 + c0 + 64 * i);
         }
     }
-    uint64_t m = filled;
-#pragma unroll
-    for (int b = 0; b < kMaxTopk; ++b) {
-        if (m == 0) break;
-        const int k = __builtin_ctzll(m);
-        m &= m - 1;
-        const float s = wave_sum(dot[b]);
-        if (lane == 0) part[wave][k] = s;
-    }
-    __syncthreads();
-    if ((int)threadIdx.x < K) {
-        float s = 0.0f;
-        if ((filled >> threadIdx.x) & 1)
-            for (int i = 0; i < kBackThreads / 64; ++i) s += part[i][threadIdx.x];
-        d_weights[(int64_t)t * K + threadIdx.x] = s;
-    }
+    dot = wave_sum(dot);
+    if (lane == 0) d_weights[slot] = dot;
 }
 
 }  // namespace
@@ -416,12 +376,14 @@ hipError_t unsort_as(const void* rows, int T, int K, int chunks, const int32_t* 
 }
 
 template <typename S>
-hipError_t unsort_backward_as(const void* d_out, const void* rows, int T, int K, int chunks,
-                              const int32_t* row_of_slot, const float* weights, void* d_rows,
-                              float* d_weights, const Launch& L) {
-    return launch_kernel(expert_unsort_backward_kernel<S>, dim3(T), dim3(kBackThreads), L,
-                         static_cast<const u32x4_t*>(d_out), static_cast<const u32x4_t*>(rows), K,
-                         chunks, (int64_t)T * K, row_of_slot, weights,
+hipError_t unsort_backward_as(const void* d_out, const void* rows, int T, int K, int H,
+                              const int32_t* row_of_slot, const int32_t* slot_of_row,
+                              const float* weights, void* d_rows, float* d_weights,
+                              const Launch& L) {
+    return launch_kernel(expert_unsort_backward_kernel<S>, dim3((int)row_blocks(T, K)),
+                         dim3(kRowThreads), L, static_cast<const u32x4_t*>(d_out),
+                         static_cast<const u32x4_t*>(rows), K, make_fastdiv((uint32_t)K),
+                         H / Chunk<S>::kN, T * K, row_of_slot, slot_of_row, weights,
                          static_cast<u32x4_t*>(d_rows), d_weights);
 }
 
@@ -439,16 +401,12 @@ hipError_t launch_expert_unsort(const void* rows, int dtype, int T, int K, int H
 
 hipError_t launch_expert_unsort_backward(const void* d_out, const void* rows, int dtype, int T,
                                          int K, int H, const int32_t* row_of_slot,
-                                         const float* weights, void* d_rows, float* d_weights,
-                                         const Launch& L) {
-    if (dtype == MOEDX_F32)
-        return unsort_backward_as<float>(d_out, rows, T, K, H / 4, row_of_slot, weights, d_rows,
-                                         d_weights, L);
-    if (dtype == MOEDX_F16)
-        return unsort_backward_as<_Float16>(d_out, rows, T, K, H / 8, row_of_slot, weights, d_rows,
-                                            d_weights, L);
-    return unsort_backward_as<__bf16>(d_out, rows, T, K, H / 8, row_of_slot, weights, d_rows,
-                                      d_weights, L);
+                                         const int32_t* slot_of_row, const float* weights,
+                                         void* d_rows, float* d_weights, const Launch& L) {
+    const auto as = dtype == MOEDX_F32   ? unsort_backward_as<float>
+                    : dtype == MOEDX_F16 ? unsort_backward_as<_Float16>
+                                         : unsort_backward_as<__bf16>;
+    return as(d_out, rows, T, K, H, row_of_slot, slot_of_row, weights, d_rows, d_weights, L);
 }
 
 }  // namespace moedx

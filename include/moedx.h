@@ -511,12 +511,14 @@ MOEDX_API int moedx_expert_unsort(moedx_ctx *ctx, const void *rows, int dtype, i
                                   const int32_t *row_of_slot, const float *weights, void *out,
                                   const moedx_exec *exec);
 
-/* The gradients of moedx_expert_unsort: d_rows[row_of_slot[t, k]] = weights[t, k]
- * * d_out[t] (other rows are left alone), d_weights[t, k] = the dot product of
- * d_out[t] and rows[row_of_slot[t, k]] in fp32 (0 for an empty slot). */
+/* The gradients of moedx_expert_unsort: d_rows[r] = weights[t, k] * d_out[t] for
+ * the pair t * K + k = slot_of_row[r] of each row (rows without one are left
+ * alone), d_weights[t, k] = the dot product of d_out[t] and rows[r] in fp32 (0
+ * for an empty slot).  row_of_slot and slot_of_row are one moedx_expert_order's. */
 MOEDX_API int moedx_expert_unsort_backward(moedx_ctx *ctx, const void *d_out, const void *rows,
                                            int dtype, int T, int K, int H,
-                                           const int32_t *row_of_slot, const float *weights,
+                                           const int32_t *row_of_slot,
+                                           const int32_t *slot_of_row, const float *weights,
                                            void *d_rows, float *d_weights,
                                            const moedx_exec *exec);
 
