@@ -60,6 +60,11 @@ CASES = [
     ([20, 33, 64, 0, 31, 17], 520, 72),
     ([16, 31, 1, 47], 4104, 48),
 ]
+# Enough rows and outputs for 256 x 256 tiles on every compute unit: tiles of
+# 256 rows, of 20, 44, 63, 68, 108, 128 and 192, outputs past the last tile,
+# reductions of 1 to 17 stages of 64.
+CASES += [([2000, 0, 300, 831, 260, 740, 128], k, 4104) for k in (8, 72, 200, 328)]
+CASES += [([2000, 0, 300, 831, 260, 740, 128], 4104, n) for n in (16, 136, 192, 1032)]
 TYPES = [torch.bfloat16, torch.float16]
 
 
@@ -186,6 +191,59 @@ def test_slots_with_counts(cap):
         check("y", y[e, :c], xs @ wt, (K + 1) * V * (xs.abs() @ wt.abs()), dt)
         check("d_x", d_x[e, :c], d @ ws, (N + 1) * V * (d.abs() @ ws.abs()), dt)
         check("d_w", d_w[e], dtr @ xs, (c + 1) * V * (dtr.abs() @ xs.abs()), dt)
+
+
+def test_wide_slots():
+    """Slots whose live rows fill 256 x 256 tiles, a prefix of each expert's."""
+    dev = device()
+    E, cap, K, N, dt = 3, 1500, 136, 4096, torch.bfloat16
+    held = [1500, 257, 1024]
+    buf = make_buffer(E, 1, 1, 1)
+    g = torch.Generator(dev).manual_seed(5)
+    x = torch.randn(E, cap, K, generator=g, device=dev).to(dt)
+    w = (torch.randn(E, N, K, generator=g, device=dev) * K ** -0.5).to(dt)
+    for e in range(E):
+        x[e, held[e]:] = float("nan")
+    rows = torch.tensor(held, dtype=torch.int32, device=dev)
+    y, _, _ = buf.expert_linear(x, w, rows, out=torch.full((E, cap, N), 7.0, dtype=dt, device=dev))
+    for e, c in enumerate(held):
+        assert (y[e, c:] == 7.0).all()
+        xs, wt = x[e, :c].double(), w[e].double().t().contiguous()
+        check("y", y[e, :c], xs @ wt, (K + 1) * V * (xs.abs() @ wt.abs()), dt)
+
+
+def test_one_gradient_at_a_time():
+    """The C call leaves out the gradient whose pointer is null."""
+    import ctypes
+
+    from combine_get_dispatch_layout_amd import _capi as C
+    dev = device()
+    counts, K, N, dt = [30, 0, 65], 72, 40, torch.bfloat16
+    E = len(counts)
+    buf = make_buffer(E, 1, 1, 1)
+    off, M, x, w, g = make(counts, K, N, dt, dev, 8, N)
+    d_y = torch.randn(M, N, generator=g, device=dev).to(dt)
+    rows = torch.tensor(off, dtype=torch.int32, device=dev)
+    d_x, d_w, _ = buf.expert_linear_backward(d_y, x, w, rows,
+                                             out=torch.zeros(M, K, dtype=dt, device=dev))
+    a, b = torch.zeros_like(d_x), torch.full_like(d_w, 7.0)
+    er = C.moedx_expert_rows(rows.data_ptr(), None, M)
+    ex = C.moedx_exec(stream=torch.cuda.current_stream().cuda_stream)
+
+    def call(px, pw, pdx, pdw):
+        C.check(C.moedx_expert_linear_backward(
+            buf.ctx, d_y.data_ptr(), px, pw, C.MOEDX_BF16, K, N, ctypes.byref(er), pdx, pdw,
+            C.MOEDX_BF16, ctypes.byref(ex)))
+
+    call(None, w.data_ptr(), a.data_ptr(), None)
+    call(x.data_ptr(), None, None, b.data_ptr())
+    torch.cuda.synchronize()
+    assert torch.equal(a, d_x) and torch.equal(b, d_w)
+    for bad in ((x.data_ptr(), None, a.data_ptr(), None), (None, w.data_ptr(), None, b.data_ptr()),
+                (x.data_ptr(), w.data_ptr(), None, None)):
+        with pytest.raises(C.MoedxError) as err:
+            call(*bad)
+        assert err.value.code == C.MOEDX_EINVAL
 
 
 def test_offsets_are_clamped():
