@@ -91,11 +91,14 @@ __device__ __forceinline__ void with_blocks(int rows, F&& f) {
 }
 
 template <typename S, bool kSwiglu, typename T>
-__global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(const S* x, const S* w, ExpertRows er,
-                                                             int K, int N, int cols, S* y, S* pre,
+__global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(const S* x, const S* w,
+                                                                ExpertRows er, int K, int N,
+                                                                int cols, S* y, S* pre,
                                                                 bool rotate) {
-    __shared__ __align__(16) S lp[T::kP * T::BP * T::BK];
-    __shared__ __align__(16) S lq[T::kQ * T::BQ * T::BK];
+    // One array: with two, the compiler reads LDS before it asks for the next
+    // stage of Q (64 experts of about 182 rows, 4096 -> 4096: 555 and 534 us).
+    __shared__ __align__(16) S lp[T::kP * T::BP * T::BK + T::kQ * T::BQ * T::BK];
+    S* const lq = lp + T::kP * T::BP * T::BK;
     const int blk = xcd_run_block<kRunLog2>((int)blockIdx.x, (int)gridDim.x);
     const RowTile tile = find_block<T::BQ, kRowGroup>(er, blk, cols);
     if (tile.e < 0) return;
@@ -115,7 +118,8 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(const S* x, cons
         constexpr int NQ = decltype(nq)::value;
         f32x4 acc[T::TP][T::TQ] = {};
         const int nk = (K + T::BK - 1) / T::BK;
-        RingLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, T::kP, T::kQ, decltype(gp), decltype(gq)>(
+        RingLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, T::kP, T::kQ, true, decltype(gp),
+                 decltype(gq)>(
             wp, wq, lane, rotate ? scattered(blk, nk) : 0, nk)
             .run(gp, gq, (lds_char*)lp, (lds_char*)lq, wave, acc);
 #pragma unroll
@@ -321,7 +325,8 @@ __global__ __launch_bounds__(T::kThreads, 2) void dgrad_kernel(const S* d_y, con
     with_blocks<T::WQ>(tile.end - tile.begin, [&](auto nq) {
         constexpr int NQ = decltype(nq)::value;
         f32x4 acc[T::TP][T::TQ] = {};
-        RingLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, T::kP, T::kQ, decltype(gp), decltype(gq)>(
+        RingLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, T::kP, T::kQ, false, decltype(gp),
+                 decltype(gq)>(
             wp, wq, lane, 0, (N + T::BK - 1) / T::BK)
             .run(gp, gq, (lds_char*)lp, (lds_char*)lq, wave, acc);
 #pragma unroll
@@ -434,19 +439,24 @@ int64_t expected_rows(const ExpertRows& er) {
     return er.E > 8 ? (int64_t)er.cap * 8 / er.E : er.cap;
 }
 
-// Whether experts that likely have `likely` rows are better served by tiles of
-// 128 x 128, two workgroups per CU: up to 120 rows, where the weights' bytes
-// count (64 experts, 7168 -> 4096, 128 x 128 against 256 x 256: 615 and 740 us
-// at 12 rows, 656 and 765 at 64, 756 and 822 at 128, 1103 and 903 at 192), and
-// where 256 x 256 would leave CUs without a tile (8 experts of 256 rows, 4096 ->
-// 2048: 56 and 83 us; of 512 rows, 4096 -> 4096, 256 tiles: 157 and 128).
-bool small_tiles(const ExpertRows& er, int64_t likely, int out) {
-    const int64_t rows = er.offsets ? er.rows : likely * er.E;
-    const int64_t tiles = (rows + Wide::BQ - 1) / Wide::BQ * tiles_of(out, Wide::BP);
-    return likely <= 120 || tiles < 256;
+// Whether 256 x 256 tiles would leave compute units without one: then 128 x 128
+// serve better (8 experts of 256 rows, 4096 -> 2048, 64 wide tiles: 54 and 83
+// us; of 512 rows, 4096 -> 4096, 256 wide tiles: 157 and 128).
+bool few_wide_tiles(const ExpertRows& er, int64_t likely, int out) {
+    return (likely + Wide::BQ - 1) / Wide::BQ * er.E * tiles_of(out, Wide::BP) < 256;
 }
 
-// Whether workgroups start at scattered places of the reduction (`scattered`).
+// Up to so many rows per expert the forward product takes 128 x 128 tiles: the
+// weights' bytes count, and two workgroups per CU keep them coming (64 experts,
+// 4096 -> 4096, 128 x 128 and 256 x 256: 364 and 375 us at 12 rows, 373 and 383
+// at 30; 7168 -> 4096: 635 both at 45, 648 and 643 at 64, 717 and 670 at about
+// 100).  The input gradient is better off with 256 x 256 at any number (4096 ->
+// 4096: 363 and 330 us at 12 rows, 417 and 378 at 100).
+constexpr int64_t kSmallRows = 48;
+
+// Whether workgroups start at scattered places of the reduction (`scattered`):
+// 64 experts of 64 rows, 4096 -> 4096, 458 us from the start and 397 scattered;
+// of about 180, 517 and 517, but of skewed numbers about 180, 317 and 356.
 bool rotates(int64_t likely, int reduction) { return likely <= 120 && reduction % 2048 == 0; }
 
 template <typename S, typename T>
@@ -475,9 +485,9 @@ hipError_t linear_as(const void* x, const void* w, const ExpertRows& er, int K, 
         return launch_kernel(swiglu ? linear_few_kernel<S, true> : linear_few_kernel<S, false>,
                              grid, dim3(kFewThreads), L, xs, ws, er, K, N, cols, ys, ps, rotate);
     }
-    if (small_tiles(er, likely, swiglu ? 2 * N : N))
+    if (likely <= kSmallRows || few_wide_tiles(er, likely, swiglu ? 2 * N : N))
         return linear_tiles<S, Small>(xs, ws, er, K, N, swiglu, rotate, ys, ps, L);
-    return linear_tiles<S, Wide>(xs, ws, er, K, N, swiglu, false, ys, ps, L);
+    return linear_tiles<S, Wide>(xs, ws, er, K, N, swiglu, rotate, ys, ps, L);
 }
 
 template <typename S, typename T>
@@ -494,7 +504,7 @@ hipError_t dgrad_as(const void* d_y, const void* w, const ExpertRows& er, int K,
                     const Launch& L) {
     const S* ds = static_cast<const S*>(d_y);
     const S* ws = static_cast<const S*>(w);
-    if (small_tiles(er, expected_rows(er), K))
+    if (few_wide_tiles(er, expected_rows(er), K))
         return dgrad_tiles<S, Small>(ds, ws, er, K, N, static_cast<S*>(d_x), L);
     return dgrad_tiles<S, Wide>(ds, ws, er, K, N, static_cast<S*>(d_x), L);
 }

@@ -19,8 +19,8 @@
 // up with 4 consecutive p of one q.  (32 x 32 x 16 was 6 to 14% slower here.)
 //
 // What bounds the two loops below on random data is power as much as issue: an
-// 8192^3 product that takes 934 us takes 754 us on zeros, whose clocks are
-// higher, and loops with 15% more idle matrix cycles measure the same.
+// 8192^3 product that takes 775 us (1420 TFLOP/s; the library's takes 756) is
+// 19% faster on zeros, whose clocks are higher.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -109,15 +109,19 @@ struct Along {
         base[h] = static_cast<const char*>(first);
         valid[h] = min(max(rows, 0), B / kHalves);
     }
-    // Stage at reduction value k0 into lds (this wave's part of it).
+    // Stage at reduction value k0 into lds (this wave's part of it): all of it,
+    // or of one half the first kSome loads of every wave, kSome * kLoadRows * NW
+    // rows.
+    template <int kSome = kLoads>
     __device__ __forceinline__ void load(lds_char* lds, int k0, int wave) const {
+        static_assert(kSome == kLoads || kHalves == 1, "a part of one half");
         const uint32_t v = k0 + col < nr ? voff : kOutside;
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
             const __amdgpu_buffer_rsrc_t rs =
                 make_rsrc(base[h] + (int64_t)k0 * 2, valid[h] * ld2 - k0 * 2);
 #pragma unroll
-            for (int j = 0; j < kLoads / kHalves; ++j) {
+            for (int j = 0; j < kSome / kHalves; ++j) {
                 const int row = h * (B / kHalves) + (j * NW + wave) * kLoadRows;
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + row * kRow), 16,
                                                          (int)(v + j * kLoadRows * NW * ld2), 0, 0,
@@ -241,9 +245,9 @@ __device__ __forceinline__ int q_block(int wq, int j) {
 // workgroups share a CU, and one multiplies while the other waits at its
 // barrier or stores its tile.  Three LDS buffers of 32 reduction values rotate:
 // while stage s is multiplied, s + 1 is arriving and s + 2 is asked for.  Best
-// for operands across r and short reductions (64 experts of 512 rows, 4096 x
-// 7168 weight gradients: 2614 us, 2930 us with WholeCuLoop); an operand along r
-// is fetched in half lines, which costs the forward product 20%.
+// where both operands are across r (weight gradients of 64 experts of 512 rows,
+// 4096 x 7168: 2614 us, 2930 us as 256 x 256 tiles of 8 waves); an operand along
+// r would be fetched in half lines, which costs the forward product 20%.
 template <typename S, int BP, int BQ, int WP, int WQ, int NQ, typename LP, typename LQ>
 struct SharedCuLoop {
     static constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;
@@ -345,13 +349,17 @@ struct SharedCuLoop {
 //
 // `stage` is told (restrict) that the buffers it reads are not the ones it
 // loads into: the compiler then puts no wait of its own before an LDS read, and
-// the one before the barrier is exact.
-template <typename S, int BP, int BQ, int WP, int WQ, int NQ, int kP, int kQ, typename LP,
-          typename LQ>
+// the one before the barrier is exact.  kPartQ: only the rows of Q that the
+// tile has are loaded (64 experts of 128 rows, 7168 -> 4096: 735 us with all of
+// them, 690 us without; no gain where P is read across r).
+template <typename S, int BP, int BQ, int WP, int WQ, int NQ, int kP, int kQ, bool kPartQ,
+          typename LP, typename LQ>
 struct RingLoop {
     static constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;
     static constexpr int kBK = 64;
     static constexpr int kPBytes = BP * kBK * 2, kQBytes = BQ * kBK * 2;
+    static constexpr int kQLoads = kPartQ ? NQ : LQ::kLoads;
+    static_assert(LQ::kLoadRows * WP * WQ == 16 * WQ, "a load of all waves is a block per wave");
     static_assert(kP >= kQ && kQ >= 2, "P is loaded at least as far ahead as Q");
     typename LP::At ap;
     typename LQ::At aq;
@@ -403,7 +411,9 @@ struct RingLoop {
                                            const s16x8 (&p1)[TP], const s16x8 (&q1)[TQ],
                                            f32x4 (&acc)[TP][TQ]) const {
         frags(rp, rq, 0, p0, q0);
-        gq.load(wq, place(it + kQ), wave);
+        gq.template load<kQLoads>(wq, place(it + kQ), wave);
+        // The waits count loads in this order: no load may pass here.
+        __builtin_amdgcn_sched_barrier(0x38e);
         gp.load(wp, place(it + kP), wave);
         products(p1, q1, acc);
         interleave<true>();
@@ -415,7 +425,7 @@ struct RingLoop {
     template <bool kLoads>
     static __device__ __forceinline__ void interleave() {
         constexpr int kReads = LP::kFragReads * TP + LQ::kFragReads * NQ;
-        constexpr int kMem = kReads + (kLoads ? LP::kLoads + LQ::kLoads : 0);
+        constexpr int kMem = kReads + (kLoads ? LP::kLoads + kQLoads : 0);
         constexpr int kPer = TP * NQ / kMem > 0 ? TP * NQ / kMem : 1;
         __builtin_amdgcn_sched_group_barrier(0x002, 12, 0);  // addresses
 #pragma unroll
@@ -425,7 +435,7 @@ struct RingLoop {
         }
         if constexpr (kLoads) {
 #pragma unroll
-            for (int i = 0; i < LP::kLoads + LQ::kLoads; ++i) {
+            for (int i = 0; i < LP::kLoads + kQLoads; ++i) {
                 __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);  // load
                 __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
             }
@@ -442,11 +452,14 @@ struct RingLoop {
         // in the order in which they are needed
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
-            if (i < kQ) gq.load(lq + i * kQBytes, place(i), wave);
+            if (i < kQ) gq.template load<kQLoads>(lq + i * kQBytes, place(i), wave);
+            __builtin_amdgcn_sched_barrier(0);
             gp.load(lp + i * kPBytes, place(i), wave);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        constexpr int kAhead = (kP - kQ) * LP::kLoads;  // loads of later stages, at a barrier
-        barrier<(kP - 1) * LP::kLoads + (kQ - 1) * LQ::kLoads>();
+        // At a barrier only a P stage that is needed later may be in flight.
+        constexpr int kAhead = kP > kQ ? LP::kLoads : 0;
+        barrier<(kP - 1) * LP::kLoads + (kQ - 1) * kQLoads>();
         s16x8 p0[TP], q0[TQ], p1[TP], q1[TQ];
         frags(lp, lq, 0, p0, q0);
         int pb = 0, qb = 0;

@@ -65,6 +65,9 @@ CASES = [
 # reductions of 1 to 17 stages of 64.
 CASES += [([2000, 0, 300, 831, 260, 740, 128], k, 4104) for k in (8, 72, 200, 328)]
 CASES += [([2000, 0, 300, 831, 260, 740, 128], 4104, n) for n in (16, 136, 192, 1032)]
+# Reductions that workgroups enter at scattered places, in each tile size.
+CASES += [([2, 1, 0, 17, 3], 4096, 72), ([9, 12, 30], 2048, 136),
+          ([60, 70, 0, 55, 61, 90, 33, 64], 2048, 4096)]
 TYPES = [torch.bfloat16, torch.float16]
 
 
