@@ -15,6 +15,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <initializer_list>
 #include <new>
 #include <vector>
 
@@ -1233,6 +1234,21 @@ struct DeviceScope {
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
+// An output and another buffer of a call (either may be NULL: left out).
+struct Bytes {
+    const void* at;
+    int64_t n;
+};
+bool overlap(Bytes a, Bytes b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return a.at && b.at && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
+}
+int check_apart(Bytes out, std::initializer_list<Bytes> others) {
+    for (const Bytes& o : others)
+        if (overlap(out, o)) return fail(MOEDX_EINVAL, "an output overlaps another buffer");
+    return MOEDX_OK;
+}
+
 int check_dtype(int dtype, bool f32_too) {
     if (dtype == MOEDX_BF16 || dtype == MOEDX_F16 || (f32_too && dtype == MOEDX_F32))
         return MOEDX_OK;
@@ -1279,8 +1295,12 @@ GateArgs gate_args(const moedx_ctx* ctx, const void* logits, int dtype, int T, i
     return a;
 }
 
+// Waves of one launch of whole 256-thread workgroups: HIP counts a grid's
+// threads in 32 bits.
+constexpr int64_t kMaxWaves = ((int64_t)1 << 26) - 4;
+
 // T tokens of K slots as pairs, and rows of H values moved by one wave per
-// (token, slice of 1024 bytes).
+// (token, slice of 1024 bytes) or, in a gradient, per pair.
 int check_pairs(int T, int K) {
     if (K < 1 || K > kMaxTopk) return fail(MOEDX_EINVAL, "K=%d outside [1, %d]", K, kMaxTopk);
     if (T < 0 || T > (1 << 28) || (int64_t)T * K > ((int64_t)1 << 30))
@@ -1293,8 +1313,8 @@ int check_moves(int dtype, int T, int K, int H) {
     if (int rc = check_pairs(T, K)) return rc;
     if (H < 8 || H % 8 != 0) return fail(MOEDX_EINVAL, "H=%d must be a positive multiple of 8", H);
     const int64_t slices = ((int64_t)H * dtype_bytes(dtype) + 1023) / 1024;
-    if ((int64_t)T * slices > ((int64_t)1 << 30))
-        return fail(MOEDX_EINVAL, "T=%d x H=%d exceeds the supported row count", T, H);
+    if (T * std::max<int64_t>(slices, K) > kMaxWaves)
+        return fail(MOEDX_EINVAL, "T=%d with K=%d, H=%d exceeds the supported row count", T, K, H);
     return MOEDX_OK;
 }
 
@@ -1433,6 +1453,8 @@ int moedx_expert_sort(moedx_ctx* ctx, const void* x, int dtype, int T, int K, in
     if (T > 0 && (!x || !row_of_slot || !rows)) return fail(MOEDX_EINVAL, "NULL device pointer");
     if (!aligned16(x) || !aligned16(rows) || !aligned4(row_of_slot))
         return fail(MOEDX_EINVAL, "x and rows must be 16-byte aligned");
+    const int64_t row = (int64_t)H * dtype_bytes(dtype);
+    if (int rc = check_apart({rows, T * K * row}, {{x, T * row}})) return rc;
     DeviceScope scope;
     Exec ex;
     if (int rc = exec_begin(ctx, exec, &ex)) return rc;
@@ -1452,6 +1474,8 @@ int moedx_expert_unsort(moedx_ctx* ctx, const void* rows, int dtype, int T, int 
     if (T > 0 && (!rows || !row_of_slot || !out)) return fail(MOEDX_EINVAL, "NULL device pointer");
     if (!aligned16(rows) || !aligned16(out) || !aligned4(row_of_slot) || !aligned4(weights))
         return fail(MOEDX_EINVAL, "rows and out must be 16-byte aligned");
+    const int64_t row = (int64_t)H * dtype_bytes(dtype);
+    if (int rc = check_apart({out, T * row}, {{rows, T * K * row}})) return rc;
     DeviceScope scope;
     Exec ex;
     if (int rc = exec_begin(ctx, exec, &ex)) return rc;
@@ -1475,6 +1499,9 @@ int moedx_expert_unsort_backward(moedx_ctx* ctx, const void* d_out, const void* 
     if (!aligned16(d_out) || !aligned16(rows) || !aligned16(d_rows) || !aligned4(row_of_slot) ||
         !aligned4(slot_of_row) || !aligned4(weights) || !aligned4(d_weights))
         return fail(MOEDX_EINVAL, "d_out, rows and d_rows must be 16-byte aligned");
+    const int64_t row = (int64_t)H * dtype_bytes(dtype);
+    if (int rc = check_apart({d_rows, T * K * row}, {{d_out, T * row}, {rows, T * K * row}}))
+        return rc;
     DeviceScope scope;
     Exec ex;
     if (int rc = exec_begin(ctx, exec, &ex)) return rc;
@@ -1497,6 +1524,10 @@ int moedx_expert_linear(moedx_ctx* ctx, const void* x, const void* w, int dtype,
     if (er->rows > 0 && (!x || !w || !y)) return fail(MOEDX_EINVAL, "NULL device pointer");
     if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(pre))
         return fail(MOEDX_EINVAL, "x, w, y and pre must be 16-byte aligned");
+    const Bytes xb{x, er->rows * K * 2}, yb{y, er->rows * N * 2}, pb{pre, er->rows * N * 4};
+    const Bytes wb{w, (int64_t)ctx->E * (swiglu ? 2 : 1) * N * K * 2};
+    if (int rc = check_apart(yb, {xb, wb, pb})) return rc;
+    if (int rc = check_apart(pb, {xb, wb})) return rc;
     DeviceScope scope;
     Exec ex;
     if (int rc = exec_begin(ctx, exec, &ex)) return rc;
@@ -1520,6 +1551,11 @@ int moedx_expert_linear_backward(moedx_ctx* ctx, const void* d_y, const void* x,
         return fail(MOEDX_EINVAL, "NULL device pointer");
     if (!aligned16(d_y) || !aligned16(x) || !aligned16(w) || !aligned16(d_x) || !aligned16(d_w))
         return fail(MOEDX_EINVAL, "d_y, x, w, d_x and d_w must be 16-byte aligned");
+    const int64_t weights = (int64_t)ctx->E * N * K;
+    const Bytes dyb{d_y, er->rows * N * 2}, xb{x, er->rows * K * 2}, wb{w, weights * 2};
+    const Bytes dxb{d_x, er->rows * K * 2}, dwb{d_w, weights * dtype_bytes(d_w_dtype)};
+    if (int rc = check_apart(dxb, {dyb, xb, wb, dwb})) return rc;
+    if (int rc = check_apart(dwb, {dyb, xb, wb})) return rc;
     DeviceScope scope;
     Exec ex;
     if (int rc = exec_begin(ctx, exec, &ex)) return rc;
@@ -1543,6 +1579,9 @@ int moedx_expert_swiglu_backward(moedx_ctx* ctx, const void* d_h, const void* pr
     if (er->rows > 0 && (!d_h || !pre || !d_pre)) return fail(MOEDX_EINVAL, "NULL device pointer");
     if (!aligned16(d_h) || !aligned16(pre) || !aligned16(d_pre))
         return fail(MOEDX_EINVAL, "d_h, pre and d_pre must be 16-byte aligned");
+    if (int rc = check_apart({d_pre, er->rows * N * 4},
+                             {{d_h, er->rows * N * 2}, {pre, er->rows * N * 4}}))
+        return rc;
     DeviceScope scope;
     Exec ex;
     if (int rc = exec_begin(ctx, exec, &ex)) return rc;

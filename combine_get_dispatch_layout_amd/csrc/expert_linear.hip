@@ -396,40 +396,47 @@ __global__ __launch_bounds__(Narrow::kThreads, 2) void wgrad_kernel(const S* d_y
 }
 
 constexpr int kActThreads = 256;
+constexpr int64_t kActGrid = 1 << 20;  // workgroups at most
 
-// One workgroup per row of the buffer; rows of no expert are left alone.
+// Workgroups go through the buffer's rows; rows of no expert are left alone.
 template <typename S>
 __global__ __launch_bounds__(kActThreads) void swiglu_backward_kernel(
     const u32x4_t* __restrict__ d_h, const u32x4_t* __restrict__ pre, ExpertRows er, int chunks,
     u32x4_t* __restrict__ d_pre) {
     constexpr int C = Chunk<S>::kN;
-    const int64_t row = blockIdx.x;
-    bool live;
-    if (er.offsets) {
-        live = row >= er.offsets[0] && row < er.offsets[er.E];
-    } else {
-        const int e = (int)(row / er.cap);
-        live = row - (int64_t)e * er.cap < er.counts[e];
-    }
-    if (!live) return;
-    for (int c = threadIdx.x; c < chunks; c += kActThreads) {
-        float d[C], g[C], u[C];
-        chunk_to_f32<S>(__builtin_nontemporal_load(d_h + row * chunks + c), d);
-        chunk_to_f32<S>(__builtin_nontemporal_load(pre + row * 2 * chunks + c), g);
-        chunk_to_f32<S>(__builtin_nontemporal_load(pre + row * 2 * chunks + chunks + c), u);
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const float s = 1.0f / (1.0f + expf(-g[i]));
-            const float du = d[i] * g[i] * s;
-            g[i] = d[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
-            u[i] = du;
+    for (int64_t row = blockIdx.x; row < er.rows; row += gridDim.x) {
+        bool live;
+        if (er.offsets) {
+            live = row >= er.offsets[0] && row < er.offsets[er.E];
+        } else {
+            const int e = (int)(row / er.cap);
+            live = row - (int64_t)e * er.cap < er.counts[e];
         }
-        d_pre[row * 2 * chunks + c] = chunk_from_f32<S>(g);
-        d_pre[row * 2 * chunks + chunks + c] = chunk_from_f32<S>(u);
+        if (!live) continue;
+        for (int c = threadIdx.x; c < chunks; c += kActThreads) {
+            float d[C], g[C], u[C];
+            chunk_to_f32<S>(__builtin_nontemporal_load(d_h + row * chunks + c), d);
+            chunk_to_f32<S>(__builtin_nontemporal_load(pre + row * 2 * chunks + c), g);
+            chunk_to_f32<S>(__builtin_nontemporal_load(pre + row * 2 * chunks + chunks + c), u);
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const float s = 1.0f / (1.0f + expf(-g[i]));
+                const float du = d[i] * g[i] * s;
+                g[i] = d[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
+                u[i] = du;
+            }
+            d_pre[row * 2 * chunks + c] = chunk_from_f32<S>(g);
+            d_pre[row * 2 * chunks + chunks + c] = chunk_from_f32<S>(u);
+        }
     }
 }
 
 int tiles_of(int n, int b) { return (n + b - 1) / b; }
+
+// A grid of so many workgroups; more than HIP takes fails at the launch.
+dim3 grid_of(int64_t workgroups) {
+    return dim3((unsigned)(workgroups < UINT32_MAX ? workgroups : UINT32_MAX));
+}
 
 // Rows an expert is likely to have, from what the host knows.  A capacity
 // buffer holds at most cap tokens, each with a few experts: 8 are taken, the
@@ -463,7 +470,7 @@ template <typename S, typename T>
 hipError_t linear_tiles(const S* x, const S* w, const ExpertRows& er, int K, int N, bool swiglu,
                         bool rotate, S* y, S* pre, const Launch& L) {
     const int cols = tiles_of(N, swiglu ? T::BP / 2 : T::BP);
-    const dim3 grid((unsigned)(max_tiles(er, T::BQ) * cols));
+    const dim3 grid = grid_of(max_tiles(er, T::BQ) * cols);
     return launch_kernel(swiglu ? linear_kernel<S, true, T> : linear_kernel<S, false, T>, grid,
                          dim3(T::kThreads), L, x, w, er, K, N, cols, y, pre, rotate);
 }
@@ -481,7 +488,7 @@ hipError_t linear_as(const void* x, const void* w, const ExpertRows& er, int K, 
     // 7168 -> 4096: 79 us, 128 x 128 tiles 113; 8 rows each in all 64: 620 and 611.
     if (likely <= 8) {
         const int cols = tiles_of(N, swiglu ? 16 : 32);
-        const dim3 grid((unsigned)(max_tiles(er, kFewRows) * cols));
+        const dim3 grid = grid_of(max_tiles(er, kFewRows) * cols);
         return launch_kernel(swiglu ? linear_few_kernel<S, true> : linear_few_kernel<S, false>,
                              grid, dim3(kFewThreads), L, xs, ws, er, K, N, cols, ys, ps, rotate);
     }
@@ -494,7 +501,7 @@ template <typename S, typename T>
 hipError_t dgrad_tiles(const S* d_y, const S* w, const ExpertRows& er, int K, int N, S* d_x,
                        const Launch& L) {
     const int cols = tiles_of(K, T::BP);
-    const dim3 grid((unsigned)(max_tiles(er, T::BQ) * cols));
+    const dim3 grid = grid_of(max_tiles(er, T::BQ) * cols);
     return launch_kernel(dgrad_kernel<S, T>, grid, dim3(T::kThreads), L, d_y, w, er, K, N, cols,
                          d_x);
 }
@@ -513,7 +520,7 @@ template <typename S>
 hipError_t wgrad_as(const void* d_y, const void* x, const ExpertRows& er, int K, int N, void* d_w,
                     bool f32_out, const Launch& L) {
     const int cols = tiles_of(K, Narrow::BP), rows = tiles_of(N, Narrow::BQ);
-    const dim3 grid((unsigned)((int64_t)cols * rows * er.E));
+    const dim3 grid = grid_of((int64_t)cols * rows * er.E);
     const S* ds = static_cast<const S*>(d_y);
     const S* xs = static_cast<const S*>(x);
     if (f32_out)
@@ -526,7 +533,8 @@ hipError_t wgrad_as(const void* d_y, const void* x, const ExpertRows& er, int K,
 template <typename S>
 hipError_t swiglu_backward_as(const void* d_h, const void* pre, const ExpertRows& er, int N,
                               void* d_pre, const Launch& L) {
-    return launch_kernel(swiglu_backward_kernel<S>, dim3((unsigned)er.rows), dim3(kActThreads), L,
+    const dim3 grid((unsigned)(er.rows < kActGrid ? er.rows : kActGrid));
+    return launch_kernel(swiglu_backward_kernel<S>, grid, dim3(kActThreads), L,
                          static_cast<const u32x4_t*>(d_h), static_cast<const u32x4_t*>(pre), er,
                          N / Chunk<S>::kN, static_cast<u32x4_t*>(d_pre));
 }

@@ -309,15 +309,19 @@ struct SharedCuLoop {
         if (nk <= 0) return;
         // The stages past a multiple of three go first, in the last buffers, so
         // that the loop always starts at buffer 0.
+        // The waits count loads, so stage 1's stay behind stage 0's.
         const int odd = nk % kBuffers;
         if (odd == 0) {
             load(gp, gq, lp0, lq0, 0, wave);
+            __builtin_amdgcn_sched_barrier(0);
             load(gp, gq, lp1, lq1, 1, wave);
         } else if (odd == 1) {
             load(gp, gq, lp2, lq2, 0, wave);
+            __builtin_amdgcn_sched_barrier(0);
             load(gp, gq, lp0, lq0, 1, wave);
         } else {
             load(gp, gq, lp1, lq1, 0, wave);
+            __builtin_amdgcn_sched_barrier(0);
             load(gp, gq, lp2, lq2, 1, wave);
         }
         arrive();

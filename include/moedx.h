@@ -426,6 +426,7 @@ MOEDX_API int moedx_ll_combine(moedx_ctx *ctx, const uint16_t *y, const int64_t 
                                uint16_t *out, const moedx_exec *exec);
 
 /* ---- element types of the calls below ------------------------------------- */
+/* In all of them an output overlaps no other buffer of the call. */
 enum { MOEDX_BF16 = 0, MOEDX_F16 = 1, MOEDX_F32 = 2 };
 
 /* ---- router: top-k expert choice with gate weights ------------------------- */
@@ -498,8 +499,8 @@ MOEDX_API int moedx_expert_order(moedx_ctx *ctx, const int64_t *topk_idx, int T,
 
 /* rows[row_of_slot[t, k]] = x[t] for every filled slot: x [T, H] and rows
  * [T * K, H] of type `dtype`, bit-exact copies; other rows are left alone.
- * Below, H % 8 == 0, data 16-byte aligned, buffers do not overlap, and a row
- * index outside [0, T * K) counts as empty. */
+ * Below, H % 8 == 0, data 16-byte aligned, T * K and T * ceil(row bytes / 1024)
+ * up to 2^26 - 4, and a row index outside [0, T * K) counts as empty. */
 MOEDX_API int moedx_expert_sort(moedx_ctx *ctx, const void *x, int dtype, int T, int K, int H,
                                 const int32_t *row_of_slot, void *rows, const moedx_exec *exec);
 

@@ -166,6 +166,24 @@ def test_swiglu_backward(N, dt):
     check("d_pre", d_pre[:n], want, acc, dt)
 
 
+def test_swiglu_backward_of_many_rows():
+    """More rows than workgroups."""
+    dev = device()
+    M, N, dt = (1 << 20) + 77, 8, torch.bfloat16
+    buf = make_buffer(2, 1, 1, 1)
+    rows = torch.tensor([1, 1 << 19, M - 1], dtype=torch.int32, device=dev)
+    pre = torch.randn(M, 2 * N, device=dev).to(dt)
+    d_h = torch.randn(M, N, device=dev).to(dt)
+    d_pre, _ = buf.expert_swiglu_backward(d_h, pre, rows,
+                                          out=torch.full((M, 2 * N), 7.0, dtype=dt, device=dev))
+    assert (d_pre[0] == 7.0).all() and (d_pre[-1] == 7.0).all()
+    part = slice(M - 100, M - 1)
+    again, _ = buf.expert_swiglu_backward(d_h[part], pre[part],
+                                          torch.tensor([0, 9, 99], dtype=torch.int32, device=dev))
+    assert torch.equal(d_pre[part], again)
+    assert not (d_pre[1:-1] == 7.0).all(1).any()
+
+
 @pytest.mark.parametrize("cap", [1, 7, 130])
 def test_slots_with_counts(cap):
     """[E, cap, *] buffers with counts (the low-latency layout); counts beyond
@@ -249,6 +267,24 @@ def test_one_gradient_at_a_time():
         assert err.value.code == C.MOEDX_EINVAL
 
 
+def test_no_rows_at_all():
+    dev = device()
+    E, K, N, dt = 3, 16, 24, torch.bfloat16
+    buf = make_buffer(E, 1, 1, 1)
+    w = torch.ones(E, N, K, device=dev, dtype=dt)
+    off = torch.zeros(E + 1, dtype=torch.int32, device=dev)
+    x, d_y = torch.empty(0, K, device=dev, dtype=dt), torch.empty(0, N, device=dev, dtype=dt)
+    y, pre, _ = buf.expert_linear(x, w, off, swiglu=False)
+    assert y.shape == (0, N) and pre is None
+    d_x, d_w, _ = buf.expert_linear_backward(d_y, x, w, off, d_w=torch.full_like(w, 7.0))
+    assert d_x.shape == (0, K) and (d_w == 0).all()
+    slots = torch.empty(E, 0, K, device=dev, dtype=dt)
+    y, _, _ = buf.expert_linear(slots, w, off[:E].contiguous())
+    assert y.shape == (E, 0, N)
+    d_pre, _ = buf.expert_swiglu_backward(d_y, torch.empty(0, 2 * N, device=dev, dtype=dt), off)
+    assert d_pre.shape == (0, 2 * N)
+
+
 def test_offsets_are_clamped():
     """Offsets outside the buffer, or falling, touch nothing outside it."""
     dev = device()
@@ -316,6 +352,20 @@ def test_refusals():
     for f in bad:
         with pytest.raises(ValueError):
             f()
+    flat = torch.zeros(4096, device=dev, dtype=dt)
+    sq = torch.zeros(E, K, K, device=dev, dtype=dt)
+    pre = torch.zeros(10, 2 * K, device=dev, dtype=dt)
+    over = [lambda: buf.expert_linear(x, sq, off, out=x),
+            lambda: buf.expert_linear(flat[:10 * K].view(10, K), sq, off,
+                                      out=flat[9 * K:19 * K].view(10, K)),
+            lambda: buf.expert_linear(x, sq, off, out=sq.view(-1, K)[:10]),
+            lambda: buf.expert_linear_backward(x, x.clone(), sq, off, out=x),
+            lambda: buf.expert_linear_backward(x, x.clone(), sq, off, d_w=sq),
+            lambda: buf.expert_swiglu_backward(x, pre, off, out=pre)]
+    for f in over:
+        with pytest.raises(C.MoedxError) as e:
+            f()
+        assert e.value.code == C.MOEDX_EINVAL
     odd = torch.zeros(10, 12, device=dev, dtype=dt)
     for f in (lambda: buf.expert_linear(odd, torch.zeros(E, N, 12, device=dev, dtype=dt), off),
               lambda: buf.expert_linear(x, torch.zeros(E, 12, K, device=dev, dtype=dt), off),

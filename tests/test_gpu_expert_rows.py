@@ -234,6 +234,21 @@ def test_refusals():
         with pytest.raises(C.MoedxError) as e:
             f()
         assert e.value.code == C.MOEDX_EINVAL
+    # outputs on their inputs, and more rows than a grid has waves
+    flat = torch.zeros(12, 16, device=dev, dtype=torch.bfloat16)
+    p = flat.data_ptr()
+    big = [(1 << 26, 1, 8), (1 << 22, 16, 8), (1 << 24, 4, 4096)]
+    for f in [lambda: buf.expert_sort(flat[:4], order, out=flat[3:11]),
+              lambda: buf.expert_unsort(flat[:8], order, out=flat[7:11]),
+              lambda: buf.expert_unsort_backward(flat[:4], x.repeat(2, 1), order,
+                                                 torch.zeros(4, 2, device=dev), out=flat[2:10]),
+              lambda: buf.expert_unsort_backward(x, flat[:8], order,
+                                                 torch.zeros(4, 2, device=dev), out=flat[:8])] + [
+            lambda n=n: C.check(C.moedx_expert_sort(buf.ctx, p, C.MOEDX_BF16, *n, p, p, None))
+            for n in big]:
+        with pytest.raises(C.MoedxError) as e:
+            f()
+        assert e.value.code == C.MOEDX_EINVAL
     # a handle of other rows, and a low-latency handle
     _, _, _, _, h, _ = buf.dispatch(x, topk_idx=idx)
     with pytest.raises(C.MoedxError) as e:
