@@ -644,7 +644,7 @@ class Buffer:
         offsets = torch.empty(self.num_experts + 1, dtype=torch.int32, device=dev)
         row_of_slot = torch.empty(T, K, dtype=torch.int32, device=dev)
         slot_of_row = torch.empty(T * K, dtype=torch.int32, device=dev)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
         C.check(C.moedx_expert_order(self.ctx, _addr(topk_idx), T, K,
                                      handle.ptr if handle is not None else None, _addr(offsets),

@@ -1392,7 +1392,8 @@ int moedx_expert_order_workspace_bytes(const moedx_ctx* ctx, int T, int K, size_
     if (int rc = check_ctx(ctx)) return rc;
     if (int rc = check_pairs(T, K)) return rc;
     if (!bytes) return fail(MOEDX_EINVAL, "bytes is NULL");
-    *bytes = align256((size_t)std::max(order_tiles((int64_t)T * K), 1) * ctx->E * 4);
+    const int tiles = order_tiles((int64_t)T * K);
+    *bytes = tiles > 1 ? align256((size_t)tiles * ctx->E * 4) : 0;  // one tile's counts stay in LDS
     return MOEDX_OK;
 }
 
@@ -1412,7 +1413,7 @@ int moedx_expert_order(moedx_ctx* ctx, const int64_t* topk_idx, int T, int K,
                         (long long)rows);
         if (K != h->K) return fail(MOEDX_ESTATE, "K=%d differs from the handle's K=%d", K, h->K);
     }
-    if (!expert_offsets || !workspace || (T > 0 && (!topk_idx || !row_of_slot || !slot_of_row)))
+    if (!expert_offsets || (need > 0 && !workspace) || (T > 0 && (!topk_idx || !row_of_slot || !slot_of_row)))
         return fail(MOEDX_EINVAL, "NULL device pointer");
     if (!aligned_to(topk_idx, 8) || !aligned4(expert_offsets) || !aligned4(row_of_slot) ||
         !aligned4(slot_of_row))

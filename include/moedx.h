@@ -475,7 +475,8 @@ MOEDX_API int moedx_gate_topk_backward(moedx_ctx *ctx, const void *logits, int d
 
 /* ---- rows in expert order ---------------------------------------------------- */
 
-/* Device bytes moedx_expert_order needs as its workspace for T tokens of K slots. */
+/* Device bytes moedx_expert_order needs as its workspace for T tokens of K
+ * slots; 0 for up to 1024 slots, where workspace may be NULL. */
 MOEDX_API int moedx_expert_order_workspace_bytes(const moedx_ctx *ctx, int T, int K,
                                                  size_t *bytes);
 
