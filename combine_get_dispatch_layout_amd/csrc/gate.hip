@@ -14,13 +14,18 @@
 //
 // Where scores are the keys, one wavefront takes a token: lane l holds experts
 // l NV .. l NV + NV - 1 in registers (one vector load where E allows it).  A
-// round takes the wave-wide maximum of the keys as unsigned integers that order
-// like them (0 = cannot be chosen), then the first lane that holds it.  Where
+// round takes the wave-wide maximum of the keys, then the first lane that holds
+// it.  Where
 // the logits are, and in the gradient, a row of 16 lanes takes a token (up to
 // 256 experts): a key is the ordered logit with the expert's number below it,
 // so keys differ, a maximum names its expert, and ties go to the lower one by
-// themselves.  What bounds these kernels is the instructions of the rounds and
-// exps, not the logits' bytes.
+// themselves.
+//
+// What bounds these kernels is the instructions of the rounds and exps, not the
+// logits' bytes: 16384 tokens of 256 bf16 logits, top-8, softmax: 8.6 us, and
+// 9.8 for the gradient (16.6 and 14.7 with a wave per token).  128
+// tokens with bias, 8 groups and renormalised sigmoids, one wave's latency: 7.2
+// us, of which 3.6 are the launch, the loads and the scores, 2 the rounds.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -76,6 +81,25 @@ __device__ __forceinline__ void load_logits(const S* logits, int E, int t, int l
     for (int j = 0; j < NV; ++j) l[j] = l[j] >= kNegInf ? l[j] : kNegInf;
 }
 
+// The bias of the lane's experts, asked for together with the logits.
+template <int NV>
+__device__ __forceinline__ void load_bias(const GateArgs& a, int lane, float (&b)[NV]) {
+    typedef float vals __attribute__((ext_vector_type(NV), aligned(4)));
+    const int e0 = lane * NV;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) b[j] = 0.0f;
+    if (!a.bias) return;
+    if (e0 + NV <= a.E) {
+        const vals v = *reinterpret_cast<const vals*>(a.bias + e0);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) b[j] = v[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (e0 + j < a.E) b[j] = a.bias[e0 + j];
+    }
+}
+
 template <int NV>
 __device__ __forceinline__ float token_max(const float (&l)[NV]) {
     float m = l[0];
@@ -90,6 +114,16 @@ __device__ __forceinline__ float exp_sum(const float (&l)[NV], float m) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) z += l[j] > kNegInf ? expf(l[j] - m) : 0.0f;
     return wave_sum(z);
+}
+
+// The renormalised weight (before scale) of a row's lane that holds a chosen
+// logit l: a softmax over the chosen (log) scores, never 0 / 0.
+__device__ __forceinline__ float row_share(bool have, bool softmax, float l) {
+    const float s = !have ? kNegInf : softmax ? l : log_sigmoid(l);
+    const float top = row_max(s);  // by every lane of the row
+    const float x = have ? expf(s - top) : 0.0f;
+    const float total = row_sum(x);
+    return have ? x / total : 0.0f;
 }
 
 // The sum of the two best of (one, two), each -inf when there is none.
@@ -112,11 +146,18 @@ __device__ __forceinline__ void keep_groups(const GateArgs& a, int lane, double*
             two = fmax(two, fmin(one, key[j]));
             one = fmax(one, key[j]);
         }
-        for (int d = 1; d < span; d <<= 1) {
-            const double o1 = __shfl_xor(one, d, 64), o2 = __shfl_xor(two, d, 64);
+        // the other half's pair: of 2, 4, 8 and 16 lanes by lane-shifted reads,
+        // of 32 and 64 through LDS
+        const auto join = [&](double o1, double o2) {
             two = fmax(fmin(one, o1), fmax(two, o2));
             one = fmax(one, o1);
-        }
+        };
+        if (span > 1) join(lane_swap<0xb1>(one), lane_swap<0xb1>(two));
+        if (span > 2) join(lane_swap<0x4e>(one), lane_swap<0x4e>(two));
+        if (span > 4) join(lane_swap<0x141>(one), lane_swap<0x141>(two));
+        if (span > 8) join(lane_swap<0x140>(one), lane_swap<0x140>(two));
+        for (int d = 16; d < span; d <<= 1)
+            join(__shfl_xor(one, d, 64), __shfl_xor(two, d, 64));
         const double score = pair_score(one, two);
         gs = __shfl(score, lane * span & 63, 64);
         if (lane >= a.groups) gs = -INFINITY;
@@ -150,18 +191,20 @@ __device__ __forceinline__ void keep_groups(const GateArgs& a, int lane, double*
     }
 }
 
-// Key: uint32_t where the logits are the keys, uint64_t where scores are.
+// Key: uint32_t where the logits are the keys, double where scores are.
 template <typename S, int NV, typename Key>
 __global__ __launch_bounds__(kGateThreads) void gate_topk_kernel(GateArgs a, bool vec,
                                                                  int64_t* __restrict__ topk_idx,
                                                                  float* __restrict__ topk_weights) {
     constexpr bool kScores = sizeof(Key) == 8;
+    constexpr Key kNone = kScores ? (Key)-INFINITY : (Key)0;  // cannot be chosen
     __shared__ double staged[kScores ? kGateWaves * NV * 64 : 1];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t = blockIdx.x * kGateWaves + wave;
     if (t >= a.T) return;
-    float l[NV];
+    float l[NV], bias[kScores ? NV : 1];
+    if constexpr (kScores) load_bias<NV>(a, lane, bias);
     load_logits<S, NV>(static_cast<const S*>(a.logits), a.E, t, lane, vec, l);
     const bool softmax = a.score == MOEDX_GATE_SOFTMAX;
 
@@ -190,18 +233,16 @@ __global__ __launch_bounds__(kGateThreads) void gate_topk_kernel(GateArgs a, boo
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int e = lane * NV + j;
-            if (a.bias && e < a.E) s[j] += (double)a.bias[e];
+            s[j] += (double)bias[j];
             if (!(l[j] > kNegInf) || !(s[j] > -INFINITY)) s[j] = -INFINITY;
         }
         if (a.groups > 1) keep_groups<NV>(a, lane, staged + wave * NV * 64, s);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) key[j] = s[j] > -INFINITY ? ordered(s[j]) : 0ull;
+        for (int j = 0; j < NV; ++j) key[j] = s[j];
     }
 
-    // K rounds; lane k keeps the k-th choice and its logit.
+    // K rounds; lane k keeps the k-th choice.
     int mine_idx = -1;
-    float mine_l = kNegInf;
     for (int k = 0; k < a.K; ++k) {
         Key best = key[0];
         int at = 0;
@@ -212,31 +253,25 @@ __global__ __launch_bounds__(kGateThreads) void gate_topk_kernel(GateArgs a, boo
                 at = j;
             }
         const Key top = wave_max(best);
-        if (top == 0) break;
+        if (top == kNone) break;
         const int from = __builtin_ctzll(__ballot(best == top));
         const int j0 = __builtin_amdgcn_readlane(at, from);
-        float lv = 0.0f;
+        const int gone = lane == from ? at : NV;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (j == j0) {
-                lv = l[j];
-                if (lane == from) key[j] = 0;
-            }
-        lv = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lv), from));
-        if (lane == k) {
-            mine_idx = from * NV + j0;
-            mine_l = lv;
-        }
+        for (int j = 0; j < NV; ++j) key[j] = j == gone ? kNone : key[j];
+        if (lane == k) mine_idx = from * NV + j0;
+    }
+    // its logit, from the lane that holds it
+    float mine_l = kNegInf;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const float v = __shfl(l[j], max(mine_idx, 0) / NV, 64);
+        if (mine_idx >= 0 && mine_idx % NV == j) mine_l = v;
     }
     const bool have = mine_idx >= 0;
     float w = 0.0f;
     if (a.renormalize) {
-        // a softmax over the chosen (log) scores: never 0 / 0
-        const float s = !have ? kNegInf : softmax ? mine_l : log_sigmoid(mine_l);
-        const float top = wave_max(s);
-        const float x = have ? expf(s - top) : 0.0f;
-        const float total = wave_sum(x);
-        w = have ? x / total : 0.0f;
+        w = row_share(have, softmax, mine_l);  // the choices are in the first row
     } else if (softmax) {
         const float z = exp_sum(l, m);
         w = have ? expf(mine_l - m) / z : 0.0f;
@@ -369,16 +404,6 @@ __device__ __forceinline__ float row_exp_sum(const float (&l)[NV], float m) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) z += l[j] > kNegInf ? exp_neg(l[j] - m) : 0.0f;
     return row_sum(z);
-}
-
-// The renormalised weight (before scale) of a row's lane that holds a chosen
-// logit l: a softmax over the chosen (log) scores, never 0 / 0.
-__device__ __forceinline__ float row_share(bool have, bool softmax, float l) {
-    const float s = !have ? kNegInf : softmax ? l : log_sigmoid(l);
-    const float top = row_max(s);  // by every lane of the row
-    const float x = have ? expf(s - top) : 0.0f;
-    const float total = row_sum(x);
-    return have ? x / total : 0.0f;
 }
 
 template <typename S, int NV>
@@ -525,7 +550,7 @@ hipError_t gate_as(const GateArgs& a, int64_t* idx, float* w, const Launch& L) {
     const dim3 waves((a.T + kGateWaves - 1) / kGateWaves), block(kGateThreads);
     if (a.bias != nullptr || a.groups > 1)
         return by_width(a.E, 64, [&](auto nv) {
-            return launch_kernel(gate_topk_kernel<S, nv(), uint64_t>, waves, block, L, a,
+            return launch_kernel(gate_topk_kernel<S, nv(), double>, waves, block, L, a,
                                  vector_rows<S, nv()>(a, nullptr), idx, w);
         });
     if (a.E > kRowExperts)

@@ -246,7 +246,8 @@ __device__ __forceinline__ int q_block(int wq, int j) {
 // barrier or stores its tile.  Three LDS buffers of 32 reduction values rotate:
 // while stage s is multiplied, s + 1 is arriving and s + 2 is asked for.  Best
 // where both operands are across r (weight gradients of 64 experts of 512 rows,
-// 4096 x 7168: 2614 us, 2930 us as 256 x 256 tiles of 8 waves); an operand along
+// 4096 x 7168: 2220 us; 2614, against 2930 as 256 x 256 tiles of 8 waves, before
+// the odd stages went first); an operand along
 // r would be fetched in half lines, which costs the forward product 20%.
 template <typename S, int BP, int BQ, int WP, int WQ, int NQ, typename LP, typename LQ>
 struct SharedCuLoop {

@@ -79,22 +79,6 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-#define MOEDX_STEP(c, r)                                                                 \
-    {                                                                                    \
-        const uint32_t lo = (uint32_t)dpp<c, r>((int)(uint32_t)v, (int)(uint32_t)v);     \
-        const uint32_t hi =                                                              \
-            (uint32_t)dpp<c, r>((int)(uint32_t)(v >> 32), (int)(uint32_t)(v >> 32));     \
-        const uint64_t o = ((uint64_t)hi << 32) | lo;                                    \
-        v = o > v ? o : v;                                                               \
-    }
-    MOEDX_DPP_STEPS(MOEDX_STEP);
-#undef MOEDX_STEP
-    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, 63);
-    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), 63);
-    return ((uint64_t)hi << 32) | lo;
-}
-
 __device__ __forceinline__ float wave_max(float v) {
 #define MOEDX_STEP(c, r) \
     v = fmaxf(v, __int_as_float(dpp<c, r>(__float_as_int(v), __float_as_int(v))))
@@ -103,7 +87,16 @@ __device__ __forceinline__ float wave_max(float v) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// The same over the 16 lanes of a row, by rotations: every lane ends with the
+// v of the lane that kCtrl (a quad permutation or a mirror) names.
+template <int kCtrl>
+__device__ __forceinline__ double lane_swap(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)dpp<kCtrl, 0xf>(0, (int)(uint32_t)b);
+    const uint32_t hi = (uint32_t)dpp<kCtrl, 0xf>(0, (int)(uint32_t)(b >> 32));
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// Reductions over the 16 lanes of a row, by rotations: every lane ends with the
 // same bits.
 #define MOEDX_ROR_STEPS(step) \
     step(0x128);              \
@@ -142,6 +135,34 @@ __device__ __forceinline__ uint64_t row_max(uint64_t v) {
     }
     MOEDX_ROR_STEPS(MOEDX_STEP);
 #undef MOEDX_STEP
+    return v;
+}
+
+// The maximum over the wave's lanes, which every lane gets: rows of 16 by
+// rotations, then rows and halves by exchanges.  No NaN.
+__device__ __forceinline__ double wave_max(double v) {
+    const auto join = [&](uint32_t lo, uint32_t hi) {
+        const double o = __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+        v = o > v ? o : v;
+    };
+#define MOEDX_STEP(c)                                                              \
+    {                                                                              \
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);                        \
+        join((uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, c, 0xf, 0xf, true), \
+             (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), c, 0xf, 0xf, true)); \
+    }
+    MOEDX_ROR_STEPS(MOEDX_STEP);
+#undef MOEDX_STEP
+    uint64_t b = __builtin_bit_cast(uint64_t, v);
+    auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false);
+    auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+    v = __builtin_bit_cast(double, ((uint64_t)hi[0] << 32) | lo[0]);
+    join(lo[1], hi[1]);
+    b = __builtin_bit_cast(uint64_t, v);
+    lo = __builtin_amdgcn_permlane32_swap((uint32_t)b, (uint32_t)b, false, false);
+    hi = __builtin_amdgcn_permlane32_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+    v = __builtin_bit_cast(double, ((uint64_t)hi[0] << 32) | lo[0]);
+    join(lo[1], hi[1]);
     return v;
 }
 
