@@ -224,3 +224,27 @@ def test_two_streams_at_once():
     for i in range(2):
         for out in got[i]:
             assert torch.equal(out, want[i])
+
+
+def test_readme_example():
+    """The README's example as written: the layer through the dispatch and in the
+    decode slots gives the layer on the tokens, each rounded a few times."""
+    import os
+    import re
+    dev = device()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "README.md")).read()
+    m = re.search(r"## From the router to the output.*?```python\n(.*?)```", text, re.S)
+    print("[path] README example", flush=True)
+    torch.manual_seed(0)
+    ns = {}
+    exec(compile(m.group(1), "README.md", "exec"), ns)
+    torch.cuda.synchronize()
+    out = ns["out"].double()
+    scale = float(out.norm())
+    assert float((ns["out2"].double() - out).norm()) < 8 * EPS * scale
+    n = ns["out3"].shape[0]
+    assert float((ns["out3"].double() - out[:n]).norm()) < 8 * EPS * float(out[:n].norm())
+    assert ns["x"].device.type == dev.type
+    for leaf, grad in (("x", "d_x"), ("w1", "d_w1"), ("w2", "d_w2"), ("logits", "d_logits")):
+        assert ns[grad].shape == ns[leaf].shape and bool(torch.isfinite(ns[grad]).all())
