@@ -267,6 +267,49 @@ def test_one_gradient_at_a_time():
         assert err.value.code == C.MOEDX_EINVAL
 
 
+def test_buffers_past_4_gib():
+    """Rows, gradients and weights whose offsets pass 32 bits."""
+    dev = device()
+    dt, K, N = torch.bfloat16, 8192, 8
+    M = (1 << 32) // (K * 2) + 1000
+    buf = make_buffer(2, 1, 1, 1)
+    g = torch.Generator(dev).manual_seed(9)
+    x = torch.zeros(M, K, device=dev, dtype=dt)
+    d_y = torch.zeros(M, N, device=dev, dtype=dt)
+    x[-40:] = torch.randn(40, K, generator=g, device=dev).to(dt)
+    d_y[-40:] = torch.randn(40, N, generator=g, device=dev).to(dt)
+    w = (torch.randn(2, N, K, generator=g, device=dev) * K ** -0.5).to(dt)
+    rows = torch.tensor([0, 7, M], dtype=torch.int32, device=dev)
+    print("[linear] rows past 4 GiB", flush=True)
+    y, _, _ = buf.expert_linear(x, w, rows)
+    d_x, d_w, _ = buf.expert_linear_backward(d_y, x, w, rows, d_w_dtype=torch.float32)
+    xs, ws, d = x[-40:].double(), w[1].double(), d_y[-40:].double()
+    wt, dtr = ws.t().contiguous(), d.t().contiguous()
+    check("y", y[-40:], xs @ wt, (K + 1) * V * (xs.abs() @ wt.abs()), dt)
+    check("d_x", d_x[-40:], d @ ws, (N + 1) * V * (d.abs() @ ws.abs()), dt)
+    check("d_w", d_w[1], dtr @ xs, 41 * V * (dtr.abs() @ xs.abs()), torch.float32)
+    assert (y[:-40] == 0).all() and (d_x[7:-40] == 0).all() and (d_w[0] == 0).all()
+    del x, y, d_x
+
+    E, N = 40, 8192
+    buf = make_buffer(E, 1, 1, 1)
+    w = torch.zeros(E, N, K, device=dev, dtype=dt)
+    w[-1] = (torch.randn(N, K, generator=g, device=dev) * K ** -0.5).to(dt)
+    x = torch.randn(5, K, generator=g, device=dev).to(dt)
+    rows = torch.zeros(E + 1, dtype=torch.int32, device=dev)
+    rows[-1] = 5
+    print("[linear] weights past 4 GiB", flush=True)
+    y, _, _ = buf.expert_linear(x, w, rows)
+    d_x, d_w, _ = buf.expert_linear_backward(y, x, w, rows)
+    ws = w[-1].double()
+    wt = ws.t().contiguous()
+    check("y", y, x.double() @ wt, (K + 1) * V * (x.double().abs() @ wt.abs()), dt)
+    check("d_x", d_x, y.double() @ ws, (N + 1) * V * (y.double().abs() @ ws.abs()), dt)
+    dtr = y.double().t().contiguous()
+    check("d_w", d_w[-1], dtr @ x.double(), 6 * V * (dtr.abs() @ x.double().abs()), dt)
+    assert (d_w[:-1] == 0).all()
+
+
 def test_no_rows_at_all():
     dev = device()
     E, K, N, dt = 3, 16, 24, torch.bfloat16
