@@ -135,7 +135,7 @@ __global__ __launch_bounds__(kOrderThreads) void order_rank_kernel(OrderArgs a, 
         if (a.tiles == 1) {  // no counts were taken: this tile's are all
             for (int w = 0; w < kOrderWaves; ++w) all[j] += base[w][x];
         } else if (x < a.E) {
-#pragma unroll 16
+#pragma unroll 32
             for (int t = 0; t < a.tiles; ++t) {
                 const int c = a.tile_counts[(int64_t)t * a.E + x];
                 all[j] += c;
