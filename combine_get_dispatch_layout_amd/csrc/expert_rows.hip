@@ -101,6 +101,21 @@ __device__ __forceinline__ int block_prefix(int v, int32_t* wave_sums, int* tota
     return before + incl - v;
 }
 
+// Adds an expert's counts in tiles t .. t + N - 1, all asked for at once, to the
+// sum over all tiles and, of those before this one, to its own.
+template <int N>
+__device__ __forceinline__ void add_counts(const int32_t*& at, int E, int t, int& all, int& mine) {
+    int c[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) c[u] = at[u * E];
+    at += N * E;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        all += c[u];
+        mine += t + u < (int)blockIdx.x ? c[u] : 0;
+    }
+}
+
 // Waves take contiguous quarters of the tile, so that ranks ascend with p.
 // A wave's lane holds 4 pairs, 64 apart, per kOrderTile pairs of the tile.
 __global__ __launch_bounds__(kOrderThreads) void order_rank_kernel(OrderArgs a, int bits) {
@@ -135,12 +150,11 @@ __global__ __launch_bounds__(kOrderThreads) void order_rank_kernel(OrderArgs a, 
         if (a.tiles == 1) {  // no counts were taken: this tile's are all
             for (int w = 0; w < kOrderWaves; ++w) all[j] += base[w][x];
         } else if (x < a.E) {
-#pragma unroll 32
-            for (int t = 0; t < a.tiles; ++t) {
-                const int c = a.tile_counts[(int64_t)t * a.E + x];
-                all[j] += c;
-                mine[j] += t < (int)blockIdx.x ? c : 0;
-            }
+            const int32_t* at = a.tile_counts + x;
+            int t = 0;
+            for (; t + 32 <= a.tiles; t += 32) add_counts<32>(at, a.E, t, all[j], mine[j]);
+            for (; t + 8 <= a.tiles; t += 8) add_counts<8>(at, a.E, t, all[j], mine[j]);
+            for (; t < a.tiles; ++t) add_counts<1>(at, a.E, t, all[j], mine[j]);
         }
     }
     int filled = 0;
