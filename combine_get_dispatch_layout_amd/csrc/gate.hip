@@ -15,17 +15,16 @@
 // Where scores are the keys, one wavefront takes a token: lane l holds experts
 // l NV .. l NV + NV - 1 in registers (one vector load where E allows it).  A
 // round takes the wave-wide maximum of the keys, then the first lane that holds
-// it.  Where
-// the logits are, and in the gradient, a row of 16 lanes takes a token (up to
-// 256 experts): a key is the ordered logit with the expert's number below it,
-// so keys differ, a maximum names its expert, and ties go to the lower one by
-// themselves.
+// it.  Where the logits are, and in the gradient, a row of 16 lanes takes a token
+// (up to 256 experts): a key is the ordered logit with the expert's number below
+// it, so keys differ, a maximum names its expert, ties go to the lower one by
+// themselves, and a round is the maximum below the last one.
 //
 // What bounds these kernels is the instructions of the rounds and exps, not the
-// logits' bytes: 16384 tokens of 256 bf16 logits, top-8, softmax: 8.6 us, and
-// 9.8 for the gradient (16.6 and 14.7 with a wave per token).  128
-// tokens with bias, 8 groups and renormalised sigmoids, one wave's latency: 7.2
-// us, of which 3.6 are the launch, the loads and the scores, 2 the rounds.
+// logits' bytes: 16384 tokens of 256 bf16 logits, top-8, softmax: 7.1 us, and
+// 7.9 for the gradient (16.6 and 14.7 with a wave per token).  128 tokens with
+// bias, 8 groups and renormalised sigmoids, one wave's latency: 7.2 us, of which
+// 3.6 are the launch, the loads and the scores, 2 the rounds.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -78,7 +77,7 @@ __device__ __forceinline__ void load_logits(const S* logits, int E, int t, int l
         for (int j = 0; j < NV; ++j) l[j] = e0 + j < E ? (float)row[e0 + j] : kNegInf;
     }
 #pragma unroll
-    for (int j = 0; j < NV; ++j) l[j] = l[j] >= kNegInf ? l[j] : kNegInf;
+    for (int j = 0; j < NV; ++j) l[j] = fmaxf(l[j], kNegInf);  // the number, of a NaN and one
 }
 
 // The bias of the lane's experts, asked for together with the logits.
@@ -364,12 +363,24 @@ __global__ __launch_bounds__(kGateThreads) void gate_topk_backward_kernel(
 
 constexpr int kRowTokens = kGateThreads / 16;  // tokens of a workgroup
 
-// A logit's key: ordered, and below it ~expert; 0 = cannot be chosen.
+// A logit's key: ordered, and below it ~expert, so that keys differ.  Keys up to
+// kNone, those of -inf among them, cannot be chosen.
 template <typename S>
-struct LogitKey;
+struct LogitKey {  // bf16 and fp16 leave the low 13 bits of their fp32 form clear
+    typedef uint32_t type;
+    static constexpr type kNone = 0x007fffffu;  // the order of -inf
+    static __device__ __forceinline__ type make(float l, int e) {
+        return (ordered(l) & ~0xffu) | (~e & 0xff);
+    }
+    static __device__ __forceinline__ int expert(type k) { return (int)(~k & 0xff); }
+    static __device__ __forceinline__ float logit(type k) {
+        return __uint_as_float((k >> 31) ? (k & ~0xffu) ^ 0x80000000u : ~(k | 0xffu));
+    }
+};
 template <>
 struct LogitKey<float> {
     typedef uint64_t type;
+    static constexpr type kNone = 0x007fffffffffffffull;
     static __device__ __forceinline__ type make(float l, int e) {
         return ((uint64_t)ordered(l) << 32) | (uint32_t)~e;
     }
@@ -379,30 +390,12 @@ struct LogitKey<float> {
         return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
     }
 };
-template <typename S>
-struct LogitKey16 {  // 16-bit logits: their own bits suffice
-    typedef uint32_t type;
-    static __device__ __forceinline__ type make(float l, int e) {
-        const uint32_t u = __builtin_bit_cast(uint16_t, (S)(l + 0.0f));
-        const uint32_t o = u ^ ((u >> 15) ? 0xffffu : 0x8000u);
-        return (o << 16) | (~e & 0xffff);
-    }
-    static __device__ __forceinline__ int expert(type k) { return (int)(~k & 0xffff); }
-    static __device__ __forceinline__ float logit(type k) {
-        const uint32_t o = k >> 16;
-        return (float)__builtin_bit_cast(S, (uint16_t)(o ^ ((o >> 15) ? 0x8000u : 0xffffu)));
-    }
-};
-template <>
-struct LogitKey<__bf16> : LogitKey16<__bf16> {};
-template <>
-struct LogitKey<_Float16> : LogitKey16<_Float16> {};
 
 template <int NV>
 __device__ __forceinline__ float row_exp_sum(const float (&l)[NV], float m) {
     float z = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) z += l[j] > kNegInf ? exp_neg(l[j] - m) : 0.0f;
+    for (int j = 0; j < NV; ++j) z += exp_neg(l[j] - m);  // 0 for -inf, whatever m is
     return row_sum(z);
 }
 
@@ -415,26 +408,32 @@ __global__ __launch_bounds__(kGateThreads) void gate_rows_kernel(GateArgs a, boo
     const int t = blockIdx.x * kRowTokens + (threadIdx.x >> 4);
     float l[NV];
     load_logits<S, NV>(static_cast<const S*>(a.logits), a.E, min(t, a.T - 1), lane, vec, l);
-    typename Key::type key[NV];
+    typedef typename Key::type key_t;
+    key_t key[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) key[j] = l[j] > kNegInf ? Key::make(l[j], lane * NV + j) : 0;
+    for (int j = 0; j < NV; ++j) key[j] = Key::make(l[j], lane * NV + j);
     const bool softmax = a.score == MOEDX_GATE_SOFTMAX;
     // lane k keeps the k-th choice and its logit
     int mine = -1;
     float mine_l = kNegInf, m = 0.0f;
+    key_t top = 0;
     for (int k = 0; k < a.K; ++k) {
-        typename Key::type top = key[0];
+        // The largest key below the last: of the differences to it, taken modulo
+        // the type's range, those of smaller keys are the largest.
+        key_t d = key[0] - top;
 #pragma unroll
-        for (int j = 1; j < NV; ++j) top = key[j] > top ? key[j] : top;
-        top = row_max(top);
-        const float lv = Key::logit(top);
-        if (lane == k && top != 0) {
-            mine = Key::expert(top);
-            mine_l = lv;
+        for (int j = 1; j < NV; ++j) {
+            const key_t o = key[j] - top;
+            d = o > d ? o : d;
         }
-        if (k == 0) m = top != 0 ? lv : 0.0f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) key[j] = key[j] == top ? 0 : key[j];
+        d = row_max(d);
+        const key_t next = d + top;
+        top = k == 0 || next < top ? next : 0;  // or there is none
+        if (lane == k && top > Key::kNone) {
+            mine = Key::expert(top);
+            mine_l = Key::logit(top);
+        }
+        if (k == 0 && top > Key::kNone) m = Key::logit(top);
     }
     const bool have = mine >= 0;
     float w;
@@ -502,9 +501,14 @@ __global__ __launch_bounds__(kGateThreads) void gate_rows_backward_kernel(
     const float per_z = a.scale / z;
     float d[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
+    for (int j = 0; j < NV; ++j)
         d[j] = spread[slot][lane * NV + j];
-        if (dense) d[j] = l[j] > kNegInf ? exp_neg(l[j] - m) * per_z * (d[j] - dot) : 0.0f;
+    if (dense) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const float v = exp_neg(l[j] - m) * per_z * (d[j] - dot);
+            d[j] = l[j] > kNegInf ? v : 0.0f;
+        }
     }
     if ((int)blockIdx.x * kRowTokens + slot >= a.T) return;
     S* out = d_logits + (int64_t)t * a.E + lane * NV;
