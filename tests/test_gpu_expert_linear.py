@@ -405,6 +405,12 @@ def test_refusals():
             lambda: buf.expert_linear_backward(x, x.clone(), sq, off, out=x),
             lambda: buf.expert_linear_backward(x, x.clone(), sq, off, d_w=sq),
             lambda: buf.expert_swiglu_backward(x, pre, off, out=pre)]
+    # contiguous views that start inside 16 bytes
+    off_x, off_w = flat[1:1 + 10 * K].view(10, K), flat[1:1 + E * N * K].view(E, N, K)
+    over += [lambda: buf.expert_linear(off_x, w, off), lambda: buf.expert_linear(x, off_w, off),
+             lambda: buf.expert_linear(x, w, off, out=flat[1:1 + 10 * N].view(10, N)),
+             lambda: buf.expert_linear_backward(d_y, off_x, w, off),
+             lambda: buf.expert_swiglu_backward(off_x, pre, off)]
     for f in over:
         with pytest.raises(C.MoedxError) as e:
             f()

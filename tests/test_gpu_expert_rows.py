@@ -203,6 +203,28 @@ def test_rows_past_4_gib():
     assert torch.equal(out, x * 2)
 
 
+def test_strided_inputs():
+    """Views with other strides give what their copies give."""
+    dev = device()
+    T, E, K, H = 37, 16, 3, 40
+    buf = make_buffer(E, 1, 1, T)
+    idx = routing("some", T, E, K, 5).to(dev)
+    wide = torch.full((T, 2 * K), -7, dtype=torch.int64, device=dev)
+    wide[:, ::2] = idx
+    order, _ = buf.expert_order(idx)
+    again, _ = buf.expert_order(wide[:, ::2])
+    assert torch.equal(order.row_of_slot, again.row_of_slot)
+    x = torch.randn(H, T, device=dev).to(torch.bfloat16).t()
+    w = torch.rand(K, T, device=dev).t()
+    rows, _ = buf.expert_sort(x, order)
+    want, _ = buf.expert_sort(x.contiguous(), order)
+    n = int(order.expert_offsets[-1])
+    assert torch.equal(rows[:n], want[:n])
+    out, _ = buf.expert_unsort(rows, order, w)
+    want, _ = buf.expert_unsort(rows, order, w.contiguous())
+    assert torch.equal(out, want)
+
+
 def test_refusals():
     from combine_get_dispatch_layout_amd import ExpertOrder
     from combine_get_dispatch_layout_amd import _capi as C
@@ -240,6 +262,8 @@ def test_refusals():
     big = [(1 << 26, 1, 8), (1 << 22, 16, 8), (1 << 24, 4, 4096)]
     for f in [lambda: buf.expert_sort(flat[:4], order, out=flat[3:11]),
               lambda: buf.expert_unsort(flat[:8], order, out=flat[7:11]),
+              lambda: buf.expert_sort(flat.view(-1)[1:65].view(4, 16), order),
+              lambda: buf.expert_unsort(flat.view(-1)[1:129].view(8, 16), order),
               lambda: buf.expert_unsort_backward(flat[:4], x.repeat(2, 1), order,
                                                  torch.zeros(4, 2, device=dev), out=flat[2:10]),
               lambda: buf.expert_unsort_backward(x, flat[:8], order,
