@@ -635,11 +635,12 @@ class Buffer:
         read on the host."""
         topk_idx = self._check("topk_idx", topk_idx, (torch.int64,), (None, None))
         T, K = topk_idx.shape
-        if self._order_size[:2] != (T, K):
+        size = self._order_size  # read once: another thread may replace it
+        if size[:2] != (T, K):
             nbytes = ctypes.c_size_t()
             C.check(C.moedx_expert_order_workspace_bytes(self.ctx, T, K, ctypes.byref(nbytes)))
-            self._order_size = (T, K, nbytes.value)
-        nbytes = self._order_size[2]
+            size = self._order_size = (T, K, nbytes.value)
+        nbytes = size[2]
         dev = self._torch_device
         offsets = torch.empty(self.num_experts + 1, dtype=torch.int32, device=dev)
         row_of_slot = torch.empty(T, K, dtype=torch.int32, device=dev)

@@ -226,6 +226,39 @@ def test_two_streams_at_once():
             assert torch.equal(out, want[i])
 
 
+def test_threads_share_a_buffer():
+    """Host threads ordering batches of different sizes on one Buffer, each on a
+    stream of its own."""
+    import threading
+    dev = device()
+    w1, w2 = weights(dev)
+    buf = make_buffer(E, 1, 1, 4096)
+    sizes = [64, 203, 1500, 3000]
+    ins = [inputs(dev, 70 + i, n) for i, n in enumerate(sizes)]
+    want = [on_tokens(buf, x, l, w1, w2)[-1] for x, l in ins]
+    torch.cuda.synchronize()
+    got, errors = [None] * len(ins), []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(5):
+                    got[i] = on_tokens(buf, *ins[i], w1, w2, no_sync=True)[-1]
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(ins))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_readme_example():
     """The README's example as written: the layer through the dispatch and in the
     decode slots gives the layer on the tokens, each rounded a few times."""
