@@ -5,7 +5,9 @@
 // bias.  With groups (contiguous, E / G experts), a group's score is the sum
 // of its two best keys and only the groups_kept best groups keep their
 // experts.  The K best keys are chosen, ties to the lower index.  An expert
-// whose logit is -inf or NaN is never chosen and has p = 0.
+// whose logit is -inf or NaN is never chosen and has p = 0.  A logit of +inf
+// makes a softmax's weights NaN; the choice is that of the limit, where the
+// experts with +inf share p = 1.
 //
 // The chosen set must not depend on how exp rounds: two keys that differ by
 // less than an fp32 rounding are common among 10^6 scores.  So keys are fp64
@@ -220,7 +222,10 @@ __global__ __launch_bounds__(kGateThreads) void gate_topk_kernel(GateArgs a, boo
             double z = 0.0;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                s[j] = l[j] > kNegInf ? exp((double)l[j] - (double)m) : 0.0;
+                // 1 at the maximum, also where it is +inf: the others are 0 then
+                s[j] = !(l[j] > kNegInf) ? 0.0
+                       : l[j] == m       ? 1.0
+                                         : exp((double)l[j] - (double)m);
                 z += s[j];
             }
             z = wave_sum(z);
@@ -271,6 +276,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_topk_kernel(GateArgs a, boo
     float w = 0.0f;
     if (a.renormalize) {
         w = row_share(have, softmax, mine_l);  // the choices are in the first row
+        if (m == INFINITY) w = NAN;  // a softmax with +inf, whether that was chosen or not
     } else if (softmax) {
         const float z = exp_sum(l, m);
         w = have ? expf(mine_l - m) / z : 0.0f;

@@ -458,8 +458,10 @@ typedef struct moedx_gate {
  * type `dtype`.  The choice is exact: keys are compared in fp64 where they go
  * through exp.  An expert whose logit is -inf or NaN, or whose key is, is
  * never chosen and counts 0 in a softmax; where fewer than K experts can be
- * chosen, the remaining slots are -1 with weight 0.  A logit of +inf makes a
- * softmax's weights NaN.
+ * chosen, the remaining slots are -1 with weight 0.  A logit of +inf makes
+ * all weights of its token's softmax NaN, renormalised or not; the choice is
+ * that of the limit: experts with +inf share a score of 1, the others have 0
+ * (without bias and groups they follow in the order of their logits).
  * T in [0, 2^24], K in [1, min(16, E)].  logits aligned to their type. */
 MOEDX_API int moedx_gate_topk(moedx_ctx *ctx, const void *logits, int dtype, int T, int K,
                               const moedx_gate *gate, int64_t *topk_idx, float *topk_weights,
@@ -467,7 +469,9 @@ MOEDX_API int moedx_gate_topk(moedx_ctx *ctx, const void *logits, int dtype, int
 
 /* d_logits [T, E] (of type `dtype`) from d_topk_weights fp32 [T, K], for the
  * choice topk_idx that moedx_gate_topk made of the same logits with the same
- * options.  The choice itself has no gradient; empty slots add nothing. */
+ * options.  The choice itself has no gradient; empty slots add nothing.  With
+ * renormalize a softmax is that of the chosen logits alone: +inf makes NaN
+ * where it was chosen. */
 MOEDX_API int moedx_gate_topk_backward(moedx_ctx *ctx, const void *logits, int dtype, int T, int K,
                                        const moedx_gate *gate, const int64_t *topk_idx,
                                        const float *d_topk_weights, void *d_logits,

@@ -226,3 +226,73 @@ def test_gate_empty_batch_and_refusals():
         buf.gate_topk_backward(w[:2], x, idx)
     with pytest.raises(ValueError):
         buf.gate_topk_backward(w, x, idx.int())
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16, torch.float16], ids=lambda d: str(d)[6:])
+@pytest.mark.parametrize("renorm", [False, True], ids=["plain", "renorm"])
+@pytest.mark.parametrize("form", ["logits", "bias", "groups", "odd groups", "groups and bias"])
+@pytest.mark.parametrize("E", [60, 512])
+def test_gate_infinite_logits(E, form, renorm, dt):
+    """A logit of +inf: the softmax scores are those of the limit (the experts
+    with +inf share 1, the others have 0) where they choose, and the token's
+    weights are NaN; sigmoid scores are 1.  Other tokens see nothing of it."""
+    dev = device()
+    K, groups, kept = 4, 1, 1
+    if "groups" in form:
+        groups, kept = (E // 5, 3) if form == "odd groups" and E == 60 else (4, 2)
+    inf = float("inf")
+    g = torch.Generator().manual_seed(3)
+    plain = torch.randn(E, generator=g) * 2.0
+    rows = [plain.clone() for _ in range(6)]
+    rows[0][5] = inf
+    rows[1][[3, 40]] = inf
+    rows[2][:] = inf
+    rows[4][:] = -inf  # three candidates only
+    rows[4][[7, 2, 50]] = torch.tensor([inf, 0.5, 1.5])
+    rows[5][20] = inf  # the bias keeps it from being chosen
+    logits = torch.stack(rows).to(dt)
+    bias = None
+    if "bias" in form:
+        bias = torch.randn(E, generator=g) * 0.2
+        bias[20] = -30.0
+    opts = dict(num_groups=groups, groups_kept=kept, renormalize=renorm, scale=1.5)
+    buf = make_buffer(E, 1, 1, 6)
+    bd = None if bias is None else bias.to(dev)
+    print(f"[gate] infinite logits {E} {form} {renorm} {dt}", flush=True)
+    idx, w, _ = buf.gate_topk(logits.to(dev), K, score="softmax", bias=bd, **opts)
+    d, _ = buf.gate_topk_backward(torch.ones(6, K, device=dev), logits.to(dev), idx,
+                                  score="softmax", bias=bd, **opts)
+    idx, w, d = idx.cpu(), w.cpu(), d.cpu()
+    l = logits.double()
+    for t in range(6):
+        if t == 3:
+            continue
+        ok, top = l[t] > -inf, l[t] == inf
+        p = top.double() / top.sum()
+        key = l[t] if form == "logits" else p if bias is None else p + bias.double()
+        cand = [e for e in range(E) if ok[e]]
+        if groups > 1:
+            per = E // groups
+            sums = []
+            for q in range(groups):
+                best = sorted((float(key[e]) for e in cand if e // per == q), reverse=True)[:2]
+                sums.append(sum(best) if best else -inf)
+            keep = sorted(range(groups), key=lambda q: (-sums[q], q))[:kept]
+            cand = [e for e in cand if e // per in keep]
+        cand = sorted(cand, key=lambda e: (-float(key[e]), e))[:K]
+        n = len(cand)
+        assert idx[t].tolist() == cand + [-1] * (K - n), t
+        assert torch.isnan(w[t, :n]).all() and (w[t, n:] == 0).all(), t
+        # the gradient of plain scores is NaN for every candidate, that of
+        # renormalised ones where one with +inf was chosen
+        if not renorm:
+            assert torch.isnan(d[t][ok]).all() and (d[t][~ok] == 0).all(), t
+        elif top[cand].any():
+            assert torch.isnan(d[t, cand]).all(), t
+    alone = [v.cpu() for v in buf.gate_topk(logits[3:4].to(dev), K, score="softmax", bias=bd, **opts)[:2]]
+    assert torch.equal(idx[3:4], alone[0]) and torch.equal(w[3:4], alone[1])
+    assert torch.isfinite(w[3]).all() and torch.isfinite(d[3]).all()
+    idx, w, _ = buf.gate_topk(logits.to(dev), K, score="sigmoid", bias=bd, **opts)
+    want_idx, want_w, _ = reference(logits, K, "sigmoid", groups, kept, renorm, 1.5, bias)
+    assert torch.equal(idx.cpu(), want_idx)
+    assert ((w.cpu().double() - want_w).abs() <= 64 * U * want_w).all()
