@@ -314,8 +314,9 @@ __global__ __launch_bounds__(kRowThreads) void expert_unsort_backward_kernel(
     const int r = row_wave();
     if (r >= n_rows) return;
     const int lane = threadIdx.x & 63;
-    // pair r, if its slot is empty, has no row to get its gradient from
-    if (lane == 0 && row_of_slot[r] < 0) d_weights[r] = 0.0f;
+    // pair r, if its slot is empty (or its row outside), has no row to get its
+    // gradient from
+    if (lane == 0 && (uint32_t)row_of_slot[r] >= (uint32_t)n_rows) d_weights[r] = 0.0f;
     const int slot = slot_of_row[r];
     if (slot < 0 || slot >= n_rows) return;
     const float w = weights[slot];

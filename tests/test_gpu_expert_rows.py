@@ -282,3 +282,36 @@ def test_refusals():
     with pytest.raises(C.MoedxError) as e:
         buf.expert_order(idx, handle=ll)
     assert e.value.code == C.MOEDX_EINVAL
+
+
+def test_gradients_with_index_outside():
+    """A row index outside [0, T * K) is an empty slot for every call: its
+    weight's gradient is zero."""
+    import ctypes
+
+    from combine_get_dispatch_layout_amd import _capi as C
+    dev = device()
+    T, E, K, H = 9, 4, 3, 40
+    buf = make_buffer(E, 1, 1, T)
+    order, _ = buf.expert_order(routing("full", T, E, K, 11).to(dev))
+    ros, sor = order.row_of_slot.clone(), order.slot_of_row.clone()
+    outside = {5: T * K, 11: (1 << 31) - 1, 20: -9}
+    for slot, row in outside.items():
+        sor[ros.view(-1)[slot].long()] = -1
+        ros.view(-1)[slot] = row
+    y, d_out = torch.randn(T * K, H, device=dev), torch.randn(T, H, device=dev)
+    w = torch.rand(T, K, device=dev)
+    d_rows, d_w = torch.full_like(y, 7.0), torch.full_like(w, 7.0)
+    ex = C.moedx_exec(stream=torch.cuda.current_stream().cuda_stream)
+    C.check(C.moedx_expert_unsort_backward(
+        buf.ctx, d_out.data_ptr(), y.data_ptr(), C.MOEDX_F32, T, K, H, ros.data_ptr(), sor.data_ptr(),
+        w.data_ptr(), d_rows.data_ptr(), d_w.data_ptr(), ctypes.byref(ex)))
+    torch.cuda.synchronize()
+    want_rows, want_w, _ = buf.expert_unsort_backward(d_out, y, order, w)
+    for slot in range(T * K):
+        row = int(order.row_of_slot.view(-1)[slot])
+        if slot in outside:
+            assert float(d_w.view(-1)[slot]) == 0.0 and (d_rows[row] == 7.0).all()
+        else:
+            assert torch.equal(d_w.view(-1)[slot], want_w.view(-1)[slot])
+            assert torch.equal(d_rows[row], want_rows[row])
