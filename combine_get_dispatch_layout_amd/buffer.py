@@ -45,6 +45,17 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _contiguous(t: Optional[torch.Tensor], previous_event) -> Optional[torch.Tensor]:
+    """`t`, or its contiguous copy, which is made on the current stream of t's
+    device: like the call it is for, behind `previous_event` (the call's own
+    wait comes later, and may be another stream's)."""
+    if t is None or t.is_contiguous():
+        return t
+    if previous_event is not None and previous_event.event is not None:
+        C.check(C.moedx_event_wait(previous_event.event, _raw_stream(t.get_device())))
+    return t.contiguous()
+
+
 # Releases that must wait until no stream capture is running.  Destroying a
 # context synchronises its stream and frees device and pinned memory, and an
 # event destroy is not a capturable call either; any of them during a capture
@@ -288,7 +299,7 @@ class Buffer:
         which do not exist on one GPU.  ``no_sync`` returns without blocking
         (stream order only), as under graph capture."""
         assert num_experts == self.num_experts
-        topk_idx = topk_idx.contiguous()
+        topk_idx = _contiguous(topk_idx, previous_event)
         T, K = topk_idx.shape
         dev = topk_idx.device
         ntr = torch.empty(self.num_ranks, dtype=torch.int32, device=dev)
@@ -311,7 +322,7 @@ class Buffer:
         get_dispatch_layout's ``is_token_in_rank`` and ``num_tokens_per_expert``
         (and optionally ``num_tokens_per_rank``), no layout runs: the handle is
         scanned from them."""
-        topk_idx = topk_idx.contiguous()
+        topk_idx = _contiguous(topk_idx, previous_event)
         T, K = topk_idx.shape
         from_layout = is_token_in_rank is not None or num_tokens_per_expert is not None
         if from_layout:
@@ -321,11 +332,11 @@ class Buffer:
             assert is_token_in_rank.dtype in (torch.bool, torch.uint8)
             assert tuple(num_tokens_per_expert.shape) == (self.num_experts,)
             assert num_tokens_per_expert.dtype == torch.int32
-            is_token_in_rank = is_token_in_rank.contiguous()
-            num_tokens_per_expert = num_tokens_per_expert.contiguous()
+            is_token_in_rank = _contiguous(is_token_in_rank, previous_event)
+            num_tokens_per_expert = _contiguous(num_tokens_per_expert, previous_event)
             if num_tokens_per_rank is not None:
                 assert tuple(num_tokens_per_rank.shape) == (self.num_ranks,)
-                num_tokens_per_rank = num_tokens_per_rank.contiguous()
+                num_tokens_per_rank = _contiguous(num_tokens_per_rank, previous_event)
         else:
             num_tokens_per_rank = None
         nbytes = ctypes.c_size_t()
@@ -365,14 +376,15 @@ class Buffer:
         x_scales = None
         if prequant:
             x, x_scales = x
-            x_scales = x_scales.contiguous() if x_scales is not None else None
+            x_scales = _contiguous(x_scales, previous_event)
             fp8 = True
         assert not (use_ue8m0 and fp8_quant_scale is not None), \
             "fp8_quant_scale and use_ue8m0 are exclusive"
         fp8 = fp8 or round_scale or use_ue8m0 or fp8_quant_scale is not None
-        x = x.contiguous()
+        x = _contiguous(x, previous_event)
         T, H = x.shape
         first = handle is None
+        inputs_ready = previous_event
         if first:
             assert topk_idx is not None, "a first dispatch needs topk_idx"
             reuse = is_token_in_rank is not None and num_tokens_per_expert is not None
@@ -416,8 +428,8 @@ class Buffer:
             C.check(C.moedx_dispatch_fp8(self.ctx, handle.ptr, _ptr(x), T, H, ctypes.byref(opts),
                                          _ptr(recv_x), _ptr(recv_s), ctypes.byref(ex)))
         else:
-            tw = topk_weights.contiguous() if topk_weights is not None else None
-            ti = topk_idx.contiguous() if (first and not fp8) else None
+            tw = _contiguous(topk_weights, inputs_ready)
+            ti = _contiguous(topk_idx, inputs_ready) if (first and not fp8) else None
             C.check(C.moedx_dispatch(self.ctx, handle.ptr, _ptr(x), T, H,
                                      C.MOEDX_QUANT_FP8_E4M3_1X128 if fp8 else C.MOEDX_QUANT_NONE,
                                      _ptr(ti), _ptr(tw if (first and not fp8) else None),
@@ -446,14 +458,14 @@ class Buffer:
         is the per-row weight payload ([rows, K]) reduced like the rows;
         ``gate_weights`` ([T, K]) scales each bucket's row by its summed gate
         weight."""
-        x = x.contiguous()
+        x = _contiguous(x, previous_event)
         H = x.shape[1]
         T, K = handle.T, handle.K
         combined = out if out is not None else torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
         cw = torch.empty(T, K, dtype=torch.float32, device=x.device) if topk_weights is not None else None
         ex, done = self._exec(previous_event, async_finish, allocate_on_comm_stream, no_sync)
-        gw = gate_weights.contiguous() if gate_weights is not None else None
-        tw = topk_weights.contiguous() if topk_weights is not None else None
+        gw = _contiguous(gate_weights, previous_event)
+        tw = _contiguous(topk_weights, previous_event)
         C.check(C.moedx_combine(self.ctx, handle.ptr, _ptr(x), H, _ptr(gw), _ptr(tw),
                                 _ptr(combined), _ptr(cw), ctypes.byref(ex)))
         self._keep(allocate_on_comm_stream, x, gw, tw, combined, cw)
@@ -469,8 +481,8 @@ class Buffer:
         the rows arrive when hook() runs (a second kernel launch on the
         current stream); otherwise hook is None."""
         assert num_experts == self.num_experts
-        x = x.contiguous()
-        topk_idx = topk_idx.contiguous()
+        x = _contiguous(x, previous_event)
+        topk_idx = _contiguous(topk_idx, previous_event)
         T, H = x.shape
         K = topk_idx.shape[1]
         cap = num_max_dispatch_tokens_per_rank
@@ -501,11 +513,12 @@ class Buffer:
         """Returns (combined [T, H] bf16, event, hook).  With return_recv_hook
         the reduction runs when hook() is called (on the current stream) and
         event is None; otherwise hook is None."""
-        x = x.contiguous()
+        x = _contiguous(x, previous_event)
         H = x.shape[-1]
         T = handle.T
         combined = out if out is not None else torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
-        ti, tw = topk_idx.contiguous(), topk_weights.contiguous()
+        ti = _contiguous(topk_idx, previous_event)
+        tw = _contiguous(topk_weights, previous_event)
 
         def run(ex):
             C.check(C.moedx_ll_combine(self.ctx, _ptr(x), _ptr(ti), _ptr(tw), handle.ptr, H,
@@ -522,9 +535,9 @@ class Buffer:
         return combined, self._event(done), None
 
     # -- router, rows in expert order, the experts' products -----------------------
-    def _check(self, name: str, t, dtypes, shape) -> torch.Tensor:
+    def _check(self, name: str, t, dtypes, shape, previous_event=None) -> torch.Tensor:
         """`t` is a tensor on this Buffer's device, of one of `dtypes` and of
-        `shape` (None = any size); made contiguous."""
+        `shape` (None = any size); made contiguous behind `previous_event`."""
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a tensor")
         if not t.is_cuda or t.get_device() != self._index:
@@ -539,15 +552,15 @@ class Buffer:
                     bad = True
         if bad:
             raise ValueError(f"{name} has shape {tuple(got)}, expected {tuple(shape)}")
-        return t if t.is_contiguous() else t.contiguous()
+        return _contiguous(t, previous_event)
 
     def _out(self, name: str, out, dtype, shape) -> torch.Tensor:
         """`out` checked (it must be contiguous), or a new tensor."""
         if out is None:
             return torch.empty(shape, dtype=dtype, device=self._torch_device)
-        if self._check(name, out, (dtype,), shape) is not out:
+        if isinstance(out, torch.Tensor) and not out.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        return out
+        return self._check(name, out, (dtype,), shape)
 
     def _exec_here(self, previous_event, async_finish, allocate_on_comm_stream, no_sync):
         """As _exec, on the current stream of this Buffer's device."""
@@ -565,11 +578,12 @@ class Buffer:
             ex.done = ctypes.addressof(done)
         return ex, done
 
-    def _gate_options(self, score, num_groups, groups_kept, renormalize, scale, bias):
+    def _gate_options(self, score, num_groups, groups_kept, renormalize, scale, bias,
+                      previous_event):
         if score not in _SCORES:
             raise ValueError(f"score={score!r} must be one of {sorted(_SCORES)}")
         if bias is not None:
-            bias = self._check("bias", bias, (torch.float32,), (self.num_experts,))
+            bias = self._check("bias", bias, (torch.float32,), (self.num_experts,), previous_event)
         return C.moedx_gate(_SCORES[score], num_groups,
                             num_groups if groups_kept is None else groups_kept,
                             1 if renormalize else 0, scale, _addr(bias)), bias
@@ -589,9 +603,10 @@ class Buffer:
         chosen scores by their sum; ``scale`` multiplies the weights.  Experts
         with a logit of -inf or NaN are never chosen; slots that stay empty
         are -1 with weight 0."""
-        logits = self._check("logits", logits, _DTYPES, (None, self.num_experts))
+        logits = self._check("logits", logits, _DTYPES, (None, self.num_experts), previous_event)
         T = logits.shape[0]
-        opts, bias = self._gate_options(score, num_groups, groups_kept, renormalize, scale, bias)
+        opts, bias = self._gate_options(score, num_groups, groups_kept, renormalize, scale, bias,
+                                        previous_event)
         dev = self._torch_device
         idx = torch.empty(T, max(topk, 0), dtype=torch.int64, device=dev)
         w = torch.empty(T, max(topk, 0), dtype=torch.float32, device=dev)
@@ -611,12 +626,13 @@ class Buffer:
         """Returns (d_logits [T, E] of the logits' dtype, event): the gradient
         of gate_topk's weights for its choice ``topk_idx`` with the same
         options (the choice, and so ``bias``, has no gradient)."""
-        logits = self._check("logits", logits, _DTYPES, (None, self.num_experts))
+        logits = self._check("logits", logits, _DTYPES, (None, self.num_experts), previous_event)
         T = logits.shape[0]
-        topk_idx = self._check("topk_idx", topk_idx, (torch.int64,), (T, None))
+        topk_idx = self._check("topk_idx", topk_idx, (torch.int64,), (T, None), previous_event)
         K = topk_idx.shape[1]
-        dw = self._check("d_topk_weights", d_topk_weights, (torch.float32,), (T, K))
-        opts, bias = self._gate_options(score, num_groups, groups_kept, renormalize, scale, bias)
+        dw = self._check("d_topk_weights", d_topk_weights, (torch.float32,), (T, K), previous_event)
+        opts, bias = self._gate_options(score, num_groups, groups_kept, renormalize, scale, bias,
+                                        previous_event)
         d = torch.empty_like(logits)
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
         C.check(C.moedx_gate_topk_backward(self.ctx, _addr(logits), _DTYPES[logits.dtype], T, K,
@@ -633,7 +649,7 @@ class Buffer:
         ``handle``, ``topk_idx`` is the recv_topk_idx of its first dispatch
         (ids local to the row's bucket; rows past N are empty).  Nothing is
         read on the host."""
-        topk_idx = self._check("topk_idx", topk_idx, (torch.int64,), (None, None))
+        topk_idx = self._check("topk_idx", topk_idx, (torch.int64,), (None, None), previous_event)
         T, K = topk_idx.shape
         size = self._order_size  # read once: another thread may replace it
         if size[:2] != (T, K):
@@ -662,9 +678,9 @@ class Buffer:
         [T, H] (bf16, fp16 or fp32) in expert order.  Rows past the last pair
         are left as they were (unspecified without ``out``)."""
         T, K = order.row_of_slot.shape
-        x = self._check("x", x, _DTYPES, (T, None))
+        x = self._check("x", x, _DTYPES, (T, None), previous_event)
         H = x.shape[1]
-        ros = self._check("row_of_slot", order.row_of_slot, (torch.int32,), (T, K))
+        ros = self._check("row_of_slot", order.row_of_slot, (torch.int32,), (T, K), previous_event)
         rows = self._out("out", out, x.dtype, (T * K, H))
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
         C.check(C.moedx_expert_sort(self.ctx, _addr(x), _DTYPES[x.dtype], T, K, H, _addr(ros),
@@ -681,11 +697,11 @@ class Buffer:
         order, scaled by ``topk_weights`` [T, K] fp32 (None = 1) and summed in
         fp32 over its filled slots; zero for a token without any."""
         T, K = order.row_of_slot.shape
-        rows = self._check("rows", rows, _DTYPES, (T * K, None))
+        rows = self._check("rows", rows, _DTYPES, (T * K, None), previous_event)
         H = rows.shape[1]
-        ros = self._check("row_of_slot", order.row_of_slot, (torch.int32,), (T, K))
-        w = None if topk_weights is None else self._check("topk_weights", topk_weights,
-                                                          (torch.float32,), (T, K))
+        ros = self._check("row_of_slot", order.row_of_slot, (torch.int32,), (T, K), previous_event)
+        w = None if topk_weights is None else self._check(
+            "topk_weights", topk_weights, (torch.float32,), (T, K), previous_event)
         out = self._out("out", out, rows.dtype, (T, H))
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
         C.check(C.moedx_expert_unsort(self.ctx, _addr(rows), _DTYPES[rows.dtype], T, K, H,
@@ -712,12 +728,12 @@ class Buffer:
         gradients of expert_unsort.  ``out``: where d_rows goes; rows past the
         last pair are left as they were."""
         T, K = order.row_of_slot.shape
-        rows = self._check("rows", rows, _DTYPES, (T * K, None))
+        rows = self._check("rows", rows, _DTYPES, (T * K, None), previous_event)
         H = rows.shape[1]
-        d_out = self._check("d_out", d_out, (rows.dtype,), (T, H))
-        ros = self._check("row_of_slot", order.row_of_slot, (torch.int32,), (T, K))
-        sor = self._check("slot_of_row", order.slot_of_row, (torch.int32,), (T * K,))
-        w = self._check("topk_weights", topk_weights, (torch.float32,), (T, K))
+        d_out = self._check("d_out", d_out, (rows.dtype,), (T, H), previous_event)
+        ros = self._check("row_of_slot", order.row_of_slot, (torch.int32,), (T, K), previous_event)
+        sor = self._check("slot_of_row", order.slot_of_row, (torch.int32,), (T * K,), previous_event)
+        w = self._check("topk_weights", topk_weights, (torch.float32,), (T, K), previous_event)
         d_rows = self._out("out", out, rows.dtype, (T * K, H))
         d_w = torch.empty(T, K, dtype=torch.float32, device=rows.device)
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
@@ -728,15 +744,15 @@ class Buffer:
         self._keep(allocate_on_comm_stream, d_out, rows, ros, sor, w, d_rows, d_w)
         return d_rows, d_w, self._event(done)
 
-    def _expert_rows(self, rows, x: torch.Tensor):
+    def _expert_rows(self, rows, x: torch.Tensor, previous_event):
         """The moedx_expert_rows of x's leading dimensions: an ExpertOrder or
         int32 offsets [E + 1] for [M, *], int32 counts [E] for [E, cap, *]."""
         E = self.num_experts
         t = rows.expert_offsets if isinstance(rows, ExpertOrder) else rows
         if x.dim() == 3:
-            t = self._check("recv_count", t, (torch.int32,), (E,))
+            t = self._check("recv_count", t, (torch.int32,), (E,), previous_event)
             return C.moedx_expert_rows(None, _addr(t), x.shape[0] * x.shape[1]), t
-        t = self._check("expert_offsets", t, (torch.int32,), (E + 1,))
+        t = self._check("expert_offsets", t, (torch.int32,), (E + 1,), previous_event)
         return C.moedx_expert_rows(_addr(t), None, x.shape[0]), t
 
     def _lead(self, name: str, x) -> tuple:
@@ -761,9 +777,9 @@ class Buffer:
         is None.  Rows of no expert are left as they were (unspecified without
         ``out``)."""
         lead = self._lead("x", x)
-        x = self._check("x", x, _PRODUCT_DTYPES, lead + (None,))
+        x = self._check("x", x, _PRODUCT_DTYPES, lead + (None,), previous_event)
         K = x.shape[-1]
-        w = self._check("w", w, (x.dtype,), (self.num_experts, None, K))
+        w = self._check("w", w, (x.dtype,), (self.num_experts, None, K), previous_event)
         N = w.shape[1]
         if swiglu:
             if N % 2 != 0:
@@ -771,7 +787,7 @@ class Buffer:
             N //= 2
         elif return_pre:
             raise ValueError("return_pre needs swiglu")
-        er, t = self._expert_rows(rows, x)
+        er, t = self._expert_rows(rows, x, previous_event)
         y = self._out("out", out, x.dtype, lead + (N,))
         pre = torch.empty(lead + (2 * N,), dtype=x.dtype, device=x.device) if return_pre else None
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
@@ -793,16 +809,16 @@ class Buffer:
         (zero without any), written to ``d_w`` (of w's dtype or fp32) or to a
         new tensor of ``d_w_dtype`` (w's dtype by default)."""
         lead = self._lead("x", x)
-        x = self._check("x", x, _PRODUCT_DTYPES, lead + (None,))
+        x = self._check("x", x, _PRODUCT_DTYPES, lead + (None,), previous_event)
         K = x.shape[-1]
-        w = self._check("w", w, (x.dtype,), (self.num_experts, None, K))
+        w = self._check("w", w, (x.dtype,), (self.num_experts, None, K), previous_event)
         N = w.shape[1]
-        d_y = self._check("d_y", d_y, (x.dtype,), lead + (N,))
+        d_y = self._check("d_y", d_y, (x.dtype,), lead + (N,), previous_event)
         if d_w_dtype is None:
             d_w_dtype = x.dtype if d_w is None else d_w.dtype
         if d_w_dtype not in (x.dtype, torch.float32):
             raise ValueError(f"d_w_dtype={d_w_dtype} must be {x.dtype} or torch.float32")
-        er, t = self._expert_rows(rows, x)
+        er, t = self._expert_rows(rows, x, previous_event)
         d_x = self._out("out", out, x.dtype, lead + (K,))
         d_w = self._out("d_w", d_w, d_w_dtype, (self.num_experts, N, K))
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
@@ -821,10 +837,10 @@ class Buffer:
         swiglu at ``pre`` = (gate, up) for ``d_h`` [*, N]; expert_linear_backward
         takes d_pre as its d_y.  Rows of no expert are left as they were."""
         lead = self._lead("d_h", d_h)
-        d_h = self._check("d_h", d_h, _PRODUCT_DTYPES, lead + (None,))
+        d_h = self._check("d_h", d_h, _PRODUCT_DTYPES, lead + (None,), previous_event)
         N = d_h.shape[-1]
-        pre = self._check("pre", pre, (d_h.dtype,), lead + (2 * N,))
-        er, t = self._expert_rows(rows, d_h)
+        pre = self._check("pre", pre, (d_h.dtype,), lead + (2 * N,), previous_event)
+        er, t = self._expert_rows(rows, d_h, previous_event)
         d_pre = self._out("out", out, d_h.dtype, lead + (2 * N,))
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
         C.check(C.moedx_expert_swiglu_backward(self.ctx, _addr(d_h), _addr(pre), _DTYPES[d_h.dtype],
