@@ -1345,6 +1345,12 @@ ExpertRows expert_rows(const moedx_ctx* ctx, const moedx_expert_rows* er) {
                       er->rows};
 }
 
+int check_grid(bool fits, const moedx_expert_rows* er, int K, int N) {
+    if (fits) return MOEDX_OK;
+    return fail(MOEDX_EINVAL, "rows=%lld with K=%d, N=%d take more workgroups than a grid has",
+                (long long)er->rows, K, N);
+}
+
 }  // namespace
 
 int moedx_gate_topk(moedx_ctx* ctx, const void* logits, int dtype, int T, int K,
@@ -1521,6 +1527,9 @@ int moedx_expert_linear(moedx_ctx* ctx, const void* x, const void* w, int dtype,
     if (int rc = check_ctx(ctx)) return rc;
     if (swiglu != 0 && swiglu != 1) return fail(MOEDX_EINVAL, "swiglu=%d must be 0 or 1", swiglu);
     if (int rc = check_products(ctx, dtype, K, N, swiglu ? 2 : 1, er)) return rc;
+    if (int rc = check_grid(
+            forward_tiles(expert_rows(ctx, er), swiglu ? 2 * N : N) != Tiles::kNone, er, K, N))
+        return rc;
     if (pre && !swiglu) return fail(MOEDX_EINVAL, "pre is only produced with swiglu");
     if (er->rows > 0 && (!x || !w || !y)) return fail(MOEDX_EINVAL, "NULL device pointer");
     if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(pre))
@@ -1548,6 +1557,12 @@ int moedx_expert_linear_backward(moedx_ctx* ctx, const void* d_y, const void* x,
     if (d_w && d_w_dtype != dtype && d_w_dtype != MOEDX_F32)
         return fail(MOEDX_EINVAL, "d_w_dtype=%d must be the dtype or MOEDX_F32", d_w_dtype);
     if (!d_x && !d_w) return fail(MOEDX_EINVAL, "neither d_x nor d_w is asked for");
+    const ExpertRows rows = expert_rows(ctx, er);
+    if (int rc = check_grid(!d_x || input_gradient_tiles(rows, K) != Tiles::kNone, er, K, N))
+        return rc;
+    if (int rc = check_grid(!d_w || grid_fits(weight_workgroups(rows, K, N), kWeightTile.threads),
+                            er, K, N))
+        return rc;
     if (er->rows > 0 && (!d_y || (d_x && !w) || (d_w && !x)))
         return fail(MOEDX_EINVAL, "NULL device pointer");
     if (!aligned16(d_y) || !aligned16(x) || !aligned16(w) || !aligned16(d_x) || !aligned16(d_w))
@@ -1560,7 +1575,6 @@ int moedx_expert_linear_backward(moedx_ctx* ctx, const void* d_y, const void* x,
     DeviceScope scope;
     Exec ex;
     if (int rc = exec_begin(ctx, exec, &ex)) return rc;
-    const ExpertRows rows = expert_rows(ctx, er);
     const bool dx = d_x && er->rows > 0;
     if (!dx && !d_w) HIP_OR_FAIL(ex.no_kernel());
     if (dx)

@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "expert_plan.h"
 #include "launch.h"
 
 namespace moedx {
@@ -74,16 +75,6 @@ hipError_t launch_expert_unsort_backward(const void* d_out, const void* rows, in
                                          void* d_rows, float* d_weights, const Launch& L);
 
 // ---- the experts' products ----------------------------------------------------
-
-// Which rows belong to an expert: [offsets[e], offsets[e + 1]), or, with
-// offsets null, the first counts[e] of the cap rows from e * cap.
-struct ExpertRows {
-    const int32_t* offsets;
-    const int32_t* counts;
-    int cap;
-    int E;
-    int64_t rows;  // rows of the buffers; nothing at or past it is touched
-};
 
 // y [rows, N] = x [rows, K] w[e]^T, w [E, N, K]; with swiglu w is [E, 2N, K]
 // (gate rows, then up rows), y = silu(gate) * up and pre (or null) receives

@@ -22,12 +22,20 @@ struct Shape {
     static constexpr int kP = kP_, kQ = kQ_;  // stages of either operand in LDS
     static constexpr int kWaves = WP * WQ, kThreads = kWaves * 64;
     static constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;
+    static constexpr TileShape kTile{BQ, BP, kThreads};
     static __device__ __forceinline__ int p_at(int wp, int i) { return p_block<BP, WP>(wp, i); }
     static __device__ __forceinline__ int q_at(int wq, int j) { return q_block<WQ>(wq, j); }
 };
 typedef Shape<256, 256, 4, 64, 3, 2> Wide;
 typedef Shape<256, 128, 2, 32, 3, 3> Narrow;
 typedef Shape<128, 128, 2, 64, 2, 2> Small;
+
+constexpr bool same(const TileShape& a, const TileShape& b) {
+    return a.rows == b.rows && a.outs == b.outs && a.threads == b.threads;
+}
+static_assert(same(Wide::kTile, kWideTile) && same(Small::kTile, kSmallTile) &&
+                  same(Narrow::kTile, kWeightTile),
+              "the plan's tiles are the kernels'");
 
 constexpr int kRunLog2 = 5;  // an XCD takes runs of 32 tiles: one per CU, sharing operands in its L2
 constexpr int kRowGroup = 8;  // row tiles that go through the columns together
@@ -174,6 +182,7 @@ constexpr int kFewP = 2;  // blocks of 16 weight rows
 constexpr int kFewRows = 32, kFewBlocks = kFewRows / 16, kFewWaves = 4, kFewThreads = kFewWaves * 64,
               kFewStep = 128 * kFewWaves;
 constexpr int kFewRunLog2 = 3;
+static_assert(same({kFewRows, kFewP * 16, kFewThreads}, kFewTile), "the plan's tile is the kernel's");
 
 // 16 rows of an operand along r, read by the whole wave: lane l takes row
 // l & 15, reduction values 8 (l >> 4) .. + 7 of each 32; zeros outside.
@@ -431,48 +440,15 @@ __global__ __launch_bounds__(kActThreads) void swiglu_backward_kernel(
     }
 }
 
-int tiles_of(int n, int b) { return (n + b - 1) / b; }
-
-// A grid of so many workgroups; more than HIP takes fails at the launch.
-dim3 grid_of(int64_t workgroups) {
-    return dim3((unsigned)(workgroups < UINT32_MAX ? workgroups : UINT32_MAX));
-}
-
-// Rows an expert is likely to have, from what the host knows.  A capacity
-// buffer holds at most cap tokens, each with a few experts: 8 are taken, the
-// top-k of the wide routings (more only moves where the kernels change).
-int64_t expected_rows(const ExpertRows& er) {
-    if (er.offsets) return er.rows / er.E;
-    return er.E > 8 ? (int64_t)er.cap * 8 / er.E : er.cap;
-}
-
-// Whether 256 x 256 tiles would leave compute units without one: then 128 x 128
-// serve better (8 experts of 256 rows, 4096 -> 2048, 64 wide tiles: 54 and 83
-// us; of 512 rows, 4096 -> 4096, 256 wide tiles: 157 and 128).
-bool few_wide_tiles(const ExpertRows& er, int64_t likely, int out) {
-    return (likely + Wide::BQ - 1) / Wide::BQ * er.E * tiles_of(out, Wide::BP) < 256;
-}
-
-// Up to so many rows per expert the forward product takes 128 x 128 tiles: the
-// weights' bytes count, and two workgroups per CU keep them coming (64 experts,
-// 4096 -> 4096, 128 x 128 and 256 x 256: 364 and 375 us at 12 rows, 373 and 383
-// at 30; 7168 -> 4096: 635 both at 45, 648 and 643 at 64, 717 and 670 at about
-// 100).  The input gradient is better off with 256 x 256 at any number (4096 ->
-// 4096: 363 and 330 us at 12 rows, 417 and 378 at 100).
-constexpr int64_t kSmallRows = 48;
-
-// Whether workgroups start at scattered places of the reduction (`scattered`):
-// 64 experts of 64 rows, 4096 -> 4096, 458 us from the start and 397 scattered;
-// of about 180, 517 and 517, but of skewed numbers about 180, 317 and 356.
-bool rotates(int64_t likely, int reduction) { return likely <= 120 && reduction % 2048 == 0; }
+dim3 grid_of(int64_t workgroups) { return dim3((unsigned)workgroups); }
 
 template <typename S, typename T>
 hipError_t linear_tiles(const S* x, const S* w, const ExpertRows& er, int K, int N, bool swiglu,
                         bool rotate, S* y, S* pre, const Launch& L) {
-    const int cols = tiles_of(N, swiglu ? T::BP / 2 : T::BP);
-    const dim3 grid = grid_of(max_tiles(er, T::BQ) * cols);
-    return launch_kernel(swiglu ? linear_kernel<S, true, T> : linear_kernel<S, false, T>, grid,
-                         dim3(T::kThreads), L, x, w, er, K, N, cols, y, pre, rotate);
+    const int outs = swiglu ? 2 * N : N, cols = (int)tiles_of(outs, T::kTile.outs);
+    return launch_kernel(swiglu ? linear_kernel<S, true, T> : linear_kernel<S, false, T>,
+                         grid_of(workgroups(er, T::kTile, outs)), dim3(T::kThreads), L, x, w, er, K,
+                         N, cols, y, pre, rotate);
 }
 
 template <typename S>
@@ -482,27 +458,27 @@ hipError_t linear_as(const void* x, const void* w, const ExpertRows& er, int K, 
     const S* ws = static_cast<const S*>(w);
     S* ys = static_cast<S*>(y);
     S* ps = static_cast<S*>(pre);
-    const int64_t likely = expected_rows(er);
-    const bool rotate = rotates(likely, K);
-    // A few rows, or a few experts' rows: 8 of 64 experts with one row each,
-    // 7168 -> 4096: 79 us, 128 x 128 tiles 113; 8 rows each in all 64: 620 and 611.
-    if (likely <= 8) {
-        const int cols = tiles_of(N, swiglu ? 16 : 32);
-        const dim3 grid = grid_of(max_tiles(er, kFewRows) * cols);
-        return launch_kernel(swiglu ? linear_few_kernel<S, true> : linear_few_kernel<S, false>,
-                             grid, dim3(kFewThreads), L, xs, ws, er, K, N, cols, ys, ps, rotate);
+    const int outs = swiglu ? 2 * N : N;
+    const bool rotate = rotates(expected_rows(er), K);
+    switch (forward_tiles(er, outs)) {
+        case Tiles::kFew:
+            return launch_kernel(swiglu ? linear_few_kernel<S, true> : linear_few_kernel<S, false>,
+                                 grid_of(workgroups(er, kFewTile, outs)), dim3(kFewThreads), L, xs,
+                                 ws, er, K, N, (int)tiles_of(outs, kFewTile.outs), ys, ps, rotate);
+        case Tiles::kSmall:
+            return linear_tiles<S, Small>(xs, ws, er, K, N, swiglu, rotate, ys, ps, L);
+        case Tiles::kWide:
+            return linear_tiles<S, Wide>(xs, ws, er, K, N, swiglu, rotate, ys, ps, L);
+        default:
+            return hipErrorInvalidValue;  // refused before
     }
-    if (likely <= kSmallRows || few_wide_tiles(er, likely, swiglu ? 2 * N : N))
-        return linear_tiles<S, Small>(xs, ws, er, K, N, swiglu, rotate, ys, ps, L);
-    return linear_tiles<S, Wide>(xs, ws, er, K, N, swiglu, rotate, ys, ps, L);
 }
 
 template <typename S, typename T>
 hipError_t dgrad_tiles(const S* d_y, const S* w, const ExpertRows& er, int K, int N, S* d_x,
                        const Launch& L) {
-    const int cols = tiles_of(K, T::BP);
-    const dim3 grid = grid_of(max_tiles(er, T::BQ) * cols);
-    return launch_kernel(dgrad_kernel<S, T>, grid, dim3(T::kThreads), L, d_y, w, er, K, N, cols,
+    return launch_kernel(dgrad_kernel<S, T>, grid_of(workgroups(er, T::kTile, K)),
+                         dim3(T::kThreads), L, d_y, w, er, K, N, (int)tiles_of(K, T::kTile.outs),
                          d_x);
 }
 
@@ -511,16 +487,21 @@ hipError_t dgrad_as(const void* d_y, const void* w, const ExpertRows& er, int K,
                     const Launch& L) {
     const S* ds = static_cast<const S*>(d_y);
     const S* ws = static_cast<const S*>(w);
-    if (few_wide_tiles(er, expected_rows(er), K))
-        return dgrad_tiles<S, Small>(ds, ws, er, K, N, static_cast<S*>(d_x), L);
-    return dgrad_tiles<S, Wide>(ds, ws, er, K, N, static_cast<S*>(d_x), L);
+    switch (input_gradient_tiles(er, K)) {
+        case Tiles::kSmall:
+            return dgrad_tiles<S, Small>(ds, ws, er, K, N, static_cast<S*>(d_x), L);
+        case Tiles::kWide:
+            return dgrad_tiles<S, Wide>(ds, ws, er, K, N, static_cast<S*>(d_x), L);
+        default:
+            return hipErrorInvalidValue;  // refused before
+    }
 }
 
 template <typename S>
 hipError_t wgrad_as(const void* d_y, const void* x, const ExpertRows& er, int K, int N, void* d_w,
                     bool f32_out, const Launch& L) {
-    const int cols = tiles_of(K, Narrow::BP), rows = tiles_of(N, Narrow::BQ);
-    const dim3 grid = grid_of((int64_t)cols * rows * er.E);
+    const int cols = (int)tiles_of(K, Narrow::BP), rows = (int)tiles_of(N, Narrow::BQ);
+    const dim3 grid = grid_of(weight_workgroups(er, K, N));
     const S* ds = static_cast<const S*>(d_y);
     const S* xs = static_cast<const S*>(x);
     if (f32_out)

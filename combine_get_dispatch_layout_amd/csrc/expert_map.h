@@ -74,11 +74,4 @@ __device__ __forceinline__ RowTile find_block(const ExpertRows& er, int i, int c
     return RowTile{-1, 0, 0, 0};
 }
 
-// The most tiles that `rows` rows of E experts can make.
-inline int64_t max_tiles(const ExpertRows& er, int bm) {
-    if (!er.offsets) return (int64_t)er.E * ((er.cap + bm - 1) / bm);
-    const int64_t n = er.rows / bm + er.E;
-    return n < er.rows ? n : er.rows;
-}
-
 }  // namespace moedx

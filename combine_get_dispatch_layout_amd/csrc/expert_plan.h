@@ -1,0 +1,109 @@
+// Which tiles an experts' product takes, from what the host knows (no device
+// code and no HIP: the rules are checked on a machine without a GPU).
+#pragma once
+
+#include <stdint.h>
+
+namespace moedx {
+
+// Which rows belong to an expert: [offsets[e], offsets[e + 1]), or, with
+// offsets null, the first counts[e] of the cap rows from e * cap.
+struct ExpertRows {
+    const int32_t* offsets;
+    const int32_t* counts;
+    int cap;
+    int E;
+    int64_t rows;  // rows of the buffers; nothing at or past it is touched
+};
+
+// A workgroup's share of an output: so many rows and columns (of a gated
+// product's weight rows, gate and up together), by so many threads.
+struct TileShape {
+    int rows, outs, threads;
+};
+constexpr TileShape kFewTile{32, 32, 256}, kSmallTile{128, 128, 256}, kWideTile{256, 256, 512};
+// Of a weight gradient: weight rows (N) and columns (K).
+constexpr TileShape kWeightTile{128, 256, 256};
+
+constexpr int64_t tiles_of(int64_t n, int b) { return (n + b - 1) / b; }
+
+// The most tiles of `bm` rows that the buffer's rows can make.
+inline int64_t max_tiles(const ExpertRows& er, int bm) {
+    if (!er.offsets) return er.E * tiles_of(er.cap, bm);
+    const int64_t n = er.rows / bm + er.E;
+    return n < er.rows ? n : er.rows;
+}
+
+inline int64_t workgroups(const ExpertRows& er, const TileShape& t, int outs) {
+    return max_tiles(er, t.rows) * tiles_of(outs, t.outs);
+}
+inline int64_t weight_workgroups(const ExpertRows& er, int K, int N) {
+    return er.E * tiles_of(N, kWeightTile.rows) * tiles_of(K, kWeightTile.outs);
+}
+
+// HIP counts a grid's threads in 32 bits.
+constexpr bool grid_fits(int64_t workgroups, int threads) {
+    return workgroups <= (int64_t)UINT32_MAX / threads;
+}
+
+// Rows an expert is likely to have, from what the host knows.  A capacity
+// buffer holds at most cap tokens, each with a few experts: 8 are taken, the
+// top-k of the wide routings (more only moves where the kernels change).
+inline int64_t expected_rows(const ExpertRows& er) {
+    if (er.offsets) return er.rows / er.E;
+    return er.E > 8 ? (int64_t)er.cap * 8 / er.E : er.cap;
+}
+
+// Whether 256 x 256 tiles would leave compute units without one: then 128 x 128
+// serve better (8 experts of 256 rows, 4096 -> 2048, 64 wide tiles: 54 and 83
+// us; of 512 rows, 4096 -> 4096, 256 wide tiles: 157 and 128).
+inline bool few_wide_tiles(const ExpertRows& er, int64_t likely, int outs) {
+    return tiles_of(likely, kWideTile.rows) * er.E * tiles_of(outs, kWideTile.outs) < 256;
+}
+
+// A few rows, or a few experts' rows: weights straight into registers (8 of 64
+// experts with one row each, 7168 -> 4096: 79 us, 128 x 128 tiles 113; 8 rows
+// each in all 64: 620 and 611).
+constexpr int64_t kFewLikely = 8;
+
+// Up to so many rows per expert the forward product takes 128 x 128 tiles: the
+// weights' bytes count, and two workgroups per CU keep them coming (64 experts,
+// 4096 -> 4096, 128 x 128 and 256 x 256: 364 and 375 us at 12 rows, 373 and 383
+// at 30; 7168 -> 4096: 635 both at 45, 648 and 643 at 64, 717 and 670 at about
+// 100).  The input gradient is better off with 256 x 256 at any number (4096 ->
+// 4096: 363 and 330 us at 12 rows, 417 and 378 at 100).
+constexpr int64_t kSmallRows = 48;
+
+enum class Tiles { kFew, kSmall, kWide, kNone };
+
+// `best`, or the next larger tiles whose grid can be launched: the rules go by
+// the likely rows, the grid covers all that the buffer can hold.
+inline Tiles launchable(Tiles best, const ExpertRows& er, int outs) {
+    if (best == Tiles::kFew && grid_fits(workgroups(er, kFewTile, outs), kFewTile.threads))
+        return Tiles::kFew;
+    if (best != Tiles::kWide && grid_fits(workgroups(er, kSmallTile, outs), kSmallTile.threads))
+        return Tiles::kSmall;
+    if (grid_fits(workgroups(er, kWideTile, outs), kWideTile.threads)) return Tiles::kWide;
+    return Tiles::kNone;
+}
+
+// `outs`: outputs per row, gate and up counted both.
+inline Tiles forward_tiles(const ExpertRows& er, int outs) {
+    const int64_t likely = expected_rows(er);
+    const bool small = likely <= kSmallRows || few_wide_tiles(er, likely, outs);
+    return launchable(likely <= kFewLikely ? Tiles::kFew : small ? Tiles::kSmall : Tiles::kWide, er,
+                      outs);
+}
+inline Tiles input_gradient_tiles(const ExpertRows& er, int outs) {
+    return launchable(few_wide_tiles(er, expected_rows(er), outs) ? Tiles::kSmall : Tiles::kWide, er,
+                      outs);
+}
+
+// Whether workgroups start at scattered places of the reduction (`scattered`):
+// 64 experts of 64 rows, 4096 -> 4096, 458 us from the start and 397 scattered;
+// of about 180, 517 and 517, but of skewed numbers about 180, 317 and 356.
+inline bool rotates(int64_t likely, int reduction) {
+    return likely <= 120 && reduction % 2048 == 0;
+}
+
+}  // namespace moedx

@@ -551,7 +551,9 @@ typedef struct moedx_expert_rows {
  * for g = gate x, u = up x, both unrounded; pre (or NULL) receives [rows, 2N]
  * = (g, u) rounded, which moedx_expert_swiglu_backward takes.
  * K and N positive multiples of 8 up to 2^20, a w[e] below 2^31 bytes, rows
- * below 2^31; data 16-byte aligned. */
+ * below 2^31; data 16-byte aligned.  One launch covers what the buffer can
+ * hold: (rows / 256 + E) * ceil(N / 256) tiles (with counts E * ceil(cap / 256)
+ * row tiles; 2N with swiglu) are below 2^23, else MOEDX_EINVAL. */
 MOEDX_API int moedx_expert_linear(moedx_ctx *ctx, const void *x, const void *w, int dtype, int K,
                                   int N, const moedx_expert_rows *er, int swiglu, void *y,
                                   void *pre, const moedx_exec *exec);
@@ -559,7 +561,9 @@ MOEDX_API int moedx_expert_linear(moedx_ctx *ctx, const void *x, const void *w, 
 /* The gradients of y = w x: d_x[m] = w[e(m)]^T d_y[m] ([rows, K]; NULL to leave
  * it out) and d_w[e] = the sum over e's rows of d_y[m] x[m]^T ([E, N, K], of
  * type d_w_dtype: `dtype` or MOEDX_F32; zero for an expert without rows; NULL
- * to leave it out; x is then not read, w not without d_x). */
+ * to leave it out; x is then not read, w not without d_x).  The tiles of d_x
+ * are limited as above, of K columns; those of d_w, E * ceil(N / 128) *
+ * ceil(K / 256), are below 2^24. */
 MOEDX_API int moedx_expert_linear_backward(moedx_ctx *ctx, const void *d_y, const void *x,
                                            const void *w, int dtype, int K, int N,
                                            const moedx_expert_rows *er, void *d_x, void *d_w,

@@ -422,3 +422,44 @@ def test_refusals():
         with pytest.raises(C.MoedxError) as e:
             f()
         assert e.value.code == C.MOEDX_EINVAL
+
+
+def test_slots_of_many_experts():
+    """1024 experts' slots of which few rows are likely: 32-row tiles of the
+    whole capacity would be 2^24 workgroups, more than a grid has threads for."""
+    dev = device()
+    E, cap, K, N, dt = 1024, 1024, 8, 8192, torch.bfloat16
+    held = {0: 3, 17: 40, 511: 1024, 1023: 129}
+    buf = make_buffer(E, 1, 1, 1)
+    g = torch.Generator(dev).manual_seed(12)
+    counts = torch.zeros(E, dtype=torch.int32, device=dev)
+    x = torch.full((E, cap, K), float("nan"), device=dev, dtype=dt)
+    w = torch.randn(E, 2 * N, K, generator=g, device=dev, dtype=torch.float32).to(dt)
+    for e, c in held.items():
+        counts[e] = c
+        x[e, :c] = torch.randn(c, K, generator=g, device=dev).to(dt)
+    out = torch.full((E, cap, N), 7.0, dtype=dt, device=dev)
+    print("[linear] slots of 1024 experts", flush=True)
+    h, _, _ = buf.expert_linear(x, w, counts, swiglu=True, out=out)
+    for e, c in held.items():
+        xs, ws = x[e, :c].double(), w[e].double().t().contiguous()
+        p, acc = xs @ ws, (K + 1) * V * (xs.abs() @ ws.abs())
+        want, err = swiglu_reference(p[:, :N], p[:, N:], acc[:, :N], acc[:, N:])
+        check("h", h[e, :c], want, err, dt)
+        assert (h[e, c:] == 7.0).all() and (e == 1023 or (h[e + 1] == 7.0).all())
+
+
+def test_more_rows_than_a_grid_has():
+    """Buffers whose tiles no grid covers are refused before anything runs."""
+    from combine_get_dispatch_layout_amd import _capi as C
+    dev = device()
+    M, dt = (1 << 31) - 1, torch.bfloat16
+    buf = make_buffer(1, 1, 1, 1)
+    x, y = torch.empty(M, 8, device=dev, dtype=dt), torch.empty(M, 8, device=dev, dtype=dt)
+    w = torch.zeros(1, 8, 8, device=dev, dtype=dt)
+    rows = torch.zeros(2, dtype=torch.int32, device=dev)
+    for f in (lambda: buf.expert_linear(x, w, rows, out=y),
+              lambda: buf.expert_linear_backward(y, x, w, rows, out=torch.empty_like(x))):
+        with pytest.raises(C.MoedxError) as e:
+            f()
+        assert e.value.code == C.MOEDX_EINVAL and "grid" in str(e.value)
