@@ -132,8 +132,8 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(const S* x, cons
             .run(gp, gq, (lds_char*)lp, (lds_char*)lq, wave, acc);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            const int m = tile.begin + T::q_at(wq, j) + (lane & 15);
-            const bool row = m < tile.end;
+            const uint32_t m = (uint32_t)tile.begin + T::q_at(wq, j) + (lane & 15);
+            const bool row = m < (uint32_t)tile.end;  // unsigned: past 2^31 for the last tiles
             S* const ym = y + (int64_t)m * N;
             if constexpr (kSwiglu) {
                 S* const gm = pre + (int64_t)m * 2 * N;
@@ -267,7 +267,7 @@ __global__ __launch_bounds__(kFewThreads) void linear_few_kernel(const S* x, con
     }
 #pragma unroll
     for (int j = 0; j < kFewBlocks; ++j)
-        xs[j].init(x + (int64_t)(tile.begin + 16 * j) * K, min(rows - 16 * j, 16), K, lane);
+        xs[j].init(x + ((int64_t)tile.begin + 16 * j) * K, min(rows - 16 * j, 16), K, lane);
     f32x4 acc[kFewP][kFewBlocks] = {};
     const int shift = rotate ? scattered(blk, (K + kFewStep - 1) / kFewStep) : 0;
     if (rows > 16)
@@ -281,8 +281,8 @@ __global__ __launch_bounds__(kFewThreads) void linear_few_kernel(const S* x, con
     __syncthreads();
     // wave j finishes block j of 16 rows
     if (wave >= kFewBlocks) return;
-    const int m = tile.begin + wave * 16 + (lane & 15);
-    if (m >= tile.end) return;
+    const uint32_t m = (uint32_t)tile.begin + wave * 16 + (lane & 15);
+    if (m >= (uint32_t)tile.end) return;
     f32x4 sum[kFewP];
 #pragma unroll
     for (int i = 0; i < kFewP; ++i) {
@@ -340,12 +340,12 @@ __global__ __launch_bounds__(T::kThreads, 2) void dgrad_kernel(const S* d_y, con
             .run(gp, gq, (lds_char*)lp, (lds_char*)lq, wave, acc);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            const int m = tile.begin + T::q_at(wq, j) + (lane & 15);
+            const uint32_t m = (uint32_t)tile.begin + T::q_at(wq, j) + (lane & 15);
 #pragma unroll
             for (int i = 0; i < T::TP; i += 2) {
                 const int k = k0 + T::p_at(wp, i) + pair_at(lane);
                 const u32x4_t v = pack_pair<S>(acc[i][j], acc[i + 1][j]);
-                if (m < tile.end && k < K) store8(d_x + (int64_t)m * K + k, v);
+                if (m < (uint32_t)tile.end && k < K) store8(d_x + (int64_t)m * K + k, v);
             }
         }
     });
@@ -381,7 +381,7 @@ __global__ __launch_bounds__(Narrow::kThreads, 2) void wgrad_kernel(const S* d_y
         SharedCuLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, decltype(gp), decltype(gq)>(wp, wq, lane).run(
             gp, gq, (lds_char*)lp0, (lds_char*)lq0, (lds_char*)lp1, (lds_char*)lq1,
             (lds_char*)lp2, (lds_char*)lq2,
-            (count + T::BK - 1) / T::BK, wave, acc);
+            row_tiles<T::BK>(count), wave, acc);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
             const int n = n0 + T::q_at(wq, j) + (lane & 15);

@@ -34,9 +34,7 @@ struct RowTile {
 
 // Tile `i` (wave-uniform; every lane of the wave takes part) where each expert
 // has ceil(c / BM) x cols tiles: up to kGroup row tiles go through the columns
-// together, so that tiles close in number share both operands.  An expert's
-// rows are dealt evenly to its tiles, in steps of 64 (16 for small tiles): two
-// full tiles and one of 20 rows would take longer than three of 192.
+// together, so that tiles close in number share both operands.
 template <int BM, int kGroup>
 __device__ __forceinline__ RowTile find_block(const ExpertRows& er, int i, int cols) {
     const int lane = threadIdx.x & 63;
@@ -45,7 +43,7 @@ __device__ __forceinline__ RowTile find_block(const ExpertRows& er, int i, int c
         const int e = e0 + lane;
         RowSpan s{0, 0};
         if (e < er.E) s = expert_span(er, e);
-        const int t = (s.end - s.begin + BM - 1) / BM;
+        const int t = row_tiles<BM>(s.end - s.begin);
         int incl = t;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -64,10 +62,9 @@ __device__ __forceinline__ RowTile find_block(const ExpertRows& er, int i, int c
             local -= grp * kGroup * cols;
             const int in_grp = min(kGroup, mine - grp * kGroup);
             const int col = local / in_grp;
-            constexpr int kUnit = BM < 64 ? 16 : 64;  // divides BM, so step <= BM
-            const int step = ((end - begin + kUnit * mine - 1) / (kUnit * mine)) * kUnit;
+            const int step = row_step<BM>(end - begin, mine);
             const int b = begin + (grp * kGroup + local - col * in_grp) * step;
-            return RowTile{e0 + l, b, min(b + step, end), col};
+            return RowTile{e0 + l, b, b + min(step, end - b), col};
         }
         base += __builtin_amdgcn_readlane(incl, 63);
     }

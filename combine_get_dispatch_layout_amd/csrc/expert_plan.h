@@ -4,6 +4,12 @@
 
 #include <stdint.h>
 
+#if defined(__HIPCC__)
+#define MOEDX_PLAN_HD __host__ __device__
+#else
+#define MOEDX_PLAN_HD
+#endif
+
 namespace moedx {
 
 // Which rows belong to an expert: [offsets[e], offsets[e + 1]), or, with
@@ -24,6 +30,21 @@ struct TileShape {
 constexpr TileShape kFewTile{32, 32, 256}, kSmallTile{128, 128, 256}, kWideTile{256, 256, 512};
 // Of a weight gradient: weight rows (N) and columns (K).
 constexpr TileShape kWeightTile{128, 256, 256};
+
+// An expert's rows (up to 2^31 - 1) are dealt evenly to its ceil(count / BM)
+// tiles, in steps of 64 rows (16 for small tiles): two full tiles and one of 20
+// rows would take longer than three of 192.  All but the last get row_step, at
+// most BM; unsigned, because the sums pass 2^31.
+template <int BM>
+MOEDX_PLAN_HD inline int row_tiles(int count) {
+    return (int)(((uint32_t)count + (BM - 1)) / BM);
+}
+template <int BM>
+MOEDX_PLAN_HD inline int row_step(int count, int tiles) {
+    constexpr uint32_t kUnit = BM < 64 ? 16 : 64;  // divides BM, so a step is at most BM
+    const uint32_t unit = kUnit * (uint32_t)tiles;
+    return (int)(((uint32_t)count + unit - 1) / unit * kUnit);
+}
 
 constexpr int64_t tiles_of(int64_t n, int b) { return (n + b - 1) / b; }
 

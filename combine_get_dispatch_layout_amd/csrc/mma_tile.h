@@ -180,10 +180,11 @@ struct Across {
         const int c = (lane & (kRowChunks - 1)) ^ swizzle(row);
         voff = c0 + c * 8 < nc ? (uint32_t)(stage_row(row) * ld2) + c * 16 : kOutside;
     }
-    __device__ __forceinline__ void load(lds_char* lds, int k0, int wave) const {
-        const uint32_t v = k0 < nr ? voff : kOutside;
+    // k0: unsigned, as a stage past 2^31 - 1 rows starts past 2^31.
+    __device__ __forceinline__ void load(lds_char* lds, uint32_t k0, int wave) const {
+        const uint32_t v = k0 < (uint32_t)nr ? voff : kOutside;
         const __amdgpu_buffer_rsrc_t rs =
-            make_rsrc(base + (int64_t)k0 * ld2, min(nr - k0, BK) * ld2 - skip2);
+            make_rsrc(base + (int64_t)k0 * ld2, min((int)((uint32_t)nr - k0), BK) * ld2 - skip2);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -263,8 +264,8 @@ struct SharedCuLoop {
     }
     __device__ __forceinline__ void load(const LP& gp, const LQ& gq, lds_char* lp, lds_char* lq,
                                          int it, int wave) const {
-        gp.load(lp, it * kBK, wave);
-        gq.load(lq, it * kBK, wave);
+        gp.load(lp, (uint32_t)it * kBK, wave);
+        gq.load(lq, (uint32_t)it * kBK, wave);
     }
     // Waits until only the last stage's loads are in flight and meets the other
     // waves.  The wait is the compiler's own instruction, so that it knows which

@@ -2,7 +2,7 @@
 // over the documented range a choice's grid can be launched (HIP counts a
 // grid's threads in 32 bits) and covers every row and column, the preferred
 // tiles are taken where they can be, and nothing is refused that 256 x 256
-// tiles can do.
+// tiles can do.  And an expert's rows, up to 2^31 - 1, are all in its tiles.
 #include <cmath>
 #include <cstdio>
 #include <random>
@@ -59,6 +59,19 @@ static ExpertRows with_offsets(int E, int64_t rows) {
     return ExpertRows{&any, nullptr, 0, E, rows};
 }
 
+// The tiles of an expert's rows are not empty, at most BM rows each, and cover
+// all of them.
+template <int BM>
+static bool check_split(int64_t count) {
+    const int64_t tiles = row_tiles<BM>((int)count), step = row_step<BM>((int)count, (int)tiles);
+    if (tiles == (count + BM - 1) / BM && step > 0 && step <= BM && (tiles - 1) * step < count &&
+        tiles * step >= count)
+        return true;
+    std::printf("FAIL %lld rows in tiles of %d: %lld of %lld\n", (long long)count, BM,
+                (long long)tiles, (long long)step);
+    return false;
+}
+
 int main() {
     // slots of 1024 experts whose likely rows are few: 32-row tiles of the
     // capacity would be 2^24 workgroups of 256 threads
@@ -87,6 +100,13 @@ int main() {
         if (!check(with_offsets(E, rows), outs) || !check(with_counts(E, (int)(rows / E)), outs))
             return 1;
     }
+    const auto splits = [&](int64_t count) {
+        return check_split<32>(count) && check_split<128>(count) && check_split<256>(count);
+    };
+    for (int64_t count = 1; count < 100000; ++count)
+        if (!splits(count) || !splits(INT32_MAX - count + 1)) return 1;
+    for (int i = 0; i < 1000000; ++i)
+        if (!splits(1 + (int64_t)(rng() % INT32_MAX)) || !splits(log_uniform(2147483648.0))) return 1;
     std::printf("ok %d\n", 2 * n);
     return 0;
 }

@@ -463,3 +463,48 @@ def test_more_rows_than_a_grid_has():
         with pytest.raises(C.MoedxError) as e:
             f()
         assert e.value.code == C.MOEDX_EINVAL and "grid" in str(e.value)
+
+
+def test_rows_near_2_31():
+    """One expert whose rows reach 2^31: every one of them is written, forward
+    and input gradient, and the products are exact (powers of two)."""
+    import ctypes
+
+    from combine_get_dispatch_layout_amd import _capi as C
+    dev = device()
+    M, dt = (1 << 31) - 1024, torch.bfloat16
+    buf = make_buffer(1, 1, 1, 1)
+    powers = 2.0 ** torch.arange(8, device=dev)
+    w = torch.zeros(1, 8, 8, device=dev, dtype=dt)
+    w[0, :, 0] = powers.to(dt)  # y[m, n] = 2^n x[m, 0]
+    x, y = torch.zeros(M, 8, device=dev, dtype=dt), torch.zeros(M, 8, device=dev, dtype=dt)
+    step = 1 << 27
+    for a in range(0, M, step):
+        b = min(a + step, M)
+        x[a:b, 0] = (torch.arange(a, b, device=dev) % 251 + 1).to(dt)
+    live = (5, M - 3)
+    rows = torch.tensor(live, dtype=torch.int32, device=dev)
+
+    def check_rows(got, weights):
+        for a in range(0, M, step):
+            b = min(a + step, M)
+            for n in range(8):
+                want = x[a:b, 0] * weights[n].to(dt)
+                if a < live[0]:
+                    want[:live[0] - a] = 0
+                if b > live[1]:
+                    want[live[1] - a:] = 0
+                assert torch.equal(got[a:b, n], want), (a, n)
+
+    print("[linear] rows near 2^31", flush=True)
+    buf.expert_linear(x, w, rows, out=y)
+    check_rows(y, powers)
+    y.zero_()
+    wt = w.transpose(1, 2).contiguous()  # d_x[m, k] = 2^k d_y[m, 0]
+    er = C.moedx_expert_rows(rows.data_ptr(), None, M)
+    ex = C.moedx_exec(stream=torch.cuda.current_stream().cuda_stream)
+    print("[linear backward] rows near 2^31", flush=True)
+    C.check(C.moedx_expert_linear_backward(buf.ctx, x.data_ptr(), None, wt.data_ptr(), C.MOEDX_BF16,
+                                           8, 8, ctypes.byref(er), y.data_ptr(), None, C.MOEDX_BF16,
+                                           ctypes.byref(ex)))
+    check_rows(y, powers)
