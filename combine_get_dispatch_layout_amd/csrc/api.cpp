@@ -1234,14 +1234,14 @@ struct DeviceScope {
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
-// An output and another buffer of a call (either may be NULL: left out).
+// An output and another buffer of a call (either may be NULL or empty: left out).
 struct Bytes {
     const void* at;
     int64_t n;
 };
 bool overlap(Bytes a, Bytes b) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
-    return a.at && b.at && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
+    return a.at && b.at && a.n > 0 && b.n > 0 && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
 }
 int check_apart(Bytes out, std::initializer_list<Bytes> others) {
     for (const Bytes& o : others)
@@ -1345,6 +1345,11 @@ ExpertRows expert_rows(const moedx_ctx* ctx, const moedx_expert_rows* er) {
                       er->rows};
 }
 
+// The array that says which rows are an expert's.
+Bytes rows_array(const moedx_ctx* ctx, const moedx_expert_rows* er) {
+    return er->offsets ? Bytes{er->offsets, (ctx->E + 1) * 4} : Bytes{er->counts, ctx->E * 4};
+}
+
 int check_grid(bool fits, const moedx_expert_rows* er, int K, int N) {
     if (fits) return MOEDX_OK;
     return fail(MOEDX_EINVAL, "rows=%lld with K=%d, N=%d take more workgroups than a grid has",
@@ -1362,6 +1367,11 @@ int moedx_gate_topk(moedx_ctx* ctx, const void* logits, int dtype, int T, int K,
         return fail(MOEDX_EINVAL, "NULL device pointer");
     if (!aligned_to(logits, dtype_bytes(dtype)))
         return fail(MOEDX_EINVAL, "logits must be aligned to their type");
+    const int64_t slots = (int64_t)T * K;
+    const Bytes lb{logits, (int64_t)T * ctx->E * dtype_bytes(dtype)}, bb{gate->bias, ctx->E * 4};
+    const Bytes wb{topk_weights, slots * 4};
+    if (int rc = check_apart({topk_idx, slots * 8}, {wb, lb, bb})) return rc;
+    if (int rc = check_apart(wb, {lb, bb})) return rc;
     DeviceScope scope;
     Exec ex;
     if (int rc = exec_begin(ctx, exec, &ex)) return rc;
@@ -1383,6 +1393,11 @@ int moedx_gate_topk_backward(moedx_ctx* ctx, const void* logits, int dtype, int 
         return fail(MOEDX_EINVAL, "NULL device pointer");
     if (!aligned_to(logits, dtype_bytes(dtype)) || !aligned_to(d_logits, dtype_bytes(dtype)))
         return fail(MOEDX_EINVAL, "logits and d_logits must be aligned to their type");
+    const int64_t slots = (int64_t)T * K, logit_bytes = (int64_t)T * ctx->E * dtype_bytes(dtype);
+    if (int rc = check_apart({d_logits, logit_bytes},
+                             {{logits, logit_bytes}, {topk_idx, slots * 8},
+                              {d_topk_weights, slots * 4}, {gate->bias, ctx->E * 4}}))
+        return rc;
     DeviceScope scope;
     Exec ex;
     if (int rc = exec_begin(ctx, exec, &ex)) return rc;
@@ -1428,6 +1443,14 @@ int moedx_expert_order(moedx_ctx* ctx, const int64_t* topk_idx, int T, int K,
         return fail(MOEDX_EINVAL, "workspace is not 256-byte aligned");
     if (workspace_bytes < need)
         return fail(MOEDX_ECAPACITY, "workspace_bytes=%zu < %zu", workspace_bytes, need);
+    const int64_t slots = (int64_t)T * K;
+    const Bytes ib{topk_idx, slots * 8}, ob{expert_offsets, (ctx->E + 1) * 4};
+    const Bytes rb{row_of_slot, slots * 4}, sb{slot_of_row, slots * 4};
+    const Bytes pb{h ? h->rank_prefix_matrix : nullptr, ctx->R * 4};
+    if (int rc = check_apart({workspace, (int64_t)need}, {ib, ob, rb, sb, pb})) return rc;
+    if (int rc = check_apart(ob, {ib, rb, sb, pb})) return rc;
+    if (int rc = check_apart(rb, {ib, sb, pb})) return rc;
+    if (int rc = check_apart(sb, {ib, pb})) return rc;
     DeviceScope scope;
     Exec ex;
     if (int rc = exec_begin(ctx, exec, &ex)) return rc;
@@ -1461,7 +1484,9 @@ int moedx_expert_sort(moedx_ctx* ctx, const void* x, int dtype, int T, int K, in
     if (!aligned16(x) || !aligned16(rows) || !aligned4(row_of_slot))
         return fail(MOEDX_EINVAL, "x and rows must be 16-byte aligned");
     const int64_t row = (int64_t)H * dtype_bytes(dtype);
-    if (int rc = check_apart({rows, T * K * row}, {{x, T * row}})) return rc;
+    const int64_t slots = (int64_t)T * K;
+    if (int rc = check_apart({rows, slots * row}, {{x, T * row}, {row_of_slot, slots * 4}}))
+        return rc;
     DeviceScope scope;
     Exec ex;
     if (int rc = exec_begin(ctx, exec, &ex)) return rc;
@@ -1482,7 +1507,10 @@ int moedx_expert_unsort(moedx_ctx* ctx, const void* rows, int dtype, int T, int 
     if (!aligned16(rows) || !aligned16(out) || !aligned4(row_of_slot) || !aligned4(weights))
         return fail(MOEDX_EINVAL, "rows and out must be 16-byte aligned");
     const int64_t row = (int64_t)H * dtype_bytes(dtype);
-    if (int rc = check_apart({out, T * row}, {{rows, T * K * row}})) return rc;
+    const int64_t slots = (int64_t)T * K;
+    if (int rc = check_apart({out, T * row},
+                             {{rows, slots * row}, {row_of_slot, slots * 4}, {weights, slots * 4}}))
+        return rc;
     DeviceScope scope;
     Exec ex;
     if (int rc = exec_begin(ctx, exec, &ex)) return rc;
@@ -1507,8 +1535,11 @@ int moedx_expert_unsort_backward(moedx_ctx* ctx, const void* d_out, const void* 
         !aligned4(slot_of_row) || !aligned4(weights) || !aligned4(d_weights))
         return fail(MOEDX_EINVAL, "d_out, rows and d_rows must be 16-byte aligned");
     const int64_t row = (int64_t)H * dtype_bytes(dtype);
-    if (int rc = check_apart({d_rows, T * K * row}, {{d_out, T * row}, {rows, T * K * row}}))
-        return rc;
+    const int64_t slots = (int64_t)T * K;
+    const Bytes db{d_out, T * row}, yb{rows, slots * row}, rb{row_of_slot, slots * 4};
+    const Bytes sb{slot_of_row, slots * 4}, wb{weights, slots * 4}, dwb{d_weights, slots * 4};
+    if (int rc = check_apart({d_rows, slots * row}, {db, yb, rb, sb, wb, dwb})) return rc;
+    if (int rc = check_apart(dwb, {db, yb, rb, sb, wb})) return rc;
     DeviceScope scope;
     Exec ex;
     if (int rc = exec_begin(ctx, exec, &ex)) return rc;
@@ -1536,8 +1567,9 @@ int moedx_expert_linear(moedx_ctx* ctx, const void* x, const void* w, int dtype,
         return fail(MOEDX_EINVAL, "x, w, y and pre must be 16-byte aligned");
     const Bytes xb{x, er->rows * K * 2}, yb{y, er->rows * N * 2}, pb{pre, er->rows * N * 4};
     const Bytes wb{w, (int64_t)ctx->E * (swiglu ? 2 : 1) * N * K * 2};
-    if (int rc = check_apart(yb, {xb, wb, pb})) return rc;
-    if (int rc = check_apart(pb, {xb, wb})) return rc;
+    const Bytes rb = rows_array(ctx, er);
+    if (int rc = check_apart(yb, {xb, wb, pb, rb})) return rc;
+    if (int rc = check_apart(pb, {xb, wb, rb})) return rc;
     DeviceScope scope;
     Exec ex;
     if (int rc = exec_begin(ctx, exec, &ex)) return rc;
@@ -1570,8 +1602,9 @@ int moedx_expert_linear_backward(moedx_ctx* ctx, const void* d_y, const void* x,
     const int64_t weights = (int64_t)ctx->E * N * K;
     const Bytes dyb{d_y, er->rows * N * 2}, xb{x, er->rows * K * 2}, wb{w, weights * 2};
     const Bytes dxb{d_x, er->rows * K * 2}, dwb{d_w, weights * dtype_bytes(d_w_dtype)};
-    if (int rc = check_apart(dxb, {dyb, xb, wb, dwb})) return rc;
-    if (int rc = check_apart(dwb, {dyb, xb, wb})) return rc;
+    const Bytes rb = rows_array(ctx, er);
+    if (int rc = check_apart(dxb, {dyb, xb, wb, dwb, rb})) return rc;
+    if (int rc = check_apart(dwb, {dyb, xb, wb, rb})) return rc;
     DeviceScope scope;
     Exec ex;
     if (int rc = exec_begin(ctx, exec, &ex)) return rc;
@@ -1594,8 +1627,9 @@ int moedx_expert_swiglu_backward(moedx_ctx* ctx, const void* d_h, const void* pr
     if (er->rows > 0 && (!d_h || !pre || !d_pre)) return fail(MOEDX_EINVAL, "NULL device pointer");
     if (!aligned16(d_h) || !aligned16(pre) || !aligned16(d_pre))
         return fail(MOEDX_EINVAL, "d_h, pre and d_pre must be 16-byte aligned");
-    if (int rc = check_apart({d_pre, er->rows * N * 4},
-                             {{d_h, er->rows * N * 2}, {pre, er->rows * N * 4}}))
+    if (int rc = check_apart({d_pre, er->rows * N * 4}, {{d_h, er->rows * N * 2},
+                                                         {pre, er->rows * N * 4},
+                                                         rows_array(ctx, er)}))
         return rc;
     DeviceScope scope;
     Exec ex;

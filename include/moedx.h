@@ -426,7 +426,8 @@ MOEDX_API int moedx_ll_combine(moedx_ctx *ctx, const uint16_t *y, const int64_t 
                                uint16_t *out, const moedx_exec *exec);
 
 /* ---- element types of the calls below ------------------------------------- */
-/* In all of them an output overlaps no other buffer of the call. */
+/* In all of them an output overlaps no other buffer of the call (else
+ * MOEDX_EINVAL). */
 enum { MOEDX_BF16 = 0, MOEDX_F16 = 1, MOEDX_F32 = 2 };
 
 /* ---- router: top-k expert choice with gate weights ------------------------- */
