@@ -1365,8 +1365,9 @@ int moedx_gate_topk(moedx_ctx* ctx, const void* logits, int dtype, int T, int K,
     if (int rc = check_gate(ctx, dtype, T, K, gate)) return rc;
     if (T > 0 && (!logits || !topk_idx || !topk_weights))
         return fail(MOEDX_EINVAL, "NULL device pointer");
-    if (!aligned_to(logits, dtype_bytes(dtype)))
-        return fail(MOEDX_EINVAL, "logits must be aligned to their type");
+    if (!aligned_to(logits, dtype_bytes(dtype)) || !aligned_to(topk_idx, 8) ||
+        !aligned4(topk_weights))
+        return fail(MOEDX_EINVAL, "logits, topk_idx and topk_weights must be aligned to their type");
     const int64_t slots = (int64_t)T * K;
     const Bytes lb{logits, (int64_t)T * ctx->E * dtype_bytes(dtype)}, bb{gate->bias, ctx->E * 4};
     const Bytes wb{topk_weights, slots * 4};
@@ -1391,8 +1392,10 @@ int moedx_gate_topk_backward(moedx_ctx* ctx, const void* logits, int dtype, int 
     if (int rc = check_gate(ctx, dtype, T, K, gate)) return rc;
     if (T > 0 && (!logits || !topk_idx || !d_topk_weights || !d_logits))
         return fail(MOEDX_EINVAL, "NULL device pointer");
-    if (!aligned_to(logits, dtype_bytes(dtype)) || !aligned_to(d_logits, dtype_bytes(dtype)))
-        return fail(MOEDX_EINVAL, "logits and d_logits must be aligned to their type");
+    if (!aligned_to(logits, dtype_bytes(dtype)) || !aligned_to(d_logits, dtype_bytes(dtype)) ||
+        !aligned_to(topk_idx, 8) || !aligned4(d_topk_weights))
+        return fail(MOEDX_EINVAL, "logits, d_logits, topk_idx and d_topk_weights must be aligned to "
+                                  "their type");
     const int64_t slots = (int64_t)T * K, logit_bytes = (int64_t)T * ctx->E * dtype_bytes(dtype);
     if (int rc = check_apart({d_logits, logit_bytes},
                              {{logits, logit_bytes}, {topk_idx, slots * 8},

@@ -463,7 +463,7 @@ typedef struct moedx_gate {
  * all weights of its token's softmax NaN, renormalised or not; the choice is
  * that of the limit: experts with +inf share a score of 1, the others have 0
  * (without bias and groups they follow in the order of their logits).
- * T in [0, 2^24], K in [1, min(16, E)].  logits aligned to their type. */
+ * T in [0, 2^24], K in [1, min(16, E)].  Arrays aligned to their type. */
 MOEDX_API int moedx_gate_topk(moedx_ctx *ctx, const void *logits, int dtype, int T, int K,
                               const moedx_gate *gate, int64_t *topk_idx, float *topk_weights,
                               const moedx_exec *exec);

@@ -1,5 +1,6 @@
 """Outputs of the router, expert-order and expert-product calls that overlap
-another buffer of the call are refused; outputs right behind one are not.  All buffers lie in one
+another buffer of the call, and buffers that are not aligned to their type, are
+refused; outputs right behind another buffer are not.  All buffers lie in one
 allocation of zeros (indexes and offsets of zero are valid), so that every call
 stays inside it."""
 
@@ -189,3 +190,14 @@ def test_empty_buffers_overlap_nothing(arena):
     assert C.moedx_expert_linear(buf.ctx, p + 4096, p + 8192, C.MOEDX_BF16, H, N, ctypes.byref(er), 0,
                                  p + 8192 + 16, None, ctypes.byref(ex)) == C.MOEDX_OK
     assert C.moedx_expert_sort(buf.ctx, p, C.MOEDX_BF16, 0, K, H, p, p, ctypes.byref(ex)) == C.MOEDX_OK
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_alignment(arena, name):
+    """A buffer that is not aligned to its type is refused."""
+    C = arena[0]
+    buffers, apart, run = runner(arena, name)
+    for i, (b, _, a, _) in enumerate(buffers):
+        at = list(apart)
+        at[i] += a // 2
+        assert run(at) == C.MOEDX_EINVAL and "aligned" in C.last_error(), b
