@@ -296,3 +296,66 @@ def test_gate_infinite_logits(E, form, renorm, dt):
     want_idx, want_w, _ = reference(logits, K, "sigmoid", groups, kept, renorm, 1.5, bias)
     assert torch.equal(idx.cpu(), want_idx)
     assert ((w.cpu().double() - want_w).abs() <= 64 * U * want_w).all()
+
+
+DTYPES = [torch.float32, torch.bfloat16, torch.float16]
+
+
+@pytest.mark.parametrize("renorm", [False, True], ids=["plain", "renorm"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dt", DTYPES, ids=lambda d: str(d)[6:])
+@pytest.mark.parametrize("K", [1, 8, 16])
+@pytest.mark.parametrize("E", [257, 300, 512, 1000, 1024])
+def test_gate_many_experts(E, K, dt, score, renorm):
+    """More than 256 experts without bias and groups: their own kernel.  16-bit
+    logits have many ties."""
+    test_gate_and_gradient((6, E, K, dt, score, 1, 1, renorm, False, 0.1))
+
+
+@pytest.mark.parametrize("renorm", [False, True], ids=["plain", "renorm"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dt", DTYPES, ids=lambda d: str(d)[6:])
+@pytest.mark.parametrize("E", [16, 33, 64, 200, 256])
+def test_gate_sixteen_choices(E, dt, score, renorm):
+    """The most choices, up to as many as there are experts, and few candidates."""
+    test_gate_and_gradient((21, E, 16, dt, score, 1, 1, renorm, False, 0.2))
+    test_gate_and_gradient((22, E, 16, dt, score, 1, 1, renorm, False, 0.95))
+
+
+@pytest.mark.parametrize("E", [512, 1000, 1024])
+def test_gate_ties_of_many_experts(E):
+    """As test_gate_extremes and test_gate_close_scores, past 256 experts: ties
+    within a lane's experts and across lanes go to the lower index, round by
+    round, and fp32 neighbours are told apart."""
+    dev = device()
+    K = 16
+    buf = make_buffer(E, 1, 1, 64)
+    for dt in DTYPES:
+        low, big = torch.finfo(dt).min, torch.finfo(dt).max
+        rows = torch.stack([torch.zeros(E), torch.full((E,), low), torch.full((E,), big),
+                            torch.full((E,), -3.0)]).to(dt)
+        tied = [E - 1, 0, E // 2, E // 2 + 1, 17, 100, 101, 102, 103]
+        rows[3, tied] = 1.0
+        want3 = sorted(tied) + [e for e in range(E) if e not in tied][:K - len(tied)]
+        for score in ("softmax", "sigmoid"):
+            idx, w, _ = buf.gate_topk(rows.to(dev), K, score=score, renormalize=True)
+            idx, w = idx.cpu(), w.cpu()
+            for t in (0, 1, 2):
+                assert idx[t].tolist() == list(range(K))
+                assert (w[t] == 1.0 / K).all()
+            assert idx[3].tolist() == want3
+            d, _ = buf.gate_topk_backward(torch.ones(4, K, device=dev), rows.to(dev), idx.to(dev),
+                                          score=score, renormalize=True)
+            assert torch.isfinite(d).all()
+    g = torch.Generator().manual_seed(9)
+    ladder = torch.full((E,), 1.0)
+    for e in range(1, E):
+        ladder[e] = torch.nextafter(ladder[e - 1], torch.tensor(2.0))
+    perm = torch.stack([torch.randperm(E, generator=g) for _ in range(64)])
+    logits = ladder[perm]
+    want = torch.argsort(perm, dim=1, descending=True)[:, :K]
+    zero = torch.zeros(E, device=dev)
+    for score in ("softmax", "sigmoid"):
+        for bias in (None, zero):
+            idx, _, _ = buf.gate_topk(logits.to(dev), K, score=score, bias=bias)
+            assert torch.equal(idx.cpu(), want), (score, bias is None)
