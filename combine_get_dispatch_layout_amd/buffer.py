@@ -775,7 +775,7 @@ class Buffer:
         up rows) and y = silu(gate) * up; ``return_pre`` also gives the rounded
         (gate, up) values [*, 2N] that expert_swiglu_backward takes, else pre
         is None.  Rows of no expert are left as they were (unspecified without
-        ``out``)."""
+        ``out``).  Weights that are not contiguous are copied on every call."""
         lead = self._lead("x", x)
         x = self._check("x", x, _PRODUCT_DTYPES, lead + (None,), previous_event)
         K = x.shape[-1]

@@ -407,7 +407,11 @@ __global__ __launch_bounds__(Narrow::kThreads, 2) void wgrad_kernel(const S* d_y
 constexpr int kActThreads = 256;
 constexpr int64_t kActGrid = 1 << 20;  // workgroups at most
 
-// Workgroups go through the buffer's rows; rows of no expert are left alone.
+// Workgroups go through the buffer's rows, one row at a time; rows of no expert
+// are left alone.  Bound by memory from rows of 1024 values on: 65536 x 1024
+// bf16 110 us (6.1 TB/s), 49152 x 2048 169 (6.0), 32768 x 4096 224 (6.0), 16384 x
+// 7168 217 (5.4).  Narrower rows leave threads idle: 65536 x 768 105 us (4.8
+// TB/s), 65536 x 256 61 us (2.8).
 template <typename S>
 __global__ __launch_bounds__(kActThreads) void swiglu_backward_kernel(
     const u32x4_t* __restrict__ d_h, const u32x4_t* __restrict__ pre, ExpertRows er, int chunks,

@@ -82,9 +82,15 @@ inline bool few_wide_tiles(const ExpertRows& er, int64_t likely, int outs) {
     return tiles_of(likely, kWideTile.rows) * er.E * tiles_of(outs, kWideTile.outs) < 256;
 }
 
-// A few rows, or a few experts' rows: weights straight into registers (8 of 64
-// experts with one row each, 7168 -> 4096: 79 us, 128 x 128 tiles 113; 8 rows
-// each in all 64: 620 and 611).
+// A few rows, or a few experts' rows: weights straight into registers.  8 of 64
+// experts with one row each, 7168 -> 4096: 79 us, 128 x 128 tiles 113.  Rows in
+// all 64, few-row kernel and 128 x 128:
+//   rows each                1           4           8           9          16
+//   7168 -> 4096        594  606    626  636    644  638    648  640    719  642
+//   4096 -> 2 x 2048    359  400    361  401    370  403    374  404    409  403
+//   2048 -> 1408         64   79     67   79     72   79     74   80     83   80
+// 1024 experts of 8 rows, 2048 -> 1024: 955 and 794, as each of the many short
+// workgroups looks through all experts' counts.
 constexpr int64_t kFewLikely = 8;
 
 // Up to so many rows per expert the forward product takes 128 x 128 tiles: the
@@ -120,9 +126,15 @@ inline Tiles input_gradient_tiles(const ExpertRows& er, int outs) {
                       outs);
 }
 
-// Whether workgroups start at scattered places of the reduction (`scattered`):
-// 64 experts of 64 rows, 4096 -> 4096, 458 us from the start and 397 scattered;
-// of about 180, 517 and 517, but of skewed numbers about 180, 317 and 356.
+// Whether workgroups start at scattered places of the reduction (`scattered`).
+// 64 experts, 4096 outputs, from the start and scattered:
+//   rows each           8          12          30          64         120
+//   2048            192  191    248  194    257  199    261  213    285  231
+//   4096            374  368    451  380    464  386    466  412    504  445
+//   6144            565  560    595  558    632  572    642  591    662  660
+//   8192            752  721    752  743    761  758    807  815    878  891
+// of about 180 rows (4096), 517 and 517, but of skewed numbers about 180, 317
+// and 356.
 inline bool rotates(int64_t likely, int reduction) {
     return likely <= 120 && reduction % 2048 == 0;
 }

@@ -302,7 +302,12 @@ __global__ __launch_bounds__(kRowThreads) void expert_unsort_kernel(
 // GB in 334 us (5.2 TB/s); by token, with d_out held and the rows gathered, 346
 // us, and with cached instead of streaming stores 343 us.  (All-zero data takes
 // 290 us: what memory reaches depends on the bits.)
-constexpr int kBackChunks = 4;  // chunks of 64 lanes whose loads go out together
+//
+// A turn of the loop takes kBackChunks chunks per lane.  fp32 has their loads in
+// flight together (43 registers); for bf16 and fp16 the compiler moves each pair
+// of loads behind the end-of-row test, so that a lane loads, waits and stores
+// chunk by chunk (27 and 21 registers), and only other waves cover the wait.
+constexpr int kBackChunks = 4;
 
 template <typename S>
 __global__ __launch_bounds__(kRowThreads) void expert_unsort_backward_kernel(

@@ -95,10 +95,9 @@ typedef struct moedx_exec {
     const moedx_event *prev;
     moedx_event **done;
     uint32_t flags;
-    /* Optional events from moedx_event_create: stamped when the op's kernel
-     * starts and when it ends (kernel-accurate timing; every op launches one
-     * kernel).  An op that launches no kernel (no token) records both on the
-     * stream instead. */
+    /* Optional events from moedx_event_create: stamped when the op's (first)
+     * kernel starts and when its (last) one ends: kernel-accurate timing.  An op
+     * that launches no kernel (no token) records both on the stream instead. */
     moedx_event *kernel_start;
     moedx_event *kernel_stop;
 } moedx_exec;
@@ -547,7 +546,9 @@ typedef struct moedx_expert_rows {
 } moedx_expert_rows;
 
 /* y[m] = w[e(m)] x[m]: x [rows, K], y [rows, N], w [E, N, K], all of `dtype`
- * (MOEDX_BF16 or MOEDX_F16), sums in fp32, one rounding.
+ * (MOEDX_BF16 or MOEDX_F16), sums in fp32, one rounding.  The order of a sum
+ * depends on the buffer's size and on where a row lies in it: equal calls give
+ * equal bits, but a row's last bits may differ in another buffer or batch.
  * swiglu = 1: w is [E, 2N, K], gate rows then up rows; y = g / (1 + exp(-g)) * u
  * for g = gate x, u = up x, both unrounded; pre (or NULL) receives [rows, 2N]
  * = (g, u) rounded, which moedx_expert_swiglu_backward takes.
@@ -571,7 +572,7 @@ MOEDX_API int moedx_expert_linear_backward(moedx_ctx *ctx, const void *d_y, cons
                                            int d_w_dtype, const moedx_exec *exec);
 
 /* d_pre [rows, 2N] = (d_g, d_u) from d_h [rows, N] and pre = (g, u) [rows, 2N]
- * for h = g / (1 + exp(-g)) * u; N a positive multiple of 8. */
+ * for h = g / (1 + exp(-g)) * u; N a positive multiple of 8 up to 2^20. */
 MOEDX_API int moedx_expert_swiglu_backward(moedx_ctx *ctx, const void *d_h, const void *pre,
                                            int dtype, int N, const moedx_expert_rows *er,
                                            void *d_pre, const moedx_exec *exec);
