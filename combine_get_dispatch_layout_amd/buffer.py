@@ -552,7 +552,7 @@ class Buffer:
                     bad = True
         if bad:
             raise ValueError(f"{name} has shape {tuple(got)}, expected {tuple(shape)}")
-        return _contiguous(t, previous_event)
+        return t if t.is_contiguous() else _contiguous(t, previous_event)
 
     def _out(self, name: str, out, dtype, shape) -> torch.Tensor:
         """`out` checked (it must be contiguous), or a new tensor."""
