@@ -89,9 +89,38 @@ inline bool few_wide_tiles(const ExpertRows& er, int64_t likely, int outs) {
 //   7168 -> 4096        594  606    626  636    644  638    648  640    719  642
 //   4096 -> 2 x 2048    359  400    361  401    370  403    374  404    409  403
 //   2048 -> 1408         64   79     67   79     72   79     74   80     83   80
-// 1024 experts of 8 rows, 2048 -> 1024: 955 and 794, as each of the many short
-// workgroups looks through all experts' counts.
+//   1024 -> 1024         25   23     28   23     29   23
 constexpr int64_t kFewLikely = 8;
+
+// But every workgroup, also one past the last tile, looks through the experts'
+// rows for its own, so small tiles of a buffer that may hold many rows cost more
+// than they save: the few-row kernel stays below so many 32-row tiles, 128 x 128
+// of slots below so many 128-row tiles unless 256-row tiles are as many.  Slots
+// may be nearly all empty, hence their lower bound.  4096 -> 2048, us, few-row
+// kernel and 128 x 128:
+//   offsets, 256 experts, 256 and 320 tiles   704  741    715  728
+//   the same, 1024 -> 1024                    106  104    124  105
+//   2048 rows of 2 of 256 experts (7168 -> 2048)          441   79
+//   slots: every expert has 1 to 4 rows; one token's 8 experts have one
+//   64 experts, 64 tiles (32 slots)           180  183     28   37
+//   128 experts, 128 tiles (32)               347  360     36   37
+//   128 experts, 256 tiles (64)               353  361     48   37
+//   256 experts, 1024 tiles (128)             797  717    176   39
+//   1024 experts, 4096 tiles (128)           4350 2814   2174  226
+// and 128 x 128 and 256 x 256 (1 to 8 rows; one token):
+//   256 experts, 512 tiles (256 slots)        738  745     53   70
+//   512 experts, 1024 tiles (256)            1482 1468    130  108
+//   1024 experts, 1024 tiles (128)           2814 2911    226  259
+//   1024 experts, 4096 tiles (512)           3475 3148    830  465
+constexpr int64_t kFewTiles = 256, kFewSlotTiles = 128, kSmallSlotTiles = 512;
+
+inline bool few_serves(const ExpertRows& er) {
+    return max_tiles(er, kFewTile.rows) <= (er.offsets ? kFewTiles : kFewSlotTiles);
+}
+inline bool small_serves(const ExpertRows& er) {
+    const int64_t tiles = max_tiles(er, kSmallTile.rows);
+    return er.offsets || tiles <= kSmallSlotTiles || tiles == max_tiles(er, kWideTile.rows);
+}
 
 // Up to so many rows per expert the forward product takes 128 x 128 tiles: the
 // weights' bytes count, and two workgroups per CU keep them coming (64 experts,
@@ -117,9 +146,12 @@ inline Tiles launchable(Tiles best, const ExpertRows& er, int outs) {
 // `outs`: outputs per row, gate and up counted both.
 inline Tiles forward_tiles(const ExpertRows& er, int outs) {
     const int64_t likely = expected_rows(er);
-    const bool small = likely <= kSmallRows || few_wide_tiles(er, likely, outs);
-    return launchable(likely <= kFewLikely ? Tiles::kFew : small ? Tiles::kSmall : Tiles::kWide, er,
-                      outs);
+    Tiles best = Tiles::kWide;
+    if (likely <= kFewLikely && few_serves(er))
+        best = Tiles::kFew;
+    else if (few_wide_tiles(er, likely, outs) || (likely <= kSmallRows && small_serves(er)))
+        best = Tiles::kSmall;
+    return launchable(best, er, outs);
 }
 inline Tiles input_gradient_tiles(const ExpertRows& er, int outs) {
     return launchable(few_wide_tiles(er, expected_rows(er), outs) ? Tiles::kSmall : Tiles::kWide, er,

@@ -33,9 +33,13 @@ static bool check(const ExpertRows& er, int outs) {
                   wide = threads(er, kWideTile, outs);
     const int64_t likely = er.offsets ? er.rows / er.E : er.E > 8 ? (int64_t)er.cap * 8 / er.E : er.cap;
     const int64_t wide_tiles = ((likely + 255) / 256) * er.E * (((int64_t)outs + 255) / 256);
-    Tiles want = likely <= 8                          ? Tiles::kFew
-                 : likely <= 48 || wide_tiles < 256 ? Tiles::kSmall
-                                                      : Tiles::kWide;
+    const auto row_tiles_of = [&](const TileShape& t) { return threads(er, t, t.outs) / t.threads; };
+    const int64_t t32 = row_tiles_of(kFewTile), t128 = row_tiles_of(kSmallTile),
+                  t256 = row_tiles_of(kWideTile);
+    Tiles want = Tiles::kWide;
+    if (wide_tiles < 256 || (likely <= 48 && (er.offsets || t128 <= 512 || t128 == t256)))
+        want = Tiles::kSmall;
+    if (likely <= 8 && t32 <= (er.offsets ? 256 : 128)) want = Tiles::kFew;
     Tiles back = wide_tiles < 256 ? Tiles::kSmall : Tiles::kWide;
     if (want == Tiles::kFew && few >= limit) want = Tiles::kSmall;
     if (want == Tiles::kSmall && small >= limit) want = Tiles::kWide;
@@ -75,8 +79,20 @@ static bool check_split(int64_t count) {
 int main() {
     // slots of 1024 experts whose likely rows are few: 32-row tiles of the
     // capacity would be 2^24 workgroups of 256 threads
-    if (forward_tiles(with_counts(1024, 1024), 16384) != Tiles::kSmall) {
+    if (grid_fits(workgroups(with_counts(1024, 1024), kFewTile, 16384), kFewTile.threads) ||
+        forward_tiles(with_counts(1024, 1024), 16384) != Tiles::kWide) {
         std::printf("FAIL slots of 1024 experts\n");
+        return 1;
+    }
+    // a decode batch's slots, many experts, and rows that may all be of a few
+    if (forward_tiles(with_counts(64, 64), 4096) != Tiles::kFew ||
+        forward_tiles(with_counts(256, 128), 4096) != Tiles::kSmall ||
+        forward_tiles(with_counts(1024, 512), 4096) != Tiles::kWide ||
+        forward_tiles(with_offsets(64, 512), 4096) != Tiles::kFew ||
+        forward_tiles(with_offsets(256, 2048), 4096) != Tiles::kSmall ||
+        forward_tiles(with_offsets(1024, 8192), 4096) != Tiles::kSmall ||
+        forward_tiles(with_offsets(1024, 8), 4096) != Tiles::kFew) {
+        std::printf("FAIL many experts\n");
         return 1;
     }
     if (forward_tiles(with_offsets(1, INT32_MAX), 8) != Tiles::kNone ||

@@ -508,3 +508,59 @@ def test_rows_near_2_31():
                                            8, 8, ctypes.byref(er), y.data_ptr(), None, C.MOEDX_BF16,
                                            ctypes.byref(ex)))
     check_rows(y, powers)
+
+
+@pytest.mark.parametrize("E,cap", [(65, 32), (128, 32), (200, 128), (512, 300), (1024, 1), (1024, 130)])
+@pytest.mark.parametrize("dense", [False, True], ids=["few live", "all live"])
+def test_many_experts(E, cap, dense):
+    """More experts than a wave has lanes, in slots and in expert order: a tile's
+    expert is found past others, whichever tiles the buffer's size picks."""
+    dev = device()
+    K, N, dt = 72, 40, torch.bfloat16
+    buf = make_buffer(E, 1, 1, 1)
+    g = torch.Generator().manual_seed(E + cap)
+    counts = torch.randint(0 if cap > 1 else 1, min(cap, 3) + 1, (E,), generator=g)
+    if not dense:
+        counts *= (torch.rand(E, generator=g) < 0.03).long()
+        counts[E - 1] = min(cap, 2)
+    if cap > 64:
+        counts[E // 2], counts[63], counts[64] = cap, cap - 1, 33
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int64), counts.cumsum(0)])
+    M = int(offsets[-1])
+    ex = torch.repeat_interleave(torch.arange(E), counts)  # the expert of each row
+    slot = (torch.arange(M) - offsets[ex]).to(dev)
+    ex = ex.to(dev)
+    x = torch.randn(M, K, generator=g).to(dev).to(dt)
+    w = (torch.randn(E, N, K, generator=g) * K ** -0.5).to(dev).to(dt)
+    d_y = torch.randn(M, N, generator=g).to(dev).to(dt)
+    rows, cnt = offsets.int().to(dev), counts.int().to(dev)
+    slots_x = torch.full((E, cap, K), float("nan"), dtype=dt, device=dev)
+    slots_d = torch.full((E, cap, N), float("nan"), dtype=dt, device=dev)
+    slots_x[ex, slot], slots_d[ex, slot] = x, d_y
+    print(f"[linear] {E} experts, slots of {cap}, {M} rows", flush=True)
+    y, _, _ = buf.expert_linear(x, w, rows)
+    sy, _, _ = buf.expert_linear(slots_x, w, cnt,
+                                 out=torch.full((E, cap, N), 7.0, dtype=dt, device=dev))
+    d_x, d_w, _ = buf.expert_linear_backward(d_y, x, w, rows)
+    s_dx, s_dw, _ = buf.expert_linear_backward(
+        slots_d, slots_x, w, cnt, out=torch.full((E, cap, K), 7.0, dtype=dt, device=dev))
+    we, xd, dd = w.double()[ex], x.double(), d_y.double()
+    want = (we * xd[:, None, :]).sum(2)
+    acc = (K + 1) * V * (we.abs() * xd.abs()[:, None, :]).sum(2)
+    check("y", y, want, acc, dt)
+    check("y in slots", sy[ex, slot], want, acc, dt)
+    want = (we * dd[:, :, None]).sum(1)
+    acc = (N + 1) * V * (we.abs() * dd.abs()[:, :, None]).sum(1)
+    check("d_x", d_x, want, acc, dt)
+    check("d_x in slots", s_dx[ex, slot], want, acc, dt)
+    want = torch.zeros(E, N, K, dtype=torch.float64, device=dev)
+    size = torch.zeros_like(want)
+    outer = dd[:, :, None] * xd[:, None, :]
+    want.index_add_(0, ex, outer)
+    size.index_add_(0, ex, outer.abs())
+    n = counts.to(dev).double()[:, None, None] + 1
+    check("d_w", d_w, want, n * V * size, dt)
+    check("d_w in slots", s_dw, want, n * V * size, dt)
+    empty = torch.ones(E, cap, dtype=torch.bool, device=dev)
+    empty[ex, slot] = False
+    assert (sy[empty] == 7.0).all() and (s_dx[empty] == 7.0).all()
