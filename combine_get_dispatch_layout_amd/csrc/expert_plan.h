@@ -94,10 +94,10 @@ constexpr int64_t kFewLikely = 8;
 
 // But every workgroup, also one past the last tile, looks through the experts'
 // rows for its own, so small tiles of a buffer that may hold many rows cost more
-// than they save: the few-row kernel stays below so many 32-row tiles, 128 x 128
-// of slots below so many 128-row tiles unless 256-row tiles are as many.  Slots
-// may be nearly all empty, hence their lower bound.  4096 -> 2048, us, few-row
-// kernel and 128 x 128:
+// than they save: the few-row kernel stays below so many 32-row tiles, of slots,
+// which may be nearly all empty, below so many looks at 64 experts; 128 x 128 of
+// slots stays below so many 128-row tiles unless 256-row tiles are as many.
+// 4096 -> 2048, us, few-row kernel and 128 x 128:
 //   offsets, 256 experts, 256 and 320 tiles   704  741    715  728
 //   the same, 1024 -> 1024                    106  104    124  105
 //   2048 rows of 2 of 256 experts (7168 -> 2048)          441   79
@@ -112,10 +112,11 @@ constexpr int64_t kFewLikely = 8;
 //   512 experts, 1024 tiles (256)            1482 1468    130  108
 //   1024 experts, 1024 tiles (128)           2814 2911    226  259
 //   1024 experts, 4096 tiles (512)           3475 3148    830  465
-constexpr int64_t kFewTiles = 256, kFewSlotTiles = 128, kSmallSlotTiles = 512;
+constexpr int64_t kFewTiles = 256, kFewSlotLooks = 256, kSmallSlotTiles = 512;
 
 inline bool few_serves(const ExpertRows& er) {
-    return max_tiles(er, kFewTile.rows) <= (er.offsets ? kFewTiles : kFewSlotTiles);
+    const int64_t tiles = max_tiles(er, kFewTile.rows);
+    return er.offsets ? tiles <= kFewTiles : tiles * tiles_of(er.E, 64) <= kFewSlotLooks;
 }
 inline bool small_serves(const ExpertRows& er) {
     const int64_t tiles = max_tiles(er, kSmallTile.rows);

@@ -39,7 +39,7 @@ static bool check(const ExpertRows& er, int outs) {
     Tiles want = Tiles::kWide;
     if (wide_tiles < 256 || (likely <= 48 && (er.offsets || t128 <= 512 || t128 == t256)))
         want = Tiles::kSmall;
-    if (likely <= 8 && t32 <= (er.offsets ? 256 : 128)) want = Tiles::kFew;
+    if (likely <= 8 && (er.offsets ? t32 : t32 * ((er.E + 63) / 64)) <= 256) want = Tiles::kFew;
     Tiles back = wide_tiles < 256 ? Tiles::kSmall : Tiles::kWide;
     if (want == Tiles::kFew && few >= limit) want = Tiles::kSmall;
     if (want == Tiles::kSmall && small >= limit) want = Tiles::kWide;
@@ -85,7 +85,8 @@ int main() {
         return 1;
     }
     // a decode batch's slots, many experts, and rows that may all be of a few
-    if (forward_tiles(with_counts(64, 64), 4096) != Tiles::kFew ||
+    if (forward_tiles(with_counts(64, 71), 4096) != Tiles::kFew ||
+        forward_tiles(with_counts(128, 64), 4096) != Tiles::kSmall ||
         forward_tiles(with_counts(256, 128), 4096) != Tiles::kSmall ||
         forward_tiles(with_counts(1024, 512), 4096) != Tiles::kWide ||
         forward_tiles(with_offsets(64, 512), 4096) != Tiles::kFew ||
