@@ -138,6 +138,13 @@ SIGNATURES = {
     "moedx_expert_linear": (_I, [_P, _P, _P, _I, _I, _I, _ROWS, _I, _P, _P, _EX]),
     "moedx_expert_linear_backward": (_I, [_P, _P, _P, _P, _I, _I, _I, _ROWS, _P, _P, _I, _EX]),
     "moedx_expert_swiglu_backward": (_I, [_P, _P, _P, _I, _I, _ROWS, _P, _EX]),
+    "moedx_expert_quantize": (_I, [_P, _P, _I, _I, _I, _ROWS, _P, _P, _EX]),
+    "moedx_expert_dequantize": (_I, [_P, _P, _P, _I, _I, _ROWS, _P, _I, _EX]),
+    "moedx_expert_sort_int8": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _EX]),
+    "moedx_expert_linear_int8": (_I, [_P, _P, _P, _P, _P, _I, _I, _ROWS, _I, _P, _I, _EX]),
+    "moedx_expert_linear_backward_int8": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _ROWS, _P, _P,
+                                               _I, _EX]),
+    "moedx_expert_swiglu_backward_int8": (_I, [_P, _P, _P, _P, _I, _I, _I, _ROWS, _P, _P, _EX]),
 }
 
 

@@ -199,6 +199,9 @@ class Handle:
 
 _DTYPES = {torch.bfloat16: C.MOEDX_BF16, torch.float16: C.MOEDX_F16, torch.float32: C.MOEDX_F32}
 _PRODUCT_DTYPES = (torch.bfloat16, torch.float16)
+# What every call takes beside its own arguments.
+_OPTIONS = {"previous_event": None, "async_finish": False, "allocate_on_comm_stream": False,
+            "no_sync": False}
 _SCORES = {"softmax": C.MOEDX_GATE_SOFTMAX, "sigmoid": C.MOEDX_GATE_SIGMOID}
 
 
@@ -848,3 +851,193 @@ class Buffer:
                                                ctypes.byref(ex)))
         self._keep(allocate_on_comm_stream, d_h, pre, t, d_pre)
         return d_pre, self._event(done)
+
+    # -- the experts' rows in int8 -----------------------------------------------------
+    # These calls take the options of every call by name: previous_event,
+    # async_finish, allocate_on_comm_stream, no_sync.
+    @staticmethod
+    def _options(options: dict) -> tuple:
+        for name in options:
+            if name not in _OPTIONS:
+                raise TypeError(f"unexpected argument {name!r}, expected one of {list(_OPTIONS)}")
+        return tuple(options.get(name, default) for name, default in _OPTIONS.items())
+
+    def _any_rows(self, rows, x: torch.Tensor, previous_event):
+        """_expert_rows, or every row of x where `rows` is None."""
+        if rows is not None:
+            return self._expert_rows(rows, x, previous_event)
+        return C.moedx_expert_rows(None, None, x.numel() // max(x.shape[-1], 1)), None
+
+    @staticmethod
+    def _scale_shape(lead: tuple, H: int, block: int) -> tuple:
+        if block not in (0, 128):
+            raise ValueError(f"block={block} must be 0 (a scale per row) or 128")
+        return lead if block == 0 else lead + ((H + block - 1) // block,)
+
+    def _codes(self, name: str, codes, scales, width, previous_event):
+        """(codes, scales, block) checked: int8 rows [*, width] with their scales."""
+        lead = self._lead(name, codes)
+        codes = self._check(name, codes, (torch.int8,), lead + (width,), previous_event)
+        if not isinstance(scales, torch.Tensor):
+            raise ValueError(f"{name}'s scales must be a tensor")
+        block = 0 if scales.dim() == len(lead) else 128
+        scales = self._check(f"{name}'s scales", scales, (torch.float32,),
+                             self._scale_shape(lead, codes.shape[-1], block), previous_event)
+        return codes, scales, block
+
+    def expert_quantize(self, x: torch.Tensor, rows=None, block: int = 0,
+                        out: Optional[torch.Tensor] = None,
+                        scales: Optional[torch.Tensor] = None, **options):
+        """Returns (codes int8, scales fp32, event) of ``x`` [M, H] with ``rows``
+        an ExpertOrder (or its int32 expert_offsets), or [E, cap, H] with
+        ``rows`` int32 recv_count (bf16, fp16 or fp32); ``rows`` None takes every
+        row (weights [E, N, K]).  ``block`` 0: a scale per row (scales [M] or
+        [E, cap]: what expert_linear_int8 takes); 128: one per 128 values
+        (scales [*, ceil(H / 128)]: finer, for saved rows).  A value is code *
+        scale; codes are in [-127, 127], a scale is the largest magnitude /
+        127.  Rows with an inf or NaN stay NaN.  Rows of no expert are left as
+        they were in ``out`` and ``scales`` (unspecified without).  The backward
+        calls in int8 and expert_dequantize take codes and scales as they are."""
+        prev, async_finish, comm, no_sync = self._options(options)
+        lead = self._lead("x", x)
+        x = self._check("x", x, _DTYPES, lead + (None,), prev)
+        H = x.shape[-1]
+        er, t = self._any_rows(rows, x, prev)
+        codes = self._out("out", out, torch.int8, lead + (H,))
+        scales = self._out("scales", scales, torch.float32, self._scale_shape(lead, H, block))
+        ex, done = self._exec_here(prev, async_finish, comm, no_sync)
+        C.check(C.moedx_expert_quantize(self.ctx, _addr(x), _DTYPES[x.dtype], H, block,
+                                        ctypes.byref(er), _addr(codes), _addr(scales),
+                                        ctypes.byref(ex)))
+        self._keep(comm, x, t, codes, scales)
+        return codes, scales, self._event(done)
+
+    def expert_dequantize(self, codes: torch.Tensor, scales: torch.Tensor, rows=None,
+                          dtype: torch.dtype = torch.bfloat16,
+                          out: Optional[torch.Tensor] = None, **options):
+        """Returns (x, event): expert_quantize's rows restored in ``dtype``, code *
+        scale rounded once.  Rows of no expert are left as they were."""
+        prev, async_finish, comm, no_sync = self._options(options)
+        codes, scales, block = self._codes("codes", codes, scales, None, prev)
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype={dtype} must be one of {list(_DTYPES)}")
+        er, t = self._any_rows(rows, codes, prev)
+        x = self._out("out", out, dtype, tuple(codes.shape))
+        ex, done = self._exec_here(prev, async_finish, comm, no_sync)
+        C.check(C.moedx_expert_dequantize(self.ctx, _addr(codes), _addr(scales), codes.shape[-1],
+                                          block, ctypes.byref(er), _addr(x), _DTYPES[dtype],
+                                          ctypes.byref(ex)))
+        self._keep(comm, codes, scales, t, x)
+        return x, self._event(done)
+
+    def expert_sort_int8(self, x: torch.Tensor, order: ExpertOrder,
+                         out: Optional[torch.Tensor] = None,
+                         scales: Optional[torch.Tensor] = None, **options):
+        """Returns (codes [T * K, H] int8, scales [T * K] fp32, event): expert_sort
+        and expert_quantize in one: each row of ``x`` [T, H] is quantised once,
+        with one scale, and put at its filled slots' rows in expert order.
+        Rows past the last pair are left as they were."""
+        prev, async_finish, comm, no_sync = self._options(options)
+        T, K = order.row_of_slot.shape
+        x = self._check("x", x, _DTYPES, (T, None), prev)
+        H = x.shape[1]
+        ros = self._check("row_of_slot", order.row_of_slot, (torch.int32,), (T, K), prev)
+        codes = self._out("out", out, torch.int8, (T * K, H))
+        scales = self._out("scales", scales, torch.float32, (T * K,))
+        ex, done = self._exec_here(prev, async_finish, comm, no_sync)
+        C.check(C.moedx_expert_sort_int8(self.ctx, _addr(x), _DTYPES[x.dtype], T, K, H, _addr(ros),
+                                         _addr(codes), _addr(scales), ctypes.byref(ex)))
+        self._keep(comm, x, ros, codes, scales)
+        return codes, scales, self._event(done)
+
+    def expert_linear_int8(self, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
+                           w_scales: torch.Tensor, rows, swiglu: bool = False,
+                           dtype: torch.dtype = torch.bfloat16,
+                           out: Optional[torch.Tensor] = None, **options):
+        """Returns (y, event): expert_linear in int8.  ``x`` and its scales are
+        expert_quantize's (or expert_sort_int8's) with a scale per row, ``w``
+        [E, N, K] int8 with ``w_scales`` [E, N] a model's weights, quantised once
+        (expert_quantize(w)).  y is of ``dtype`` (bf16 or fp16): the exact
+        integer sum times both scales, with ``swiglu`` as expert_linear.  A
+        row's results do not depend on its place or on other rows."""
+        prev, async_finish, comm, no_sync = self._options(options)
+        x, x_scales, block = self._codes("x", x, x_scales, None, prev)
+        if block:
+            raise ValueError("x's scales must be one per row (block=0)")
+        lead, K = tuple(x.shape[:-1]), x.shape[-1]
+        w = self._check("w", w, (torch.int8,), (self.num_experts, None, K), prev)
+        N = w.shape[1]
+        w_scales = self._check("w_scales", w_scales, (torch.float32,), (self.num_experts, N), prev)
+        if dtype not in _PRODUCT_DTYPES:
+            raise ValueError(f"dtype={dtype} must be one of {list(_PRODUCT_DTYPES)}")
+        if swiglu:
+            if N % 2 != 0:
+                raise ValueError(f"w has {N} rows per expert, expected gate and up halves")
+            N //= 2
+        er, t = self._expert_rows(rows, x, prev)
+        y = self._out("out", out, dtype, lead + (N,))
+        ex, done = self._exec_here(prev, async_finish, comm, no_sync)
+        C.check(C.moedx_expert_linear_int8(self.ctx, _addr(x), _addr(x_scales), _addr(w),
+                                           _addr(w_scales), K, N, ctypes.byref(er),
+                                           1 if swiglu else 0, _addr(y), _DTYPES[dtype],
+                                           ctypes.byref(ex)))
+        self._keep(comm, x, x_scales, w, w_scales, t, y)
+        return y, self._event(done)
+
+    def expert_linear_backward_int8(self, d_y: torch.Tensor, x: torch.Tensor,
+                                    x_scales: torch.Tensor, w: Optional[torch.Tensor], rows,
+                                    out: Optional[torch.Tensor] = None,
+                                    d_w: Optional[torch.Tensor] = None, d_w_dtype=None, **options):
+        """Returns (d_x, d_w, event): expert_linear_backward of rows that were
+        saved in int8 (expert_quantize, either block): d_w is that of
+        expert_dequantize(x) in d_y's dtype, without the restored rows in
+        memory.  ``w`` None leaves d_x out (None)."""
+        prev, async_finish, comm, no_sync = self._options(options)
+        x, x_scales, block = self._codes("x", x, x_scales, None, prev)
+        lead, K = tuple(x.shape[:-1]), x.shape[-1]
+        d_y = self._check("d_y", d_y, _PRODUCT_DTYPES, lead + (None,), prev)
+        N = d_y.shape[-1]
+        if w is not None:
+            w = self._check("w", w, (d_y.dtype,), (self.num_experts, N, K), prev)
+        elif out is not None:
+            raise ValueError("out needs w")
+        if d_w_dtype is None:
+            d_w_dtype = d_y.dtype if d_w is None else d_w.dtype
+        if d_w_dtype not in (d_y.dtype, torch.float32):
+            raise ValueError(f"d_w_dtype={d_w_dtype} must be {d_y.dtype} or torch.float32")
+        er, t = self._expert_rows(rows, x, prev)
+        d_x = None if w is None else self._out("out", out, d_y.dtype, lead + (K,))
+        d_w = self._out("d_w", d_w, d_w_dtype, (self.num_experts, N, K))
+        ex, done = self._exec_here(prev, async_finish, comm, no_sync)
+        C.check(C.moedx_expert_linear_backward_int8(
+            self.ctx, _addr(d_y), _addr(x), _addr(x_scales), block, _addr(w), _DTYPES[d_y.dtype], K,
+            N, ctypes.byref(er), _addr(d_x), _addr(d_w), _DTYPES[d_w_dtype], ctypes.byref(ex)))
+        self._keep(comm, d_y, x, x_scales, w, t, d_x, d_w)
+        return d_x, d_w, self._event(done)
+
+    def expert_swiglu_backward_int8(self, d_h: torch.Tensor, pre: torch.Tensor,
+                                    pre_scales: torch.Tensor, rows, return_h: bool = False,
+                                    out: Optional[torch.Tensor] = None,
+                                    h: Optional[torch.Tensor] = None, **options):
+        """Returns (d_pre [*, 2N], h, event): expert_swiglu_backward at (gate, up)
+        values saved in int8 (expert_quantize of expert_linear's pre).  With
+        ``return_h`` (or ``h`` to write to) also the activation's output [*, N] at
+        them, which the next weight gradient takes: neither pre nor h need be
+        kept in 16 bits.  Rows of no expert are left as they were."""
+        prev, async_finish, comm, no_sync = self._options(options)
+        lead = self._lead("d_h", d_h)
+        d_h = self._check("d_h", d_h, _PRODUCT_DTYPES, lead + (None,), prev)
+        N = d_h.shape[-1]
+        pre, pre_scales, block = self._codes("pre", pre, pre_scales, 2 * N, prev)
+        if tuple(pre.shape[:-1]) != lead:
+            raise ValueError(f"pre has shape {tuple(pre.shape)}, expected {lead + (2 * N,)}")
+        er, t = self._expert_rows(rows, d_h, prev)
+        d_pre = self._out("out", out, d_h.dtype, lead + (2 * N,))
+        if return_h or h is not None:
+            h = self._out("h", h, d_h.dtype, lead + (N,))
+        ex, done = self._exec_here(prev, async_finish, comm, no_sync)
+        C.check(C.moedx_expert_swiglu_backward_int8(
+            self.ctx, _addr(d_h), _addr(pre), _addr(pre_scales), block, _DTYPES[d_h.dtype], N,
+            ctypes.byref(er), _addr(d_pre), _addr(h), ctypes.byref(ex)))
+        self._keep(comm, d_h, pre, pre_scales, t, d_pre, h)
+        return d_pre, h, self._event(done)

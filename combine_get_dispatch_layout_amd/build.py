@@ -18,7 +18,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoedx.so")
 
 SOURCES = ["layout.hip", "pack.hip", "combine.hip", "ll.hip", "gate.hip",
-           "expert_rows.hip", "expert_linear.hip", "api.cpp"]
+           "expert_rows.hip", "expert_linear.hip", "expert_int8.hip", "expert_linear_int8.hip",
+           "api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1318,15 +1318,7 @@ int check_moves(int dtype, int T, int K, int H) {
     return MOEDX_OK;
 }
 
-int check_products(const moedx_ctx* ctx, int dtype, int K, int N, int w_rows_per_out,
-                   const moedx_expert_rows* er) {
-    if (int rc = check_dtype(dtype, false)) return rc;
-    if (K < 8 || K % 8 != 0 || K > (1 << 20))
-        return fail(MOEDX_EINVAL, "K=%d must be a positive multiple of 8 up to 2^20", K);
-    if (N < 8 || N % 8 != 0 || N > (1 << 20))
-        return fail(MOEDX_EINVAL, "N=%d must be a positive multiple of 8 up to 2^20", N);
-    if ((int64_t)w_rows_per_out * N * K * 2 >= ((int64_t)1 << 31))
-        return fail(MOEDX_EINVAL, "an expert's weights (N=%d, K=%d) exceed 2^31 bytes", N, K);
+int check_rows(const moedx_ctx* ctx, const moedx_expert_rows* er) {
     if (!er) return fail(MOEDX_EINVAL, "expert rows are NULL");
     if (er->rows < 0 || er->rows > INT32_MAX)
         return fail(MOEDX_EINVAL, "rows=%lld outside [0, 2^31)", (long long)er->rows);
@@ -1340,6 +1332,18 @@ int check_products(const moedx_ctx* ctx, int dtype, int K, int N, int w_rows_per
     return MOEDX_OK;
 }
 
+int check_products(const moedx_ctx* ctx, int dtype, int K, int N, int w_rows_per_out,
+                   const moedx_expert_rows* er) {
+    if (int rc = check_dtype(dtype, false)) return rc;
+    if (K < 8 || K % 8 != 0 || K > (1 << 20))
+        return fail(MOEDX_EINVAL, "K=%d must be a positive multiple of 8 up to 2^20", K);
+    if (N < 8 || N % 8 != 0 || N > (1 << 20))
+        return fail(MOEDX_EINVAL, "N=%d must be a positive multiple of 8 up to 2^20", N);
+    if ((int64_t)w_rows_per_out * N * K * 2 >= ((int64_t)1 << 31))
+        return fail(MOEDX_EINVAL, "an expert's weights (N=%d, K=%d) exceed 2^31 bytes", N, K);
+    return check_rows(ctx, er);
+}
+
 ExpertRows expert_rows(const moedx_ctx* ctx, const moedx_expert_rows* er) {
     return ExpertRows{er->offsets, er->counts, er->counts ? (int)(er->rows / ctx->E) : 0, ctx->E,
                       er->rows};
@@ -1348,6 +1352,27 @@ ExpertRows expert_rows(const moedx_ctx* ctx, const moedx_expert_rows* er) {
 // The array that says which rows are an expert's.
 Bytes rows_array(const moedx_ctx* ctx, const moedx_expert_rows* er) {
     return er->offsets ? Bytes{er->offsets, (ctx->E + 1) * 4} : Bytes{er->counts, ctx->E * 4};
+}
+
+// Rows of H codes with their scales.
+int check_codes(int H, int block) {
+    if (H < 16 || H % 16 != 0 || H > (1 << 20))
+        return fail(MOEDX_EINVAL, "a row of %d codes must be a positive multiple of 16 up to 2^20", H);
+    if (block != 0 && block != 128) return fail(MOEDX_EINVAL, "block=%d must be 0 or 128", block);
+    return MOEDX_OK;
+}
+
+int64_t scales_bytes(int64_t rows, int H, int block) {
+    return rows * (block ? (H + block - 1) / block : 1) * 4;
+}
+
+// As check_products' expert rows, but neither array is needed.
+int check_any_rows(const moedx_ctx* ctx, const moedx_expert_rows* er) {
+    if (!er) return fail(MOEDX_EINVAL, "expert rows are NULL");
+    if (er->offsets || er->counts) return check_rows(ctx, er);
+    if (er->rows < 0 || er->rows > INT32_MAX)
+        return fail(MOEDX_EINVAL, "rows=%lld outside [0, 2^31)", (long long)er->rows);
+    return MOEDX_OK;
 }
 
 int check_grid(bool fits, const moedx_expert_rows* er, int K, int N) {
@@ -1642,6 +1667,190 @@ int moedx_expert_swiglu_backward(moedx_ctx* ctx, const void* d_h, const void* pr
     else
         HIP_OR_FAIL(launch_swiglu_backward(d_h, pre, dtype, expert_rows(ctx, er), N, d_pre,
                                            ex.launch()));
+    return exec_end(ex);
+}
+
+// ---- rows in int8 ---------------------------------------------------------------
+
+int moedx_expert_quantize(moedx_ctx* ctx, const void* x, int dtype, int H, int block,
+                          const moedx_expert_rows* er, int8_t* codes, float* scales,
+                          const moedx_exec* exec) {
+    if (int rc = check_ctx(ctx)) return rc;
+    if (int rc = check_dtype(dtype, true)) return rc;
+    if (int rc = check_codes(H, block)) return rc;
+    if (int rc = check_any_rows(ctx, er)) return rc;
+    if (er->rows > 0 && (!x || !codes || !scales)) return fail(MOEDX_EINVAL, "NULL device pointer");
+    if (!aligned16(x) || !aligned16(codes) || !aligned4(scales))
+        return fail(MOEDX_EINVAL, "x and codes must be 16-byte, scales 4-byte aligned");
+    const Bytes xb{x, er->rows * H * dtype_bytes(dtype)}, cb{codes, er->rows * H};
+    const Bytes sb{scales, scales_bytes(er->rows, H, block)}, rb = rows_array(ctx, er);
+    if (int rc = check_apart(cb, {xb, sb, rb})) return rc;
+    if (int rc = check_apart(sb, {xb, rb})) return rc;
+    DeviceScope scope;
+    Exec ex;
+    if (int rc = exec_begin(ctx, exec, &ex)) return rc;
+    if (er->rows == 0)
+        HIP_OR_FAIL(ex.no_kernel());
+    else
+        HIP_OR_FAIL(launch_expert_quantize(x, dtype, expert_rows(ctx, er), H, block, codes, scales,
+                                           ex.launch()));
+    return exec_end(ex);
+}
+
+int moedx_expert_dequantize(moedx_ctx* ctx, const int8_t* codes, const float* scales, int H,
+                            int block, const moedx_expert_rows* er, void* x, int dtype,
+                            const moedx_exec* exec) {
+    if (int rc = check_ctx(ctx)) return rc;
+    if (int rc = check_dtype(dtype, true)) return rc;
+    if (int rc = check_codes(H, block)) return rc;
+    if (int rc = check_any_rows(ctx, er)) return rc;
+    if (er->rows > 0 && (!x || !codes || !scales)) return fail(MOEDX_EINVAL, "NULL device pointer");
+    if (!aligned16(x) || !aligned16(codes) || !aligned4(scales))
+        return fail(MOEDX_EINVAL, "x and codes must be 16-byte, scales 4-byte aligned");
+    if (int rc = check_apart({x, er->rows * H * dtype_bytes(dtype)},
+                             {{codes, er->rows * H}, {scales, scales_bytes(er->rows, H, block)},
+                              rows_array(ctx, er)}))
+        return rc;
+    DeviceScope scope;
+    Exec ex;
+    if (int rc = exec_begin(ctx, exec, &ex)) return rc;
+    if (er->rows == 0)
+        HIP_OR_FAIL(ex.no_kernel());
+    else
+        HIP_OR_FAIL(launch_expert_dequantize(codes, scales, expert_rows(ctx, er), H, block, x, dtype,
+                                             ex.launch()));
+    return exec_end(ex);
+}
+
+int moedx_expert_sort_int8(moedx_ctx* ctx, const void* x, int dtype, int T, int K, int H,
+                           const int32_t* row_of_slot, int8_t* codes, float* scales,
+                           const moedx_exec* exec) {
+    if (int rc = check_ctx(ctx)) return rc;
+    if (int rc = check_moves(dtype, T, K, H)) return rc;
+    if (int rc = check_codes(H, 0)) return rc;
+    if (T > 0 && (!x || !row_of_slot || !codes || !scales))
+        return fail(MOEDX_EINVAL, "NULL device pointer");
+    if (!aligned16(x) || !aligned16(codes) || !aligned4(row_of_slot) || !aligned4(scales))
+        return fail(MOEDX_EINVAL,
+                    "x and codes must be 16-byte, row_of_slot and scales 4-byte aligned");
+    const int64_t slots = (int64_t)T * K;
+    const Bytes xb{x, (int64_t)T * H * dtype_bytes(dtype)}, rb{row_of_slot, slots * 4};
+    const Bytes sb{scales, slots * 4};
+    if (int rc = check_apart({codes, slots * H}, {xb, rb, sb})) return rc;
+    if (int rc = check_apart(sb, {xb, rb})) return rc;
+    DeviceScope scope;
+    Exec ex;
+    if (int rc = exec_begin(ctx, exec, &ex)) return rc;
+    if (T == 0)
+        HIP_OR_FAIL(ex.no_kernel());
+    else
+        HIP_OR_FAIL(launch_expert_sort_int8(x, dtype, T, K, H, row_of_slot, codes, scales,
+                                            ex.launch()));
+    return exec_end(ex);
+}
+
+int moedx_expert_linear_int8(moedx_ctx* ctx, const int8_t* x, const float* x_scales, const int8_t* w,
+                             const float* w_scales, int K, int N, const moedx_expert_rows* er,
+                             int swiglu, void* y, int dtype, const moedx_exec* exec) {
+    if (int rc = check_ctx(ctx)) return rc;
+    if (swiglu != 0 && swiglu != 1) return fail(MOEDX_EINVAL, "swiglu=%d must be 0 or 1", swiglu);
+    if (K < 16 || K % 16 != 0 || K > (1 << 17) - 16)
+        return fail(MOEDX_EINVAL, "K=%d must be a positive multiple of 16 up to 2^17 - 16", K);
+    // K / 2 pairs of codes have the bytes of K / 2 values of 16 bits
+    if (int rc = check_products(ctx, dtype, K / 2, N, swiglu ? 2 : 1, er)) return rc;
+    if (int rc = check_grid(
+            forward_tiles(expert_rows(ctx, er), swiglu ? 2 * N : N) != Tiles::kNone, er, K, N))
+        return rc;
+    if (er->rows > 0 && (!x || !x_scales || !w || !w_scales || !y))
+        return fail(MOEDX_EINVAL, "NULL device pointer");
+    if (!aligned16(x) || !aligned16(w) || !aligned16(w_scales) || !aligned16(y) ||
+        !aligned4(x_scales))
+        return fail(MOEDX_EINVAL,
+                    "x, w, w_scales and y must be 16-byte, x_scales 4-byte aligned");
+    const int64_t outs = (int64_t)ctx->E * (swiglu ? 2 : 1) * N;
+    if (int rc = check_apart({y, er->rows * N * 2},
+                             {{x, er->rows * K}, {x_scales, er->rows * 4}, {w, outs * K},
+                              {w_scales, outs * 4}, rows_array(ctx, er)}))
+        return rc;
+    DeviceScope scope;
+    Exec ex;
+    if (int rc = exec_begin(ctx, exec, &ex)) return rc;
+    if (er->rows == 0)
+        HIP_OR_FAIL(ex.no_kernel());
+    else
+        HIP_OR_FAIL(launch_expert_linear_int8(x, x_scales, w, w_scales, expert_rows(ctx, er), K, N,
+                                              swiglu != 0, y, dtype, ex.launch()));
+    return exec_end(ex);
+}
+
+int moedx_expert_linear_backward_int8(moedx_ctx* ctx, const void* d_y, const int8_t* x,
+                                      const float* x_scales, int block, const void* w, int dtype,
+                                      int K, int N, const moedx_expert_rows* er, void* d_x,
+                                      void* d_w, int d_w_dtype, const moedx_exec* exec) {
+    if (int rc = check_ctx(ctx)) return rc;
+    if (int rc = check_products(ctx, dtype, K, N, 1, er)) return rc;
+    if (int rc = check_codes(K, block)) return rc;
+    if (d_w && d_w_dtype != dtype && d_w_dtype != MOEDX_F32)
+        return fail(MOEDX_EINVAL, "d_w_dtype=%d must be the dtype or MOEDX_F32", d_w_dtype);
+    if (!d_x && !d_w) return fail(MOEDX_EINVAL, "neither d_x nor d_w is asked for");
+    const ExpertRows rows = expert_rows(ctx, er);
+    if (int rc = check_grid(!d_x || input_gradient_tiles(rows, K) != Tiles::kNone, er, K, N))
+        return rc;
+    if (int rc = check_grid(!d_w || grid_fits(weight_workgroups(rows, K, N), kWeightTile.threads),
+                            er, K, N))
+        return rc;
+    if (er->rows > 0 && (!d_y || (d_x && !w) || (d_w && (!x || !x_scales))))
+        return fail(MOEDX_EINVAL, "NULL device pointer");
+    if (!aligned16(d_y) || !aligned16(x) || !aligned16(w) || !aligned16(d_x) || !aligned16(d_w) ||
+        !aligned4(x_scales))
+        return fail(MOEDX_EINVAL,
+                    "d_y, x, w, d_x and d_w must be 16-byte, x_scales 4-byte aligned");
+    const int64_t weights = (int64_t)ctx->E * N * K;
+    const Bytes dyb{d_y, er->rows * N * 2}, xb{x, er->rows * K}, wb{w, weights * 2};
+    const Bytes sb{x_scales, scales_bytes(er->rows, K, block)}, rb = rows_array(ctx, er);
+    const Bytes dxb{d_x, er->rows * K * 2}, dwb{d_w, weights * dtype_bytes(d_w_dtype)};
+    if (int rc = check_apart(dxb, {dyb, xb, sb, wb, dwb, rb})) return rc;
+    if (int rc = check_apart(dwb, {dyb, xb, sb, wb, rb})) return rc;
+    DeviceScope scope;
+    Exec ex;
+    if (int rc = exec_begin(ctx, exec, &ex)) return rc;
+    const bool dx = d_x && er->rows > 0;
+    if (!dx && !d_w) HIP_OR_FAIL(ex.no_kernel());
+    if (dx)
+        HIP_OR_FAIL(launch_expert_dgrad(d_y, w, dtype, rows, K, N, d_x,
+                                        Launch{ex.run, ex.start, d_w ? nullptr : ex.stop, 0u}));
+    if (d_w)
+        HIP_OR_FAIL(launch_expert_wgrad_int8(d_y, x, x_scales, block, dtype, rows, K, N, d_w,
+                                             d_w_dtype == MOEDX_F32,
+                                             Launch{ex.run, dx ? nullptr : ex.start, ex.stop, 0u}));
+    return exec_end(ex);
+}
+
+int moedx_expert_swiglu_backward_int8(moedx_ctx* ctx, const void* d_h, const int8_t* pre,
+                                      const float* pre_scales, int block, int dtype, int N,
+                                      const moedx_expert_rows* er, void* d_pre, void* h,
+                                      const moedx_exec* exec) {
+    if (int rc = check_ctx(ctx)) return rc;
+    if (int rc = check_products(ctx, dtype, 8, N, 2, er)) return rc;
+    if (int rc = check_codes(2 * N, block)) return rc;
+    if (er->rows > 0 && (!d_h || !pre || !pre_scales || !d_pre))
+        return fail(MOEDX_EINVAL, "NULL device pointer");
+    if (!aligned16(d_h) || !aligned16(pre) || !aligned16(d_pre) || !aligned16(h) ||
+        !aligned4(pre_scales))
+        return fail(MOEDX_EINVAL,
+                    "d_h, pre, d_pre and h must be 16-byte, pre_scales 4-byte aligned");
+    const Bytes db{d_h, er->rows * N * 2}, cb{pre, er->rows * N * 2}, hb{h, er->rows * N * 2};
+    const Bytes sb{pre_scales, scales_bytes(er->rows, 2 * N, block)}, rb = rows_array(ctx, er);
+    if (int rc = check_apart({d_pre, er->rows * N * 4}, {db, cb, sb, hb, rb})) return rc;
+    if (int rc = check_apart(hb, {db, cb, sb, rb})) return rc;
+    DeviceScope scope;
+    Exec ex;
+    if (int rc = exec_begin(ctx, exec, &ex)) return rc;
+    if (er->rows == 0)
+        HIP_OR_FAIL(ex.no_kernel());
+    else
+        HIP_OR_FAIL(launch_swiglu_backward_int8(d_h, pre, pre_scales, block, dtype,
+                                                expert_rows(ctx, er), N, d_pre, h, ex.launch()));
     return exec_end(ex);
 }
 

@@ -1,0 +1,446 @@
+// The experts' rows in int8 for gfx950: quantised (in place of order, or moved
+// into expert order), restored, and the gated activation's gradient from saved
+// (gate, up) values.
+//
+// A group (a row, or 128 values of it) with largest magnitude a:
+//   m = max(a, 2^-100), scale = m / 127, code = nearest even of x (127 / m),
+// every operation one fp32 rounding, so |code| <= 127 without a clamp (x (127 /
+// m) is at most 127 (1 + 2^-23)^2) and codes are the same on any machine.
+// Restored, a value is code * scale: off by at most half a scale and 2^-22 of
+// itself.  The floor keeps 127 / m finite; values below 2^-108 become 0.
+// Magnitudes are compared as bit patterns, NaN above inf: a group that holds
+// one gets a scale of inf or NaN and is NaN when it is restored.
+//
+// All of it is bound by memory.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "expert_launch.h"
+#include "expert_tile.h"
+#include "moedx.h"
+#include "numeric.h"
+
+namespace moedx {
+
+namespace {
+
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int64_t kGrid = 1 << 20;  // workgroups at most: they go on through the rows
+
+// Eight values of type S: what a lane takes of a row at a time.
+template <typename S>
+struct Unit {
+    static constexpr int kChunks = (int)sizeof(S) / 2;
+    u32x4_t c[kChunks];
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+            c[i] = __builtin_bit_cast(
+                u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(off + i * 16), 0, 0));
+    }
+    __device__ __forceinline__ void values(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            float part[Chunk<S>::kN];
+            chunk_to_f32<S>(c[i], part);
+#pragma unroll
+            for (int j = 0; j < Chunk<S>::kN; ++j) f[i * Chunk<S>::kN + j] = part[j];
+        }
+    }
+    // Adds its magnitudes to `top`: bit patterns, two of 16 bits or one of 32.
+    __device__ __forceinline__ uint32_t magnitude(uint32_t top) const {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(S) == 2)
+                    top = __builtin_bit_cast(
+                        uint32_t,
+                        __builtin_elementwise_max(__builtin_bit_cast(u16x2, top),
+                                                  __builtin_bit_cast(u16x2, c[i][j] & 0x7fff7fffu)));
+                else
+                    top = max(top, c[i][j] & 0x7fffffffu);
+            }
+        return top;
+    }
+};
+// One bit pattern of what magnitude() gave, and its value.
+template <typename S>
+__device__ __forceinline__ uint32_t one_magnitude(uint32_t top) {
+    return sizeof(S) == 2 ? max(top >> 16, top & 0xffffu) : top;
+}
+template <typename S>
+__device__ __forceinline__ float magnitude_value(uint32_t bits) {
+    if constexpr (sizeof(S) == 2) return (float)__builtin_bit_cast(S, (uint16_t)bits);
+    else return __builtin_bit_cast(float, bits);
+}
+
+struct Scale {
+    float scale, factor;
+    __device__ __forceinline__ explicit Scale(float a) {
+        const float m = a < 0x1p-100f ? 0x1p-100f : a;  // NaN stays
+        scale = m / 127.0f;
+        factor = 127.0f / m;
+    }
+};
+
+// Adding 1.5 * 2^23 leaves the nearest integer in the low bits.
+__device__ __forceinline__ uint32_t code_bits(float x, float factor) {
+    return __builtin_bit_cast(uint32_t, x * factor + 12582912.0f);
+}
+template <typename S>
+__device__ __forceinline__ u32x2_t codes_of(const Unit<S>& v, float factor) {
+    float f[8];
+    v.values(f);
+    u32x2_t o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t a = code_bits(f[4 * i], factor), b = code_bits(f[4 * i + 1], factor);
+        const uint32_t c = code_bits(f[4 * i + 2], factor), d = code_bits(f[4 * i + 3], factor);
+        o[i] = __builtin_amdgcn_perm(b, a, 0x0c0c0400u) | __builtin_amdgcn_perm(d, c, 0x04000c0cu);
+    }
+    return o;
+}
+
+// The eight values of a lane's codes.
+__device__ __forceinline__ void restored(u32x2_t c, float scale, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = in_fp32((float)(int8_t)(c[i >> 2] >> (8 * (i & 3))) * scale);
+}
+
+// Whether a row of the buffer is an expert's (with neither array, each is).
+struct LiveRows {
+    ExpertRows er;
+    FastDiv cap;  // by er.cap
+    __device__ __forceinline__ bool operator()(uint32_t row) const {
+        if (er.offsets) return (int)row >= er.offsets[0] && (int)row < er.offsets[er.E];
+        if (!er.counts) return true;
+        const uint32_t e = cap.div(row);
+        return (int)(row - e * (uint32_t)er.cap) < er.counts[e];
+    }
+};
+
+// A row by one wave, held in registers between its largest magnitude and its
+// codes: NU units a lane; longer rows (kLong) are read twice.  `to` gives the
+// codes and the scale their places.
+template <typename S, int NU, bool kLong, typename F>
+__device__ __forceinline__ void quantize_row(const S* x, int H, int lane, F&& to) {
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(x, H * (int)sizeof(S));
+    constexpr int kSpan = 64 * 8 * NU;  // values of one batch of loads
+    Unit<S> v[NU];
+    uint32_t top = 0;
+    const auto fetch = [&](int at) {
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+            v[u].load(rs, (uint32_t)(at + (u * 64 + lane) * 8) * (uint32_t)sizeof(S));
+    };
+    for (int at = 0; at < (kLong ? H : 1); at += kSpan) {
+        fetch(at);
+#pragma unroll
+        for (int u = 0; u < NU; ++u) top = v[u].magnitude(top);
+    }
+    const Scale s(magnitude_value<S>(wave_max(one_magnitude<S>(top))));
+    for (int at = 0; at < (kLong ? H : 1); at += kSpan) {
+        if (kLong) fetch(at);
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            const int k = at + (u * 64 + lane) * 8;
+            const u32x2_t c = codes_of(v[u], s.factor);
+            if (k < H) to.codes(k, c);
+        }
+    }
+    if (lane == 0) to.scale(s.scale);
+}
+
+template <typename S, int NU, bool kLong>
+__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const S* x, LiveRows live, int H,
+                                                                 int8_t* codes, float* scales) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int64_t row = (int64_t)blockIdx.x * kWaves + wave; row < live.er.rows;
+         row += (int64_t)gridDim.x * kWaves) {
+        if (!live((uint32_t)row)) continue;
+        struct {
+            int8_t* c;
+            float* s;
+            __device__ __forceinline__ void codes(int k, u32x2_t v) const {
+                *reinterpret_cast<u32x2_t*>(c + k) = v;
+            }
+            __device__ __forceinline__ void scale(float v) const { *s = v; }
+        } to{codes + row * H, scales + row};
+        quantize_row<S, NU, kLong>(x + row * H, H, lane, to);
+    }
+}
+
+// A token's row, quantised once, at the rows of its filled slots.
+template <typename S, int NU, bool kLong>
+__global__ __launch_bounds__(kThreads) void sort_int8_kernel(const S* x, int T, int K, int H,
+                                                             int64_t rows,
+                                                             const int32_t* row_of_slot,
+                                                             int8_t* codes, float* scales) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < T; t += (int64_t)gridDim.x * kWaves) {
+        int row = -1;
+        if (lane < K) row = row_of_slot[t * K + lane];
+        uint64_t filled = __ballot(row >= 0 && row < rows);
+        if (!filled) continue;
+        struct {
+            int8_t* c;
+            float* s;
+            uint64_t filled;
+            int row, H;
+            __device__ __forceinline__ void codes(int k, u32x2_t v) const {
+                for (uint64_t f = filled; f; f &= f - 1) {
+                    const int64_t r = __builtin_amdgcn_readlane(row, __builtin_ctzll(f));
+                    *reinterpret_cast<u32x2_t*>(c + r * H + k) = v;
+                }
+            }
+            __device__ __forceinline__ void scale(float v) const {
+                for (uint64_t f = filled; f; f &= f - 1)
+                    s[__builtin_amdgcn_readlane(row, __builtin_ctzll(f))] = v;
+            }
+        } to{codes, scales, filled, row, H};
+        quantize_row<S, NU, kLong>(x + t * H, H, lane, to);
+    }
+}
+
+constexpr int kBlock = 128, kBlockLanes = kBlock / 8;  // a lane has 8 values
+
+// Rows in groups of `per` to a workgroup, so that narrow rows fill it too.
+struct RowGroups {
+    int items;    // of a row
+    FastDiv div;  // by items
+    int per;
+};
+
+// 16 lanes to a block of 128 values.
+template <typename S>
+__global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const S* x, LiveRows live, int H,
+                                                                   RowGroups rg, int8_t* codes,
+                                                                   float* scales) {
+    constexpr int U = 4, kSlots = kThreads / kBlockLanes;
+    const int in = threadIdx.x % kBlockLanes, slot = threadIdx.x / kBlockLanes;
+    for (int64_t row0 = (int64_t)blockIdx.x * rg.per; row0 < live.er.rows;
+         row0 += (int64_t)gridDim.x * rg.per) {
+        const int rows = (int)min((int64_t)rg.per, live.er.rows - row0);
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(x + row0 * H, rows * H * (int)sizeof(S));
+        for (int i0 = 0; i0 < rows * rg.items; i0 += U * kSlots) {
+            Unit<S> v[U];
+            int r[U], g[U];
+            bool here[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * kSlots + slot;
+                r[u] = (int)rg.div.div((uint32_t)i);
+                g[u] = i - r[u] * rg.items;
+                const int k = g[u] * kBlock + in * 8;
+                here[u] = i < rows * rg.items && live((uint32_t)(row0 + r[u]));
+                v[u].load(rs, here[u] && k < H ? (uint32_t)(r[u] * H + k) * (uint32_t)sizeof(S)
+                                               : kOutside);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const Scale s(magnitude_value<S>(row_max(one_magnitude<S>(v[u].magnitude(0)))));
+                const int k = g[u] * kBlock + in * 8;
+                const int64_t row = row0 + r[u];
+                const u32x2_t c = codes_of(v[u], s.factor);
+                if (here[u] && k < H) *reinterpret_cast<u32x2_t*>(codes + row * H + k) = c;
+                if (here[u] && in == 0) scales[row * rg.items + g[u]] = s.scale;
+            }
+        }
+    }
+}
+
+template <typename S>
+__device__ __forceinline__ void store_unit(S* at, const float (&f)[8]) {
+    constexpr int N = Chunk<S>::kN;
+#pragma unroll
+    for (int i = 0; i < 8 / N; ++i) {
+        float part[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) part[j] = f[i * N + j];
+        *reinterpret_cast<u32x4_t*>(at + i * N) = chunk_from_f32<S>(part);
+    }
+}
+
+template <typename S>
+__global__ __launch_bounds__(kThreads) void dequantize_kernel(const int8_t* codes,
+                                                              const float* scales, LiveRows live,
+                                                              int H, int groups, RowGroups rg,
+                                                              S* x) {
+    constexpr int U = 4;
+    for (int64_t row0 = (int64_t)blockIdx.x * rg.per; row0 < live.er.rows;
+         row0 += (int64_t)gridDim.x * rg.per) {
+        const int rows = (int)min((int64_t)rg.per, live.er.rows - row0);
+        for (int i0 = threadIdx.x; i0 < rows * rg.items; i0 += U * kThreads) {
+            u32x2_t c[U];
+            float s[U];
+            int64_t at[U];
+            bool here[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * kThreads;
+                const int r = (int)rg.div.div((uint32_t)i), k = (i - r * rg.items) * 8;
+                const int64_t row = row0 + r;
+                here[u] = i < rows * rg.items && live((uint32_t)row);
+                at[u] = row * H + k;
+                if (here[u]) {
+                    c[u] = *reinterpret_cast<const u32x2_t*>(codes + at[u]);
+                    s[u] = groups ? scales[row * groups + k / kBlock] : scales[row];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (!here[u]) continue;
+                float f[8];
+                restored(c[u], s[u], f);
+                store_unit<S>(x + at[u], f);
+            }
+        }
+    }
+}
+
+template <typename S>
+__global__ __launch_bounds__(kThreads) void swiglu_backward_int8_kernel(
+    const S* d_h, const int8_t* codes, const float* scales, LiveRows live, int N, int groups,
+    RowGroups rg, S* d_pre, S* h) {
+    for (int64_t row0 = (int64_t)blockIdx.x * rg.per; row0 < live.er.rows;
+         row0 += (int64_t)gridDim.x * rg.per) {
+        const int rows = (int)min((int64_t)rg.per, live.er.rows - row0);
+        for (int i = threadIdx.x; i < rows * rg.items; i += kThreads) {
+            const int r = (int)rg.div.div((uint32_t)i), k = (i - r * rg.items) * 8;
+            const int64_t row = row0 + r;
+            if (!live((uint32_t)row)) continue;
+            const float* sr = scales + row * (groups ? groups : 1);
+            const float sg = sr[groups ? k / kBlock : 0], su = sr[groups ? (N + k) / kBlock : 0];
+            float d[8], g[8], u[8], out[8];
+            chunk_to_f32<S>(*reinterpret_cast<const u32x4_t*>(d_h + row * N + k), d);
+            restored(*reinterpret_cast<const u32x2_t*>(codes + row * 2 * N + k), sg, g);
+            restored(*reinterpret_cast<const u32x2_t*>(codes + row * 2 * N + N + k), su, u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float s = 1.0f / (1.0f + expf(-g[j]));
+                const float gs = g[j] * s;
+                out[j] = gs * u[j];
+                const float du = d[j] * gs;
+                g[j] = d[j] * u[j] * s * (1.0f + g[j] * (1.0f - s));
+                u[j] = du;
+            }
+            store_unit<S>(d_pre + row * 2 * N + k, g);
+            store_unit<S>(d_pre + row * 2 * N + N + k, u);
+            if (h) store_unit<S>(h + row * N + k, out);
+        }
+    }
+}
+
+LiveRows live_rows(const ExpertRows& er) {
+    return LiveRows{er, make_fastdiv((uint32_t)(er.cap > 0 ? er.cap : 1))};
+}
+// About `items` items to a workgroup, a row at least.
+RowGroups row_groups(int of_row, int items) {
+    return RowGroups{of_row, make_fastdiv((uint32_t)of_row), items > of_row ? items / of_row : 1};
+}
+dim3 grid_for(int64_t rows, int per) {
+    const int64_t n = (rows + per - 1) / per;
+    return dim3((unsigned)(n < kGrid ? n : kGrid));
+}
+
+// Calls f with the number of units per lane that hold a row, and whether it is
+// longer than any.
+template <typename F>
+hipError_t with_units(int H, F&& f) {
+    const int units = (H + 511) / 512;
+    if (units <= 1) return f(std::integral_constant<int, 1>{}, std::false_type{});
+    if (units <= 2) return f(std::integral_constant<int, 2>{}, std::false_type{});
+    if (units <= 4) return f(std::integral_constant<int, 4>{}, std::false_type{});
+    if (units <= 8) return f(std::integral_constant<int, 8>{}, std::false_type{});
+    if (units <= 16) return f(std::integral_constant<int, 16>{}, std::false_type{});
+    return f(std::integral_constant<int, 8>{}, std::true_type{});
+}
+
+template <typename S>
+hipError_t quantize_as(const void* x, const ExpertRows& er, int H, int block, int8_t* codes,
+                       float* scales, const Launch& L) {
+    const S* xs = static_cast<const S*>(x);
+    if (block) {
+        const RowGroups rg = row_groups((H + kBlock - 1) / kBlock, 64);
+        return launch_kernel(quantize_blocks_kernel<S>, grid_for(er.rows, rg.per), dim3(kThreads), L,
+                             xs, live_rows(er), H, rg, codes, scales);
+    }
+    return with_units(H, [&](auto nu, auto longer) {
+        return launch_kernel(quantize_rows_kernel<S, decltype(nu)::value, decltype(longer)::value>,
+                             grid_for(er.rows, kWaves), dim3(kThreads), L, xs, live_rows(er), H,
+                             codes, scales);
+    });
+}
+
+template <typename S>
+hipError_t sort_int8_as(const void* x, int T, int K, int H, const int32_t* row_of_slot,
+                        int8_t* codes, float* scales, const Launch& L) {
+    return with_units(H, [&](auto nu, auto longer) {
+        return launch_kernel(sort_int8_kernel<S, decltype(nu)::value, decltype(longer)::value>,
+                             grid_for(T, kWaves), dim3(kThreads), L, static_cast<const S*>(x), T, K,
+                             H, (int64_t)T * K, row_of_slot, codes, scales);
+    });
+}
+
+template <typename S>
+hipError_t dequantize_as(const int8_t* codes, const float* scales, const ExpertRows& er, int H,
+                         int block, void* x, const Launch& L) {
+    const RowGroups rg = row_groups(H / 8, 4 * kThreads);
+    return launch_kernel(dequantize_kernel<S>, grid_for(er.rows, rg.per), dim3(kThreads), L, codes,
+                         scales, live_rows(er), H, block ? (H + kBlock - 1) / kBlock : 0, rg,
+                         static_cast<S*>(x));
+}
+
+template <typename S>
+hipError_t swiglu_backward_int8_as(const void* d_h, const int8_t* codes, const float* scales,
+                                   const ExpertRows& er, int N, int block, void* d_pre, void* h,
+                                   const Launch& L) {
+    const RowGroups rg = row_groups(N / 8, kThreads);
+    return launch_kernel(swiglu_backward_int8_kernel<S>, grid_for(er.rows, rg.per), dim3(kThreads),
+                         L, static_cast<const S*>(d_h), codes, scales, live_rows(er), N,
+                         block ? (2 * N + kBlock - 1) / kBlock : 0, rg, static_cast<S*>(d_pre),
+                         static_cast<S*>(h));
+}
+
+}  // namespace
+
+hipError_t launch_expert_quantize(const void* x, int dtype, const ExpertRows& er, int H, int block,
+                                  int8_t* codes, float* scales, const Launch& L) {
+    const auto as = dtype == MOEDX_F32   ? quantize_as<float>
+                    : dtype == MOEDX_F16 ? quantize_as<_Float16>
+                                         : quantize_as<__bf16>;
+    return as(x, er, H, block, codes, scales, L);
+}
+
+hipError_t launch_expert_sort_int8(const void* x, int dtype, int T, int K, int H,
+                                   const int32_t* row_of_slot, int8_t* codes, float* scales,
+                                   const Launch& L) {
+    const auto as = dtype == MOEDX_F32   ? sort_int8_as<float>
+                    : dtype == MOEDX_F16 ? sort_int8_as<_Float16>
+                                         : sort_int8_as<__bf16>;
+    return as(x, T, K, H, row_of_slot, codes, scales, L);
+}
+
+hipError_t launch_expert_dequantize(const int8_t* codes, const float* scales, const ExpertRows& er,
+                                    int H, int block, void* x, int dtype, const Launch& L) {
+    const auto as = dtype == MOEDX_F32   ? dequantize_as<float>
+                    : dtype == MOEDX_F16 ? dequantize_as<_Float16>
+                                         : dequantize_as<__bf16>;
+    return as(codes, scales, er, H, block, x, L);
+}
+
+hipError_t launch_swiglu_backward_int8(const void* d_h, const int8_t* codes, const float* scales,
+                                       int block, int dtype, const ExpertRows& er, int N,
+                                       void* d_pre, void* h, const Launch& L) {
+    const auto as =
+        dtype == MOEDX_F16 ? swiglu_backward_int8_as<_Float16> : swiglu_backward_int8_as<__bf16>;
+    return as(d_h, codes, scales, er, N, block, d_pre, h, L);
+}
+
+}  // namespace moedx

@@ -91,4 +91,28 @@ hipError_t launch_expert_wgrad(const void* d_y, const void* x, int dtype, const 
 hipError_t launch_swiglu_backward(const void* d_h, const void* pre, int dtype,
                                   const ExpertRows& er, int N, void* d_pre, const Launch& L);
 
+// ---- rows in int8 ---------------------------------------------------------------
+
+// block: 0 (a scale per row) or 128 (one per 128 values).  With neither offsets
+// nor counts every row counts.
+hipError_t launch_expert_quantize(const void* x, int dtype, const ExpertRows& er, int H, int block,
+                                  int8_t* codes, float* scales, const Launch& L);
+hipError_t launch_expert_sort_int8(const void* x, int dtype, int T, int K, int H,
+                                   const int32_t* row_of_slot, int8_t* codes, float* scales,
+                                   const Launch& L);
+hipError_t launch_expert_dequantize(const int8_t* codes, const float* scales, const ExpertRows& er,
+                                    int H, int block, void* x, int dtype, const Launch& L);
+// y [rows, N] of `dtype` from codes x [rows, K] and w [E, N or 2N, K]
+hipError_t launch_expert_linear_int8(const int8_t* x, const float* x_scales, const int8_t* w,
+                                     const float* w_scales, const ExpertRows& er, int K, int N,
+                                     bool swiglu, void* y, int dtype, const Launch& L);
+// d_w [E, N, K] from d_y [rows, N] of `dtype` and codes x [rows, K]
+hipError_t launch_expert_wgrad_int8(const void* d_y, const int8_t* x, const float* x_scales,
+                                    int block, int dtype, const ExpertRows& er, int K, int N,
+                                    void* d_w, bool f32_out, const Launch& L);
+// d_pre [rows, 2N] and h [rows, N] (or null) from d_h and codes of pre [rows, 2N]
+hipError_t launch_swiglu_backward_int8(const void* d_h, const int8_t* codes, const float* scales,
+                                       int block, int dtype, const ExpertRows& er, int N,
+                                       void* d_pre, void* h, const Launch& L);
+
 }  // namespace moedx

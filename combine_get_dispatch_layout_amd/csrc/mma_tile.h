@@ -29,6 +29,7 @@
 namespace moedx {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
@@ -36,6 +37,7 @@ template <typename S>
 struct Mfma;
 template <>
 struct Mfma<__bf16> {
+    typedef f32x4 Acc;
     typedef __bf16 vec __attribute__((ext_vector_type(8)));
     static __device__ __forceinline__ f32x4 mul(s16x8 a, s16x8 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(vec, a),
@@ -44,13 +46,28 @@ struct Mfma<__bf16> {
 };
 template <>
 struct Mfma<_Float16> {
+    typedef f32x4 Acc;
     typedef _Float16 vec __attribute__((ext_vector_type(8)));
     static __device__ __forceinline__ f32x4 mul(s16x8 a, s16x8 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(vec, a),
                                                       __builtin_bit_cast(vec, b), c, 0, 0, 0);
     }
 };
-
+// Two int8 values: a reduction of K int8 values is one of K / 2 of these, with
+// the same bytes per row, stage and fragment.  A fragment's 16 bytes are 16
+// reduction values of one row, the same ones in both operands; the sums are
+// exact integers.  16 x 16 x 64.
+struct Codes2 {
+    int8_t v[2];
+};
+template <>
+struct Mfma<Codes2> {
+    typedef i32x4 Acc;
+    static __device__ __forceinline__ i32x4 mul(s16x8 a, s16x8 b, i32x4 c) {
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
+                                                     __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+    }
+};
 
 // LDS is addressed through pointers of its own address space, one offset from
 // the array's start per access: the compiler then knows which array a load
@@ -252,6 +269,7 @@ __device__ __forceinline__ int q_block(int wq, int j) {
 // r would be fetched in half lines, which costs the forward product 20%.
 template <typename S, int BP, int BQ, int WP, int WQ, int NQ, typename LP, typename LQ>
 struct SharedCuLoop {
+    typedef typename Mfma<S>::Acc Acc;
     static constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;
     static constexpr int kBK = 32, kBuffers = 3;
     static constexpr int kStageLoads = LP::kLoads + LQ::kLoads;
@@ -281,7 +299,7 @@ struct SharedCuLoop {
     // every wave has read.  Past the reduction's end a load leaves zeros.
     __device__ __forceinline__ void stage(const LP& gp, const LQ& gq, const lds_char* lp,
                                           const lds_char* lq, lds_char* np, lds_char* nq, int it,
-                                          int wave, f32x4 (&acc)[TP][TQ]) const {
+                                          int wave, Acc (&acc)[TP][TQ]) const {
         s16x8 p[TP], q[NQ];
         load(gp, gq, np, nq, it + 2, wave);
 #pragma unroll
@@ -307,7 +325,7 @@ struct SharedCuLoop {
     }
     __device__ __forceinline__ void run(const LP& gp, const LQ& gq, lds_char* lp0, lds_char* lq0,
                                         lds_char* lp1, lds_char* lq1, lds_char* lp2, lds_char* lq2,
-                                        int nk, int wave, f32x4 (&acc)[TP][TQ]) const {
+                                        int nk, int wave, Acc (&acc)[TP][TQ]) const {
         if (nk <= 0) return;
         // The stages past a multiple of three go first, in the last buffers, so
         // that the loop always starts at buffer 0.
@@ -361,6 +379,7 @@ struct SharedCuLoop {
 template <typename S, int BP, int BQ, int WP, int WQ, int NQ, int kP, int kQ, bool kPartQ,
           typename LP, typename LQ>
 struct RingLoop {
+    typedef typename Mfma<S>::Acc Acc;
     static constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;
     static constexpr int kBK = 64;
     static constexpr int kPBytes = BP * kBK * 2, kQBytes = BQ * kBK * 2;
@@ -389,7 +408,7 @@ struct RingLoop {
         for (int j = 0; j < NQ; ++j) q[j] = aq.frag(lq, j * 16 * WQ, kk);
     }
     static __device__ __forceinline__ void products(const s16x8 (&p)[TP], const s16x8 (&q)[TQ],
-                                                    f32x4 (&acc)[TP][TQ]) {
+                                                    Acc (&acc)[TP][TQ]) {
 #pragma unroll
         for (int j = 0; j < NQ; ++j)
 #pragma unroll
@@ -400,7 +419,7 @@ struct RingLoop {
     __device__ __forceinline__ void first(const lds_char* rp, const lds_char* rq,
                                           const s16x8 (&p0)[TP], const s16x8 (&q0)[TQ],
                                           s16x8 (&p1)[TP], s16x8 (&q1)[TQ],
-                                          f32x4 (&acc)[TP][TQ]) const {
+                                          Acc (&acc)[TP][TQ]) const {
         frags(rp, rq, 1, p1, q1);
         products(p0, q0, acc);
         interleave<false>();
@@ -415,7 +434,7 @@ struct RingLoop {
                                            lds_char* __restrict wp, lds_char* __restrict wq, int it,
                                            int wave, s16x8 (&p0)[TP], s16x8 (&q0)[TQ],
                                            const s16x8 (&p1)[TP], const s16x8 (&q1)[TQ],
-                                           f32x4 (&acc)[TP][TQ]) const {
+                                           Acc (&acc)[TP][TQ]) const {
         frags(rp, rq, 0, p0, q0);
         gq.template load<kQLoads>(wq, place(it + kQ), wave);
         // The waits count loads in this order: no load may pass here.
@@ -453,7 +472,7 @@ struct RingLoop {
         __builtin_amdgcn_sched_barrier(0);
     }
     __device__ __forceinline__ void run(const LP& gp, const LQ& gq, lds_char* lp, lds_char* lq,
-                                        int wave, f32x4 (&acc)[TP][TQ]) const {
+                                        int wave, Acc (&acc)[TP][TQ]) const {
         if (stages <= 0) return;
         // in the order in which they are needed
 #pragma unroll

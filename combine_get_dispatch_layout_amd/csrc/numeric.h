@@ -33,6 +33,13 @@ __device__ __forceinline__ u32x4_t chunk_from_f32(const float (&f)[Chunk<S>::kN]
     return __builtin_bit_cast(u32x4_t, v);
 }
 
+// v, rounded to fp32: the compiler may fold a product into its conversion to
+// fp16 (one rounding instead of two), in one kernel and not in another.
+__device__ __forceinline__ float in_fp32(float v) {
+    asm("" : "+v"(v));
+    return v;
+}
+
 // Reductions over the 64 lanes of a wave by lane-shifted operands (no LDS
 // traffic): rows of 16 first, then across rows; lane 63 holds the result,
 // which every lane gets.  The order is fixed.

@@ -577,6 +577,73 @@ MOEDX_API int moedx_expert_swiglu_backward(moedx_ctx *ctx, const void *d_h, cons
                                            int dtype, int N, const moedx_expert_rows *er,
                                            void *d_pre, const moedx_exec *exec);
 
+/* ---- the experts' rows in int8 --------------------------------------------------- */
+
+/* A row of H values (H a multiple of 16 up to 2^20) is held as H int8 codes and
+ * fp32 scales: with block 0 one scale for the row ([rows]), with block 128 one
+ * for each 128 values of it and for the rest ([rows, ceil(H / 128)]).  For a
+ * group's largest magnitude a: m = max(a, 2^-100), scale = m / 127, and a code
+ * is x * (127 / m) to nearest even, each operation rounded once to fp32; codes
+ * are in [-127, 127].  A value held is code * scale.  A group with an inf or
+ * a NaN has a scale of inf or NaN, unspecified codes, and is NaN when it is
+ * restored or multiplied.  codes are 16-byte aligned, scales 4-byte (16 in
+ * moedx_expert_linear_int8's w_scales).  moedx_expert_rows as above; to
+ * quantize and to dequantize, offsets and counts may both be NULL: all rows are
+ * taken (weights [E, N, K] are E * N of them). */
+
+/* codes [rows, H] and scales of x [rows, H] of type `dtype` (MOEDX_BF16, F16 or
+ * F32), 16-byte aligned.  Rows of no expert are neither read nor written. */
+MOEDX_API int moedx_expert_quantize(moedx_ctx *ctx, const void *x, int dtype, int H, int block,
+                                    const moedx_expert_rows *er, int8_t *codes, float *scales,
+                                    const moedx_exec *exec);
+
+/* x [rows, H] of type `dtype` (MOEDX_BF16, F16 or F32): code * scale in fp32,
+ * rounded once. */
+MOEDX_API int moedx_expert_dequantize(moedx_ctx *ctx, const int8_t *codes, const float *scales,
+                                      int H, int block, const moedx_expert_rows *er, void *x,
+                                      int dtype, const moedx_exec *exec);
+
+/* moedx_expert_sort of quantized rows: codes[row_of_slot[t, k]] and
+ * scales[row_of_slot[t, k]] = x[t]'s (block 0) for every filled slot; x [T, H]
+ * of type `dtype`, codes [T * K, H], scales [T * K].  Limits as there, and
+ * H % 16 == 0. */
+MOEDX_API int moedx_expert_sort_int8(moedx_ctx *ctx, const void *x, int dtype, int T, int K, int H,
+                                     const int32_t *row_of_slot, int8_t *codes, float *scales,
+                                     const moedx_exec *exec);
+
+/* y[m, n] = (sum_k x[m, k] w[e(m), n, k]) * x_scales[m] * w_scales[e(m), n] of
+ * type `dtype` (MOEDX_BF16 or F16): codes x [rows, K] and w [E, N, K] with a scale
+ * per row (x_scales [rows], w_scales [E, N]); int32 sums, which are exact, then
+ * two fp32 products in this order and one rounding: a row's outputs do not
+ * depend on the buffer or its place in it.  swiglu as in moedx_expert_linear (w
+ * [E, 2N, K], w_scales [E, 2N]), from the scaled fp32 values.  K a multiple of 16
+ * up to 2^17 - 16 (sums of any codes, -128 too, stay within 31 bits); N and
+ * the rest as there. */
+MOEDX_API int moedx_expert_linear_int8(moedx_ctx *ctx, const int8_t *x, const float *x_scales,
+                                       const int8_t *w, const float *w_scales, int K, int N,
+                                       const moedx_expert_rows *er, int swiglu, void *y, int dtype,
+                                       const moedx_exec *exec);
+
+/* moedx_expert_linear_backward with x held in int8 (codes [rows, K], scales by
+ * block): d_w is that of the values moedx_expert_dequantize restores in `dtype`
+ * (MOEDX_BF16 or F16, the type of d_y, w and d_x); d_x does not need x.  K a
+ * multiple of 16; limits, NULL outputs and d_w_dtype as there. */
+MOEDX_API int moedx_expert_linear_backward_int8(moedx_ctx *ctx, const void *d_y, const int8_t *x,
+                                                const float *x_scales, int block, const void *w,
+                                                int dtype, int K, int N,
+                                                const moedx_expert_rows *er, void *d_x, void *d_w,
+                                                int d_w_dtype, const moedx_exec *exec);
+
+/* moedx_expert_swiglu_backward with pre = (g, u) held in int8 (codes [rows, 2N],
+ * scales by block, groups of a row's 2N values), restored in fp32; h (or NULL)
+ * receives [rows, N] = g / (1 + exp(-g)) * u, the activation computed again.  N
+ * a multiple of 8 up to 2^19. */
+MOEDX_API int moedx_expert_swiglu_backward_int8(moedx_ctx *ctx, const void *d_h,
+                                                const int8_t *pre, const float *pre_scales,
+                                                int block, int dtype, int N,
+                                                const moedx_expert_rows *er, void *d_pre, void *h,
+                                                const moedx_exec *exec);
+
 #ifdef __cplusplus
 }
 #endif
