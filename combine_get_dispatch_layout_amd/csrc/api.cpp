@@ -1796,8 +1796,9 @@ int moedx_expert_linear_backward_int8(moedx_ctx* ctx, const void* d_y, const int
     const ExpertRows rows = expert_rows(ctx, er);
     if (int rc = check_grid(!d_x || input_gradient_tiles(rows, K) != Tiles::kNone, er, K, N))
         return rc;
-    if (int rc = check_grid(!d_w || grid_fits(weight_workgroups(rows, K, N), kWeightTile.threads),
-                            er, K, N))
+    if (int rc = check_grid(
+            !d_w || grid_fits(weight_workgroups(rows, K, N, kSavedTile), kSavedTile.threads), er, K,
+            N))
         return rc;
     if (er->rows > 0 && (!d_y || (d_x && !w) || (d_w && (!x || !x_scales))))
         return fail(MOEDX_EINVAL, "NULL device pointer");

@@ -232,13 +232,138 @@ struct AcrossCodes {
     }
 };
 
+// The weight gradient's loop with P in codes.  Q's stages go straight into one of
+// four LDS buffers, three stages ahead; P's come into registers as far ahead and
+// are restored into the other of two LDS buffers one stage ahead, under the
+// products.  Buffers are arrays of their own and stages a compile-time place
+// among them: then the compiler knows which one a load into LDS writes and adds
+// no wait before the reads of another.
+template <typename S, int BP, int BQ, int WP, int WQ, int NQ, typename LP, typename LQ>
+struct SavedLoop {
+    typedef typename Mfma<S>::Acc Acc;
+    typedef typename LP::Stage Hold;
+    static constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;
+    static constexpr int kBK = 32, kAhead = 3, kQ = kAhead + 1, kP = 2;
+    static constexpr int kStageLoads = LQ::kLoads + 2 * LP::kLoads;
+    typename LP::At ap;
+    typename LQ::At aq;
+    lds_char *lp[kP], *lq[kQ];
+    int wave, lane;
+
+    __device__ __forceinline__ SavedLoop(int wp, int wq, int wave_, int lane_)
+        : wave(wave_), lane(lane_) {
+        ap.init(wp * (BP / WP), lane);
+        aq.init(wq * 16, lane);
+    }
+    // Past this only the kAhead - 1 stages after the next one are in flight.
+    static __device__ __forceinline__ void arrive() {
+        constexpr int kLeft = (kAhead - 1) * kStageLoads;
+        static_assert(kLeft < 64, "the wait's count has 6 bits");
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt((kLeft & 15) | (kLeft >> 4) << 14 | 0x70);  // lgkmcnt 0
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    // Asks for stage `it`, whose place is V.
+    template <int V>
+    __device__ __forceinline__ void ask(const LP& gp, const LQ& gq, Hold& hold, int it) const {
+        gq.load(lq[V % kQ], (uint32_t)it * kBK, wave);
+        gp.fetch(hold, (uint32_t)it * kBK);
+    }
+    // Multiplies stage `it` (place V), restores stage it + 1 and asks for stage it
+    // + kAhead.
+    template <int V>
+    __device__ __forceinline__ void stage(const LP& gp, const LQ& gq, Hold (&hold)[2], int it,
+                                          Acc (&acc)[TP][TQ]) const {
+        s16x8 p[TP], q[NQ];
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) q[j] = aq.frag(lq[V % kQ], j * 16 * WQ, 0);
+#pragma unroll
+        for (int i = 0; i < TP; ++i) p[i] = ap.frag(lp[V % kP], i * 16, 0);
+        gp.store(hold[(V + 1) % 2], lp[(V + 1) % kP], wave, lane);
+        ask<V + kAhead>(gp, gq, hold[(V + kAhead) % 2], it + kAhead);
+#pragma unroll
+        for (int i = 0; i < TP; ++i)
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) acc[i][j] = Mfma<S>::mul(p[i], q[j], acc[i][j]);
+        arrive();
+    }
+    // Stages 0 .. kAhead - 1 at places V ..
+    template <int V>
+    __device__ __forceinline__ void begin(const LP& gp, const LQ& gq, Hold (&hold)[2]) const {
+        Hold first;
+        ask<V>(gp, gq, first, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        ask<V + 1>(gp, gq, hold[(V + 1) % 2], 1);
+        __builtin_amdgcn_sched_barrier(0);
+        ask<V + 2>(gp, gq, hold[(V + 2) % 2], 2);
+        __builtin_amdgcn_sched_barrier(0);
+        gp.store(first, lp[V % kP], wave, lane);
+        arrive();
+    }
+    __device__ __forceinline__ void run(const LP& gp, const LQ& gq, int nk,
+                                        Acc (&acc)[TP][TQ]) const {
+        if (nk <= 0) return;
+        Hold hold[2];
+        // Stages past a multiple of four go first, at the last places, so that the
+        // loop always starts at place 0.  Each number has a path of its own: where
+        // paths with different loads in flight meet, the compiler waits for all.
+        int it = nk % 4;
+        if (it == 0) {
+            begin<0>(gp, gq, hold);
+        } else if (it == 1) {
+            begin<3>(gp, gq, hold);
+            stage<3>(gp, gq, hold, 0, acc);
+        } else if (it == 2) {
+            begin<2>(gp, gq, hold);
+            stage<2>(gp, gq, hold, 0, acc);
+            stage<3>(gp, gq, hold, 1, acc);
+        } else {
+            begin<1>(gp, gq, hold);
+            stage<1>(gp, gq, hold, 0, acc);
+            stage<2>(gp, gq, hold, 1, acc);
+            stage<3>(gp, gq, hold, 2, acc);
+        }
+        for (; it < nk; it += 4) {
+            stage<0>(gp, gq, hold, it, acc);
+            stage<1>(gp, gq, hold, it + 1, acc);
+            stage<2>(gp, gq, hold, it + 2, acc);
+            stage<3>(gp, gq, hold, it + 3, acc);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS is left in flight
+    }
+};
+
+// 128 x 256: the P side, which is restored, is the narrow one (256 x 128: 1015 us
+// for 966 at 64 experts of 768 rows, 4096 x 2048); two workgroups share a CU.
+typedef Shape<128, 256, 2, 32, 2, 4> Saved;
+static_assert(same(Saved::kTile, kSavedTile), "the plan's tile is the kernel's");
+
+// Runs f with the number of Q blocks per wave that `rows` rows need, made even.
+template <int WQ, typename F>
+__device__ __forceinline__ void with_even_blocks(int rows, F&& f) {
+    const int n = (rows + 16 * WQ - 1) / (16 * WQ);
+    if (n > 6) f(std::integral_constant<int, 8>{});
+    else if (n > 4) f(std::integral_constant<int, 6>{});
+    else if (n > 2) f(std::integral_constant<int, 4>{});
+    else f(std::integral_constant<int, 2>{});
+}
+
+// The gradient is written once, as whole cache lines past the caches: a wave's
+// sums go through LDS in strips of 16 rows.  64 experts, 4096 x 2048, us per
+// call with lines, with 64-byte pieces from the registers, and what writing the
+// gradient alone takes at 6.5 TB/s (165; fp32 330):
+//   rows each    16       48       96       192      384      768
+//   bf16       166 249  195 298  246 368  330 470  597 626  942 975
+//   fp32       447 503  425 429  422 539  454 715  788 886 1126 1174
 template <typename S, typename D>
-__global__ __launch_bounds__(Narrow::kThreads, 2) void wgrad_int8_kernel(
+__global__ __launch_bounds__(Saved::kThreads, 2) void wgrad_int8_kernel(
     const S* d_y, const int8_t* x, const float* scales, int groups, ExpertRows er, int K, int N,
     int cols, int rows, D* d_w) {
-    typedef Narrow T;
-    __shared__ __align__(16) S lp[T::BP * T::BK];
-    __shared__ __align__(16) S lq[T::BQ * T::BK];
+    typedef Saved T;
+    __shared__ __align__(16) S lp0[T::BP * T::BK], lp1[T::BP * T::BK];
+    __shared__ __align__(16) S lq0[T::BQ * T::BK], lq1[T::BQ * T::BK], lq2[T::BQ * T::BK],
+        lq3[T::BQ * T::BK];
     int b = xcd_run_block<kRunLog2>((int)blockIdx.x, (int)gridDim.x);
     const int e = b / (cols * rows);
     b -= e * cols * rows;
@@ -252,57 +377,58 @@ __global__ __launch_bounds__(Narrow::kThreads, 2) void wgrad_int8_kernel(
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wp = wave % T::WP, wq = wave / T::WP;
     const int count = s.end - s.begin;
-    typedef AcrossCodes<S, T::BP, T::kWaves, T::BK> GP;
-    typedef Across<T::BQ, T::kWaves, T::BK> GQ;
-    GP gp;
+    AcrossCodes<S, T::BP, T::kWaves, T::BK> gp;
     gp.init(x + (int64_t)s.begin * K, scales + (int64_t)s.begin * (groups ? groups : 1), K, groups,
             count, k0, K, wave, lane);
-    GQ gq;
+    Across<T::BQ, T::kWaves, T::BK> gq;
     gq.init(d_y + (int64_t)s.begin * N, N * 2, count, n0, N, wave, lane);
-    with_blocks<T::WQ>(N - n0, [&](auto nq) {
+    with_even_blocks<T::WQ>(N - n0, [&](auto nq) {
         constexpr int NQ = decltype(nq)::value;
         f32x4 acc[T::TP][T::TQ] = {};
-        typename GP::At ap;
-        typename GQ::At aq;
-        ap.init(wp * (T::BP / 2 / T::WP), lane);
-        aq.init(wq * 16, lane);
-        const int nk = row_tiles<T::BK>(count);
-        for (int it = 0; it < nk; ++it) {
-            typename GP::Stage st;
-            gq.load((lds_char*)lq, (uint32_t)it * T::BK, wave);
-            gp.fetch(st, (uint32_t)it * T::BK);
-            gp.store(st, (lds_char*)lp, wave, lane);
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            s16x8 p[T::TP], q[NQ];
-#pragma unroll
-            for (int j = 0; j < NQ; ++j) q[j] = aq.frag((lds_char*)lq, j * 16 * T::WQ, 0);
-#pragma unroll
-            for (int i = 0; i < T::TP; ++i)
-                p[i] = ap.frag((lds_char*)lp, p_step<T::BP, T::WP>(i), 0);
-#pragma unroll
-            for (int i = 0; i < T::TP; ++i)
-#pragma unroll
-                for (int j = 0; j < NQ; ++j) acc[i][j] = Mfma<S>::mul(p[i], q[j], acc[i][j]);
-            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        }
+        SavedLoop<S, T::BP, T::BQ, T::WP, T::WQ, NQ, decltype(gp), decltype(gq)> loop(wp, wq, wave,
+                                                                                      lane);
+        loop.lp[0] = (lds_char*)lp0;
+        loop.lp[1] = (lds_char*)lp1;
+        loop.lq[0] = (lds_char*)lq0;
+        loop.lq[1] = (lds_char*)lq1;
+        loop.lq[2] = (lds_char*)lq2;
+        loop.lq[3] = (lds_char*)lq3;
+        loop.run(gp, gq, row_tiles<T::BK>(count), acc);
+        __syncthreads();  // every wave's reads and loads are done: Q's buffers are free
+        lds_char* const mine = wave == 0   ? loop.lq[0]
+                               : wave == 1 ? loop.lq[1]
+                               : wave == 2 ? loop.lq[2]
+                                           : loop.lq[3];
+        constexpr int kCols = T::BP / T::WP, kRow = kCols * (int)sizeof(D) + 16;
+        constexpr int kLanes = kCols * (int)sizeof(D) / 16, kRows = 64 / kLanes;
+        static_assert(2 * 16 * kRow <= T::BQ * T::BK * 2, "two strips in a buffer");
+        typedef __attribute__((address_space(3))) u32x4_t lds_u32x4;
+        typedef D vec4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) vec4 lds_vec4;
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            const int n = n0 + T::q_at(wq, j) + (lane & 15);
-            D* const row = d_w + ((int64_t)e * N + n) * K;
-            if constexpr (sizeof(D) == 2) {
+            lds_char* const strip = mine + j % 2 * 16 * kRow;
 #pragma unroll
-                for (int i = 0; i < T::TP; i += 2) {
-                    const int k = k0 + T::p_at(wp, i) + pair_at(lane);
-                    const u32x4_t v = pack_pair<D>(acc[i][j], acc[i + 1][j]);
-                    if (n < N && k < K) store8(row + k, v);
-                }
-            } else {
+            for (int i = 0; i < T::TP; ++i) {
+                vec4 v;
 #pragma unroll
-                for (int i = 0; i < T::TP; ++i) {
-                    const int k = k0 + T::p_at(wp, i) + 4 * (lane >> 4);
-                    if (n < N && k < K) store4(row + k, acc[i][j]);
-                }
+                for (int r = 0; r < 4; ++r) v[r] = (D)acc[i][j][r];
+                *(lds_vec4*)(strip + (lane & 15) * kRow +
+                             (i * 16 + 4 * (lane >> 4)) * (int)sizeof(D)) = v;
             }
+            // the wave's own strip: its LDS accesses are in order, the compiler's are
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int h = 0; h < 16 / kRows; ++h) {
+                const int row = h * kRows + lane / kLanes, c = lane % kLanes;
+                const u32x4_t v = *(lds_u32x4*)(strip + row * kRow + c * 16);
+                const int n = n0 + T::q_at(wq, j) + row;
+                const int k = k0 + wp * kCols + c * (16 / (int)sizeof(D));
+                if (n < N && k < K)
+                    __builtin_nontemporal_store(
+                        v, reinterpret_cast<u32x4_t*>(d_w + ((int64_t)e * N + n) * K + k));
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
     });
 }
@@ -345,13 +471,13 @@ template <typename S>
 hipError_t wgrad_int8_as(const void* d_y, const int8_t* x, const float* scales, int groups,
                          const ExpertRows& er, int K, int N, void* d_w, bool f32_out,
                          const Launch& L) {
-    const int cols = (int)tiles_of(K, Narrow::BP), rows = (int)tiles_of(N, Narrow::BQ);
-    const dim3 grid = grid_of(weight_workgroups(er, K, N));
+    const int cols = (int)tiles_of(K, Saved::BP), rows = (int)tiles_of(N, Saved::BQ);
+    const dim3 grid = grid_of(weight_workgroups(er, K, N, kSavedTile));
     const S* ds = static_cast<const S*>(d_y);
     if (f32_out)
-        return launch_kernel(wgrad_int8_kernel<S, float>, grid, dim3(Narrow::kThreads), L, ds, x,
+        return launch_kernel(wgrad_int8_kernel<S, float>, grid, dim3(Saved::kThreads), L, ds, x,
                              scales, groups, er, K, N, cols, rows, static_cast<float*>(d_w));
-    return launch_kernel(wgrad_int8_kernel<S, S>, grid, dim3(Narrow::kThreads), L, ds, x, scales,
+    return launch_kernel(wgrad_int8_kernel<S, S>, grid, dim3(Saved::kThreads), L, ds, x, scales,
                          groups, er, K, N, cols, rows, static_cast<S*>(d_w));
 }
 

@@ -30,6 +30,8 @@ struct TileShape {
 constexpr TileShape kFewTile{32, 32, 256}, kSmallTile{128, 128, 256}, kWideTile{256, 256, 512};
 // Of a weight gradient: weight rows (N) and columns (K).
 constexpr TileShape kWeightTile{128, 256, 256};
+// The same from rows saved in int8.
+constexpr TileShape kSavedTile{256, 128, 256};
 
 // An expert's rows (up to 2^31 - 1) are dealt evenly to its ceil(count / BM)
 // tiles, in steps of 64 rows (16 for small tiles): two full tiles and one of 20
@@ -58,8 +60,9 @@ inline int64_t max_tiles(const ExpertRows& er, int bm) {
 inline int64_t workgroups(const ExpertRows& er, const TileShape& t, int outs) {
     return max_tiles(er, t.rows) * tiles_of(outs, t.outs);
 }
-inline int64_t weight_workgroups(const ExpertRows& er, int K, int N) {
-    return er.E * tiles_of(N, kWeightTile.rows) * tiles_of(K, kWeightTile.outs);
+inline int64_t weight_workgroups(const ExpertRows& er, int K, int N,
+                                 const TileShape& t = kWeightTile) {
+    return er.E * tiles_of(N, t.rows) * tiles_of(K, t.outs);
 }
 
 // HIP counts a grid's threads in 32 bits.

@@ -627,7 +627,8 @@ MOEDX_API int moedx_expert_linear_int8(moedx_ctx *ctx, const int8_t *x, const fl
 /* moedx_expert_linear_backward with x held in int8 (codes [rows, K], scales by
  * block): d_w is that of the values moedx_expert_dequantize restores in `dtype`
  * (MOEDX_BF16 or F16, the type of d_y, w and d_x); d_x does not need x.  K a
- * multiple of 16; limits, NULL outputs and d_w_dtype as there. */
+ * multiple of 16; NULL outputs, d_w_dtype and limits as there, but the tiles of
+ * d_w, E * ceil(N / 256) * ceil(K / 128), are below 2^24. */
 MOEDX_API int moedx_expert_linear_backward_int8(moedx_ctx *ctx, const void *d_y, const int8_t *x,
                                                 const float *x_scales, int block, const void *w,
                                                 int dtype, int K, int N,
