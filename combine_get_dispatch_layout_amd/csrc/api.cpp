@@ -1759,7 +1759,7 @@ int moedx_expert_linear_int8(moedx_ctx* ctx, const int8_t* x, const float* x_sca
     // K / 2 pairs of codes have the bytes of K / 2 values of 16 bits
     if (int rc = check_products(ctx, dtype, K / 2, N, swiglu ? 2 : 1, er)) return rc;
     if (int rc = check_grid(
-            forward_tiles(expert_rows(ctx, er), swiglu ? 2 * N : N) != Tiles::kNone, er, K, N))
+            int8_tiles(expert_rows(ctx, er), swiglu ? 2 * N : N) != Int8Tiles::kNone, er, K, N))
         return rc;
     if (er->rows > 0 && (!x || !x_scales || !w || !w_scales || !y))
         return fail(MOEDX_EINVAL, "NULL device pointer");

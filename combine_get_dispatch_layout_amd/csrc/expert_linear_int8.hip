@@ -15,6 +15,8 @@ namespace moedx {
 
 namespace {
 
+constexpr int kStream = 2;  // a load's policy: past the caches
+
 // The tiles are those of the 16-bit product (mma_tile.h) over Codes2: the same
 // bytes per stage and the same instructions, each of twice the multiplications.
 // Sums are exact integers, so a row's outputs depend on nothing but the row and
@@ -33,7 +35,7 @@ __device__ __forceinline__ f32x4 scales4(const float* ws, int n, int N) {
     return v;
 }
 
-template <typename S, bool kSwiglu, typename T>
+template <typename S, bool kSwiglu, typename T, int kPolicy>
 __global__ __launch_bounds__(T::kThreads, 2) void linear_int8_kernel(
     const int8_t* x, const float* xs, const int8_t* w, const float* ws, ExpertRows er, int K, int N,
     int cols, S* y, bool rotate) {
@@ -48,7 +50,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_int8_kernel(
     const int n0 = tile.col * (kSwiglu ? T::BP / 2 : T::BP);
     const int64_t first = (int64_t)tile.e * (kSwiglu ? 2 : 1) * N;  // the expert's weight rows
     const int8_t* we = w + (first + n0) * K;
-    Along<T::BP, T::kWaves, T::BK, kSwiglu ? 2 : 1> gp;
+    Along<T::BP, T::kWaves, T::BK, kSwiglu ? 2 : 1, kPolicy> gp;
     gp.init(K, K / 2, wave, lane);
     gp.half(0, we, N - n0);
     if constexpr (kSwiglu) gp.half(1, we + (int64_t)N * K, N - n0);
@@ -101,68 +103,122 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_int8_kernel(
     });
 }
 
-// Few rows per expert: weights straight into registers (few_products).
-template <typename S, bool kSwiglu>
-__global__ __launch_bounds__(kFewThreads) void linear_int8_few_kernel(
+// Few rows per expert: the weights' bytes are all that counts.  A tile has BP
+// weight rows (gate and up halves in a gated product) and up to BQ rows of x;
+// each of its 4 waves multiplies a quarter of the weight rows with all of x.
+// Stages of 128 codes go straight into a ring of kStages LDS buffers, all but one
+// of them in flight, the weights in whole cache lines past the caches.
+constexpr int kThinRunLog2 = 3;  // as in the 16-bit few-row kernel
+template <int BP_, int BQ_, int kStages_>
+struct Thin {
+    static constexpr int BP = BP_, BQ = BQ_, kStages = kStages_, kWaves = 4;
+    static constexpr TileShape kTile{BQ, BP, kWaves * 64};
+};
+typedef Thin<64, 32, 6> ThinNarrow;   // 72 KB of LDS each: two workgroups share a CU
+typedef Thin<128, 64, 3> ThinWhole;
+static_assert(same(ThinNarrow::kTile, kNarrowTile) && same(ThinWhole::kTile, kThinTile),
+              "the plan's tiles are the kernels'");
+
+// 64 experts of 7168 -> 4096, one row each: 266 us, the weights at 7.06 TB/s (loaded
+// through the caches, in the first kernel's 64-byte pieces: 318).
+template <typename S, bool kSwiglu, typename T>
+__global__ __launch_bounds__(T::kTile.threads) void linear_int8_thin_kernel(
     const int8_t* x, const float* xs, const int8_t* w, const float* ws, ExpertRows er, int K, int N,
     int cols, S* y, bool rotate) {
-    constexpr int kOut = kSwiglu ? kFewP / 2 : kFewP;  // blocks of outputs
-    __shared__ i32x4 part[kFewWaves][kFewBlocks][kFewP][64];
-    const int blk = xcd_run_block<kFewRunLog2>((int)blockIdx.x, (int)gridDim.x);
-    const RowTile tile = find_block<kFewRows, kRowGroup>(er, blk, cols);
+    constexpr int BP = T::BP, BQ = T::BQ, BK = 64, NW = T::kWaves, R = T::kStages;
+    constexpr int TP = BP / 64, TQ = BQ / 16;
+    constexpr int kPBytes = BP * BK * 2, kQBytes = BQ * BK * 2;
+    __shared__ __align__(16) char lds[R * (kPBytes + kQBytes)];
+    const int blk = xcd_run_block<kThinRunLog2>((int)blockIdx.x, (int)gridDim.x);
+    const RowTile tile = find_block<BQ, kRowGroup>(er, blk, cols);
     if (tile.e < 0) return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = tile.col * kOut * 16;
+    constexpr int kOuts = kSwiglu ? BP / 2 : BP;
+    const int n0 = tile.col * kOuts;
     const int64_t first = (int64_t)tile.e * (kSwiglu ? 2 : 1) * N;
     const int rows = tile.end - tile.begin;
-    FewRows wr[kFewP], xr[kFewBlocks];
+    typedef Along<BP, NW, BK, kSwiglu ? 2 : 1, kStream> GP;
+    typedef Along<BQ, NW, BK, 1> GQ;
+    GP gp;
+    gp.init(K, K / 2, wave, lane);
+    gp.half(0, w + (first + n0) * K, N - n0);
+    if constexpr (kSwiglu) gp.half(1, w + (first + N + n0) * K, N - n0);
+    GQ gq;
+    gq.init(K, K / 2, wave, lane);
+    gq.half(0, x + (int64_t)tile.begin * K, rows);
+    typename GP::At ap;
+    ap.init(wave * 16, lane);
+    typename GQ::At aq;
+    aq.init(0, lane);
+    const int nk = (K / 2 + BK - 1) / BK, shift = rotate ? scattered(blk, nk) : 0;
+    lds_char* const lp = (lds_char*)lds;
+    lds_char* const lq = lp + R * kPBytes;
+    const auto ask = [&](int it, int buf) {
+        int s = it + shift;
+        s -= s >= nk ? nk : 0;
+        const int k0 = (it < nk ? s : nk) * BK;  // past the last stage: nothing
+        gp.load(lp + buf * kPBytes, k0, wave);
+        gq.load(lq + buf * kQBytes, k0, wave);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    i32x4 acc[TP][TQ] = {};
+    for (int s = 0; s < R - 1; ++s) ask(s, s);
+    int buf = 0;
+    for (int it = 0; it < nk; ++it) {
+        // this stage has arrived, and every wave has read the one before it
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(
+                         (R - 2) * (GP::kLoads + GQ::kLoads))
+                     : "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        const lds_char* const rp = lp + buf * kPBytes;
+        const lds_char* const rq = lq + buf * kQBytes;
+        s16x8 p[2][TP], q[2][TQ];
 #pragma unroll
-    for (int i = 0; i < kFewP; ++i) {
-        const int n = n0 + i % kOut * 16;
-        wr[i].init(w + (first + (i < kOut ? n : N + n)) * K, min(N - n, 16), K / 2, lane);
-    }
+        for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
-    for (int j = 0; j < kFewBlocks; ++j)
-        xr[j].init(x + ((int64_t)tile.begin + 16 * j) * K, min(rows - 16 * j, 16), K / 2, lane);
-    i32x4 acc[kFewP][kFewBlocks] = {};
-    const int shift = rotate ? scattered(blk, (K / 2 + kFewStep - 1) / kFewStep) : 0;
-    if (rows > 16)
-        few_products<Codes2, 2>(wr, xr, K / 2, shift, wave, lane, acc);
-    else
-        few_products<Codes2, 1>(wr, xr, K / 2, shift, wave, lane, acc);
+            for (int i = 0; i < TP; ++i) p[kk][i] = ap.frag(rp, i * 64, kk);
 #pragma unroll
-    for (int j = 0; j < kFewBlocks; ++j)
-#pragma unroll
-        for (int i = 0; i < kFewP; ++i) part[wave][j][i][lane] = acc[i][j];
-    __syncthreads();
-    // wave j finishes block j of 16 rows
-    if (wave >= kFewBlocks) return;
-    const uint32_t m = (uint32_t)tile.begin + wave * 16 + (lane & 15);
-    if (m >= (uint32_t)tile.end) return;
-    const float xm = xs[m];
-    const float* const wse = ws + first;
-    f32x4 v[kFewP];
-#pragma unroll
-    for (int i = 0; i < kFewP; ++i) {
-        i32x4 sum = part[0][wave][i][lane];
-#pragma unroll
-        for (int u = 1; u < kFewWaves; ++u) sum += part[u][wave][i][lane];
-        const int n = n0 + i % kOut * 16 + 4 * (lane >> 4);
-        v[i] = scaled(sum, xm, scales4(wse + (i < kOut ? 0 : N), n, N));
-    }
-#pragma unroll
-    for (int i = 0; i < kOut; ++i) {
-        const int n = n0 + i * 16 + 4 * (lane >> 4);
-        if (n >= N) return;
-        if constexpr (kSwiglu) {
-            f32x4 h;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) h[r] = in_fp32(silu(v[i][r]) * v[kOut + i][r]);
-            store4(y + (int64_t)m * N + n, h);
-        } else {
-            store4(y + (int64_t)m * N + n, v[i]);
+            for (int j = 0; j < TQ; ++j) q[kk][j] = aq.frag(rq, j * 16, kk);
         }
+        ask(it + R - 1, buf == 0 ? R - 1 : buf - 1);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int j = 0; j < TQ; ++j)
+#pragma unroll
+                for (int i = 0; i < TP; ++i)
+                    acc[i][j] = Mfma<Codes2>::mul(p[kk][i], q[kk][j], acc[i][j]);
+        buf = buf + 1 == R ? 0 : buf + 1;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS is left in flight
+    __syncthreads();
+    // block b of 16 weight rows and q of 16 rows of x: sums[b][q]
+    static_assert(BP / 16 * TQ * 1024 <= R * (kPBytes + kQBytes), "the sums fit");
+    typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
+    lds_i32x4* const sums = (lds_i32x4*)lp;
+#pragma unroll
+    for (int i = 0; i < TP; ++i)
+#pragma unroll
+        for (int j = 0; j < TQ; ++j) sums[((i * 4 + wave) * TQ + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    const float* const wse = ws + first;
+    constexpr int kBlocks = kOuts / 16;
+    for (int t = wave; t < kBlocks * TQ; t += NW) {
+        const int b = t % kBlocks, j = t / kBlocks;
+        const uint32_t m = (uint32_t)tile.begin + j * 16 + (lane & 15);
+        const int n = n0 + b * 16 + 4 * (lane >> 4);
+        if (m >= (uint32_t)tile.end || n >= N) continue;
+        const float xm = xs[m];
+        const i32x4 g = sums[(b * TQ + j) * 64 + lane];
+        f32x4 v = scaled(g, xm, scales4(wse, n, N));
+        if constexpr (kSwiglu) {
+            const i32x4 us = sums[((b + kBlocks) * TQ + j) * 64 + lane];
+            const f32x4 u = scaled(us, xm, scales4(wse + N, n, N));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = in_fp32(silu(v[r]) * u[r]);
+        }
+        store4(y + (int64_t)m * N + n, v);
     }
 }
 
@@ -435,35 +491,50 @@ __global__ __launch_bounds__(Saved::kThreads, 2) void wgrad_int8_kernel(
 
 dim3 grid_of(int64_t workgroups) { return dim3((unsigned)workgroups); }
 
-template <typename S, typename T>
-hipError_t linear_int8_tiles(const int8_t* x, const float* xs, const int8_t* w, const float* ws,
-                             const ExpertRows& er, int K, int N, bool swiglu, bool rotate, S* y,
-                             const Launch& L) {
-    const int outs = swiglu ? 2 * N : N, cols = (int)tiles_of(outs, T::kTile.outs);
-    return launch_kernel(swiglu ? linear_int8_kernel<S, true, T> : linear_int8_kernel<S, false, T>,
-                         grid_of(workgroups(er, T::kTile, outs)), dim3(T::kThreads), L, x, xs, w, ws,
-                         er, K, N, cols, y, rotate);
-}
+template <typename S>
+struct Int8Product {
+    const int8_t* x;
+    const float* xs;
+    const int8_t* w;
+    const float* ws;
+    const ExpertRows& er;
+    int K, N;
+    bool swiglu;
+    S* y;
+    const Launch& L;
+
+    int outs() const { return swiglu ? 2 * N : N; }
+    template <typename F>
+    hipError_t run(F kernel, const TileShape& t, bool rotate) const {
+        return launch_kernel(kernel, grid_of(workgroups(er, t, outs())), dim3(t.threads), L, x, xs, w,
+                             ws, er, K, N, (int)tiles_of(outs(), t.outs), y, rotate);
+    }
+    template <typename T>
+    hipError_t thin(bool rotate) const {
+        return run(swiglu ? linear_int8_thin_kernel<S, true, T> : linear_int8_thin_kernel<S, false, T>,
+                   T::kTile, rotate);
+    }
+    template <typename T, int kPolicy>
+    hipError_t tiles(bool rotate) const {
+        return run(swiglu ? linear_int8_kernel<S, true, T, kPolicy>
+                          : linear_int8_kernel<S, false, T, kPolicy>,
+                   T::kTile, rotate);
+    }
+};
 
 template <typename S>
 hipError_t linear_int8_as(const int8_t* x, const float* xs, const int8_t* w, const float* ws,
                           const ExpertRows& er, int K, int N, bool swiglu, void* y,
                           const Launch& L) {
-    S* ys = static_cast<S*>(y);
-    const int outs = swiglu ? 2 * N : N;
+    const Int8Product<S> p{x, xs, w, ws, er, K, N, swiglu, static_cast<S*>(y), L};
     const bool rotate = rotates(expected_rows(er), K / 2);
-    switch (forward_tiles(er, outs)) {
-        case Tiles::kFew:
-            return launch_kernel(
-                swiglu ? linear_int8_few_kernel<S, true> : linear_int8_few_kernel<S, false>,
-                grid_of(workgroups(er, kFewTile, outs)), dim3(kFewThreads), L, x, xs, w, ws, er, K,
-                N, (int)tiles_of(outs, kFewTile.outs), ys, rotate);
-        case Tiles::kSmall:
-            return linear_int8_tiles<S, Small>(x, xs, w, ws, er, K, N, swiglu, rotate, ys, L);
-        case Tiles::kWide:
-            return linear_int8_tiles<S, Wide>(x, xs, w, ws, er, K, N, swiglu, rotate, ys, L);
-        default:
-            return hipErrorInvalidValue;  // refused before
+    switch (int8_tiles(er, p.outs())) {
+        case Int8Tiles::kNarrow: return p.template thin<ThinNarrow>(rotate);
+        case Int8Tiles::kThin: return p.template thin<ThinWhole>(rotate);
+        case Int8Tiles::kSmallOnce: return p.template tiles<Small, kStream>(rotate);
+        case Int8Tiles::kSmall: return p.template tiles<Small, 0>(rotate);
+        case Int8Tiles::kWide: return p.template tiles<Wide, 0>(rotate);
+        default: return hipErrorInvalidValue;  // refused before
     }
 }
 

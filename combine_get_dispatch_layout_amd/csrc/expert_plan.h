@@ -28,6 +28,8 @@ struct TileShape {
     int rows, outs, threads;
 };
 constexpr TileShape kFewTile{32, 32, 256}, kSmallTile{128, 128, 256}, kWideTile{256, 256, 512};
+// Of an int8 product of few rows, and of very few workgroups.
+constexpr TileShape kThinTile{64, 128, 256}, kNarrowTile{32, 64, 256};
 // Of a weight gradient: weight rows (N) and columns (K).
 constexpr TileShape kWeightTile{128, 256, 256};
 // The same from rows saved in int8.
@@ -160,6 +162,60 @@ inline Tiles forward_tiles(const ExpertRows& er, int outs) {
 inline Tiles input_gradient_tiles(const ExpertRows& er, int outs) {
     return launchable(few_wide_tiles(er, expected_rows(er), outs) ? Tiles::kSmall : Tiles::kWide, er,
                       outs);
+}
+
+// The int8 product's tiles (kSmallOnce: 128 x 128 with the weights past the
+// caches).  64 experts with the same number of rows each, us:
+//   rows each                    1    8   16   32   40   64   96  128
+//   7168 -> 4096   32 x 64     266  271  277  298  570  524  798  944
+//                  64 x 128    271  275  280  292  302  328  608  568
+//                  128 x 128   280  283  290  302  313  336  383  408
+//                  through the caches
+//                              318  320  322  325  332  342  370  403
+//                  256 x 256   328  331  333  336  339  345  369  382
+//   2048 -> 1408   64 x 128     34   34   35   39   40   42   63   64
+//                  128 x 128    42   42   42   44   46   50   54   60
+//                  256 x 256    46   46   47   49   50   52   59   62
+// As routed at random, 64 on average (4096 -> 4096): 293, 217, 230 (through the
+// caches) and 219; 32: 191, 201, 211 and 203.
+//
+// One or a few tokens ask for the weights of as many experts: below two
+// workgroups of 64 x 128 per compute unit, 32 x 64 keep more in flight (rows in
+// 1, 8 and 16 experts, 7168 -> 2048: 15 21 37 and 33 35 39; one expert of 32 rows,
+// 8192 -> 8192: 20 and 38); and so do 64 x 128 where 128 x 128 leave compute units
+// without one (one expert of 256 rows, 8192 -> 8192: 41 and 48; 8 of 128, 4096 ->
+// 2048: 26 and 30; but 8 of 256: 38 and 30).
+//
+// Slots may be nearly all empty and every workgroup looks for its tile, so small
+// tiles stay below so many looks at 64 experts (4096 -> 1024; every expert has 4
+// rows, and 8 have one; 32 x 64, 64 x 128 and 128 x 128):
+//   128 experts, 64 slots       85   85   86      15   22   30
+//   256 experts, 128 slots     201  166  171      64   22   31
+//   256 experts, 256 slots     258  181  179     121   36   37
+//   1024 experts, 128 slots   1236  728  709     812  210  125
+constexpr int64_t kNarrowLikely = 32, kThinLikely = 40, kOnceLikely = 80;
+constexpr int64_t kNarrowLooks = 512, kThinLooks = 4096;
+
+enum class Int8Tiles { kNarrow, kThin, kSmallOnce, kSmall, kWide, kNone };
+
+inline bool slots_serve(const ExpertRows& er, const TileShape& t, int64_t looks) {
+    return er.offsets || max_tiles(er, t.rows) * tiles_of(er.E, 64) <= looks;
+}
+
+inline Int8Tiles int8_tiles(const ExpertRows& er, int outs) {
+    const int64_t likely = expected_rows(er), cols = tiles_of(outs, kThinTile.outs);
+    const int64_t rows = er.offsets ? er.rows : 8 * (int64_t)er.cap;
+    const int64_t active = rows < er.E ? rows : er.E;  // experts with rows, at most
+    const auto fits = [&](const TileShape& t) { return grid_fits(workgroups(er, t, outs), t.threads); };
+    if (likely <= kNarrowLikely && active * cols <= 512 &&
+        slots_serve(er, kNarrowTile, kNarrowLooks) && fits(kNarrowTile))
+        return Int8Tiles::kNarrow;
+    if ((likely <= kThinLikely || tiles_of(likely, kThinTile.rows) * er.E * cols <= 256) &&
+        slots_serve(er, kThinTile, kThinLooks) && fits(kThinTile))
+        return Int8Tiles::kThin;
+    if (likely <= kOnceLikely && small_serves(er) && fits(kSmallTile)) return Int8Tiles::kSmallOnce;
+    if (few_wide_tiles(er, likely, outs) && fits(kSmallTile)) return Int8Tiles::kSmall;
+    return fits(kWideTile) ? Int8Tiles::kWide : Int8Tiles::kNone;
 }
 
 // Whether workgroups start at scattered places of the reduction (`scattered`).

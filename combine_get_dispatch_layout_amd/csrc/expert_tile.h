@@ -1,5 +1,5 @@
 // What the experts' products share beside the tiles' loops (device code): the
-// tile shapes, the epilogue's stores, and the loop of a product of few rows.
+// tile shapes and the epilogue's pieces.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -95,74 +95,6 @@ __device__ __forceinline__ void with_blocks(int rows, F&& f) {
     else if (n == 3) f(std::integral_constant<int, 3>{});
     else if (n == 2) f(std::integral_constant<int, 2>{});
     else f(std::integral_constant<int, 1>{});
-}
-
-constexpr int kFewP = 2;  // blocks of 16 weight rows
-constexpr int kFewRows = 32, kFewBlocks = kFewRows / 16, kFewWaves = 4, kFewThreads = kFewWaves * 64,
-              kFewStep = 128 * kFewWaves;
-constexpr int kFewRunLog2 = 3;
-static_assert(same({kFewRows, kFewP * 16, kFewThreads}, kFewTile), "the plan's tile is the kernel's");
-
-// 16 rows of an operand along r, read by the whole wave: lane l takes row
-// l & 15, reduction values 8 (l >> 4) .. + 7 of each 32; zeros outside.
-struct FewRows {
-    __amdgpu_buffer_rsrc_t rs;
-    int off;
-    __device__ __forceinline__ void init(const void* first, int rows, int K, int lane) {
-        rs = make_rsrc(first, rows * K * 2);
-        off = (lane & 15) * K * 2 + (lane >> 4) * 16;
-    }
-    __device__ __forceinline__ s16x8 load(int k, bool inside) const {
-        return __builtin_bit_cast(s16x8, __builtin_amdgcn_raw_buffer_load_b128(
-                                             rs, inside ? off + k * 2 : (int)kOutside, 0, 0));
-    }
-};
-
-// Two blocks of 16 weight rows times NQ blocks of 16 rows of x.
-template <typename S, int NQ>
-__device__ __forceinline__ void few_products(const FewRows* ws, const FewRows* xs, int K, int shift,
-                                             int wave, int lane,
-                                             typename Mfma<S>::Acc (&acc)[kFewP][kFewBlocks]) {
-    constexpr int kU = 4, kStep = kFewStep;
-    static_assert(kStep == 32 * kU * kFewWaves, "a step of all waves");
-    const int steps = (K + kStep - 1) / kStep;
-    s16x8 a[2][kFewP][kU], b[2][NQ][kU];
-    const int in = (lane >> 4) * 8;
-    // Steps go around the reduction from `shift` on; past the last one nothing
-    // is read.  The scheduling barriers keep the loads of one step ahead of the
-    // products of the other.
-    const auto fetch = [&](int s, int step) {
-        int at = step + shift;
-        at -= at >= steps ? steps : 0;
-        const int k0 = step < steps ? at * kStep + wave * 32 * kU : K;
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int k = k0 + u * 32;
-            const bool inside = k + in < K;
-#pragma unroll
-            for (int i = 0; i < kFewP; ++i) a[s][i][u] = ws[i].load(k, inside);
-#pragma unroll
-            for (int j = 0; j < NQ; ++j) b[s][j][u] = xs[j].load(k, inside);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    const auto multiply = [&](int s) {
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-#pragma unroll
-            for (int j = 0; j < NQ; ++j)
-#pragma unroll
-                for (int i = 0; i < kFewP; ++i)
-                    acc[i][j] = Mfma<S>::mul(a[s][i][u], b[s][j][u], acc[i][j]);
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    fetch(0, 0);
-    for (int step = 0; step < steps; step += 2) {
-        fetch(1, step + 1);
-        multiply(0);
-        fetch(0, step + 2);
-        multiply(1);
-    }
 }
 
 }  // namespace moedx

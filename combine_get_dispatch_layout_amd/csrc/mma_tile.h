@@ -95,7 +95,7 @@ constexpr uint32_t kOutside = 0x80000000u;  // past any descriptor's range (belo
 
 // An operand along r: `halves` blocks of B / halves rows, each with its own
 // first row (a gated product's gate and up rows).
-template <int B, int NW, int BK, int kHalves>
+template <int B, int NW, int BK, int kHalves, int kPolicy = 0>
 struct Along {
     static constexpr int kRow = BK * 2;                // bytes per LDS row
     static constexpr int kRowChunks = BK / 8;
@@ -142,7 +142,7 @@ struct Along {
                 const int row = h * (B / kHalves) + (j * NW + wave) * kLoadRows;
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + row * kRow), 16,
                                                          (int)(v + j * kLoadRows * NW * ld2), 0, 0,
-                                                         0);
+                                                         kPolicy);
             }
         }
     }

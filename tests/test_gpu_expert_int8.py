@@ -208,6 +208,9 @@ CASES += [([2000, 0, 300, 831, 260, 740, 128], 4112, n) for n in (16, 136, 192, 
 # reductions that workgroups enter at scattered places, in each tile size
 CASES += [([2, 1, 0, 17, 3], 8192, 72), ([9, 12, 30], 4096, 136),
           ([60, 70, 0, 55, 61, 90, 33, 64], 4096, 4096)]
+# 128 x 128 tiles, with the weights through the caches and past them
+CASES += [([256, 100, 0, 300, 280, 511, 256, 200], k, 2056) for k in (16, 272, 1040, 4112)]
+CASES += [([60, 70, 0, 129, 61, 90, 33, 64], k, 4104) for k in (16, 272, 4096)]
 ids = lambda c: f"{len(c[0])}e{sum(c[0])}r-{c[1]}-{c[2]}"  # noqa: E731
 
 
@@ -272,15 +275,14 @@ def test_linear_int8_slots(cap):
 
 
 def test_linear_int8_rows_alone():
-    """A row's outputs are the same bits in any buffer: one row by the few-row
-    kernel, the same among many by each tile size."""
+    """A row's outputs are the same bits in any buffer, by any of the tiles."""
     dev = device()
     E, K, N = 4, 4096, 1032
     buf = make_buffer(E, 1, 1, 1)
     off, M, x, xs, w, ws = int8_inputs([700, 1200, 300, 900], K, N, dev, 7)
     y, _ = buf.expert_linear_int8(x, xs, w, ws, torch.tensor(off, dtype=torch.int32, device=dev))
     for row, e in ((0, 0), (699, 0), (700, 1), (1899, 1), (2100, 2), (3099, 3)):
-        for n in (1, 40, 200):
+        for n in (1, 40, 300):
             a = max(off[e], min(row, off[e + 1] - n))
             part = slice(a, min(a + n, off[e + 1]))
             k = part.stop - part.start
