@@ -199,9 +199,9 @@ class Handle:
 
 _DTYPES = {torch.bfloat16: C.MOEDX_BF16, torch.float16: C.MOEDX_F16, torch.float32: C.MOEDX_F32}
 _PRODUCT_DTYPES = (torch.bfloat16, torch.float16)
+_INT8, _FP32 = (torch.int8,), (torch.float32,)
 # What every call takes beside its own arguments.
-_OPTIONS = {"previous_event": None, "async_finish": False, "allocate_on_comm_stream": False,
-            "no_sync": False}
+_OPTIONS = ("previous_event", "async_finish", "allocate_on_comm_stream", "no_sync")
 _SCORES = {"softmax": C.MOEDX_GATE_SOFTMAX, "sigmoid": C.MOEDX_GATE_SIGMOID}
 
 
@@ -859,8 +859,10 @@ class Buffer:
     def _options(options: dict) -> tuple:
         for name in options:
             if name not in _OPTIONS:
-                raise TypeError(f"unexpected argument {name!r}, expected one of {list(_OPTIONS)}")
-        return tuple(options.get(name, default) for name, default in _OPTIONS.items())
+                raise TypeError(f"unexpected argument {name!r}, expected one of {_OPTIONS}")
+        get = options.get
+        return (get("previous_event"), get("async_finish", False),
+                get("allocate_on_comm_stream", False), get("no_sync", False))
 
     def _any_rows(self, rows, x: torch.Tensor, previous_event):
         """_expert_rows, or every row of x where `rows` is None."""
@@ -877,13 +879,14 @@ class Buffer:
     def _codes(self, name: str, codes, scales, width, previous_event):
         """(codes, scales, block) checked: int8 rows [*, width] with their scales."""
         lead = self._lead(name, codes)
-        codes = self._check(name, codes, (torch.int8,), lead + (width,), previous_event)
+        codes = self._check(name, codes, _INT8, lead + (width,), previous_event)
         if not isinstance(scales, torch.Tensor):
-            raise ValueError(f"{name}'s scales must be a tensor")
-        block = 0 if scales.dim() == len(lead) else 128
-        scales = self._check(f"{name}'s scales", scales, (torch.float32,),
-                             self._scale_shape(lead, codes.shape[-1], block), previous_event)
-        return codes, scales, block
+            raise ValueError(f"{name}_scales must be a tensor")
+        if scales.dim() == len(lead):
+            block, shape = 0, lead
+        else:
+            block, shape = 128, lead + ((codes.shape[-1] + 127) // 128,)
+        return codes, self._check(f"{name}_scales", scales, _FP32, shape, previous_event), block
 
     def expert_quantize(self, x: torch.Tensor, rows=None, block: int = 0,
                         out: Optional[torch.Tensor] = None,
@@ -965,9 +968,9 @@ class Buffer:
         if block:
             raise ValueError("x's scales must be one per row (block=0)")
         lead, K = tuple(x.shape[:-1]), x.shape[-1]
-        w = self._check("w", w, (torch.int8,), (self.num_experts, None, K), prev)
+        w = self._check("w", w, _INT8, (self.num_experts, None, K), prev)
         N = w.shape[1]
-        w_scales = self._check("w_scales", w_scales, (torch.float32,), (self.num_experts, N), prev)
+        w_scales = self._check("w_scales", w_scales, _FP32, (self.num_experts, N), prev)
         if dtype not in _PRODUCT_DTYPES:
             raise ValueError(f"dtype={dtype} must be one of {list(_PRODUCT_DTYPES)}")
         if swiglu:

@@ -66,38 +66,57 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_int8_kernel(
             .run(gp, gq, (lds_char*)lp, (lds_char*)lq, wave, acc);
         const float* const wse = ws + first;
         const int mine = 4 * (lane >> 4);  // this lane's first output of a block of 16
+        // A wave's outputs of 16 rows, kRun neighbours at a time, change lanes in
+        // LDS: whole cache lines (half ones in 128 x 128 tiles) are stored, past
+        // the caches.  64 experts, us, in 64-byte pieces through the caches, as
+        // lines through them and past them: 192 rows, 1424 -> 4096: 157, 152, 143;
+        // 64 rows, 4096 -> 4096: 207, 205, 181; 512 rows, 7168 -> 4096, gated: 833, 832,
+        // 830; the first with a quantize of the outputs behind it: 181, 176, 175.
+        constexpr int kRun = T::BP / 2 / T::WP, kRunBlocks = kRun / 16, kRowBytes = kRun * 2 + 16;
+        constexpr int kLanes = kRun / 8, kRows = 64 / kLanes;
+        typedef __attribute__((address_space(3))) u32x4_t lds_u32x4;
+        typedef S vec4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) vec4 lds_vec4;
+        lds_char* const strip = (lds_char*)lp + wave * (2 * 16 * kRowBytes);
+        static_assert(T::kWaves * 2 * 16 * kRowBytes <= (T::kP * T::BP + T::kQ * T::BQ) * T::BK * 2,
+                      "the strips fit");
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
             const uint32_t m = (uint32_t)tile.begin + T::q_at(wq, j) + (lane & 15);
             const bool row = m < (uint32_t)tile.end;  // unsigned: past 2^31 for the last tiles
             const float xm = row ? xs[m] : 0.0f;
-            S* const ym = y + (int64_t)m * N;
-            if constexpr (kSwiglu) {
 #pragma unroll
-                for (int i = 0; i < T::TP / 2; i += 2) {
-                    f32x4 h[2];
+            for (int half = 0; half < (kSwiglu ? 1 : 2); ++half) {
+                lds_char* const at = strip + (kSwiglu ? j & 1 : half) * 16 * kRowBytes;
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const int n = n0 + T::p_at(wp, i + b) + mine;
-                        const f32x4 g = scaled(acc[i + b][j], xm, scales4(wse, n, N));
+                for (int b = 0; b < kRunBlocks; ++b) {
+                    const int i = half * kRunBlocks + b;
+                    const int n = n0 + T::p_at(wp, i) + mine;
+                    f32x4 v = scaled(acc[i][j], xm, scales4(wse, n, N));
+                    if constexpr (kSwiglu) {
                         const f32x4 u =
-                            scaled(acc[i + b + T::TP / 2][j], xm, scales4(wse + N, n, N));
+                            scaled(acc[i + kRunBlocks][j], xm, scales4(wse + N, n, N));
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) h[b][r] = in_fp32(silu(g[r]) * u[r]);
+                        for (int r = 0; r < 4; ++r) v[r] = in_fp32(silu(v[r]) * u[r]);
                     }
-                    const int n = n0 + T::p_at(wp, i) + pair_at(lane);
-                    const u32x4_t hv = pack_pair<S>(h[0], h[1]);
-                    if (row && n < N) store8(ym + n, hv);
-                }
-            } else {
+                    vec4 o;
 #pragma unroll
-                for (int i = 0; i < T::TP; i += 2) {
-                    const int a = n0 + T::p_at(wp, i) + mine, b = n0 + T::p_at(wp, i + 1) + mine;
-                    const u32x4_t v = pack_pair<S>(scaled(acc[i][j], xm, scales4(wse, a, N)),
-                                                   scaled(acc[i + 1][j], xm, scales4(wse, b, N)));
-                    const int n = n0 + T::p_at(wp, i) + pair_at(lane);
-                    if (row && n < N) store8(ym + n, v);
+                    for (int r = 0; r < 4; ++r) o[r] = (S)v[r];
+                    *(lds_vec4*)(at + (lane & 15) * kRowBytes + (b * 16 + mine) * 2) = o;
                 }
+                // the wave's own strip: its LDS accesses are in order, the compiler's are
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+                for (int h = 0; h < 16 / kRows; ++h) {
+                    const int r = h * kRows + lane / kLanes, c = lane % kLanes;
+                    const u32x4_t v = *(lds_u32x4*)(at + r * kRowBytes + c * 16);
+                    const uint32_t mr = (uint32_t)tile.begin + T::q_at(wq, j) + r;
+                    const int n = n0 + T::p_at(wp, half * kRunBlocks) + c * 8;
+                    if (mr < (uint32_t)tile.end && n < N)
+                        __builtin_nontemporal_store(
+                            v, reinterpret_cast<u32x4_t*>(y + (int64_t)mr * N + n));
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             }
         }
     });
