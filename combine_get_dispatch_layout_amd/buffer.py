@@ -800,7 +800,8 @@ class Buffer:
         self._keep(allocate_on_comm_stream, x, w, t, y, pre)
         return y, pre, self._event(done)
 
-    def expert_linear_backward(self, d_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor, rows,
+    def expert_linear_backward(self, d_y: torch.Tensor, x: Optional[torch.Tensor],
+                               w: Optional[torch.Tensor], rows,
                                out: Optional[torch.Tensor] = None,
                                d_w: Optional[torch.Tensor] = None, d_w_dtype=None,
                                previous_event: Optional[EventOverlap] = None,
@@ -810,23 +811,39 @@ class Buffer:
         its activation: d_x[m] = w[e]^T d_y[m] (rows of no expert left as they
         were in ``out``) and d_w[e] = the sum of d_y[m] x[m]^T over e's rows
         (zero without any), written to ``d_w`` (of w's dtype or fp32) or to a
-        new tensor of ``d_w_dtype`` (w's dtype by default)."""
-        lead = self._lead("x", x)
-        x = self._check("x", x, _PRODUCT_DTYPES, lead + (None,), previous_event)
-        K = x.shape[-1]
-        w = self._check("w", w, (x.dtype,), (self.num_experts, None, K), previous_event)
-        N = w.shape[1]
-        d_y = self._check("d_y", d_y, (x.dtype,), lead + (N,), previous_event)
+        new tensor of ``d_w_dtype`` (w's dtype by default).  ``w`` None leaves
+        d_x out, ``x`` None d_w (each is then None): where x is computed again
+        from d_x, as with expert_swiglu_backward_int8, the two are asked for
+        one after the other."""
+        lead = self._lead("d_y" if x is None else "x", d_y if x is None else x)
+        if x is not None:
+            x = self._check("x", x, _PRODUCT_DTYPES, lead + (None,), previous_event)
+            K, dtype = x.shape[-1], x.dtype
+            if w is not None:
+                w = self._check("w", w, (dtype,), (self.num_experts, None, K), previous_event)
+        elif w is None:
+            raise ValueError("x or w is needed")
+        else:
+            w = self._check("w", w, _PRODUCT_DTYPES, (self.num_experts, None, None), previous_event)
+            K, dtype = w.shape[2], w.dtype
+        N = None if w is None else w.shape[1]
+        d_y = self._check("d_y", d_y, (dtype,), lead + (N,), previous_event)
+        N = d_y.shape[-1]
+        if x is None and (d_w is not None or d_w_dtype is not None):
+            raise ValueError("d_w needs x")
+        if w is None and out is not None:
+            raise ValueError("out needs w")
         if d_w_dtype is None:
-            d_w_dtype = x.dtype if d_w is None else d_w.dtype
-        if d_w_dtype not in (x.dtype, torch.float32):
-            raise ValueError(f"d_w_dtype={d_w_dtype} must be {x.dtype} or torch.float32")
-        er, t = self._expert_rows(rows, x, previous_event)
-        d_x = self._out("out", out, x.dtype, lead + (K,))
-        d_w = self._out("d_w", d_w, d_w_dtype, (self.num_experts, N, K))
+            d_w_dtype = dtype if d_w is None else d_w.dtype
+        if d_w_dtype not in (dtype, torch.float32):
+            raise ValueError(f"d_w_dtype={d_w_dtype} must be {dtype} or torch.float32")
+        er, t = self._expert_rows(rows, d_y, previous_event)
+        d_x = None if w is None else self._out("out", out, dtype, lead + (K,))
+        if x is not None:
+            d_w = self._out("d_w", d_w, d_w_dtype, (self.num_experts, N, K))
         ex, done = self._exec_here(previous_event, async_finish, allocate_on_comm_stream, no_sync)
         C.check(C.moedx_expert_linear_backward(self.ctx, _addr(d_y), _addr(x), _addr(w),
-                                               _DTYPES[x.dtype], K, N, ctypes.byref(er), _addr(d_x),
+                                               _DTYPES[dtype], K, N, ctypes.byref(er), _addr(d_x),
                                                _addr(d_w), _DTYPES[d_w_dtype], ctypes.byref(ex)))
         self._keep(allocate_on_comm_stream, d_y, x, w, t, d_x, d_w)
         return d_x, d_w, self._event(done)
