@@ -35,6 +35,9 @@ __device__ __forceinline__ f32x4 scales4(const float* ws, int n, int N) {
     return v;
 }
 
+typedef Shape<128, 128, 2, 64, 3, 2> Deep;  // 80 KB of LDS: two workgroups share a CU
+static_assert(same(Deep::kTile, kSmallTile), "the plan's tile is the kernel's");
+
 template <typename S, bool kSwiglu, typename T, int kPolicy>
 __global__ __launch_bounds__(T::kThreads, 2) void linear_int8_kernel(
     const int8_t* x, const float* xs, const int8_t* w, const float* ws, ExpertRows er, int K, int N,
@@ -550,8 +553,9 @@ hipError_t linear_int8_as(const int8_t* x, const float* xs, const int8_t* w, con
     switch (int8_tiles(er, p.outs())) {
         case Int8Tiles::kNarrow: return p.template thin<ThinNarrow>(rotate);
         case Int8Tiles::kThin: return p.template thin<ThinWhole>(rotate);
-        case Int8Tiles::kSmallOnce: return p.template tiles<Small, kStream>(rotate);
-        case Int8Tiles::kSmall: return p.template tiles<Small, 0>(rotate);
+        case Int8Tiles::kOnce: return p.template tiles<Small, kStream>(rotate);
+        case Int8Tiles::kDeepOnce: return p.template tiles<Deep, kStream>(rotate);
+        case Int8Tiles::kDeep: return p.template tiles<Deep, 0>(rotate);
         case Int8Tiles::kWide: return p.template tiles<Wide, 0>(rotate);
         default: return hipErrorInvalidValue;  // refused before
     }

@@ -164,39 +164,49 @@ inline Tiles input_gradient_tiles(const ExpertRows& er, int outs) {
                       outs);
 }
 
-// The int8 product's tiles (kSmallOnce: 128 x 128 with the weights past the
-// caches).  64 experts with the same number of rows each, us:
+// The int8 product's tiles.  kOnce: 128 x 128 with the weights past the caches;
+// kDeep, kDeepOnce: 128 x 128 with three stages of the weights, through the caches
+// and past them.  64 experts with the same number of rows each, us:
 //   rows each                    1    8   16   32   40   64   96  128
 //   7168 -> 4096   32 x 64     266  271  277  298  570  524  798  944
-//                  64 x 128    271  275  280  292  302  328  608  568
-//                  128 x 128   280  283  290  302  313  336  383  408
-//                  through the caches
-//                              318  320  322  325  332  342  370  403
-//                  256 x 256   328  331  333  336  339  345  369  382
+//                  64 x 128    271  275  280  292  300  328  609  569
+//                  kOnce       280  283  290  302  298  309  342  375
+//                  kDeepOnce                       297  306  341  374
+//                  kDeep                           332  337  362  394
+//                  256 x 256   328  331  333  336  336  340  358  366
 //   2048 -> 1408   64 x 128     34   34   35   39   40   42   63   64
-//                  128 x 128    42   42   42   44   46   50   54   60
-//                  256 x 256    46   46   47   49   50   52   59   62
-// As routed at random, 64 on average (4096 -> 4096): 293, 217, 230 (through the
-// caches) and 219; 32: 191, 201, 211 and 203.
+//                  kOnce        42   42   42   44   45   47   52   58
+//                  256 x 256    46   46   47   49   48   49   54   56
+// and with rows that vary, as uniform and as skewed routing gives them (4096 ->
+// 4096; on average 32, 48, 64, 80 and 96):
+//   64 x 128       190 223   203 257   293 295   369 344   393 387
+//   kOnce          189 218   193 230   203 253   213 288   239 306
+//   256 x 256      211 213   217 237   227 254   237 264   244 274
 //
-// One or a few tokens ask for the weights of as many experts: below two
+// One or a few tokens ask for the weights of as many experts: up to two
 // workgroups of 64 x 128 per compute unit, 32 x 64 keep more in flight (rows in
 // 1, 8 and 16 experts, 7168 -> 2048: 15 21 37 and 33 35 39; one expert of 32 rows,
-// 8192 -> 8192: 20 and 38); and so do 64 x 128 where 128 x 128 leave compute units
-// without one (one expert of 256 rows, 8192 -> 8192: 41 and 48; 8 of 128, 4096 ->
-// 2048: 26 and 30; but 8 of 256: 38 and 30).
+// 8192 -> 8192: 20 and 38).  Where 256 x 256 leave compute units without a tile
+// (8 experts, 7168 -> 4096, 48, 96, 128, 256 and 512 rows):
+//   kOnce           57   60   62   82  153
+//   kDeepOnce       42   47   51
+//   kDeep           51   56   60   79  140
+//   256 x 256       60   66   70   97  108 (256 tiles)
+// (Weights that the 256 MB memory-side cache holds from the call before, as a
+// small model's may be, are better read through the caches: 8 of 48 rows, 4096 ->
+// 2048: 20 by kDeep, 23 by kDeepOnce.)
 //
 // Slots may be nearly all empty and every workgroup looks for its tile, so small
 // tiles stay below so many looks at 64 experts (4096 -> 1024; every expert has 4
-// rows, and 8 have one; 32 x 64, 64 x 128 and 128 x 128):
+// rows, and 8 have one; 32 x 64, 64 x 128 and kOnce):
 //   128 experts, 64 slots       85   85   86      15   22   30
 //   256 experts, 128 slots     201  166  171      64   22   31
 //   256 experts, 256 slots     258  181  179     121   36   37
 //   1024 experts, 128 slots   1236  728  709     812  210  125
-constexpr int64_t kNarrowLikely = 32, kThinLikely = 40, kOnceLikely = 80;
+constexpr int64_t kNarrowLikely = 32, kThinLikely = 40, kOnceLikely = 80, kDeepOnceLikely = 128;
 constexpr int64_t kNarrowLooks = 512, kThinLooks = 4096;
 
-enum class Int8Tiles { kNarrow, kThin, kSmallOnce, kSmall, kWide, kNone };
+enum class Int8Tiles { kNarrow, kThin, kOnce, kDeepOnce, kDeep, kWide, kNone };
 
 inline bool slots_serve(const ExpertRows& er, const TileShape& t, int64_t looks) {
     return er.offsets || max_tiles(er, t.rows) * tiles_of(er.E, 64) <= looks;
@@ -210,11 +220,11 @@ inline Int8Tiles int8_tiles(const ExpertRows& er, int outs) {
     if (likely <= kNarrowLikely && active * cols <= 512 &&
         slots_serve(er, kNarrowTile, kNarrowLooks) && fits(kNarrowTile))
         return Int8Tiles::kNarrow;
-    if ((likely <= kThinLikely || tiles_of(likely, kThinTile.rows) * er.E * cols <= 256) &&
-        slots_serve(er, kThinTile, kThinLooks) && fits(kThinTile))
+    if (likely <= kThinLikely && slots_serve(er, kThinTile, kThinLooks) && fits(kThinTile))
         return Int8Tiles::kThin;
-    if (likely <= kOnceLikely && small_serves(er) && fits(kSmallTile)) return Int8Tiles::kSmallOnce;
-    if (few_wide_tiles(er, likely, outs) && fits(kSmallTile)) return Int8Tiles::kSmall;
+    if (few_wide_tiles(er, likely, outs) && fits(kSmallTile))
+        return likely <= kDeepOnceLikely ? Int8Tiles::kDeepOnce : Int8Tiles::kDeep;
+    if (likely <= kOnceLikely && small_serves(er) && fits(kSmallTile)) return Int8Tiles::kOnce;
     return fits(kWideTile) ? Int8Tiles::kWide : Int8Tiles::kNone;
 }
 

@@ -37,8 +37,9 @@ static bool check(const ExpertRows& er, int outs) {
     switch (got) {
         case Int8Tiles::kNarrow: n = threads(er, 32, 64, 256, outs); break;
         case Int8Tiles::kThin: n = threads(er, 64, 128, 256, outs); break;
-        case Int8Tiles::kSmallOnce:
-        case Int8Tiles::kSmall: n = threads(er, 128, 128, 256, outs); break;
+        case Int8Tiles::kOnce:
+        case Int8Tiles::kDeepOnce:
+        case Int8Tiles::kDeep: n = threads(er, 128, 128, 256, outs); break;
         case Int8Tiles::kWide: n = threads(er, 256, 256, 512, outs); break;
         case Int8Tiles::kNone: n = 0; break;
     }
@@ -64,14 +65,15 @@ int main() {
         {with_offsets(64, 8), 4096, Int8Tiles::kNarrow},      // one token's experts
         {with_offsets(64, 256), 4096, Int8Tiles::kThin},      // a few rows in each
         {with_offsets(64, 2048), 4096, Int8Tiles::kThin},
-        {with_offsets(64, 4096), 4096, Int8Tiles::kSmallOnce},
+        {with_offsets(64, 4096), 4096, Int8Tiles::kOnce},
         {with_offsets(64, 32768), 4096, Int8Tiles::kWide},
-        {with_offsets(8, 2048), 2048, Int8Tiles::kSmall},     // too few wide tiles
-        {with_offsets(1, 256), 8192, Int8Tiles::kThin},
+        {with_offsets(8, 512), 4096, Int8Tiles::kDeepOnce},   // too few wide tiles
+        {with_offsets(8, 2048), 2048, Int8Tiles::kDeep},
+        {with_offsets(1, 256), 8192, Int8Tiles::kDeep},
         {with_offsets(1, 32), 8192, Int8Tiles::kNarrow},
         {with_counts(64, 128), 4096, Int8Tiles::kThin},       // a decode batch's slots
         {with_counts(64, 1), 4096, Int8Tiles::kNarrow},
-        {with_counts(1024, 128), 1024, Int8Tiles::kSmallOnce},  // too many looks
+        {with_counts(1024, 128), 1024, Int8Tiles::kOnce},     // too many looks
         {with_counts(1024, 1 << 20), 16384, Int8Tiles::kNone},
         {with_offsets(1, INT32_MAX), 8, Int8Tiles::kNone},
         {with_offsets(1, ((int64_t)1 << 31) - 513), 8, Int8Tiles::kWide},

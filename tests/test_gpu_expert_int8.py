@@ -208,9 +208,14 @@ CASES += [([2000, 0, 300, 831, 260, 740, 128], 4112, n) for n in (16, 136, 192, 
 # reductions that workgroups enter at scattered places, in each tile size
 CASES += [([2, 1, 0, 17, 3], 8192, 72), ([9, 12, 30], 4096, 136),
           ([60, 70, 0, 55, 61, 90, 33, 64], 4096, 4096)]
-# 128 x 128 tiles, with the weights through the caches and past them
+# 128 x 128 tiles, two and three stages deep, the weights through the caches and
+# past them
 CASES += [([256, 100, 0, 300, 280, 511, 256, 200], k, 2056) for k in (16, 272, 1040, 4112)]
 CASES += [([60, 70, 0, 129, 61, 90, 33, 64], k, 4104) for k in (16, 272, 4096)]
+CASES += [([60, 70, 0, 129, 61, 90, 33, 64] * 2, k, 4104) for k in (80, 4096)]
+# 64 x 128 tiles: rows of one tile, one more, two; stages fewer and more than the ring
+CASES += [([33, 40, 0, 64, 38, 65, 36, 30], k, 136) for k in (16, 272, 400, 4096, 7168)]
+CASES += [([5, 0, 17, 64, 33, 1] * 11, 400, 1032)]
 ids = lambda c: f"{len(c[0])}e{sum(c[0])}r-{c[1]}-{c[2]}"  # noqa: E731
 
 
