@@ -402,3 +402,29 @@ def test_buffers_past_4_gib():
     d, xs = d_y.double().t().contiguous(), values(c, cs).to(dt).double()
     check("d_w", d_w[-1], d @ xs, 6 * V * (d.abs() @ xs.abs()), dt)
     assert not d_w[:-1].any()
+
+
+def test_readme_example():
+    """The README's example as written runs, and its served, decoded and trained
+    parts are what the same calls give here."""
+    import os
+    import re
+    device()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "README.md")).read()
+    m = re.search(r"## The experts in 8 bits.*?```python\n(.*?)```", text, re.S)
+    print("[int8] README example", flush=True)
+    torch.manual_seed(0)
+    ns = {}
+    exec(compile(m.group(1), "README.md", "exec"), ns)
+    torch.cuda.synchronize()
+    buf, idx, gates, order = ns["buf"], ns["idx"], ns["gates"], ns["order"]
+    q = [ns[k] for k in ("q1", "s1", "q2", "s2")]
+    hq, hs, _ = buf.expert_quantize(
+        buf.expert_linear_int8(ns["rows"], ns["scales"], q[0], q[1], order, swiglu=True)[0], order)
+    y, _ = buf.expert_linear_int8(hq, hs, q[2], q[3], order)
+    assert torch.equal(ns["served"], buf.expert_unsort(y, order, gates)[0])
+    # rows do not depend on their place: the slots give the same sums
+    assert torch.equal(ns["decoded"], ns["served"][:128])
+    for leaf, grad in (("x", "d_x"), ("w1", "d_w1"), ("w2", "d_w2"), ("logits", "d_logits")):
+        assert ns[grad].shape == ns[leaf].shape and bool(torch.isfinite(ns[grad]).all())
