@@ -378,6 +378,41 @@ def test_linear_backward_int8_slots():
             check("d_w", d_w[e], dtr @ xs, (c + 1) * V * (dtr.abs() @ xs.abs()), dt)
 
 
+def test_weight_gradient_against_differences():
+    """d_w of the loss sum(y * d_y) over y = saved x w^T, by central differences of
+    the loss in fp64 (it is linear in w: the step is 1) at some weights."""
+    dev = device()
+    E, K, N, dt = 3, 144, 40, torch.bfloat16
+    counts = [5, 0, 70]
+    buf = make_buffer(E, 1, 1, 1)
+    g = torch.Generator(dev).manual_seed(21)
+    off = spans(counts)
+    x = torch.randn(off[-1], K, generator=g, device=dev).to(dt)
+    d_y = torch.randn(off[-1], N, generator=g, device=dev).to(dt)
+    w = torch.randn(E, N, K, generator=g, device=dev).double()
+    rows = torch.tensor(off, dtype=torch.int32, device=dev)
+    for block in (0, 128):
+        codes, scales, _ = buf.expert_quantize(x, rows, block=block)
+        saved = values(codes, scales).to(dt).double()
+        _, d_w, _ = buf.expert_linear_backward_int8(d_y, codes, scales, None, rows,
+                                                    d_w_dtype=torch.float32)
+
+        def terms(v):
+            return torch.cat([saved[off[e]:off[e + 1]] @ v[e].t() for e in range(E)]) * d_y.double()
+
+        # the loss is a sum of n terms, each of a sum of K: fp64 roundings
+        noise = 2 ** -52 * K * d_y.numel() * terms(w.abs()).abs().sum().item()
+        for e, n, k in ((0, 0, 0), (0, 39, 143), (1, 7, 9), (2, 0, 128), (2, 17, 66), (2, 39, 127)):
+            up, down = w.clone(), w.clone()
+            up[e, n, k] += 1
+            down[e, n, k] -= 1
+            diff = (terms(up).sum() - terms(down).sum()) / 2
+            a, b = off[e], off[e + 1]
+            each = (d_y[a:b, n].double() * saved[a:b, k]).abs().sum()
+            check("d_w", d_w[e, n, k].view(1), diff.view(1),
+                  ((b - a + 1) * V * each + noise).view(1), torch.float32)
+
+
 def swiglu_gradients(g, u, d):
     s, s1 = torch.sigmoid(g), torch.sigmoid(-g)
     return torch.cat([d * u * s * (1 + g * s1), d * g * s], 1), g * s * u

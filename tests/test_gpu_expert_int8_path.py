@@ -15,6 +15,7 @@ import torch
 from tests.gpu_common import device, make_buffer
 from tests.test_gpu_expert_int8 import product, quantized, values
 from tests.test_gpu_expert_linear import V, check, swiglu_reference
+from tests.test_gpu_strided_events import late, outputs, side  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -286,6 +287,51 @@ def test_comm_stream_and_events():
     same(got_h, want_h, n)
     same(got_x, want_x, n)
     assert torch.equal(got_w, want_w)
+
+
+@pytest.mark.parametrize("comm", [False, True], ids=["caller", "comm"])
+def test_late_strided_inputs(side, comm):  # noqa: F811
+    """Strided inputs that are written behind previous_event are copied behind it."""
+    from combine_get_dispatch_layout_amd import ExpertOrder
+    dev = device()
+    w1, w2 = weights(dev)
+    x, logits = inputs(dev, 12)
+    buf = make_buffer(E, 1, 1, T)
+    q1, s1, q2, s2 = in_int8(buf, w1, w2)
+    order, _ = buf.expert_order(buf.gate_topk(logits, K)[0])
+    off = order.expert_offsets
+    assert int(off[-1]) == T * K  # every row of every buffer is somebody's
+    rq, rs, _ = buf.expert_sort_int8(x, order)
+    r16, _ = buf.expert_dequantize(rq, rs, order)
+    bq, bs, _ = buf.expert_quantize(r16, order, block=128)
+    h, pre, _ = buf.expert_linear(r16, w1, order, swiglu=True, return_pre=True)
+    pq, ps, _ = buf.expert_quantize(pre, order, block=128)
+    kw = dict(allocate_on_comm_stream=comm)
+    cases = {
+        "expert_quantize": ((r16, off), buf.expert_quantize),
+        "expert_dequantize": ((bq, bs, off), buf.expert_dequantize),
+        "expert_sort_int8": ((x, order.row_of_slot), lambda v, r, **k: buf.expert_sort_int8(
+            v, ExpertOrder(None, r, None), **k)),
+        "expert_linear_int8": ((rq, rs, q1, s1, off), lambda *a, **k: buf.expert_linear_int8(
+            *a, swiglu=True, **k)),
+        "expert_swiglu_backward_int8": ((h, pq, ps, off),
+                                        lambda *a, **k: buf.expert_swiglu_backward_int8(
+                                            *a, return_h=True, **k)),
+        "expert_linear_backward_int8": ((pre, bq, bs, w1, off), buf.expert_linear_backward_int8),
+        "d_x alone": ((pre, w1, off), lambda d, w, o, **k: buf.expert_linear_backward(
+            d, None, w, o, **k)),
+        "d_w alone": ((pre, r16, off), lambda d, v, o, **k: buf.expert_linear_backward(
+            d, v, None, o, **k)),
+    }
+    for name, (tensors, call) in cases.items():
+        print(f"[int8] late strided inputs: {name} comm={comm}", flush=True)
+        want = outputs(call(*tensors, **kw))
+        strided, ready = late(side, *tensors)
+        got = outputs(call(*strided, previous_event=ready, **kw))
+        torch.cuda.synchronize()
+        assert len(got) == len(want) > 0
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), name
 
 
 def test_two_streams_and_threads():
