@@ -65,7 +65,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_int8_kernel(
         i32x4 acc[T::TP][T::TQ] = {};
         const int nk = (K / 2 + T::BK - 1) / T::BK;
         RingLoop<Codes2, T::BP, T::BQ, T::WP, T::WQ, NQ, T::kP, T::kQ, true, decltype(gp),
-                 decltype(gq)>(wp, wq, lane, rotate ? scattered(blk, nk) : 0, nk)
+                 decltype(gq), true>(wp, wq, lane, rotate ? scattered(blk, nk) : 0, nk)
             .run(gp, gq, (lds_char*)lp, (lds_char*)lq, wave, acc);
         const float* const wse = ws + first;
         const int mine = 4 * (lane >> 4);  // this lane's first output of a block of 16
@@ -133,6 +133,211 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_int8_kernel(
             }
         }
     });
+}
+
+// A value in LDS that no load on its way into LDS writes: told so, the compiler
+// does not wait for those.
+template <typename V>
+__device__ __forceinline__ V in_lds(const lds_char* __restrict at) {
+    return *(const __attribute__((address_space(3))) V*)at;
+}
+
+// The lane, as known from here on: neither it nor what is computed from it is kept
+// in registers from before.
+__device__ __forceinline__ int lane_here() {
+    int zero = 0;
+    asm volatile("" : "+v"(zero));
+    return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero));
+}
+
+// 256 x 256 tiles, one workgroup per CU that goes through tiles, so that nothing
+// else would use the CU while it starts or ends one.  Under a tile's last products the
+// next one's first two stages are asked for; its outputs are on their way to
+// memory while the next one multiplies its first stage.
+//
+// Waits count loads and stores in order, so every tile issues the same number:
+// stores of rows that it does not have fall outside its descriptor's range, and so
+// do the loads after the last tile.
+template <typename S, bool kSwiglu>
+__global__ __launch_bounds__(Wide::kThreads, 2) void linear_int8_wide_kernel(
+    const int8_t* x, const float* xs, const int8_t* w, const float* ws, ExpertRows er, int K, int N,
+    int cols, S* y, bool rotate, int total) {
+    typedef Wide T;
+    constexpr int kP = T::kP, kQ = T::kQ;
+    __shared__ __align__(16) Codes2 lds[kP * T::BP * T::BK + kQ * T::BQ * T::BK];
+    lds_char* const lp = (lds_char*)lds;
+    lds_char* const lq = (lds_char*)(lds + kP * T::BP * T::BK);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wp = wave % T::WP, wq = wave / T::WP;
+    const int nk = (K / 2 + T::BK - 1) / T::BK;
+    constexpr int kOuts = kSwiglu ? T::BP / 2 : T::BP;
+
+    int blk = 0;
+    TileSearch search(er);
+    const auto tile_at = [&](int v, const TileSearch::Entries& n, int ln) {
+        if (v >= total) return RowTile{-1, 0, 0, 0};
+        blk = xcd_run_block<kRunLog2>(v, total);
+        return search.find<T::BQ, kRowGroup>(er, n, ln, blk, cols);
+    };
+    typedef Along<T::BP, T::kWaves, T::BK, kSwiglu ? 2 : 1> GP;
+    typedef Along<T::BQ, T::kWaves, T::BK, 1> GQ;
+    GP gp;
+    GQ gq;
+    gp.init(K, K / 2, wave, lane);
+    gq.init(K, K / 2, wave, lane);
+    int shift = 0;
+    const auto aim = [&](const RowTile& t) {
+        const int e = max(t.e, 0), n0 = t.col * kOuts, outs = t.e < 0 ? 0 : N - n0;
+        const int8_t* const we = w + ((int64_t)e * (kSwiglu ? 2 : 1) * N + n0) * K;
+        gp.half(0, we, outs);
+        if constexpr (kSwiglu) gp.half(1, we + (int64_t)N * K, outs);
+        gq.half(0, x + (int64_t)t.begin * K, t.end - t.begin);
+        shift = rotate ? scattered(blk, nk) : 0;
+    };
+    constexpr int kPBytes = T::BP * T::BK * 2, kQBytes = T::BQ * T::BK * 2;
+    const auto place = [&](int i) {
+        return (shift + i >= nk && shift > 0 ? shift + i - nk : shift + i) * T::BK;
+    };
+    // Stages 0 .. kP - 2; the last place of P is the strips' until the outputs are out.
+    const auto ask = [&] {
+#pragma unroll
+        for (int i = 0; i < kP - 1; ++i) {
+            if (i < kQ) gq.load(lq + i * kQBytes, place(i), wave);
+            __builtin_amdgcn_sched_barrier(0);
+            gp.load(lp + i * kPBytes, place(i), wave);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    const auto ask_last = [&] {
+        gp.load(lp + (kP - 1) * kPBytes, place(kP - 1), wave);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    static_assert(kP == 3 && kQ == 2, "as the waits count them");
+
+    constexpr int kRun = T::BP / 2 / T::WP, kRunBlocks = kRun / 16, kRowBytes = kRun * 2 + 16;
+    constexpr int kLanes = kRun / 8, kRows = 64 / kLanes, kHalves = kSwiglu ? 1 : 2;
+    constexpr int kStores = T::TQ * kHalves * (16 / kRows);
+    typedef __attribute__((address_space(3))) u32x4_t lds_u32x4;
+    typedef S vec4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) vec4 lds_vec4;
+    // Each wave's strip, and the scales of its 64 rows and 128 outputs.
+    lds_char* const strip = lp + (kP - 1) * kPBytes + wave * (16 * kRowBytes);
+    lds_char* const own = lp + (kP - 1) * kPBytes + T::kWaves * 16 * kRowBytes + wave * 768;
+    static_assert(T::kWaves * (16 * kRowBytes + 768) <= kPBytes, "they fit");
+    static_assert(T::TQ == 4 && kRunBlocks == 4, "64 rows, two runs of 64 outputs");
+    const auto load_scale = [&](__amdgpu_buffer_rsrc_t rs, lds_char* to, int i) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)to, 4, i * 4, 0, 0, 0);
+    };
+
+    int v = (int)blockIdx.x;
+    RowTile tile = tile_at(v, search.ask(lane), lane);
+    if (tile.e < 0) return;
+    aim(tile);
+    ask();
+    ask_last();
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    for (;;) {
+        const RowTile cur = tile;
+        with_blocks<T::WQ>(cur.end - cur.begin, [&](auto nq) {
+            constexpr int NQ = decltype(nq)::value;
+            typedef RingLoop<Codes2, T::BP, T::BQ, T::WP, T::WQ, NQ, kP, kQ, true, GP, GQ, true> Loop;
+            const Loop loop(wp, wq, lane_here(), shift, nk);
+            i32x4 acc[T::TP][T::TQ] = {};
+            s16x8 p0[T::TP], q0[T::TQ], p1[T::TP], q1[T::TQ];
+            Loop::template barrier<GQ::kLoads + 2 * GP::kLoads + kStores>();
+            loop.frags(lp, lq, 0, p0, q0);
+            int pb = 0, qb = 0;
+#pragma clang loop unroll(disable)
+            for (int it = 0; it + 1 < nk; ++it) {
+                lds_char* const rp = lp + pb * kPBytes;
+                lds_char* const rq = lq + qb * kQBytes;
+                pb = pb + 1 == kP ? 0 : pb + 1;
+                qb = qb + 1 == kQ ? 0 : qb + 1;
+                loop.first(rp, rq, p0, q0, p1, q1, acc);
+                if (it == 0) Loop::template barrier<GP::kLoads + kStores>();
+                else Loop::template barrier<GP::kLoads>();
+                loop.second(gp, gq, lp + pb * kPBytes, lq + qb * kQBytes, rp, rq, it, wave, p0, q0, p1,
+                            q1, acc);
+            }
+            const int ln = lane_here();
+            const TileSearch::Entries entries = search.ask(ln);
+            loop.first(lp + pb * kPBytes, lq + qb * kQBytes, p0, q0, p1, q1, acc);
+            Loop::template barrier<0>();  // no load is in flight, every place has been read
+            v += (int)gridDim.x;
+            tile = tile_at(v, entries, ln);
+            __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0, where the compiler sees it
+            const int mine = 4 * (ln >> 4);  // this lane's first output of a block of 16
+            const int n0 = cur.col * kOuts, rows = cur.end - cur.begin;
+            const float* const wse = ws + (int64_t)cur.e * (kSwiglu ? 2 : 1) * N;
+            {
+                const __amdgpu_buffer_rsrc_t rx = make_rsrc(xs + cur.begin, rows * 4);
+                const int m = T::q_at(wq, ln >> 4) + (ln & 15), o = wp * kRun + ln;
+                load_scale(rx, own, m);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const __amdgpu_buffer_rsrc_t rw =
+                        make_rsrc(wse + n0 + (kSwiglu && h ? N : 0), (N - n0) * 4);
+                    load_scale(rw, own + (h + 1) * 256, kSwiglu ? o : h * (T::BP / 2) + o);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            aim(tile);
+            ask();
+            Loop::products(p1, q1, acc);
+            __builtin_amdgcn_sched_barrier(0);
+            // the scales are here
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kP - 1) * (GQ::kLoads + GP::kLoads)) : "memory");
+            const __amdgpu_buffer_rsrc_t out = make_rsrc(y + (int64_t)cur.begin * N, rows * N * 2);
+#pragma unroll
+            for (int j = 0; j < T::TQ; ++j) {
+#pragma unroll
+                for (int half = 0; half < kHalves; ++half) {
+                    if (j < NQ) {
+#pragma unroll
+                        for (int b = 0; b < kRunBlocks; ++b) {
+                            const int i = half * kRunBlocks + b;
+                            const float xm = in_lds<float>(own + (j * 16 + (ln & 15)) * 4);
+                            f32x4 f = scaled(acc[i][j], xm,
+                                             in_lds<f32x4>(own + 256 + (i * 16 + mine) * 4));
+                            if constexpr (kSwiglu) {
+                                const f32x4 u = scaled(
+                                    acc[i + kRunBlocks][j], xm,
+                                    in_lds<f32x4>(own + 512 + (i * 16 + mine) * 4));
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) f[r] = in_fp32(silu(f[r]) * u[r]);
+                            }
+                            vec4 o;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) o[r] = (S)f[r];
+                            *(lds_vec4*)(strip + (ln & 15) * kRowBytes + (b * 16 + mine) * 2) = o;
+                            if constexpr (kSwiglu) __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
+                    // the wave's own strip: its LDS accesses are in order, the compiler's are
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+                    for (int h = 0; h < 16 / kRows; ++h) {
+                        const int r = h * kRows + ln / kLanes, c = ln % kLanes;
+                        const u32x4_t o = in_lds<u32x4_t>(strip + r * kRowBytes + c * 16);
+                        const int m = T::q_at(wq, j) + r;
+                        const int n = n0 + T::p_at(wp, half * kRunBlocks) + c * 8;
+                        const bool in = j < NQ && n < N;
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            o, out, (int)(in ? (uint32_t)(m * N + n) * 2 : kOutside), 0, kStream);
+                    }
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        });
+        if (tile.e < 0) break;
+        // every wave has read its strips
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        ask_last();
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS is left in flight
 }
 
 // Few rows per expert: the weights' bytes are all that counts.  A tile has BP
@@ -527,6 +732,8 @@ __global__ __launch_bounds__(Saved::kThreads, 2) void wgrad_int8_kernel(
     });
 }
 
+constexpr int64_t kUnits = 256;  // compute units
+
 dim3 grid_of(int64_t workgroups) { return dim3((unsigned)workgroups); }
 
 template <typename S>
@@ -552,6 +759,13 @@ struct Int8Product {
         return run(swiglu ? linear_int8_thin_kernel<S, true, T> : linear_int8_thin_kernel<S, false, T>,
                    T::kTile, rotate);
     }
+    hipError_t wide(bool rotate) const {
+        const int64_t total = workgroups(er, kWideTile, outs());
+        return launch_kernel(
+            swiglu ? linear_int8_wide_kernel<S, true> : linear_int8_wide_kernel<S, false>,
+            grid_of(total < kUnits ? total : kUnits), dim3(kWideTile.threads), L, x, xs, w, ws, er, K,
+            N, (int)tiles_of(outs(), kWideTile.outs), y, rotate, (int)total);
+    }
     template <typename T, int kPolicy>
     hipError_t tiles(bool rotate) const {
         return run(swiglu ? linear_int8_kernel<S, true, T, kPolicy>
@@ -572,7 +786,7 @@ hipError_t linear_int8_as(const int8_t* x, const float* xs, const int8_t* w, con
         case Int8Tiles::kOnce: return p.template tiles<Small, kStream>(rotate);
         case Int8Tiles::kDeepOnce: return p.template tiles<Deep, kStream>(rotate);
         case Int8Tiles::kDeep: return p.template tiles<Deep, 0>(rotate);
-        case Int8Tiles::kWide: return p.template tiles<Wide, 0>(rotate);
+        case Int8Tiles::kWide: return p.wide(rotate);
         default: return hipErrorInvalidValue;  // refused before
     }
 }

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "expert_launch.h"
+#include "numeric.h"
 
 namespace moedx {
 
@@ -32,6 +33,18 @@ struct RowTile {
     int col;         // its column tile
 };
 
+// Tile `local` of expert e, whose rows begin .. end have `mine` row tiles.
+template <int BM, int kGroup>
+__device__ __forceinline__ RowTile tile_of(int e, int begin, int end, int mine, int local, int cols) {
+    const int grp = local / (kGroup * cols);
+    local -= grp * kGroup * cols;
+    const int in_grp = min(kGroup, mine - grp * kGroup);
+    const int col = local / in_grp;
+    const int step = row_step<BM>(end - begin, mine);
+    const int b = begin + (grp * kGroup + local - col * in_grp) * step;
+    return RowTile{e, b, b + min(step, end - b), col};
+}
+
 // Tile `i` (wave-uniform; every lane of the wave takes part) where each expert
 // has ceil(c / BM) x cols tiles: up to kGroup row tiles go through the columns
 // together, so that tiles close in number share both operands.
@@ -53,22 +66,58 @@ __device__ __forceinline__ RowTile find_block(const ExpertRows& er, int i, int c
         const uint64_t past = __ballot((int64_t)(base + incl) * cols > i);
         if (past) {
             const int l = __builtin_ctzll(past);
-            const int begin = __builtin_amdgcn_readlane(s.begin, l);
-            const int end = __builtin_amdgcn_readlane(s.end, l);
-            const int mine = __builtin_amdgcn_readlane(t, l);
-            const int first = base + __builtin_amdgcn_readlane(incl - t, l);
-            int local = i - first * cols;
-            const int grp = local / (kGroup * cols);
-            local -= grp * kGroup * cols;
-            const int in_grp = min(kGroup, mine - grp * kGroup);
-            const int col = local / in_grp;
-            const int step = row_step<BM>(end - begin, mine);
-            const int b = begin + (grp * kGroup + local - col * in_grp) * step;
-            return RowTile{e0 + l, b, b + min(step, end - b), col};
+            return tile_of<BM, kGroup>(e0 + l, __builtin_amdgcn_readlane(s.begin, l),
+                                       __builtin_amdgcn_readlane(s.end, l),
+                                       __builtin_amdgcn_readlane(t, l),
+                                       i - (base + __builtin_amdgcn_readlane(incl - t, l)) * cols,
+                                       cols);
         }
         base += __builtin_amdgcn_readlane(incl, 63);
     }
     return RowTile{-1, 0, 0, 0};
 }
+
+// find_block for growing tile numbers: the rows of the 64 experts that the last
+// tile was found among may be asked for ahead.
+struct TileSearch {
+    const int32_t* rows;  // offsets or counts
+    int last;             // their last entry
+    int e0 = 0, base = 0;  // the first of 64 experts, tiles before them
+    struct Entries {
+        int a, b;
+    };
+
+    __device__ __forceinline__ explicit TileSearch(const ExpertRows& er)
+        : rows(er.offsets ? er.offsets : er.counts), last(er.offsets ? er.E : er.E - 1) {}
+    __device__ __forceinline__ Entries ask(int lane) const {
+        return Entries{rows[min(e0 + lane, last)], rows[min(e0 + lane + 1, last)]};
+    }
+    template <int BM, int kGroup>
+    __device__ __forceinline__ RowTile find(const ExpertRows& er, Entries n, int lane, int i,
+                                            int cols) {
+        for (;;) {
+            const int all = (int)er.rows, first = er.offsets ? n.a : min(e0 + lane, er.E) * er.cap;
+            const int begin = min(max(first, 0), all);
+            const int end = er.offsets ? min(max(n.b, begin), all)
+                            : e0 + lane < er.E ? begin + min(max(n.a, 0), er.cap)
+                                               : begin;
+            const int t = row_tiles<BM>(end - begin);
+            const int incl = wave_scan(t);
+            const uint64_t past = __ballot((int64_t)(base + incl) * cols > i);
+            if (past) {
+                const int l = __builtin_ctzll(past);
+                return tile_of<BM, kGroup>(e0 + l, __builtin_amdgcn_readlane(begin, l),
+                                           __builtin_amdgcn_readlane(end, l),
+                                           __builtin_amdgcn_readlane(t, l),
+                                           i - (base + __builtin_amdgcn_readlane(incl - t, l)) * cols,
+                                           cols);
+            }
+            if (e0 + 64 >= er.E) return RowTile{-1, 0, 0, 0};
+            base += __builtin_amdgcn_readlane(incl, 63);
+            e0 += 64;
+            n = ask(lane);
+        }
+    }
+};
 
 }  // namespace moedx

@@ -377,7 +377,7 @@ struct SharedCuLoop {
 // tile has are loaded (64 experts of 128 rows, 7168 -> 4096: 735 us with all of
 // them, 690 us without; no gain where P is read across r).
 template <typename S, int BP, int BQ, int WP, int WQ, int NQ, int kP, int kQ, bool kPartQ,
-          typename LP, typename LQ>
+          typename LP, typename LQ, bool kStop = false>
 struct RingLoop {
     typedef typename Mfma<S>::Acc Acc;
     static constexpr int TP = BP / WP / 16, TQ = BQ / WQ / 16;
@@ -398,7 +398,7 @@ struct RingLoop {
     }
     __device__ __forceinline__ int place(int it) const {
         const int s = it + shift;
-        return (s - (s >= stages ? stages : 0)) * kBK;
+        return (kStop && shift == 0 ? s : s - (s >= stages ? stages : 0)) * kBK;
     }
     __device__ __forceinline__ void frags(const lds_char* lp, const lds_char* lq, int kk,
                                           s16x8 (&p)[TP], s16x8 (&q)[TQ]) const {

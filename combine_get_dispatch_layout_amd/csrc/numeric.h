@@ -94,6 +94,14 @@ __device__ __forceinline__ float wave_max(float v) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
+// The sum of v over this lane and those below it.
+__device__ __forceinline__ int wave_scan(int v) {
+#define MOEDX_STEP(c, r) v += dpp<c, r>(0, v)
+    MOEDX_DPP_STEPS(MOEDX_STEP);
+#undef MOEDX_STEP
+    return v;
+}
+
 // v of the lane that kCtrl (a quad permutation or a mirror) names.
 template <int kCtrl>
 __device__ __forceinline__ double lane_swap(double v) {
