@@ -38,6 +38,9 @@ __device__ __forceinline__ f32x4 scales4(const float* ws, int n, int N) {
 typedef Shape<128, 128, 2, 64, 3, 2> Deep;  // 80 KB of LDS: two workgroups share a CU
 static_assert(same(Deep::kTile, kSmallTile), "the plan's tile is the kernel's");
 
+// 128 x 128 tiles, two workgroups to a CU.  Loads past a reduction's last stage
+// fetch nothing (kStop): 64 experts of 48 rows, 2048 -> 1408: 44 us with them, 42; of
+// 64 rows, 7168 -> 4096: 306 and 299.
 template <typename S, bool kSwiglu, typename T, int kPolicy>
 __global__ __launch_bounds__(T::kThreads, 2) void linear_int8_kernel(
     const int8_t* x, const float* xs, const int8_t* w, const float* ws, ExpertRows er, int K, int N,
@@ -70,11 +73,8 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_int8_kernel(
         const float* const wse = ws + first;
         const int mine = 4 * (lane >> 4);  // this lane's first output of a block of 16
         // A wave's outputs of 16 rows, kRun neighbours at a time, change lanes in
-        // LDS: whole cache lines (half ones in 128 x 128 tiles) are stored, past
-        // the caches.  64 experts, us, in 64-byte pieces through the caches, as
-        // lines through them and past them: 192 rows, 1424 -> 4096: 157, 152, 143;
-        // 64 rows, 4096 -> 4096: 207, 205, 181; 512 rows, 7168 -> 4096, gated: 833, 832,
-        // 830; the first with a quantize of the outputs behind it: 181, 176, 175.
+        // LDS: half cache lines are stored, past the caches (64 experts of 64 rows,
+        // 4096 -> 4096: 181 us; 205 through the caches, 207 in 64-byte pieces).
         constexpr int kRun = T::BP / 2 / T::WP, kRunBlocks = kRun / 16, kRowBytes = kRun * 2 + 16;
         constexpr int kLanes = kRun / 8, kRows = 64 / kLanes;
         typedef __attribute__((address_space(3))) u32x4_t lds_u32x4;
@@ -83,8 +83,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_int8_kernel(
         lds_char* const strip = (lds_char*)lp + wave * (2 * 16 * kRowBytes);
         static_assert(T::kWaves * 2 * 16 * kRowBytes <= (T::kP * T::BP + T::kQ * T::BQ) * T::BK * 2,
                       "the strips fit");
-        // All scales at once, ahead of the stores that they cannot pass (the first
-        // product above 145 to 134 us, 64 x 512 rows, 2048 -> 7168: 538 to 489).
+        // all scales at once, ahead of the stores that they cannot pass
         float xm[NQ];
         f32x4 wm[T::TP];
 #pragma unroll
@@ -150,10 +149,20 @@ __device__ __forceinline__ int lane_here() {
     return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero));
 }
 
-// 256 x 256 tiles, one workgroup per CU that goes through tiles, so that nothing
-// else would use the CU while it starts or ends one.  Under a tile's last products the
-// next one's first two stages are asked for; its outputs are on their way to
-// memory while the next one multiplies its first stage.
+// 256 x 256 tiles, one workgroup per CU that goes through tiles, as nothing else
+// uses the CU while it starts or ends one.  Under a tile's last products the next
+// one's first two stages are asked for; its outputs are on their way to memory
+// while the next one multiplies its first stage.  64 experts, us, a workgroup
+// to each tile and this way: 192 rows, 1424 -> 4096: 133, 123; 512 rows, 2048 -> 7168:
+// 479, 450; 256 rows, 4096 -> 2 x 2048, gated: 324, 303; 512 rows, 7168 -> 2 x 2048, gated:
+// 822, 815 (power bounds it: 2360 TOP/s; one expert of 8192 rows, 8192 -> 8192: 388,
+// 384, 2860 TOP/s).  Without the loads past a reduction's end, which are left out
+// here (kStop), a few of the first two's microseconds: 126 and 456.
+//
+// Outputs change lanes in LDS and are stored as whole cache lines past the caches,
+// the scales come through LDS (the first product with a workgroup to each tile:
+// stored in 64-byte pieces through the caches 157, in lines through them 152, past
+// them 143; the scales asked for at once 134).
 //
 // Waits count loads and stores in order, so every tile issues the same number:
 // stores of rows that it does not have fall outside its descriptor's range, and so
@@ -634,7 +643,7 @@ struct SavedLoop {
 };
 
 // 128 x 256: the P side, which is restored, is the narrow one (256 x 128: 1015 us
-// for 966 at 64 experts of 768 rows, 4096 x 2048); two workgroups share a CU.
+// for 966 at 64 experts of 768 rows, 4096 x 2048, 917 by now); two workgroups share a CU.
 typedef Shape<128, 256, 2, 32, 2, 4> Saved;
 static_assert(same(Saved::kTile, kSavedTile), "the plan's tile is the kernel's");
 
@@ -655,6 +664,8 @@ __device__ __forceinline__ void with_even_blocks(int rows, F&& f) {
 //   rows each    16       48       96       192      384      768
 //   bf16       166 249  195 298  246 368  330 470  597 626  942 975
 //   fp32       447 503  425 429  422 539  454 715  788 886 1126 1174
+// (both before the products' raised priority, which takes the longest to 917 and
+// 1081).
 template <typename S, typename D>
 __global__ __launch_bounds__(Saved::kThreads, 2) void wgrad_int8_kernel(
     const S* d_y, const int8_t* x, const float* scales, int groups, ExpertRows er, int K, int N,

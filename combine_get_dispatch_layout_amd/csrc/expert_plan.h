@@ -167,44 +167,51 @@ inline Tiles input_gradient_tiles(const ExpertRows& er, int outs) {
 // The int8 product's tiles.  kOnce: 128 x 128 with the weights past the caches;
 // kDeep, kDeepOnce: 128 x 128 with three stages of the weights, through the caches
 // and past them.  64 experts with the same number of rows each, us:
-//   rows each                    1    8   16   32   40   64   96  128
-//   7168 -> 4096   32 x 64     266  271  277  298  570  524  798  944
-//                  64 x 128    271  275  280  292  300  328  609  569
-//                  kOnce       280  283  290  302  298  309  342  375
-//                  kDeepOnce                       297  306  341  374
-//                  kDeep                           332  337  362  394
-//                  256 x 256   328  331  333  336  336  340  358  366
-//   2048 -> 1408   64 x 128     34   34   35   39   40   42   63   64
-//                  kOnce        42   42   42   44   45   47   52   58
-//                  256 x 256    46   46   47   49   48   49   54   56
+//   rows each                    1    8   16   24   32   40   64   96  128
+//   7168 -> 4096   32 x 64     267  277  287  302  322
+//                  64 x 128    270  281  291  299  309  321  339  661  564
+//                  kOnce       272  275  277  280  281  287  298  328  357
+//                  kDeepOnce   271  276  276  277  277  283  292  326  360
+//                  kDeep                           314  318  323  344  372
+//                  256 x 256                       316  318  321  332  342
+//   2048 -> 1408   64 x 128     34   34   35   36   39   40   42   63   63
+//                  kOnce        39   40   39   40   40   41   43   47   51
+//                  256 x 256                        47   47   48   51   53
 // and with rows that vary, as uniform and as skewed routing gives them (4096 ->
-// 4096; on average 32, 48, 64, 80 and 96):
-//   64 x 128       190 223   203 257   293 295   369 344   393 387
-//   kOnce          189 218   193 230   203 253   213 288   239 306
-//   256 x 256      211 213   217 237   227 254   237 264   244 274
+// 4096; on average 8, 12, 16, 32, 64, 80 and 96):
+//   64 x 128    168 162  172 179  175 189  184 219  288 295
+//   kOnce       170 162  171 168  171 172  175 209  182 229  191 264  212 287
+//   kDeepOnce   177 164  178 174  179 177  182 208
+//   256 x 256                                       199 233  201 246  205 255
 //
 // One or a few tokens ask for the weights of as many experts: up to two
 // workgroups of 64 x 128 per compute unit, 32 x 64 keep more in flight (rows in
-// 1, 8 and 16 experts, 7168 -> 2048: 15 21 37 and 33 35 39; one expert of 32 rows,
-// 8192 -> 8192: 20 and 38).  Where 256 x 256 leave compute units without a tile
-// (8 experts, 7168 -> 4096, 48, 96, 128, 256 and 512 rows):
-//   kOnce           57   60   62   82  153
-//   kDeepOnce       42   47   51
-//   kDeep           51   56   60   79  140
-//   256 x 256       60   66   70   97  108 (256 tiles)
+// 1, 8 and 16 experts, 7168 -> 2048: 15 21 37, by 64 x 128 34 35 40, by kDeepOnce 28
+// 31 38; one expert of 32 rows, 8192 -> 8192: 20, 38 and 34).  Where 256 x 256 leave
+// compute units without a tile (8 experts, 7168 -> 4096, 48, 96, 128, 256 and 512
+// rows):
+//   kOnce           56   58   60   81  148
+//   kDeepOnce       40   44   48   83  148
+//   kDeep           50   54   58   78  134
+//   256 x 256       61   66   69   95  104 (256 tiles)
 // (Weights that the 256 MB memory-side cache holds from the call before, as a
 // small model's may be, are better read through the caches: 8 of 48 rows, 4096 ->
 // 2048: 20 by kDeep, 23 by kDeepOnce.)
 //
 // Slots may be nearly all empty and every workgroup looks for its tile, so small
 // tiles stay below so many looks at 64 experts (4096 -> 1024; every expert has 4
-// rows, and 8 have one; 32 x 64, 64 x 128 and kOnce):
-//   128 experts, 64 slots       85   85   86      15   22   30
-//   256 experts, 128 slots     201  166  171      64   22   31
-//   256 experts, 256 slots     258  181  179     121   36   37
-//   1024 experts, 128 slots   1236  728  709     812  210  125
-constexpr int64_t kNarrowLikely = 32, kThinLikely = 40, kOnceLikely = 80, kDeepOnceLikely = 128;
-constexpr int64_t kNarrowLooks = 512, kThinLooks = 4096;
+// rows, and 8 have one; 32 x 64, 64 x 128, kOnce and 256 x 256, whose workgroups
+// look on until there is no tile left):
+//    64 experts, 128 slots            44   45   51           22   30   34
+//   128 experts, 64 slots       85    84   87   98     15    22   31   34
+//   256 experts, 128 slots     201   167  174  188     64    22   31   34
+//   256 experts, 256 slots     258   182  178  189    121    35   37   34
+//   1024 experts, 128 slots   1236   730  707  721    812   209  125   38
+// Below that, 64 x 128 serve slots of more rows, too: which experts have any is not
+// known.
+constexpr int64_t kNarrowLikely = 32, kThinLikely = 12, kThinLikelySlots = 40;
+constexpr int64_t kOnceLikely = 72, kDeepOnceLikely = 128;
+constexpr int64_t kNarrowLooks = 512, kSlotLooks = 4096;
 
 enum class Int8Tiles { kNarrow, kThin, kOnce, kDeepOnce, kDeep, kWide, kNone };
 
@@ -220,11 +227,13 @@ inline Int8Tiles int8_tiles(const ExpertRows& er, int outs) {
     if (likely <= kNarrowLikely && active * cols <= 512 &&
         slots_serve(er, kNarrowTile, kNarrowLooks) && fits(kNarrowTile))
         return Int8Tiles::kNarrow;
-    if (likely <= kThinLikely && slots_serve(er, kThinTile, kThinLooks) && fits(kThinTile))
+    if (likely <= (er.offsets ? kThinLikely : kThinLikelySlots) &&
+        slots_serve(er, kThinTile, kSlotLooks) && fits(kThinTile))
         return Int8Tiles::kThin;
     if (few_wide_tiles(er, likely, outs) && fits(kSmallTile))
         return likely <= kDeepOnceLikely ? Int8Tiles::kDeepOnce : Int8Tiles::kDeep;
-    if (likely <= kOnceLikely && small_serves(er) && fits(kSmallTile)) return Int8Tiles::kOnce;
+    if (likely <= kOnceLikely && slots_serve(er, kSmallTile, kSlotLooks) && fits(kSmallTile))
+        return Int8Tiles::kOnce;
     return fits(kWideTile) ? Int8Tiles::kWide : Int8Tiles::kNone;
 }
 

@@ -64,7 +64,8 @@ int main() {
     } examples[] = {
         {with_offsets(64, 8), 4096, Int8Tiles::kNarrow},      // one token's experts
         {with_offsets(64, 256), 4096, Int8Tiles::kThin},      // a few rows in each
-        {with_offsets(64, 2048), 4096, Int8Tiles::kThin},
+        {with_offsets(64, 768), 4096, Int8Tiles::kThin},
+        {with_offsets(64, 2048), 4096, Int8Tiles::kOnce},
         {with_offsets(64, 4096), 4096, Int8Tiles::kOnce},
         {with_offsets(64, 32768), 4096, Int8Tiles::kWide},
         {with_offsets(8, 512), 4096, Int8Tiles::kDeepOnce},   // too few wide tiles
@@ -73,7 +74,8 @@ int main() {
         {with_offsets(1, 32), 8192, Int8Tiles::kNarrow},
         {with_counts(64, 128), 4096, Int8Tiles::kThin},       // a decode batch's slots
         {with_counts(64, 1), 4096, Int8Tiles::kNarrow},
-        {with_counts(1024, 128), 1024, Int8Tiles::kOnce},     // too many looks
+        {with_counts(1024, 128), 1024, Int8Tiles::kWide},     // too many looks
+        {with_counts(128, 512), 4096, Int8Tiles::kThin},
         {with_counts(1024, 1 << 20), 16384, Int8Tiles::kNone},
         {with_offsets(1, INT32_MAX), 8, Int8Tiles::kNone},
         {with_offsets(1, ((int64_t)1 << 31) - 513), 8, Int8Tiles::kWide},

@@ -216,6 +216,9 @@ CASES += [([60, 70, 0, 129, 61, 90, 33, 64] * 2, k, 4104) for k in (80, 4096)]
 # 64 x 128 tiles: rows of one tile, one more, two; stages fewer and more than the ring
 CASES += [([33, 40, 0, 64, 38, 65, 36, 30], k, 136) for k in (16, 272, 400, 4096, 7168)]
 CASES += [([5, 0, 17, 64, 33, 1] * 11, 400, 1032)]
+CASES += [([64, 0, 1, 33, 0, 0, 2, 0, 0, 65, 0, 0, 16, 0, 5, 3] * 4, k, 1032) for k in (16, 272, 400, 8192)]
+# 256 x 256 tiles that start at scattered places, more than a workgroup's first
+CASES += [([100, 90, 120, 81] * 16, 4096, 1032), ([100, 90, 120, 81] * 16, 112, 1032)]
 ids = lambda c: f"{len(c[0])}e{sum(c[0])}r-{c[1]}-{c[2]}"  # noqa: E731
 
 

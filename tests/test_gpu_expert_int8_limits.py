@@ -126,6 +126,56 @@ def test_many_experts(E, cap, dense):
     check("h of slots", h[ex, slot], want_h, 8 * V * want_h.abs(), dt)
 
 
+@pytest.mark.parametrize("K", [16, 160, 400, 1040])
+def test_wide_tiles_of_many_experts(K):
+    """256 x 256 tiles, several to a workgroup, among more experts than a wave has
+    lanes: runs of experts without rows, a few rows and many, in expert order
+    and in slots."""
+    dev = device()
+    E, N, cap, dt = 200, 1032, 2048, torch.bfloat16
+    g = torch.Generator().manual_seed(K)
+    counts = torch.randint(0, 40, (E,), generator=g)
+    counts[60:140] = 0
+    for e, c in ((0, 700), (63, 1), (64, 513), (65, 256), (127, 2048), (128, 300), (139, 0),
+                 (140, 1900), (191, 255), (192, 257), (199, 2000)):
+        counts[e] = c
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int64), counts.cumsum(0)])
+    M = int(offsets[-1]) + 9000  # rows behind the last expert's: more than 72 an expert
+    assert M >= 73 * E
+    buf = make_buffer(E, 1, 1, 1)
+    gd = torch.Generator(dev).manual_seed(K)
+    x = torch.randint(-128, 128, (M, K), generator=gd, device=dev, dtype=torch.int8)
+    w = torch.randint(-128, 128, (E, 2 * N, K), generator=gd, device=dev, dtype=torch.int8)
+    xs = torch.rand(M, generator=gd, device=dev) * 0.02
+    ws = torch.rand(E, 2 * N, generator=gd, device=dev) * K ** -0.5 * 0.02
+    xs[int(offsets[-1]):] = float("nan")
+    wn, wsn = w[:, :N].contiguous(), ws[:, :N].contiguous()
+    rows, cnt = offsets.int().to(dev), counts.int().to(dev)
+    print(f"[int8] wide tiles of many experts, K={K}", flush=True)
+    sevens = lambda *s: torch.full(s + (N,), 7.0, dtype=dt, device=dev)  # noqa: E731
+    y, _ = buf.expert_linear_int8(x, xs, wn, wsn, rows, out=sevens(M))
+    h, _ = buf.expert_linear_int8(x, xs, w, ws, rows, swiglu=True, out=sevens(M))
+    assert (y[int(offsets[-1]):] == 7.0).all() and (h[int(offsets[-1]):] == 7.0).all()
+    sx = torch.zeros(E, cap, K, dtype=torch.int8, device=dev)
+    ss = torch.full((E, cap), float("nan"), device=dev)
+    for e in range(E):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        if a == b:
+            continue
+        p = product(x[a:b], xs[a:b], w[e], ws[e])
+        assert torch.equal(y[a:b], p[:, :N].to(dt)), e
+        gt, u = p[:, :N].double(), p[:, N:].double()
+        want = gt * torch.sigmoid(gt) * u
+        check("h", h[a:b], want, 8 * V * want.abs(), dt)
+        sx[e, :b - a], ss[e, :b - a] = x[a:b], xs[a:b]
+    sy, _ = buf.expert_linear_int8(sx, ss, wn, wsn, cnt, out=sevens(E, cap))
+    sh, _ = buf.expert_linear_int8(sx, ss, w, ws, cnt, swiglu=True, out=sevens(E, cap))
+    for e in range(E):
+        a, c = int(offsets[e]), int(counts[e])
+        assert torch.equal(sy[e, :c], y[a:a + c]) and torch.equal(sh[e, :c], h[a:a + c]), e
+        assert (sy[e, c:] == 7.0).all() and (sh[e, c:] == 7.0).all(), e
+
+
 def test_slots_of_many_experts():
     """1024 experts' slots of which few rows are likely."""
     dev = device()
