@@ -38,102 +38,6 @@ __device__ __forceinline__ f32x4 scales4(const float* ws, int n, int N) {
 typedef Shape<128, 128, 2, 64, 3, 2> Deep;  // 80 KB of LDS: two workgroups share a CU
 static_assert(same(Deep::kTile, kSmallTile), "the plan's tile is the kernel's");
 
-// 128 x 128 tiles, two workgroups to a CU.  Loads past a reduction's last stage
-// fetch nothing (kStop): 64 experts of 48 rows, 2048 -> 1408: 44 us with them, 42; of
-// 64 rows, 7168 -> 4096: 306 and 299.
-template <typename S, bool kSwiglu, typename T, int kPolicy>
-__global__ __launch_bounds__(T::kThreads, 2) void linear_int8_kernel(
-    const int8_t* x, const float* xs, const int8_t* w, const float* ws, ExpertRows er, int K, int N,
-    int cols, S* y, bool rotate) {
-    __shared__ __align__(16) Codes2 lp[T::kP * T::BP * T::BK + T::kQ * T::BQ * T::BK];
-    Codes2* const lq = lp + T::kP * T::BP * T::BK;
-    const int blk = xcd_run_block<kRunLog2>((int)blockIdx.x, (int)gridDim.x);
-    const RowTile tile = find_block<T::BQ, kRowGroup>(er, blk, cols);
-    if (tile.e < 0) return;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wp = wave % T::WP, wq = wave / T::WP;
-    const int n0 = tile.col * (kSwiglu ? T::BP / 2 : T::BP);
-    const int64_t first = (int64_t)tile.e * (kSwiglu ? 2 : 1) * N;  // the expert's weight rows
-    const int8_t* we = w + (first + n0) * K;
-    Along<T::BP, T::kWaves, T::BK, kSwiglu ? 2 : 1, kPolicy> gp;
-    gp.init(K, K / 2, wave, lane);
-    gp.half(0, we, N - n0);
-    if constexpr (kSwiglu) gp.half(1, we + (int64_t)N * K, N - n0);
-    Along<T::BQ, T::kWaves, T::BK, 1> gq;
-    gq.init(K, K / 2, wave, lane);
-    gq.half(0, x + (int64_t)tile.begin * K, tile.end - tile.begin);
-    with_blocks<T::WQ>(tile.end - tile.begin, [&](auto nq) {
-        constexpr int NQ = decltype(nq)::value;
-        i32x4 acc[T::TP][T::TQ] = {};
-        const int nk = (K / 2 + T::BK - 1) / T::BK;
-        RingLoop<Codes2, T::BP, T::BQ, T::WP, T::WQ, NQ, T::kP, T::kQ, true, decltype(gp),
-                 decltype(gq), true>(wp, wq, lane, rotate ? scattered(blk, nk) : 0, nk)
-            .run(gp, gq, (lds_char*)lp, (lds_char*)lq, wave, acc);
-        const float* const wse = ws + first;
-        const int mine = 4 * (lane >> 4);  // this lane's first output of a block of 16
-        // A wave's outputs of 16 rows, kRun neighbours at a time, change lanes in
-        // LDS: half cache lines are stored, past the caches (64 experts of 64 rows,
-        // 4096 -> 4096: 181 us; 205 through the caches, 207 in 64-byte pieces).
-        constexpr int kRun = T::BP / 2 / T::WP, kRunBlocks = kRun / 16, kRowBytes = kRun * 2 + 16;
-        constexpr int kLanes = kRun / 8, kRows = 64 / kLanes;
-        typedef __attribute__((address_space(3))) u32x4_t lds_u32x4;
-        typedef S vec4 __attribute__((ext_vector_type(4)));
-        typedef __attribute__((address_space(3))) vec4 lds_vec4;
-        lds_char* const strip = (lds_char*)lp + wave * (2 * 16 * kRowBytes);
-        static_assert(T::kWaves * 2 * 16 * kRowBytes <= (T::kP * T::BP + T::kQ * T::BQ) * T::BK * 2,
-                      "the strips fit");
-        // all scales at once, ahead of the stores that they cannot pass
-        float xm[NQ];
-        f32x4 wm[T::TP];
-#pragma unroll
-        for (int j = 0; j < NQ; ++j) {
-            const uint32_t m = (uint32_t)tile.begin + T::q_at(wq, j) + (lane & 15);
-            xm[j] = m < (uint32_t)tile.end ? xs[m] : 0.0f;  // unsigned: past 2^31 for the last tiles
-        }
-#pragma unroll
-        for (int i = 0; i < T::TP; ++i) {
-            const bool up = kSwiglu && i >= kRunBlocks;
-            const int n = n0 + T::p_at(wp, up ? i - kRunBlocks : i) + mine;
-            wm[i] = scales4(up ? wse + N : wse, n, N);
-        }
-#pragma unroll
-        for (int j = 0; j < NQ; ++j) {
-#pragma unroll
-            for (int half = 0; half < (kSwiglu ? 1 : 2); ++half) {
-                lds_char* const at = strip + (kSwiglu ? j & 1 : half) * 16 * kRowBytes;
-#pragma unroll
-                for (int b = 0; b < kRunBlocks; ++b) {
-                    const int i = half * kRunBlocks + b;
-                    f32x4 v = scaled(acc[i][j], xm[j], wm[i]);
-                    if constexpr (kSwiglu) {
-                        const f32x4 u = scaled(acc[i + kRunBlocks][j], xm[j], wm[i + kRunBlocks]);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) v[r] = in_fp32(silu(v[r]) * u[r]);
-                    }
-                    vec4 o;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) o[r] = (S)v[r];
-                    *(lds_vec4*)(at + (lane & 15) * kRowBytes + (b * 16 + mine) * 2) = o;
-                }
-                // the wave's own strip: its LDS accesses are in order, the compiler's are
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-                for (int h = 0; h < 16 / kRows; ++h) {
-                    const int r = h * kRows + lane / kLanes, c = lane % kLanes;
-                    const u32x4_t v = *(lds_u32x4*)(at + r * kRowBytes + c * 16);
-                    const uint32_t mr = (uint32_t)tile.begin + T::q_at(wq, j) + r;
-                    const int n = n0 + T::p_at(wp, half * kRunBlocks) + c * 8;
-                    if (mr < (uint32_t)tile.end && n < N)
-                        __builtin_nontemporal_store(
-                            v, reinterpret_cast<u32x4_t*>(y + (int64_t)mr * N + n));
-                }
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            }
-        }
-    });
-}
-
 // A value in LDS that no load on its way into LDS writes: told so, the compiler
 // does not wait for those.
 template <typename V>
@@ -149,33 +53,44 @@ __device__ __forceinline__ int lane_here() {
     return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero));
 }
 
-// 256 x 256 tiles, one workgroup per CU that goes through tiles, as nothing else
-// uses the CU while it starts or ends one.  Under a tile's last products the next
-// one's first two stages are asked for; its outputs are on their way to memory
-// while the next one multiplies its first stage.  64 experts, us, a workgroup
-// to each tile and this way: 192 rows, 1424 -> 4096: 133, 123; 512 rows, 2048 -> 7168:
-// 479, 450; 256 rows, 4096 -> 2 x 2048, gated: 324, 303; 512 rows, 7168 -> 2 x 2048, gated:
-// 822, 815 (power bounds it: 2360 TOP/s; one expert of 8192 rows, 8192 -> 8192: 388,
-// 384, 2860 TOP/s).  Without the loads past a reduction's end, which are left out
-// here (kStop), a few of the first two's microseconds: 126 and 456.
+// Tiles of 256 x 256, one workgroup per CU, and of 128 x 128, two.  A workgroup goes
+// through tiles: under one's last products the next one's first two stages are
+// asked for, and its outputs are on their way to memory while the next one
+// multiplies its first stage.  64 experts, us, a workgroup to each tile and this
+// way: 192 rows, 1424 -> 4096: 133, 123; 512 rows, 2048 -> 7168: 479, 450; 256 rows,
+// 4096 -> 2 x 2048, gated: 324, 303; 512 rows, 7168 -> 2 x 2048, gated: 822, 815 (power
+// bounds it: 2360 TOP/s; one expert of 8192 rows, 8192 -> 8192: 388, 384, 2860
+// TOP/s); 128 x 128: 48 rows, 2048 -> 1408: 41.8, 39.1; 64 rows, 4096 -> 2048: 91.9, 88.7.
+// In the first of each pair for 256 x 256 loads past a reduction's last stage
+// start over; left out (kStop), they save the first two products 3 and 7 of these
+// us, and 48 rows, 2048 -> 1408, 44.5 to 41.8.
 //
-// Outputs change lanes in LDS and are stored as whole cache lines past the caches,
-// the scales come through LDS (the first product with a workgroup to each tile:
-// stored in 64-byte pieces through the caches 157, in lines through them 152, past
-// them 143; the scales asked for at once 134).
+// Outputs change lanes in LDS and are stored past the caches, as whole cache lines
+// (half ones in 128 x 128 tiles), the scales come through LDS.  With a workgroup
+// to each tile, in 64-byte pieces through the caches, as lines through them and
+// past them: 192 rows, 1424 -> 4096: 157, 152, 143 (the scales asked for at once: 134);
+// 64 rows, 4096 -> 4096: 207, 205, 181.
 //
 // Waits count loads and stores in order, so every tile issues the same number:
-// stores of rows that it does not have fall outside its descriptor's range, and so
-// do the loads after the last tile.
-template <typename S, bool kSwiglu>
-__global__ __launch_bounds__(Wide::kThreads, 2) void linear_int8_wide_kernel(
+// stores of rows that it does not have fall outside its descriptor's range, as do
+// those ahead of the first tile.
+template <typename S, bool kSwiglu, typename T, int kPolicy>
+__global__ __launch_bounds__(T::kThreads, 2) void linear_int8_kernel(
     const int8_t* x, const float* xs, const int8_t* w, const float* ws, ExpertRows er, int K, int N,
     int cols, S* y, bool rotate, int total) {
-    typedef Wide T;
     constexpr int kP = T::kP, kQ = T::kQ;
-    __shared__ __align__(16) Codes2 lds[kP * T::BP * T::BK + kQ * T::BQ * T::BK];
+    constexpr int kPBytes = T::BP * T::BK * 2, kQBytes = T::BQ * T::BK * 2;
+    // A wave's strip of 16 rows, and the scales of its rows and outputs.
+    constexpr int kRun = T::BP / 2 / T::WP, kRunBlocks = kRun / 16, kRowBytes = kRun * 2 + 16;
+    constexpr int kOwn = 16 * kRowBytes + T::TQ * 64 + 2 * kRun * 4;
+    // They have P's last place until the outputs are out, or one of their own.
+    constexpr bool kApart = kP == kQ;
+    constexpr int kAsked = kApart ? kP : kP - 1;  // stages asked for under the last products
+    static_assert(kAsked == 2 && kQ == 2, "as the waits count them");
+    static_assert(kApart || T::kWaves * kOwn <= kPBytes, "they fit");
+    __shared__ __align__(16) char lds[kP * kPBytes + kQ * kQBytes + (kApart ? T::kWaves * kOwn : 0)];
     lds_char* const lp = (lds_char*)lds;
-    lds_char* const lq = (lds_char*)(lds + kP * T::BP * T::BK);
+    lds_char* const lq = lp + kP * kPBytes;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wp = wave % T::WP, wq = wave / T::WP;
@@ -189,7 +104,7 @@ __global__ __launch_bounds__(Wide::kThreads, 2) void linear_int8_wide_kernel(
         blk = xcd_run_block<kRunLog2>(v, total);
         return search.find<T::BQ, kRowGroup>(er, n, ln, blk, cols);
     };
-    typedef Along<T::BP, T::kWaves, T::BK, kSwiglu ? 2 : 1> GP;
+    typedef Along<T::BP, T::kWaves, T::BK, kSwiglu ? 2 : 1, kPolicy> GP;
     typedef Along<T::BQ, T::kWaves, T::BK, 1> GQ;
     GP gp;
     GQ gq;
@@ -197,21 +112,19 @@ __global__ __launch_bounds__(Wide::kThreads, 2) void linear_int8_wide_kernel(
     gq.init(K, K / 2, wave, lane);
     int shift = 0;
     const auto aim = [&](const RowTile& t) {
-        const int e = max(t.e, 0), n0 = t.col * kOuts, outs = t.e < 0 ? 0 : N - n0;
-        const int8_t* const we = w + ((int64_t)e * (kSwiglu ? 2 : 1) * N + n0) * K;
-        gp.half(0, we, outs);
-        if constexpr (kSwiglu) gp.half(1, we + (int64_t)N * K, outs);
+        const int n0 = t.col * kOuts;
+        const int8_t* const we = w + ((int64_t)t.e * (kSwiglu ? 2 : 1) * N + n0) * K;
+        gp.half(0, we, N - n0);
+        if constexpr (kSwiglu) gp.half(1, we + (int64_t)N * K, N - n0);
         gq.half(0, x + (int64_t)t.begin * K, t.end - t.begin);
         shift = rotate ? scattered(blk, nk) : 0;
     };
-    constexpr int kPBytes = T::BP * T::BK * 2, kQBytes = T::BQ * T::BK * 2;
     const auto place = [&](int i) {
         return (shift + i >= nk && shift > 0 ? shift + i - nk : shift + i) * T::BK;
     };
-    // Stages 0 .. kP - 2; the last place of P is the strips' until the outputs are out.
     const auto ask = [&] {
 #pragma unroll
-        for (int i = 0; i < kP - 1; ++i) {
+        for (int i = 0; i < kAsked; ++i) {
             if (i < kQ) gq.load(lq + i * kQBytes, place(i), wave);
             __builtin_amdgcn_sched_barrier(0);
             gp.load(lp + i * kPBytes, place(i), wave);
@@ -219,22 +132,20 @@ __global__ __launch_bounds__(Wide::kThreads, 2) void linear_int8_wide_kernel(
         }
     };
     const auto ask_last = [&] {
-        gp.load(lp + (kP - 1) * kPBytes, place(kP - 1), wave);
+        if constexpr (!kApart) gp.load(lp + (kP - 1) * kPBytes, place(kP - 1), wave);
         __builtin_amdgcn_sched_barrier(0);
     };
-    static_assert(kP == 3 && kQ == 2, "as the waits count them");
+    constexpr int kStage = GQ::kLoads + GP::kLoads, kLast = kApart ? 0 : GP::kLoads;
 
-    constexpr int kRun = T::BP / 2 / T::WP, kRunBlocks = kRun / 16, kRowBytes = kRun * 2 + 16;
     constexpr int kLanes = kRun / 8, kRows = 64 / kLanes, kHalves = kSwiglu ? 1 : 2;
     constexpr int kStores = T::TQ * kHalves * (16 / kRows);
     typedef __attribute__((address_space(3))) u32x4_t lds_u32x4;
     typedef S vec4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) vec4 lds_vec4;
-    // Each wave's strip, and the scales of its 64 rows and 128 outputs.
-    lds_char* const strip = lp + (kP - 1) * kPBytes + wave * (16 * kRowBytes);
-    lds_char* const own = lp + (kP - 1) * kPBytes + T::kWaves * 16 * kRowBytes + wave * 768;
-    static_assert(T::kWaves * (16 * kRowBytes + 768) <= kPBytes, "they fit");
-    static_assert(T::TQ == 4 && kRunBlocks == 4, "64 rows, two runs of 64 outputs");
+    lds_char* const strip = (kApart ? lq + kQ * kQBytes : lp + (kP - 1) * kPBytes) + wave * kOwn;
+    lds_char* const own = strip + 16 * kRowBytes;
+    lds_char* const own_w = own + T::TQ * 64;
+    static_assert(T::TQ == 4, "64 rows: a scale each for a lane");
     const auto load_scale = [&](__amdgpu_buffer_rsrc_t rs, lds_char* to, int i) {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)to, 4, i * 4, 0, 0, 0);
     };
@@ -244,8 +155,13 @@ __global__ __launch_bounds__(Wide::kThreads, 2) void linear_int8_wide_kernel(
     if (tile.e < 0) return;
     aim(tile);
     ask();
+    // the stores of the tile before, as the waits count them: outside any range
+#pragma unroll
+    for (int i = 0; i < kStores; ++i)
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{}, make_rsrc(y, 0), (int)(kOutside + i * 16), 0,
+                                               kStream);
+    __builtin_amdgcn_sched_barrier(0);
     ask_last();
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     for (;;) {
         const RowTile cur = tile;
         with_blocks<T::WQ>(cur.end - cur.begin, [&](auto nq) {
@@ -254,20 +170,28 @@ __global__ __launch_bounds__(Wide::kThreads, 2) void linear_int8_wide_kernel(
             const Loop loop(wp, wq, lane_here(), shift, nk);
             i32x4 acc[T::TP][T::TQ] = {};
             s16x8 p0[T::TP], q0[T::TQ], p1[T::TP], q1[T::TQ];
-            Loop::template barrier<GQ::kLoads + 2 * GP::kLoads + kStores>();
+            Loop::template barrier<kStage + kStores + kLast>();
             loop.frags(lp, lq, 0, p0, q0);
             int pb = 0, qb = 0;
-#pragma clang loop unroll(disable)
-            for (int it = 0; it + 1 < nk; ++it) {
+            const auto stage = [&](int it) {
                 lds_char* const rp = lp + pb * kPBytes;
                 lds_char* const rq = lq + qb * kQBytes;
                 pb = pb + 1 == kP ? 0 : pb + 1;
                 qb = qb + 1 == kQ ? 0 : qb + 1;
                 loop.first(rp, rq, p0, q0, p1, q1, acc);
-                if (it == 0) Loop::template barrier<GP::kLoads + kStores>();
-                else Loop::template barrier<GP::kLoads>();
-                loop.second(gp, gq, lp + pb * kPBytes, lq + qb * kQBytes, rp, rq, it, wave, p0, q0, p1,
-                            q1, acc);
+                if (it == 0) Loop::template barrier<kStores + kLast>();
+                else Loop::template barrier<kLast>();
+                loop.second(gp, gq, lp + pb * kPBytes, lq + qb * kQBytes, rp, rq, it, wave, p0, q0,
+                            p1, q1, acc);
+            };
+            // Small tiles: the compiler takes stage 0 out of the loop (8 experts of 256
+            // rows, 7168 -> 4096: 78 us; 81 with it inside); wide ones have no
+            // registers for that.
+            if constexpr (same(T::kTile, kWideTile)) {
+#pragma clang loop unroll(disable)
+                for (int it = 0; it + 1 < nk; ++it) stage(it);
+            } else {
+                for (int it = 0; it + 1 < nk; ++it) stage(it);
             }
             const int ln = lane_here();
             const TileSearch::Entries entries = search.ask(ln);
@@ -281,22 +205,27 @@ __global__ __launch_bounds__(Wide::kThreads, 2) void linear_int8_wide_kernel(
             const float* const wse = ws + (int64_t)cur.e * (kSwiglu ? 2 : 1) * N;
             {
                 const __amdgpu_buffer_rsrc_t rx = make_rsrc(xs + cur.begin, rows * 4);
-                const int m = T::q_at(wq, ln >> 4) + (ln & 15), o = wp * kRun + ln;
-                load_scale(rx, own, m);
+                load_scale(rx, own, T::q_at(wq, ln >> 4) + (ln & 15));
+                // run after run of the outputs, gate and up in a gated product
+                const __amdgpu_buffer_rsrc_t rw =
+                    make_rsrc(wse + n0, ((kSwiglu ? 2 * N : N) - n0) * 4);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const __amdgpu_buffer_rsrc_t rw =
-                        make_rsrc(wse + n0 + (kSwiglu && h ? N : 0), (N - n0) * 4);
-                    load_scale(rw, own + (h + 1) * 256, kSwiglu ? o : h * (T::BP / 2) + o);
+                for (int l = 0; l < 2 * kRun; l += 64) {
+                    const int i = l + ln, at = wp * kRun + i % kRun;
+                    load_scale(rw, own_w + l * 4, i < kRun ? at : at + (kSwiglu ? N : T::BP / 2));
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
-            aim(tile);
-            ask();
+            const bool more = tile.e >= 0;
+            if (more) {
+                aim(tile);
+                ask();
+            }
             Loop::products(p1, q1, acc);
             __builtin_amdgcn_sched_barrier(0);
             // the scales are here
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kP - 1) * (GQ::kLoads + GP::kLoads)) : "memory");
+            if (more) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kAsked * kStage) : "memory");
+            else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             const __amdgpu_buffer_rsrc_t out = make_rsrc(y + (int64_t)cur.begin * N, rows * N * 2);
 #pragma unroll
             for (int j = 0; j < T::TQ; ++j) {
@@ -308,11 +237,11 @@ __global__ __launch_bounds__(Wide::kThreads, 2) void linear_int8_wide_kernel(
                             const int i = half * kRunBlocks + b;
                             const float xm = in_lds<float>(own + (j * 16 + (ln & 15)) * 4);
                             f32x4 f = scaled(acc[i][j], xm,
-                                             in_lds<f32x4>(own + 256 + (i * 16 + mine) * 4));
+                                             in_lds<f32x4>(own_w + (i * 16 + mine) * 4));
                             if constexpr (kSwiglu) {
                                 const f32x4 u = scaled(
                                     acc[i + kRunBlocks][j], xm,
-                                    in_lds<f32x4>(own + 512 + (i * 16 + mine) * 4));
+                                    in_lds<f32x4>(own_w + kRun * 4 + (i * 16 + mine) * 4));
 #pragma unroll
                                 for (int r = 0; r < 4; ++r) f[r] = in_fp32(silu(f[r]) * u[r]);
                             }
@@ -331,9 +260,12 @@ __global__ __launch_bounds__(Wide::kThreads, 2) void linear_int8_wide_kernel(
                         const u32x4_t o = in_lds<u32x4_t>(strip + r * kRowBytes + c * 16);
                         const int m = T::q_at(wq, j) + r;
                         const int n = n0 + T::p_at(wp, half * kRunBlocks) + c * 8;
+                        // stores outside have places of their own: the compiler keeps each
+                        const uint32_t outside =
+                            kOutside + ((j * kHalves + half) * (16 / kRows) + h) * 16;
                         const bool in = j < NQ && n < N;
                         __builtin_amdgcn_raw_buffer_store_b128(
-                            o, out, (int)(in ? (uint32_t)(m * N + n) * 2 : kOutside), 0, kStream);
+                            o, out, (int)(in ? (uint32_t)(m * N + n) * 2 : outside), 0, kStream);
                     }
                     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                     __builtin_amdgcn_sched_barrier(0);
@@ -341,9 +273,10 @@ __global__ __launch_bounds__(Wide::kThreads, 2) void linear_int8_wide_kernel(
             }
         });
         if (tile.e < 0) break;
-        // every wave has read its strips
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!kApart) {  // every wave has read its strip
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        }
         ask_last();
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS is left in flight
@@ -770,18 +703,14 @@ struct Int8Product {
         return run(swiglu ? linear_int8_thin_kernel<S, true, T> : linear_int8_thin_kernel<S, false, T>,
                    T::kTile, rotate);
     }
-    hipError_t wide(bool rotate) const {
-        const int64_t total = workgroups(er, kWideTile, outs());
-        return launch_kernel(
-            swiglu ? linear_int8_wide_kernel<S, true> : linear_int8_wide_kernel<S, false>,
-            grid_of(total < kUnits ? total : kUnits), dim3(kWideTile.threads), L, x, xs, w, ws, er, K,
-            N, (int)tiles_of(outs(), kWideTile.outs), y, rotate, (int)total);
-    }
     template <typename T, int kPolicy>
     hipError_t tiles(bool rotate) const {
-        return run(swiglu ? linear_int8_kernel<S, true, T, kPolicy>
-                          : linear_int8_kernel<S, false, T, kPolicy>,
-                   T::kTile, rotate);
+        const int64_t total = workgroups(er, T::kTile, outs());
+        const int64_t most = kUnits * (T::kThreads == 512 ? 1 : 2);
+        return launch_kernel(swiglu ? linear_int8_kernel<S, true, T, kPolicy>
+                                    : linear_int8_kernel<S, false, T, kPolicy>,
+                             grid_of(total < most ? total : most), dim3(T::kThreads), L, x, xs, w, ws,
+                             er, K, N, (int)tiles_of(outs(), T::kTile.outs), y, rotate, (int)total);
     }
 };
 
@@ -797,7 +726,7 @@ hipError_t linear_int8_as(const int8_t* x, const float* xs, const int8_t* w, con
         case Int8Tiles::kOnce: return p.template tiles<Small, kStream>(rotate);
         case Int8Tiles::kDeepOnce: return p.template tiles<Deep, kStream>(rotate);
         case Int8Tiles::kDeep: return p.template tiles<Deep, 0>(rotate);
-        case Int8Tiles::kWide: return p.wide(rotate);
+        case Int8Tiles::kWide: return p.template tiles<Wide, 0>(rotate);
         default: return hipErrorInvalidValue;  // refused before
     }
 }
