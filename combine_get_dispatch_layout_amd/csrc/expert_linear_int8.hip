@@ -120,7 +120,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_int8_kernel(
         shift = rotate ? scattered(blk, nk) : 0;
     };
     const auto place = [&](int i) {
-        return (shift + i >= nk && shift > 0 ? shift + i - nk : shift + i) * T::BK;
+        return (i >= nk ? nk : shift + i >= nk ? shift + i - nk : shift + i) * T::BK;
     };
     const auto ask = [&] {
 #pragma unroll
@@ -282,28 +282,25 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_int8_kernel(
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS is left in flight
 }
 
-// Few rows per expert: the weights' bytes are all that counts.  A tile has BP
-// weight rows (gate and up halves in a gated product) and up to BQ rows of x;
+// Few rows of few experts: the weights' bytes are all that counts.  A tile has 64
+// weight rows (gate and up halves in a gated product) and up to 32 rows of x;
 // each of its 4 waves multiplies a quarter of the weight rows with all of x.
-// Stages of 128 codes go straight into a ring of kStages LDS buffers, all but one
-// of them in flight, the weights in whole cache lines past the caches.
+// Stages of 128 codes go straight into a ring of 6 LDS buffers, all but one of
+// them in flight, the weights in whole cache lines past the caches.  64 experts of
+// 7168 -> 4096, one row each: 267 us, the weights at 7.04 TB/s (loaded through the
+// caches, in pieces of 64 bytes: 318).
 constexpr int kThinRunLog2 = 3;  // as in the 16-bit few-row kernel
-template <int BP_, int BQ_, int kStages_>
 struct Thin {
-    static constexpr int BP = BP_, BQ = BQ_, kStages = kStages_, kWaves = 4;
-    static constexpr TileShape kTile{BQ, BP, kWaves * 64};
+    static constexpr int BP = 64, BQ = 32, kStages = 6, kWaves = 4;
+    static constexpr TileShape kTile{BQ, BP, kWaves * 64};  // 72 KB of LDS: two share a CU
 };
-typedef Thin<64, 32, 6> ThinNarrow;   // 72 KB of LDS each: two workgroups share a CU
-typedef Thin<128, 64, 3> ThinWhole;
-static_assert(same(ThinNarrow::kTile, kNarrowTile) && same(ThinWhole::kTile, kThinTile),
-              "the plan's tiles are the kernels'");
+static_assert(same(Thin::kTile, kNarrowTile), "the plan's tile is the kernel's");
 
-// 64 experts of 7168 -> 4096, one row each: 266 us, the weights at 7.06 TB/s (loaded
-// through the caches, in the first kernel's 64-byte pieces: 318).
-template <typename S, bool kSwiglu, typename T>
-__global__ __launch_bounds__(T::kTile.threads) void linear_int8_thin_kernel(
+template <typename S, bool kSwiglu>
+__global__ __launch_bounds__(Thin::kTile.threads) void linear_int8_thin_kernel(
     const int8_t* x, const float* xs, const int8_t* w, const float* ws, ExpertRows er, int K, int N,
     int cols, S* y, bool rotate) {
+    typedef Thin T;
     constexpr int BP = T::BP, BQ = T::BQ, BK = 64, NW = T::kWaves, R = T::kStages;
     constexpr int TP = BP / 64, TQ = BQ / 16;
     constexpr int kPBytes = BP * BK * 2, kQBytes = BQ * BK * 2;
@@ -693,15 +690,11 @@ struct Int8Product {
     const Launch& L;
 
     int outs() const { return swiglu ? 2 * N : N; }
-    template <typename F>
-    hipError_t run(F kernel, const TileShape& t, bool rotate) const {
-        return launch_kernel(kernel, grid_of(workgroups(er, t, outs())), dim3(t.threads), L, x, xs, w,
-                             ws, er, K, N, (int)tiles_of(outs(), t.outs), y, rotate);
-    }
-    template <typename T>
     hipError_t thin(bool rotate) const {
-        return run(swiglu ? linear_int8_thin_kernel<S, true, T> : linear_int8_thin_kernel<S, false, T>,
-                   T::kTile, rotate);
+        return launch_kernel(
+            swiglu ? linear_int8_thin_kernel<S, true> : linear_int8_thin_kernel<S, false>,
+            grid_of(workgroups(er, kNarrowTile, outs())), dim3(kNarrowTile.threads), L, x, xs, w, ws,
+            er, K, N, (int)tiles_of(outs(), kNarrowTile.outs), y, rotate);
     }
     template <typename T, int kPolicy>
     hipError_t tiles(bool rotate) const {
@@ -721,8 +714,7 @@ hipError_t linear_int8_as(const int8_t* x, const float* xs, const int8_t* w, con
     const Int8Product<S> p{x, xs, w, ws, er, K, N, swiglu, static_cast<S*>(y), L};
     const bool rotate = rotates(expected_rows(er), K / 2);
     switch (int8_tiles(er, p.outs())) {
-        case Int8Tiles::kNarrow: return p.template thin<ThinNarrow>(rotate);
-        case Int8Tiles::kThin: return p.template thin<ThinWhole>(rotate);
+        case Int8Tiles::kNarrow: return p.thin(rotate);
         case Int8Tiles::kOnce: return p.template tiles<Small, kStream>(rotate);
         case Int8Tiles::kDeepOnce: return p.template tiles<Deep, kStream>(rotate);
         case Int8Tiles::kDeep: return p.template tiles<Deep, 0>(rotate);

@@ -28,8 +28,8 @@ struct TileShape {
     int rows, outs, threads;
 };
 constexpr TileShape kFewTile{32, 32, 256}, kSmallTile{128, 128, 256}, kWideTile{256, 256, 512};
-// Of an int8 product of few rows, and of very few workgroups.
-constexpr TileShape kThinTile{64, 128, 256}, kNarrowTile{32, 64, 256};
+// Of an int8 product of few rows and very few workgroups.
+constexpr TileShape kNarrowTile{32, 64, 256};
 // Of a weight gradient: weight rows (N) and columns (K).
 constexpr TileShape kWeightTile{128, 256, 256};
 // The same from rows saved in int8.
@@ -164,76 +164,69 @@ inline Tiles input_gradient_tiles(const ExpertRows& er, int outs) {
                       outs);
 }
 
-// The int8 product's tiles.  kOnce: 128 x 128 with the weights past the caches;
-// kDeep, kDeepOnce: 128 x 128 with three stages of the weights, through the caches
-// and past them.  64 experts with the same number of rows each, us:
-//   rows each                    1    8   16   24   32   40   64   96  128
-//   7168 -> 4096   32 x 64     267  277  287  302  322
-//                  64 x 128    270  281  291  299  309  321  339  661  564
-//                  kOnce       272  275  277  280  281  287  298  328  357
-//                  kDeepOnce   271  276  276  277  277  283  292  326  360
-//                  kDeep                           314  318  323  344  372
-//                  256 x 256                       316  318  321  332  342
-//   2048 -> 1408   64 x 128     34   34   35   36   39   40   42   63   63
-//                  kOnce        39   40   39   40   40   41   43   47   51
-//                  256 x 256                        47   47   48   51   53
+// The int8 product's tiles.  kNarrow: 32 x 64; kOnce: 128 x 128 with the weights
+// past the caches; kDeep, kDeepOnce: 128 x 128 with three stages of the weights,
+// through the caches and past them; kWide: 256 x 256.  64 experts with the same
+// number of rows each, us:
+//   rows each                    1    8   16   32   64   96  128
+//   7168 -> 4096   kNarrow     267  277  287  322
+//                  kOnce       270  275  276  281  298  329  355
+//                  kDeepOnce   268  274  275  276  294  328  358
+//                  kWide       306  311  312  314  320  330  340
+//   4096 -> 4096   kOnce       157  161  163  164  169  185  247
+//                  kDeepOnce   157  162  164  166  171  191  234
+//                  kWide       176  180  181  183  189  196  258
+//   2048 -> 1408   kOnce        38   38   38   38   40   43   47
+//                  kDeepOnce    33   33   33   34   37   41   45
+//                  kWide        44   45   45   45   47   51   53
 // and with rows that vary, as uniform and as skewed routing gives them (4096 ->
 // 4096; on average 8, 12, 16, 32, 64, 80 and 96):
-//   64 x 128    168 162  172 179  175 189  184 219  288 295
-//   kOnce       170 162  171 168  171 172  175 209  182 229  191 264  212 287
-//   kDeepOnce   177 164  178 174  179 177  182 208
-//   256 x 256                                       199 233  201 246  205 255
+//   kOnce       161 153  163 159  163 163  166 198  174 226  181 265  201 283
+//   kDeepOnce   162 151  164 161  165 164  169 190  176 233  186 262  205 284
+//   kWide       180 171  182 177  182 180  185 190  192 231  195 240  198 251
+// A decode batch's slots (64 x 128, 12 live each, 4096 -> 2 x 2048, gated, quantizing
+// included): 172 by kOnce, 177 by kDeepOnce.
 //
 // One or a few tokens ask for the weights of as many experts: up to two
-// workgroups of 64 x 128 per compute unit, 32 x 64 keep more in flight (rows in
-// 1, 8 and 16 experts, 7168 -> 2048: 15 21 37, by 64 x 128 34 35 40, by kDeepOnce 28
-// 31 38; one expert of 32 rows, 8192 -> 8192: 20, 38 and 34).  Where 256 x 256 leave
-// compute units without a tile (8 experts, 7168 -> 4096, 48, 96, 128, 256 and 512
-// rows):
+// workgroups of 128 x 128 per compute unit, 32 x 64 keep more in flight (rows in
+// 1, 8 and 16 experts, 7168 -> 2048: 15 21 37, by kDeepOnce 28 31 38; one expert of 32
+// rows, 8192 -> 8192: 20 and 34).  Where 256 x 256 leave compute units without a
+// tile (8 experts, 7168 -> 4096, 48, 96, 128, 256 and 512 rows):
 //   kOnce           56   58   60   81  148
 //   kDeepOnce       40   44   48   83  148
 //   kDeep           50   54   58   78  134
-//   256 x 256       61   66   69   95  104 (256 tiles)
+//   kWide           61   66   69   95  102 (256 tiles)
 // (Weights that the 256 MB memory-side cache holds from the call before, as a
 // small model's may be, are better read through the caches: 8 of 48 rows, 4096 ->
 // 2048: 20 by kDeep, 23 by kDeepOnce.)
 //
-// Slots may be nearly all empty and every workgroup looks for its tile, so small
-// tiles stay below so many looks at 64 experts (4096 -> 1024; every expert has 4
-// rows, and 8 have one; 32 x 64, 64 x 128, kOnce and 256 x 256, whose workgroups
-// look on until there is no tile left):
-//    64 experts, 128 slots            44   45   51           22   30   34
-//   128 experts, 64 slots       85    84   87   98     15    22   31   34
-//   256 experts, 128 slots     201   167  174  188     64    22   31   34
-//   256 experts, 256 slots     258   182  178  189    121    35   37   34
-//   1024 experts, 128 slots   1236   730  707  721    812   209  125   38
-// Below that, 64 x 128 serve slots of more rows, too: which experts have any is not
-// known.
-constexpr int64_t kNarrowLikely = 32, kThinLikely = 12, kThinLikelySlots = 40;
-constexpr int64_t kOnceLikely = 72, kDeepOnceLikely = 128;
-constexpr int64_t kNarrowLooks = 512, kSlotLooks = 4096;
+// Slots may be nearly all empty (4096 -> 1024; every expert has 4 rows, and 8 have
+// one):
+//                              kNarrow      kOnce   kDeepOnce      kWide
+//    64 experts, 128 slots                  43  29     43  19     49  32
+//   128 experts, 64 slots       85   15     83  30     83  20     94  32
+//   256 experts, 128 slots     201   64    162  30    162  20    181  32
+//   1024 experts, 128 slots   1236  812    628  33    627  23    698  36
+// kNarrow has a workgroup to each tile, and each looks at 64 experts at a time.
+constexpr int64_t kNarrowLikely = 32, kOnceLikely = 80, kDeepOnceLikely = 128;
+constexpr int64_t kNarrowLooks = 512, kOnceLikelySlots = 8;
 
-enum class Int8Tiles { kNarrow, kThin, kOnce, kDeepOnce, kDeep, kWide, kNone };
-
-inline bool slots_serve(const ExpertRows& er, const TileShape& t, int64_t looks) {
-    return er.offsets || max_tiles(er, t.rows) * tiles_of(er.E, 64) <= looks;
-}
+enum class Int8Tiles { kNarrow, kOnce, kDeepOnce, kDeep, kWide, kNone };
 
 inline Int8Tiles int8_tiles(const ExpertRows& er, int outs) {
-    const int64_t likely = expected_rows(er), cols = tiles_of(outs, kThinTile.outs);
+    const int64_t likely = expected_rows(er);
     const int64_t rows = er.offsets ? er.rows : 8 * (int64_t)er.cap;
     const int64_t active = rows < er.E ? rows : er.E;  // experts with rows, at most
+    const int64_t tiles = active * tiles_of(outs, kSmallTile.outs);
+    const int64_t looks = er.offsets ? 0 : max_tiles(er, kNarrowTile.rows) * tiles_of(er.E, 64);
     const auto fits = [&](const TileShape& t) { return grid_fits(workgroups(er, t, outs), t.threads); };
-    if (likely <= kNarrowLikely && active * cols <= 512 &&
-        slots_serve(er, kNarrowTile, kNarrowLooks) && fits(kNarrowTile))
+    if (likely <= kNarrowLikely && tiles <= 512 && looks <= kNarrowLooks && fits(kNarrowTile))
         return Int8Tiles::kNarrow;
-    if (likely <= (er.offsets ? kThinLikely : kThinLikelySlots) &&
-        slots_serve(er, kThinTile, kSlotLooks) && fits(kThinTile))
-        return Int8Tiles::kThin;
+    if (likely <= kOnceLikely && fits(kSmallTile))
+        return tiles >= 1024 && (er.offsets || likely >= kOnceLikelySlots) ? Int8Tiles::kOnce
+                                                                           : Int8Tiles::kDeepOnce;
     if (few_wide_tiles(er, likely, outs) && fits(kSmallTile))
         return likely <= kDeepOnceLikely ? Int8Tiles::kDeepOnce : Int8Tiles::kDeep;
-    if (likely <= kOnceLikely && slots_serve(er, kSmallTile, kSlotLooks) && fits(kSmallTile))
-        return Int8Tiles::kOnce;
     return fits(kWideTile) ? Int8Tiles::kWide : Int8Tiles::kNone;
 }
 

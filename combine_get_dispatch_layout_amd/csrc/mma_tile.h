@@ -398,7 +398,8 @@ struct RingLoop {
     }
     __device__ __forceinline__ int place(int it) const {
         const int s = it + shift;
-        return (kStop && shift == 0 ? s : s - (s >= stages ? stages : 0)) * kBK;
+        const int at = s - (s >= stages ? stages : 0);
+        return (kStop && it >= stages ? stages : at) * kBK;
     }
     __device__ __forceinline__ void frags(const lds_char* lp, const lds_char* lq, int kk,
                                           s16x8 (&p)[TP], s16x8 (&q)[TQ]) const {

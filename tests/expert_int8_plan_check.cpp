@@ -1,7 +1,7 @@
 // Checks the tile choice of the int8 products (expert_plan.h) on the host: over
 // the documented range a choice's grid can be launched (HIP counts a grid's
 // threads in 32 bits), nothing is refused that 256 x 256 tiles can do, the rules'
-// examples are taken, and an expert's rows are all in its 64-row tiles.
+// examples are taken, and an expert's rows are all in its tiles.
 #include <cmath>
 #include <cstdio>
 #include <random>
@@ -36,7 +36,6 @@ static bool check(const ExpertRows& er, int outs) {
     int64_t n = 0;
     switch (got) {
         case Int8Tiles::kNarrow: n = threads(er, 32, 64, 256, outs); break;
-        case Int8Tiles::kThin: n = threads(er, 64, 128, 256, outs); break;
         case Int8Tiles::kOnce:
         case Int8Tiles::kDeepOnce:
         case Int8Tiles::kDeep: n = threads(er, 128, 128, 256, outs); break;
@@ -50,10 +49,15 @@ static bool check(const ExpertRows& er, int outs) {
     return false;
 }
 
-static bool check_split(int64_t count) {
-    const int64_t tiles = row_tiles<64>((int)count), step = row_step<64>((int)count, (int)tiles);
-    return tiles == (count + 63) / 64 && step > 0 && step <= 64 && (tiles - 1) * step < count &&
+template <int BM>
+static bool split(int64_t count) {
+    const int64_t tiles = row_tiles<BM>((int)count), step = row_step<BM>((int)count, (int)tiles);
+    return tiles == (count + BM - 1) / BM && step > 0 && step <= BM && (tiles - 1) * step < count &&
            tiles * step >= count;
+}
+
+static bool check_split(int64_t count) {
+    return split<32>(count) && split<128>(count) && split<256>(count);
 }
 
 int main() {
@@ -63,19 +67,20 @@ int main() {
         Int8Tiles want;
     } examples[] = {
         {with_offsets(64, 8), 4096, Int8Tiles::kNarrow},      // one token's experts
-        {with_offsets(64, 256), 4096, Int8Tiles::kThin},      // a few rows in each
-        {with_offsets(64, 768), 4096, Int8Tiles::kThin},
-        {with_offsets(64, 2048), 4096, Int8Tiles::kOnce},
+        {with_offsets(64, 256), 4096, Int8Tiles::kOnce},      // a few rows in each
+        {with_offsets(64, 256), 1408, Int8Tiles::kDeepOnce},  // about a tile per workgroup
         {with_offsets(64, 4096), 4096, Int8Tiles::kOnce},
         {with_offsets(64, 32768), 4096, Int8Tiles::kWide},
         {with_offsets(8, 512), 4096, Int8Tiles::kDeepOnce},   // too few wide tiles
+        {with_offsets(8, 1024), 4096, Int8Tiles::kDeepOnce},
         {with_offsets(8, 2048), 2048, Int8Tiles::kDeep},
         {with_offsets(1, 256), 8192, Int8Tiles::kDeep},
         {with_offsets(1, 32), 8192, Int8Tiles::kNarrow},
-        {with_counts(64, 128), 4096, Int8Tiles::kThin},       // a decode batch's slots
+        {with_counts(64, 128), 4096, Int8Tiles::kOnce},       // a decode batch's slots
+        {with_counts(64, 32), 4096, Int8Tiles::kDeepOnce},    // a few tokens'
         {with_counts(64, 1), 4096, Int8Tiles::kNarrow},
-        {with_counts(1024, 128), 1024, Int8Tiles::kWide},     // too many looks
-        {with_counts(128, 512), 4096, Int8Tiles::kThin},
+        {with_counts(1024, 128), 1024, Int8Tiles::kDeepOnce},
+        {with_counts(64, 4096), 4096, Int8Tiles::kWide},
         {with_counts(1024, 1 << 20), 16384, Int8Tiles::kNone},
         {with_offsets(1, INT32_MAX), 8, Int8Tiles::kNone},
         {with_offsets(1, ((int64_t)1 << 31) - 513), 8, Int8Tiles::kWide},
