@@ -375,7 +375,8 @@ struct SharedCuLoop {
 // loads into: the compiler then puts no wait of its own before an LDS read, and
 // the one before the barrier is exact.  kPartQ: only the rows of Q that the
 // tile has are loaded (64 experts of 128 rows, 7168 -> 4096: 735 us with all of
-// them, 690 us without; no gain where P is read across r).
+// them, 690 us without; no gain where P is read across r).  kStop: past the
+// last stage nothing is fetched (else the reduction's first stages are, unused).
 template <typename S, int BP, int BQ, int WP, int WQ, int NQ, int kP, int kQ, bool kPartQ,
           typename LP, typename LQ, bool kStop = false>
 struct RingLoop {

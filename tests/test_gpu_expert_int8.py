@@ -213,7 +213,7 @@ CASES += [([2, 1, 0, 17, 3], 8192, 72), ([9, 12, 30], 4096, 136),
 CASES += [([256, 100, 0, 300, 280, 511, 256, 200], k, 2056) for k in (16, 272, 1040, 4112)]
 CASES += [([60, 70, 0, 129, 61, 90, 33, 64], k, 4104) for k in (16, 272, 4096)]
 CASES += [([60, 70, 0, 129, 61, 90, 33, 64] * 2, k, 4104) for k in (80, 4096)]
-# 64 x 128 tiles: rows of one tile, one more, two; stages fewer and more than the ring
+# a few rows in each expert, about 32 and 64; stages fewer and more than a ring has
 CASES += [([33, 40, 0, 64, 38, 65, 36, 30], k, 136) for k in (16, 272, 400, 4096, 7168)]
 CASES += [([5, 0, 17, 64, 33, 1] * 11, 400, 1032)]
 CASES += [([64, 0, 1, 33, 0, 0, 2, 0, 0, 65, 0, 0, 16, 0, 5, 3] * 4, k, 1032) for k in (16, 272, 400, 8192)]

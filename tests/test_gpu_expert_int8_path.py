@@ -474,3 +474,50 @@ def test_readme_example():
     assert torch.equal(ns["decoded"], ns["served"][:128])
     for leaf, grad in (("x", "d_x"), ("w1", "d_w1"), ("w2", "d_w2"), ("logits", "d_logits")):
         assert ns[grad].shape == ns[leaf].shape and bool(torch.isfinite(ns[grad]).all())
+
+
+def test_many_tiles_captured_and_at_once():
+    """Products whose workgroups go through several tiles: replayed with other rows in
+    each expert, and by two streams at the same time."""
+    dev = device()
+    E_, Kd = 8, 272
+    buf = make_buffer(E_, 1, 1, 1)
+    g = torch.Generator(dev).manual_seed(31)
+    counts = [[1024] * 8, [0, 3000, 1, 700, 65, 0, 4000, 300], [0] * 8, [8192] + [0] * 7]
+    offsets = [torch.tensor([0] + c, device=dev).cumsum(0).int() for c in counts]
+    for N in (2056, 392):  # 256 x 256 and 128 x 128 tiles
+        x = torch.randint(-128, 128, (8192, Kd), generator=g, device=dev, dtype=torch.int8)
+        xs = torch.rand(8192, generator=g, device=dev) * 0.01
+        w = torch.randint(-128, 128, (E_, 2 * N, Kd), generator=g, device=dev, dtype=torch.int8)
+        ws = torch.rand(E_, 2 * N, generator=g, device=dev) * 0.01
+        out = lambda: torch.full((8192, N), 7.0, dtype=torch.bfloat16, device=dev)  # noqa: E731
+        call = lambda o, y: buf.expert_linear_int8(x, xs, w, ws, o, swiglu=True, out=y,  # noqa: E731
+                                                   no_sync=True)
+        want = []
+        for o in offsets:
+            want.append(call(o, out())[0])
+        o, y = offsets[0].clone(), out()
+        graph = torch.cuda.CUDAGraph()
+        call(o, y)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            call(o, y)
+        for turn in range(2):
+            for v, expected in zip(offsets, want):
+                o.copy_(v)
+                y.fill_(7.0)
+                graph.replay()
+                assert torch.equal(y, expected)
+        streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+        torch.cuda.synchronize()
+        got = [[], []]
+        ys = [[out() for _ in range(6)] for _ in streams]
+        torch.cuda.synchronize()
+        for i in range(6):
+            for k, s in enumerate(streams):
+                with torch.cuda.stream(s):
+                    got[k].append(call(offsets[(i + k) % 4], ys[k][i])[0])
+        torch.cuda.synchronize()
+        for i in range(6):
+            for k in range(2):
+                assert torch.equal(got[k][i], want[(i + k) % 4])
