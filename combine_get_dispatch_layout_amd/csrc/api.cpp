@@ -1332,14 +1332,15 @@ int check_rows(const moedx_ctx* ctx, const moedx_expert_rows* er) {
     return MOEDX_OK;
 }
 
+// w_bytes: of one of the weights.
 int check_products(const moedx_ctx* ctx, int dtype, int K, int N, int w_rows_per_out,
-                   const moedx_expert_rows* er) {
+                   const moedx_expert_rows* er, int w_bytes = 2) {
     if (int rc = check_dtype(dtype, false)) return rc;
     if (K < 8 || K % 8 != 0 || K > (1 << 20))
         return fail(MOEDX_EINVAL, "K=%d must be a positive multiple of 8 up to 2^20", K);
     if (N < 8 || N % 8 != 0 || N > (1 << 20))
         return fail(MOEDX_EINVAL, "N=%d must be a positive multiple of 8 up to 2^20", N);
-    if ((int64_t)w_rows_per_out * N * K * 2 >= ((int64_t)1 << 31))
+    if ((int64_t)w_rows_per_out * N * K * w_bytes >= ((int64_t)1 << 31))
         return fail(MOEDX_EINVAL, "an expert's weights (N=%d, K=%d) exceed 2^31 bytes", N, K);
     return check_rows(ctx, er);
 }
@@ -1756,8 +1757,7 @@ int moedx_expert_linear_int8(moedx_ctx* ctx, const int8_t* x, const float* x_sca
     if (swiglu != 0 && swiglu != 1) return fail(MOEDX_EINVAL, "swiglu=%d must be 0 or 1", swiglu);
     if (K < 16 || K % 16 != 0 || K > (1 << 17) - 16)
         return fail(MOEDX_EINVAL, "K=%d must be a positive multiple of 16 up to 2^17 - 16", K);
-    // K / 2 pairs of codes have the bytes of K / 2 values of 16 bits
-    if (int rc = check_products(ctx, dtype, K / 2, N, swiglu ? 2 : 1, er)) return rc;
+    if (int rc = check_products(ctx, dtype, K, N, swiglu ? 2 : 1, er, 1)) return rc;
     if (int rc = check_grid(
             int8_tiles(expert_rows(ctx, er), swiglu ? 2 * N : N) != Int8Tiles::kNone, er, K, N))
         return rc;
