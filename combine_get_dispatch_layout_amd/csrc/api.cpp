@@ -1758,9 +1758,11 @@ int moedx_expert_linear_int8(moedx_ctx* ctx, const int8_t* x, const float* x_sca
     if (K < 16 || K % 16 != 0 || K > (1 << 17) - 16)
         return fail(MOEDX_EINVAL, "K=%d must be a positive multiple of 16 up to 2^17 - 16", K);
     if (int rc = check_products(ctx, dtype, K, N, swiglu ? 2 : 1, er, 1)) return rc;
-    if (int rc = check_grid(
-            int8_tiles(expert_rows(ctx, er), swiglu ? 2 * N : N) != Int8Tiles::kNone, er, K, N))
-        return rc;
+    if (int8_tiles(expert_rows(ctx, er), swiglu ? 2 * N : N) == Int8Tiles::kNone)
+        return fail(MOEDX_EINVAL,
+                    "rows=%lld with K=%d, N=%d are 2^23 or more tiles of 256 x 256, past a grid's "
+                    "limit with a workgroup to each",
+                    (long long)er->rows, K, N);
     if (er->rows > 0 && (!x || !x_scales || !w || !w_scales || !y))
         return fail(MOEDX_EINVAL, "NULL device pointer");
     if (!aligned16(x) || !aligned16(w) || !aligned16(w_scales) || !aligned16(y) ||

@@ -208,6 +208,10 @@ inline Tiles input_gradient_tiles(const ExpertRows& er, int outs) {
 //   256 experts, 128 slots     201   64    162  30    162  20    181  32
 //   1024 experts, 128 slots   1236  812    628  33    627  23    698  36
 // kNarrow has a workgroup to each tile, and each looks at 64 experts at a time.
+//
+// The others launch 512 workgroups at most, but are held to the tiles of a grid
+// with a workgroup to each all the same: the limit is the 16-bit product's, and
+// tile numbers (and what workgroups add to them) stay far below 2^31.
 constexpr int64_t kNarrowLikely = 32, kOnceLikely = 80, kDeepOnceLikely = 128;
 constexpr int64_t kNarrowLooks = 512, kOnceLikelySlots = 8;
 

@@ -617,8 +617,8 @@ MOEDX_API int moedx_expert_sort_int8(moedx_ctx *ctx, const void *x, int dtype, i
  * two fp32 products in this order and one rounding: a row's outputs do not
  * depend on the buffer or its place in it.  swiglu as in moedx_expert_linear (w
  * [E, 2N, K], w_scales [E, 2N]), from the scaled fp32 values.  K a multiple of 16
- * up to 2^17 - 16 (sums of any codes, -128 too, stay within 31 bits); N and
- * the rest as there. */
+ * up to 2^17 - 16 (sums of any codes, -128 too, stay within 31 bits); N, the
+ * tiles below 2^23 and the rest as there, but a w[e] has a byte to each weight. */
 MOEDX_API int moedx_expert_linear_int8(moedx_ctx *ctx, const int8_t *x, const float *x_scales,
                                        const int8_t *w, const float *w_scales, int K, int N,
                                        const moedx_expert_rows *er, int swiglu, void *y, int dtype,

@@ -42,3 +42,13 @@ def test_weights_past_2_gib(linear, K, N, swiglu):
     assert f"N={N}, K={K}" in said and "2^31 bytes" in said, said
     # the next smaller product is taken
     assert linear(K, N - 8 if not swiglu else N - 16, 0, swiglu)[0] == linear.ok
+
+
+def test_too_many_tiles(linear):
+    """The limit is 2^23 tiles of 256 x 256, not the workgroups that the call would
+    launch (512 at most)."""
+    M = (1 << 31) - 1
+    rc, said = linear(16, 8, M)
+    assert rc == linear.refused
+    assert f"rows={M}" in said and "2^23" in said and "256 x 256" in said, said
+    assert "workgroups than a grid has" not in said, said
