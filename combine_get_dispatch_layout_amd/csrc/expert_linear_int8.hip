@@ -673,8 +673,6 @@ __global__ __launch_bounds__(Saved::kThreads, 2) void wgrad_int8_kernel(
     });
 }
 
-constexpr int64_t kUnits = 256;  // compute units
-
 dim3 grid_of(int64_t workgroups) { return dim3((unsigned)workgroups); }
 
 template <typename S>
@@ -699,11 +697,11 @@ struct Int8Product {
     template <typename T, int kPolicy>
     hipError_t tiles(bool rotate) const {
         const int64_t total = workgroups(er, T::kTile, outs());
-        const int64_t most = kUnits * (T::kThreads == 512 ? 1 : 2);
         return launch_kernel(swiglu ? linear_int8_kernel<S, true, T, kPolicy>
                                     : linear_int8_kernel<S, false, T, kPolicy>,
-                             grid_of(total < most ? total : most), dim3(T::kThreads), L, x, xs, w, ws,
-                             er, K, N, (int)tiles_of(outs(), T::kTile.outs), y, rotate, (int)total);
+                             grid_of(workgroups_through(T::kTile, total)), dim3(T::kThreads), L, x, xs,
+                             w, ws, er, K, N, (int)tiles_of(outs(), T::kTile.outs), y, rotate,
+                             (int)total);
     }
 };
 

@@ -4,6 +4,8 @@
 
 #include <stdint.h>
 
+#include "xcd.h"
+
 #if defined(__HIPCC__)
 #define MOEDX_PLAN_HD __host__ __device__
 #else
@@ -65,6 +67,20 @@ inline int64_t workgroups(const ExpertRows& er, const TileShape& t, int outs) {
 inline int64_t weight_workgroups(const ExpertRows& er, int K, int N,
                                  const TileShape& t = kWeightTile) {
     return er.E * tiles_of(N, t.rows) * tiles_of(K, t.outs);
+}
+
+constexpr int kRunLog2 = 5;  // an XCD takes runs of 32 tiles: one per CU, sharing operands in its L2
+
+// Workgroups of a kernel that goes through `total` tiles: one of 512 threads to a
+// compute unit, two of 256.  Workgroup b takes the tiles xcd_run_block(v) for v =
+// b, b + workgroups, ...  Their numbers have to grow: it searches the experts' rows
+// forwards only and ends at the first tile that is not there.  They do among the
+// numbers of one XCD, b % 8, which a multiple of 8 keeps.
+constexpr int64_t kUnits = 256;
+static_assert(kUnits % kXcds == 0, "a workgroup's tiles are those of one XCD");
+inline int64_t workgroups_through(const TileShape& t, int64_t total) {
+    const int64_t most = kUnits * (t.threads == 512 ? 1 : 2);
+    return total < most ? total : most;
 }
 
 // HIP counts a grid's threads in 32 bits.

@@ -36,7 +36,6 @@ static_assert(same(Wide::kTile, kWideTile) && same(Small::kTile, kSmallTile) &&
                   same(Narrow::kTile, kWeightTile),
               "the plan's tiles are the kernels'");
 
-constexpr int kRunLog2 = 5;  // an XCD takes runs of 32 tiles: one per CU, sharing operands in its L2
 constexpr int kRowGroup = 8;  // row tiles that go through the columns together
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
