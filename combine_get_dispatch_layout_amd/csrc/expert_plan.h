@@ -183,46 +183,77 @@ inline Tiles input_gradient_tiles(const ExpertRows& er, int outs) {
 // The int8 product's tiles.  kNarrow: 32 x 64; kOnce: 128 x 128 with the weights
 // past the caches; kDeep, kDeepOnce: 128 x 128 with three stages of the weights,
 // through the caches and past them; kWide: 256 x 256.  64 experts with the same
-// number of rows each, us:
+// number of rows each, us, the weights from memory (other ones in between):
 //   rows each                    1    8   16   32   64   96  128
-//   7168 -> 4096   kNarrow     267  277  287  322
-//                  kOnce       270  275  276  281  298  329  355
-//                  kDeepOnce   268  274  275  276  294  328  358
-//                  kWide       306  311  312  314  320  330  340
-//   4096 -> 4096   kOnce       157  161  163  164  169  185  247
-//                  kDeepOnce   157  162  164  166  171  191  234
-//                  kWide       176  180  181  183  189  196  258
-//   2048 -> 1408   kOnce        38   38   38   38   40   43   47
-//                  kDeepOnce    33   33   33   34   37   41   45
-//                  kWide        44   45   45   45   47   51   53
-// and with rows that vary, as uniform and as skewed routing gives them (4096 ->
-// 4096; on average 8, 12, 16, 32, 64, 80 and 96):
-//   kOnce       161 153  163 159  163 163  166 198  174 226  181 265  201 283
-//   kDeepOnce   162 151  164 161  165 164  169 190  176 233  186 262  205 284
-//   kWide       180 171  182 177  182 180  185 190  192 231  195 240  198 251
-// A decode batch's slots (64 x 128, 12 live each, 4096 -> 2 x 2048, gated, quantizing
-// included): 172 by kOnce, 177 by kDeepOnce.
+//   7168 -> 4096   kNarrow     267  276  287  322
+//                  kOnce       270  276  277  280  299  324  357
+//                  kDeepOnce   269  274  275  276  293  336  358
+//                  kWide       307  310  313  313  321  330  340
+//   4096 -> 4096   kNarrow     163  164  170  186
+//                  kOnce       166  162  163  164  169  184  249
+//                  kDeepOnce   163  163  163  165  170  190  233
+//                  kWide       182  180  181  183  189  196  260
+//   2048 -> 1408   kNarrow      36   35   36   39
+//                  kOnce        40   38   37   37   39   42   46
+//                  kDeepOnce    35   33   33   33   36   39   44
+//                  kWide        47   44   44   44   46   49   51
+// and with rows that vary, as uniform and as skewed routing of top-8 gives them
+// (on average 8, 12, 16, 32, 64, 80, 96 and 128):
+//   4096 -> 4096
+//   kOnce       163 157  163 162  164 164  166 195  172 222  181 264  189 279  334 311
+//   kDeepOnce   163 159  164 164  165 166  166 188  174 229  185 262  196 278  336 307
+//   kWide       180 176  181 182  183 185  184 193  191 234  195 248  198 250  260 266
+//   7168 -> 4096
+//   kOnce                                           302 367  318 437  331 436  552 525
+//   kDeepOnce                                       302 377  325 430  342 438  554 533
+//   kWide                                           322 380  326 384  331 395  348 413
+//   4096 -> 2048
+//   kOnce                                            90 119   94 133   99 148  167 170
+//   kDeepOnce                                        89 114   94 136   98 148  167 156
+//   kWide                                           101 135  102 139  106 143  138 147
+//   2048 -> 1408
+//   kOnce                                            43  43   42  45   43  46   64  61
+//   kDeepOnce                                        39  43   39  46   41  47   62  57
+//   kWide                                            50  48   49  48   49  48   52  55
+//   256 experts, 7168 -> 4096
+//   kOnce                                         1265 1601         1387 1923 2287 2247
+//   kDeepOnce                                     1287 1609         1437 1938 2293 2288
+//   kWide                                         1281 1439         1308 1602 1399 1753
+//   256 experts, 2048 -> 1408
+//   kOnce                                          140  168          147  198  226  229
+//   kDeepOnce                                      138  167          148  196  231  225
+//   kWide                                          150  169          156  193  168  199
+// At 128 the experts past 128 rows take a second 128-row tile, and kWide wins
+// whatever the reduction (with just 128 rows in each, which no routing gives,
+// kDeepOnce: 44 and 51, 233 and 260).  Between 80 and 128 neither does: at 96 kWide
+// takes 20% more than kDeepOnce for 2048 -> 1408 of uniform numbers, 8% for 4096 ->
+// 2048, and up to 17% less for skewed ones.  The rule knows neither the skew nor the
+// reduction.
+//
+// A decode batch's slots (64 x 128, 12 live each, 4096 -> 2 x 2048, gated): 172 by
+// kOnce, 177 by kDeepOnce.  Of 256 experts (128 tokens, top-8, 7168 -> 2 x 2048, gated):
+// 1060 by kDeepOnce, 1075 by kOnce, 1193 by kWide.
 //
 // One or a few tokens ask for the weights of as many experts: up to two
 // workgroups of 128 x 128 per compute unit, 32 x 64 keep more in flight (rows in
-// 1, 8 and 16 experts, 7168 -> 2048: 15 21 37, by kDeepOnce 28 31 38; one expert of 32
-// rows, 8192 -> 8192: 20 and 34).  Where 256 x 256 leave compute units without a
+// 1, 8 and 16 experts, 7168 -> 2048: 14 21 38, by kDeepOnce 27 31 38; one expert of 32
+// rows, 8192 -> 8192: 23 and 33).  Where 256 x 256 leave compute units without a
 // tile (8 experts, 7168 -> 4096, 48, 96, 128, 256 and 512 rows):
-//   kOnce           56   58   60   81  148
-//   kDeepOnce       40   44   48   83  148
-//   kDeep           50   54   58   78  134
-//   kWide           61   66   69   95  102 (256 tiles)
+//   kOnce           56   58   61   81  148
+//   kDeepOnce       39   43   47   82  153
+//   kDeep           44   48   52   77  133
+//   kWide           60   65   68   95  102 (256 tiles)
 // (Weights that the 256 MB memory-side cache holds from the call before, as a
 // small model's may be, are better read through the caches: 8 of 48 rows, 4096 ->
-// 2048: 20 by kDeep, 23 by kDeepOnce.)
+// 2048: 19 by kDeep, 20 by kDeepOnce; from memory 22 and 20.)
 //
 // Slots may be nearly all empty (4096 -> 1024; every expert has 4 rows, and 8 have
 // one):
 //                              kNarrow      kOnce   kDeepOnce      kWide
-//    64 experts, 128 slots                  43  29     43  19     49  32
-//   128 experts, 64 slots       85   15     83  30     83  20     94  32
-//   256 experts, 128 slots     201   64    162  30    162  20    181  32
-//   1024 experts, 128 slots   1236  812    628  33    627  23    698  36
+//    64 experts, 128 slots     47   11     43  29     43  19     50  32
+//   128 experts, 64 slots      86   14     83  29     83  19     94  33
+//   256 experts, 128 slots    201   65    162  30    162  20    182  33
+//   1024 experts, 128 slots  1234  808    629  33    626  22    701  36
 // kNarrow has a workgroup to each tile, and each looks at 64 experts at a time.
 //
 // The others launch 512 workgroups at most, but are held to the tiles of a grid
