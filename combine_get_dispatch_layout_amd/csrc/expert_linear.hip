@@ -269,10 +269,10 @@ __global__ __launch_bounds__(T::kThreads, 2) void dgrad_kernel(const S* d_y, con
 }
 
 template <typename S, typename D>
-__global__ __launch_bounds__(Narrow::kThreads, 2) void wgrad_kernel(const S* d_y, const S* x, ExpertRows er,
-                                                            int K, int N, int cols, int rows,
-                                                            D* d_w) {
-    typedef Narrow T;
+__global__ __launch_bounds__(WeightGrad::kThreads, 2) void wgrad_kernel(const S* d_y, const S* x,
+                                                                        ExpertRows er, int K, int N,
+                                                                        int cols, int rows, D* d_w) {
+    typedef WeightGrad T;
     __shared__ __align__(16) S lp0[T::BP * T::BK], lp1[T::BP * T::BK], lp2[T::BP * T::BK];
     __shared__ __align__(16) S lq0[T::BQ * T::BK], lq1[T::BQ * T::BK], lq2[T::BQ * T::BK];
     int b = xcd_run_block<kRunLog2>((int)blockIdx.x, (int)gridDim.x);
@@ -421,15 +421,15 @@ hipError_t dgrad_as(const void* d_y, const void* w, const ExpertRows& er, int K,
 template <typename S>
 hipError_t wgrad_as(const void* d_y, const void* x, const ExpertRows& er, int K, int N, void* d_w,
                     bool f32_out, const Launch& L) {
-    const int cols = (int)tiles_of(K, Narrow::BP), rows = (int)tiles_of(N, Narrow::BQ);
+    const int cols = (int)tiles_of(K, WeightGrad::BP), rows = (int)tiles_of(N, WeightGrad::BQ);
     const dim3 grid = grid_of(weight_workgroups(er, K, N));
     const S* ds = static_cast<const S*>(d_y);
     const S* xs = static_cast<const S*>(x);
     if (f32_out)
-        return launch_kernel(wgrad_kernel<S, float>, grid, dim3(Narrow::kThreads), L, ds, xs, er, K, N,
-                             cols, rows, static_cast<float*>(d_w));
-    return launch_kernel(wgrad_kernel<S, S>, grid, dim3(Narrow::kThreads), L, ds, xs, er, K, N, cols, rows,
-                         static_cast<S*>(d_w));
+        return launch_kernel(wgrad_kernel<S, float>, grid, dim3(WeightGrad::kThreads), L, ds, xs,
+                             er, K, N, cols, rows, static_cast<float*>(d_w));
+    return launch_kernel(wgrad_kernel<S, S>, grid, dim3(WeightGrad::kThreads), L, ds, xs, er, K,
+                         N, cols, rows, static_cast<S*>(d_w));
 }
 
 template <typename S>

@@ -139,7 +139,6 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_int8_kernel(
 
     constexpr int kLanes = kRun / 8, kRows = 64 / kLanes, kHalves = kSwiglu ? 1 : 2;
     constexpr int kStores = T::TQ * kHalves * (16 / kRows);
-    typedef __attribute__((address_space(3))) u32x4_t lds_u32x4;
     typedef S vec4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) vec4 lds_vec4;
     lds_char* const strip = (kApart ? lq + kQ * kQBytes : lp + (kP - 1) * kPBytes) + wave * kOwn;

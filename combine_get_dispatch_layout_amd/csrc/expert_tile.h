@@ -26,14 +26,14 @@ struct Shape {
     static __device__ __forceinline__ int q_at(int wq, int j) { return q_block<WQ>(wq, j); }
 };
 typedef Shape<256, 256, 4, 64, 3, 2> Wide;
-typedef Shape<256, 128, 2, 32, 3, 3> Narrow;
+typedef Shape<256, 128, 2, 32, 3, 3> WeightGrad;
 typedef Shape<128, 128, 2, 64, 2, 2> Small;
 
 constexpr bool same(const TileShape& a, const TileShape& b) {
     return a.rows == b.rows && a.outs == b.outs && a.threads == b.threads;
 }
 static_assert(same(Wide::kTile, kWideTile) && same(Small::kTile, kSmallTile) &&
-                  same(Narrow::kTile, kWeightTile),
+                  same(WeightGrad::kTile, kWeightTile),
               "the plan's tiles are the kernels'");
 
 constexpr int kRowGroup = 8;  // row tiles that go through the columns together
